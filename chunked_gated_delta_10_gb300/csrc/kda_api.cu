@@ -15,8 +15,6 @@ constexpr size_t kAlign = 256;
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
 // Validate dims; fills the device-side problem description (pointers unset).
 kda_status check_dims(const kda_dims* d, Prob* p) {
     if (!d) return KDA_ERR_INVALID_ARG;
@@ -212,12 +210,12 @@ thread_local const char* t_names[kMaxLaunches];
 thread_local int t_count = 0;
 thread_local const char* t_cuda_err = "no error";
 
+}  // namespace
+
 kda_status cuda_fail(cudaError_t e) {
     t_cuda_err = cudaGetErrorString(e);
     return KDA_ERR_CUDA;
 }
-
-}  // namespace
 
 void begin_launches(cudaStream_t st) {
     t_count = 0;

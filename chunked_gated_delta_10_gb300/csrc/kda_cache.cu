@@ -1,0 +1,177 @@
+// kda_cache_append: new keys and values into a paged cache, keys and queries
+// rotated by their position on the way. Declared in include/kda_serve.h.
+//
+// A rotation turns each pair of channels by the position's angle for that pair,
+//   x' = x cos - y sin,   y' = y cos + x sin,
+// in fp32, rounded once to the cache's type. A thread moves 16-byte units; one
+// that turns channel i with channel i + rope_dim / 2 takes the unit of each.
+//
+// Bound: every new row is read once and written once; for one token a sequence
+// it is the latency of a launch.
+#include "kda_cache.cuh"
+
+namespace kda {
+namespace {
+
+struct AppendArgs {
+    kda_cache c;
+    const void *k, *v, *q;
+    void* q_out;
+    int64_t k_stride, v_stride, q_stride, R, table_stride;
+    int HQ, N;
+    const int64_t* cu;
+    const float* rope;
+    int rope_len, rope_dim, interleaved;
+    const int32_t *table, *kv_lens;
+    int max_pages;
+    int32_t* status;
+};
+
+// The sequence of new row r: the last n with cu[n] <= r.
+__device__ __forceinline__ int seq_of(const int64_t* cu, int N, int64_t r) {
+    int lo = 0, hi = N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (cu[mid] <= r)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+template <typename TI>
+__global__ void __launch_bounds__(256) k_append(AppendArgs a) {
+    constexpr int E = Unit<TI>::n;
+    const int64_t r = blockIdx.x;
+    int64_t n, idx;
+    if (a.cu) {
+        n = seq_of(a.cu, a.N, r);
+        idx = r - a.cu[n];
+    } else {
+        const int64_t per = a.R / a.N;
+        n = r / per;
+        idx = r % per;
+    }
+    const int32_t len = a.kv_lens[n];
+    const int64_t pos = len + idx, pg = pos / a.c.page_size;
+    int64_t page = -1;
+    if (len >= 0) {
+        bool ok = idx >= 0 && pg < a.max_pages && (!a.rope || pos < a.rope_len);
+        if (ok) {
+            page = a.table[n * a.table_stride + pg];
+            ok = page >= 0 && page < a.c.num_pages;
+        }
+        if (!ok) {
+            page = -1;
+            if (a.status && threadIdx.x == 0) *a.status = KDA_ERR_INVALID_ARG;
+        }
+    }
+    const int64_t row = pos % a.c.page_size;
+    // units of a head: the pairs of units that turn together, then the rest
+    const int half = a.interleaved ? 0 : a.rope_dim / 2 / E;
+    const int uk = a.c.K / E - half, uv = a.c.V / E;
+    const int units_q = a.HQ * uk, units_k = a.c.HKV * uk, units = units_q + units_k + a.c.HKV * uv;
+    for (int i = threadIdx.x; i < units; i += blockDim.x) {
+        if (i >= units_q + units_k) {
+            const int j = i - units_q - units_k, h = j / uv, u = j % uv;
+            if (page >= 0) {
+                const TI* src = (const TI*)a.v + r * a.v_stride + h * a.c.V + u * E;
+                TI* dst = (TI*)a.c.v + page * a.c.v_page + row * a.c.v_row + h * a.c.v_head + u * E;
+                *(uint4*)dst = *(const uint4*)src;
+            }
+            continue;
+        }
+        const bool is_q = i < units_q;
+        const int j = is_q ? i : i - units_q, h = j / uk, u = j % uk;
+        if (!is_q && page < 0) continue;
+        const TI* src = is_q ? (const TI*)a.q + r * a.q_stride + h * a.c.K : (const TI*)a.k + r * a.k_stride + h * a.c.K;
+        TI* dst = is_q ? (TI*)a.q_out + (r * a.HQ + h) * a.c.K
+                       : (TI*)a.c.k + page * a.c.k_page + row * a.c.k_row + h * a.c.k_head;
+        float x[E], y[E];
+        if (page < 0) {  // a query row of a dropped or inactive token
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = 0.f;
+            if (u < half) Unit<TI>::store(dst + u * E, x);
+            Unit<TI>::store(dst + (u + half) * E, x);
+            continue;
+        }
+        const float* cs = a.rope + pos * a.rope_dim;
+        if (u < half) {
+            Unit<TI>::load(src + u * E, x);
+            Unit<TI>::load(src + (u + half) * E, y);
+            float co[E], si[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                co[e] = cs[u * E + e];
+                si[e] = cs[a.rope_dim / 2 + u * E + e];
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float t = x[e];
+                x[e] = t * co[e] - y[e] * si[e];
+                y[e] = y[e] * co[e] + t * si[e];
+            }
+            Unit<TI>::store(dst + u * E, x);
+            Unit<TI>::store(dst + (u + half) * E, y);
+            continue;
+        }
+        const int at = (u + half) * E;
+        Unit<TI>::load(src + at, x);
+        if (a.interleaved && at < a.rope_dim) {
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float co = cs[(at + e) / 2], si = cs[a.rope_dim / 2 + (at + e) / 2], t = x[e];
+                x[e] = t * co - x[e + 1] * si;
+                x[e + 1] = x[e + 1] * co + t * si;
+            }
+        }
+        Unit<TI>::store(dst + at, x);
+    }
+}
+
+}  // namespace
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" kda_status kda_cache_append(const kda_cache* c, const void* k, int64_t k_stride, const void* v,
+                                       int64_t v_stride, const void* q, int64_t q_stride, void* q_out, int32_t HQ,
+                                       int32_t N, int64_t R, const int64_t* cu_seqlens, const float* rope,
+                                       int32_t rope_len, int32_t rope_dim, int32_t interleaved,
+                                       const int32_t* page_table, int64_t table_stride, int32_t max_pages,
+                                       const int32_t* kv_lens, int32_t* status, kda_stream_t stream) {
+    const kda_status s = check_cache(c);
+    if (s != KDA_OK) return s;
+    const int64_t unit = c->dtype == KDA_DTYPE_BF16 ? 8 : 4;
+    if (N < 0 || R < 0 || HQ < 0 || max_pages < 0 || table_stride < 0) return KDA_ERR_INVALID_ARG;
+    if (R > 0 && (N == 0 || (!cu_seqlens && R % N != 0))) return KDA_ERR_INVALID_ARG;
+    if ((HQ > 0) != (q != nullptr) && R > 0) return KDA_ERR_INVALID_ARG;
+    if ((q != nullptr) != (q_out != nullptr)) return KDA_ERR_INVALID_ARG;
+    if (k_stride < (int64_t)c->HKV * c->K || v_stride < (int64_t)c->HKV * c->V || k_stride % unit || v_stride % unit)
+        return KDA_ERR_INVALID_ARG;
+    if (q && (q_stride < (int64_t)HQ * c->K || q_stride % unit)) return KDA_ERR_INVALID_ARG;
+    if (q && q == q_out && q_stride != (int64_t)HQ * c->K) return KDA_ERR_INVALID_ARG;
+    if (rope_dim < 0 || rope_dim % 16 != 0 || rope_dim > c->K || rope_len < 0 || (rope != nullptr) != (rope_dim > 0))
+        return KDA_ERR_INVALID_ARG;
+    if (R == 0) return KDA_OK;
+    if (!k || !v || !kv_lens || (!page_table && max_pages > 0)) return KDA_ERR_INVALID_ARG;
+    for (const void* x : {k, v, q, (const void*)q_out, (const void*)rope})
+        if (!aligned16(x)) return KDA_ERR_INVALID_ARG;
+    if (((uintptr_t)page_table & 3u) || ((uintptr_t)kv_lens & 3u) || ((uintptr_t)status & 3u) ||
+        ((uintptr_t)cu_seqlens & 7u))
+        return KDA_ERR_INVALID_ARG;
+    if (R > INT32_MAX || ((int64_t)HQ + 2 * (int64_t)c->HKV) * 32 > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    AppendArgs a{*c, k, v, q, q_out, k_stride, v_stride, q_stride, R, table_stride, HQ, N, cu_seqlens, rope, rope_len,
+                 rope_dim, interleaved, page_table, kv_lens, max_pages, status};
+    cudaStream_t st = (cudaStream_t)stream;
+    begin_launches(st);
+    if (c->dtype == KDA_DTYPE_BF16)
+        k_append<__nv_bfloat16><<<(unsigned)R, 256, 0, st>>>(a);
+    else
+        k_append<float><<<(unsigned)R, 256, 0, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e);
+    note_launch("cache_append", st);
+    return KDA_OK;
+}

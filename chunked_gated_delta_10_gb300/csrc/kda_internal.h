@@ -4,6 +4,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/kda.h"
+
 namespace kda {
 
 struct Prob;
@@ -35,6 +37,11 @@ struct Ws {
 // profiling events, if any, and the launch name).
 void begin_launches(cudaStream_t st);
 void note_launch(const char* name, cudaStream_t st);
+
+// Records the error text for kda_last_cuda_error and returns KDA_ERR_CUDA.
+kda_status cuda_fail(cudaError_t e);
+
+inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 cudaError_t simt_fwd(const Prob& p, bool bf16, const IO& io, const Ws& ws, cudaStream_t st);
 cudaError_t simt_bwd(const Prob& p, bool bf16, const IO& io, const Ws& ws, cudaStream_t st);
