@@ -22,6 +22,9 @@ struct AttendArgs {
     void* o;
     float* lse;
     int32_t* status;
+    int parts;        // CTAs over a sequence's rows
+    float* part_acc;  // [N, HQ, parts, V]: each part's weighted sum, relative to its maximum
+    float2* part_ml;  // [N, HQ, parts]: its maximum (log2 units) and its sum of weights
 };
 
 // The rows [begin, end) that sequence n attends.
@@ -37,81 +40,520 @@ __device__ __forceinline__ void kv_range(const AttendArgs& a, int64_t n, int& be
 __device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
 
 constexpr int kWarps = 4;
+constexpr int kPartRows = 64;        // a part's rows are a multiple: a tile of 16 for each warp
+constexpr int kWantedCtas = 152 * 3; // parts are cut until there are so many CTAs
 
-// One CTA per (query head, sequence); its warps take the rows in turn, a lane
-// holding K / 32 and V / 32 channels.
-template <typename TI, int K, int V>
-__global__ void __launch_bounds__(kWarps * 32) k_attend(AttendArgs a) {
-    constexpr int KL = K / 32, VL = V / 32;
-    __shared__ float sm[kWarps], sl[kWarps], sacc[kWarps][V];
-    const int64_t n = blockIdx.x / a.HQ;
-    const int hq = blockIdx.x % a.HQ, hkv = hq / (a.HQ / a.c.HKV);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    int begin, end;
-    kv_range(a, n, begin, end);
-    float q[KL], acc[VL];
-#pragma unroll
-    for (int i = 0; i < KL; ++i)
-        q[i] = a.scale_log2 * to_f(((const TI*)a.q)[n * a.q_stride + hq * K + lane * KL + i]);
-#pragma unroll
-    for (int i = 0; i < VL; ++i) acc[i] = 0.f;
-    float m = -INFINITY, l = 0.f;
-    for (int t = begin + warp; t < end; t += kWarps) {
-        const int64_t page = a.table[n * a.table_stride + t / a.c.page_size];
-        if (page < 0 || page >= a.c.num_pages) {
-            if (a.status && lane == 0) *a.status = KDA_ERR_INVALID_ARG;
-            continue;
-        }
-        const int64_t row = t % a.c.page_size;
-        const TI* kp = (const TI*)a.c.k + page * a.c.k_page + row * a.c.k_row + hkv * a.c.k_head + lane * KL;
-        const TI* vp = (const TI*)a.c.v + page * a.c.v_page + row * a.c.v_row + hkv * a.c.v_head + lane * VL;
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < KL; ++i) s = fmaf(q[i], to_f(kp[i]), s);
-#pragma unroll
-        for (int w = 16; w > 0; w /= 2) s += __shfl_xor_sync(0xffffffffu, s, w);
-        const float top = fmaxf(m, s), base = finite_base(top);
-        const float keep = exp2f(m - base), p = exp2f(s - base);
-        m = top;
-        l = fmaf(l, keep, p);
-#pragma unroll
-        for (int i = 0; i < VL; ++i) acc[i] = fmaf(acc[i], keep, p * to_f(vp[i]));
-    }
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
-    }
-#pragma unroll
-    for (int i = 0; i < VL; ++i) sacc[warp][lane * VL + i] = acc[i];
-    __syncthreads();
-    float top = sm[0];
-    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm[w]);
-    const float base = finite_base(top);
-    float total = 0.f;
-    for (int w = 0; w < kWarps; ++w) total = fmaf(sl[w], exp2f(sm[w] - base), total);
-    for (int d = threadIdx.x; d < V; d += kWarps * 32) {
-        float x = 0.f;
-        for (int w = 0; w < kWarps; ++w) x = fmaf(sacc[w][d], exp2f(sm[w] - base), x);
-        ((TI*)a.o)[(n * a.HQ + hq) * V + d] = from_f<TI>(total == 0.f ? 0.f : x / total);
-    }
-    if (threadIdx.x == 0 && a.lse) a.lse[n * a.HQ + hq] = (base + log2f(total)) * kLn2;
+// ------------------------------------------------------------------ split
+//
+// The rows of a sequence are cut into equal parts, a CTA each. How many CTAs there are is the host's choice (it knows
+// the sizes but not the lengths); how a sequence's own rows fill them follows from its length on the device.
+
+// Rows [lo, hi) of part s, and the number of parts that hold any.
+__device__ __forceinline__ int part_rows(int begin, int end, int parts, int s, int& lo, int& hi) {
+    const int len = end - begin;
+    int per = (len + parts - 1) / parts;
+    per = (max(per, 1) + kPartRows - 1) / kPartRows * kPartRows;
+    lo = min(begin + s * per, end);
+    hi = min(lo + per, end);
+    return max((len + per - 1) / per, 1);
 }
 
-template <typename TI>
-void launch_attend(const AttendArgs& a, cudaStream_t st) {
-    const unsigned grid = (unsigned)((int64_t)a.N * a.HQ);
+// ------------------------------------------------------------------ rows of a tile
+//
+// R rows in a warp's tile: lane l looks up row l % R. Pages may be of any size, so every row has its own; the lookup
+// of the next tile's pages is in flight while a tile is computed.
+template <int R> struct Rows {
+    const int32_t* table;
+    int hi, row, pg, off, page;      // the next tile's row of this lane
+    int step_pg, step_off, step;
+    int64_t k_off, v_off;            // this tile's row of this lane
+    unsigned valid;                  // bit r: row r is in range and its page exists
+
+    __device__ __forceinline__ Rows(const AttendArgs& a, int64_t n, int lo, int hi_, int stride)
+        : table(a.table + n * a.table_stride), hi(hi_), row(lo + threadIdx.x % 32 % R), step(stride) {
+        pg = row / a.c.page_size;
+        off = row - pg * a.c.page_size;
+        step_pg = stride / a.c.page_size;
+        step_off = stride - step_pg * a.c.page_size;
+        page = row < hi ? table[pg] : -1;
+    }
+    __device__ __forceinline__ void next(const AttendArgs& a, int hkv) {
+        const bool in = row < hi, ok = (unsigned)page < (unsigned)a.c.num_pages;
+        if (in && !ok && a.status) *a.status = KDA_ERR_INVALID_ARG;
+        valid = __ballot_sync(0xffffffffu, ok);
+        const int64_t p = ok ? page : 0;
+        k_off = p * a.c.k_page + off * a.c.k_row;
+        v_off = p * a.c.v_page + off * a.c.v_row;
+        row += step;
+        pg += step_pg;
+        off += step_off;
+        if (off >= a.c.page_size) {
+            off -= a.c.page_size;
+            ++pg;
+        }
+        page = row < hi ? table[pg] : -1;
+    }
+    __device__ __forceinline__ int64_t k_of(int r) const { return __shfl_sync(0xffffffffu, k_off, r); }
+    __device__ __forceinline__ int64_t v_of(int r) const { return __shfl_sync(0xffffffffu, v_off, r); }
+};
+
+__device__ __forceinline__ uint4 load16(const void* p, bool ok) {
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (ok) x = __ldcs((const uint4*)p);
+    return x;
+}
+
+template <int C> __device__ __forceinline__ void load_channels(const float* p, bool ok, float (&x)[C]) {
+    if constexpr (C == 4) {
+        const float4 y = ok ? __ldcs((const float4*)p) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+    } else {
+        const float2 y = ok ? __ldcs((const float2*)p) : make_float2(0.f, 0.f);
+        x[0] = y.x, x[1] = y.y;
+    }
+}
+
+// ------------------------------------------------------------------ joins
+
+// The warps' results for `heads` heads (m, l, and acc relative to m) joined, and written as the result or, with more
+// than one part, as this part's.
+template <typename TI, int V, int HT>
+__device__ __forceinline__ void join_warps(const AttendArgs& a, int64_t n, int h0, int heads, int part, int used,
+                                           const float (*sm)[HT], const float (*sl)[HT],
+                                           const float (*sacc)[HT][V + 4]) {
+    for (int i = threadIdx.x; i < heads * V; i += kWarps * 32) {
+        const int h = i / V, d = i % V;
+        float m = sm[0][h];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sm[w][h]);
+        const float base = finite_base(m);
+        float l = 0.f, x = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = exp2f(sm[w][h] - base);
+            l = fmaf(sl[w][h], f, l);
+            x = fmaf(sacc[w][h][d], f, x);
+        }
+        const int64_t at = n * a.HQ + h0 + h;
+        if (used == 1) {
+            ((TI*)a.o)[at * V + d] = from_f<TI>(l == 0.f ? 0.f : x / l);
+            if (d == 0 && a.lse) a.lse[at] = (base + log2f(l)) * kLn2;
+        } else {
+            a.part_acc[(at * a.parts + part) * V + d] = x;
+            if (d == 0) a.part_ml[at * a.parts + part] = make_float2(m, l);
+        }
+    }
+}
+
+// The parts of one query head, joined in order.
+template <typename TI, int V>
+__global__ void __launch_bounds__(128) k_attend_join(AttendArgs a) {
+    constexpr int G = 128 / (V / 4);  // groups of threads, each taking every G-th part
+    __shared__ float4 sx[G][V / 4];
+    __shared__ float sl[G];
+    const int64_t at = blockIdx.x, n = at / a.HQ;
+    int begin, end, lo, hi;
+    kv_range(a, n, begin, end);
+    const int used = part_rows(begin, end, a.parts, 0, lo, hi);
+    if (used == 1) return;
+    const float2* ml = a.part_ml + at * a.parts;
+    float m = -INFINITY;
+    for (int s = threadIdx.x % 32; s < used; s += 32) m = fmaxf(m, ml[s].x);
+#pragma unroll
+    for (int w = 16; w > 0; w /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+    const float base = finite_base(m);
+    const int g = threadIdx.x / (V / 4), c = threadIdx.x % (V / 4);
+    const float4* acc = (const float4*)(a.part_acc + at * a.parts * V) + c;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 4
+    for (int s = g; s < used; s += G) {
+        const float2 e = ml[s];
+        const float4 y = acc[s * (V / 4)];
+        const float f = exp2f(e.x - base);
+        l = fmaf(e.y, f, l);
+        x.x = fmaf(y.x, f, x.x);
+        x.y = fmaf(y.y, f, x.y);
+        x.z = fmaf(y.z, f, x.z);
+        x.w = fmaf(y.w, f, x.w);
+    }
+    sx[g][c] = x;
+    if (c == 0) sl[g] = l;
+    __syncthreads();
+    if (threadIdx.x < V) {
+        const int d = threadIdx.x;
+        float total = 0.f, y = 0.f;
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            total += sl[i];
+            y += ((const float*)&sx[i][d / 4])[d % 4];
+        }
+        ((TI*)a.o)[at * V + d] = from_f<TI>(total == 0.f ? 0.f : y / total);
+        if (d == 0 && a.lse) a.lse[at] = (base + log2f(total)) * kLn2;
+    }
+}
+
+// ------------------------------------------------------------------ bf16
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of 16-bit values (lane 4 i + j holds columns 2 j, 2 j + 1 of row i), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *(const uint32_t*)&b;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// How far above the running maximum a score may lie (log2 units) before acc and l are rescaled: up to 2^8 is no loss
+// in fp32 or in a pair of bf16 values, and most tiles then only ask whether any score is higher.
+constexpr float kSlack = 8.f;
+
+// Tensor-core kernel: one CTA per (part, up to 8 NT query heads of one cache head, sequence), each warp a tile of 16
+// rows at a time. The products are taken transposed,
+//   S^T [16 rows x 8 heads] = K Q^T,     O^T [V x 8 heads] += V^T P^T,
+// so that the rows of the cache are the 16-row operand and a group's few heads the 8 columns. The cache goes from
+// memory straight to the registers in which mma.sync wants it, with no copy in shared memory:
+//   - lane 4 g + t loads 16-byte units t, t + 4, .. of rows g and g + 8 of K. The order of the channels within the
+//     contraction is free as long as Q has the same.
+//   - of V it loads unit g (and g + 8) of rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9; a byte permutation pairs the rows, and
+//     row i of the product is channel 8 (i % 8) + j of the j-th product.
+//   - P^T comes from S^T by an 8 x 8 transposition in registers; it is split into a pair of bf16 values (2^-16).
+// A tensor core of the fifth generation wants its operands in shared memory and 128 rows in a product; with at most 16
+// query heads against it, the memory's time would cover none of that traffic.
+template <int K, int V, int NT>
+__global__ void __launch_bounds__(kWarps * 32) k_attend_mma(AttendArgs a) {
+    using TI = __nv_bfloat16;
+    constexpr int KI = K / 32, VC = V / 64, VJ = V / 16, HT = 8 * NT;
+    __shared__ float sm[kWarps][HT], sl[kWarps][HT], sacc[kWarps][HT][V + 4];
+    const int part = blockIdx.x % a.parts, group = a.HQ / a.c.HKV, tiles = (group + HT - 1) / HT;
+    const int64_t unit = blockIdx.x / a.parts, n = unit / (a.c.HKV * tiles);
+    const int hkv = (int)(unit / tiles % a.c.HKV), qt = (int)(unit % tiles);
+    const int h0 = hkv * group + qt * HT, heads = min(HT, group - qt * HT);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    int begin, end, lo, hi;
+    kv_range(a, n, begin, end);
+    const int used = part_rows(begin, end, a.parts, part, lo, hi);
+    if (part >= used) return;
+
+    uint4 q[NT][KI];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < KI; ++i)
+            q[j][i] = load16((const TI*)a.q + n * a.q_stride + (h0 + 8 * j + g) * K + (4 * i + t) * 8, 8 * j + g < heads);
+    float acc[NT][VJ][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        m[j][0] = m[j][1] = -INFINITY;
+        l[j][0] = l[j][1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < VJ; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][i][e] = 0.f;
+    }
+    const TI* kh = (const TI*)a.c.k + hkv * a.c.k_head + t * 8;
+    const TI* vh = (const TI*)a.c.v + hkv * a.c.v_head + g * 8;
+    uint4 kr[2][KI], vr[4][VC];
+    Rows<16> rows(a, n, lo + warp * 16, hi, kWarps * 16);
+    auto load_k = [&]() {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const TI* p = kh + rows.k_of(g + 8 * r);
+            const bool ok = rows.valid >> (g + 8 * r) & 1;
+#pragma unroll
+            for (int i = 0; i < KI; ++i) kr[r][i] = load16(p + 32 * i, ok);
+        }
+    };
+    auto load_v = [&]() {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int at = 2 * t + (r & 1) + 4 * (r & 2);
+            const TI* p = vh + rows.v_of(at);
+            const bool ok = rows.valid >> at & 1;
+#pragma unroll
+            for (int i = 0; i < VC; ++i) vr[r][i] = load16(p + 64 * i, ok);
+        }
+    };
+    rows.next(a, hkv);
+    load_k();
+    load_v();
+    for (int first = lo + warp * 16; first < hi; first += kWarps * 16) {
+        float s[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+#pragma unroll
+            for (int i = 0; i < KI; ++i) {
+                mma(s[j], kr[0][i].x, kr[1][i].x, kr[0][i].y, kr[1][i].y, q[j][i].x, q[j][i].y);
+                mma(s[j], kr[0][i].z, kr[1][i].z, kr[0][i].w, kr[1][i].w, q[j][i].z, q[j][i].w);
+            }
+        }
+        const bool in0 = rows.valid >> g & 1, in1 = rows.valid >> (g + 8) & 1;
+        rows.next(a, hkv);
+        load_k();
+        bool higher = false;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[j][e] = (e < 2 ? in0 : in1) ? s[j][e] * a.scale_log2 : -INFINITY;
+                higher |= s[j][e] > m[j][e & 1] + kSlack;
+            }
+        }
+        if (__any_sync(0xffffffffu, higher)) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float top = fmaxf(m[j][e], fmaxf(s[j][e], s[j][e + 2]));
+#pragma unroll
+                    for (int w = 4; w < 32; w *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+                    const float f = ex2(m[j][e] - finite_base(top));
+                    m[j][e] = top;
+                    l[j][e] *= f;
+#pragma unroll
+                    for (int i = 0; i < VJ; ++i) {
+                        acc[j][i][e] *= f;
+                        acc[j][i][e + 2] *= f;
+                    }
+                }
+        }
+        uint32_t hi_p[NT][2], lo_p[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const float b0 = finite_base(m[j][0]), b1 = finite_base(m[j][1]);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float p0 = ex2(s[j][2 * r] - b0), p1 = ex2(s[j][2 * r + 1] - b1);
+                l[j][0] += p0;
+                l[j][1] += p1;
+                const uint32_t h = pack(p0, p1);
+                hi_p[j][r] = transpose8(h);
+                lo_p[j][r] = transpose8(pack(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u)));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VJ; ++i) {
+            // product i: rows 0-7 are channels 8 g + i (V = 64: 8 g + i), rows 8-15 channels 64 + 8 g + i (8 g + i + 4)
+            uint32_t x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int c = VC == 2 ? e & 1 : 0, j = VC == 2 ? i : i + 4 * (e & 1), r = e & 2;
+                const uint32_t* even = (const uint32_t*)&vr[r][c];
+                const uint32_t* odd = (const uint32_t*)&vr[r + 1][c];
+                x[e] = __byte_perm(even[j / 2], odd[j / 2], j % 2 ? 0x7632 : 0x5410);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                mma(acc[j][i], x[0], x[1], x[2], x[3], hi_p[j][0], hi_p[j][1]);
+                mma(acc[j][i], x[0], x[1], x[2], x[3], lo_p[j][0], lo_p[j][1]);
+            }
+        }
+        load_v();
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int h = 8 * j + 2 * t + e;
+#pragma unroll
+            for (int w = 4; w < 32; w *= 2) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], w);
+            if (g == 0) {
+                sm[warp][h] = m[j][e];
+                sl[warp][h] = l[j][e];
+            }
+            float* row = &sacc[warp][h][8 * g];
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int i = 0; i < VJ; i += 4)
+                    *(float4*)(row + (VC == 2 ? 64 : 4) * r + i) =
+                        make_float4(acc[j][i][e + 2 * r], acc[j][i + 1][e + 2 * r], acc[j][i + 2][e + 2 * r],
+                                    acc[j][i + 3][e + 2 * r]);
+        }
+    __syncthreads();
+    join_warps<TI, V, HT>(a, n, h0, heads, part, used, sm, sl, sacc);
+}
+
+// ------------------------------------------------------------------ fp32
+
+// FFMA kernel: one CTA per (part, up to HT query heads of one cache head, sequence), each warp R rows at a time, a
+// lane holding K / 32 and V / 32 channels of each row and of every head. The R HT scores are sums over the lanes: a
+// butterfly that halves the values with the lanes leaves value i, summed, in the lanes l with l % (R HT) == i.
+template <int K, int V, int HT, int R>
+__global__ void __launch_bounds__(kWarps * 32) k_attend_simt(AttendArgs a) {
+    constexpr int KL = K / 32, VL = V / 32, NV = R * HT;
+    __shared__ float sm[kWarps][HT], sl[kWarps][HT], sacc[kWarps][HT][V + 4];
+    const int part = blockIdx.x % a.parts, group = a.HQ / a.c.HKV, tiles = (group + HT - 1) / HT;
+    const int64_t unit = blockIdx.x / a.parts, n = unit / (a.c.HKV * tiles);
+    const int hkv = (int)(unit / tiles % a.c.HKV), qt = (int)(unit % tiles);
+    const int h0 = hkv * group + qt * HT, heads = min(HT, group - qt * HT);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    int begin, end, lo, hi;
+    kv_range(a, n, begin, end);
+    const int used = part_rows(begin, end, a.parts, part, lo, hi);
+    if (part >= used) return;
+
+    float q[HT][KL], acc[HT][VL];
+#pragma unroll
+    for (int h = 0; h < HT; ++h) {
+#pragma unroll
+        for (int i = 0; i < KL; ++i)
+            q[h][i] = h < heads ? ((const float*)a.q)[n * a.q_stride + (h0 + h) * K + lane * KL + i] : 0.f;
+#pragma unroll
+        for (int i = 0; i < VL; ++i) acc[h][i] = 0.f;
+    }
+    float m = -INFINITY, l = 0.f;  // of head lane % HT
+    const float* kh = (const float*)a.c.k + hkv * a.c.k_head + lane * KL;
+    const float* vh = (const float*)a.c.v + hkv * a.c.v_head + lane * VL;
+    float kr[R][KL], vr[R][VL];
+    Rows<R> rows(a, n, lo + warp * R, hi, kWarps * R);
+    auto load_k = [&]() {
+#pragma unroll
+        for (int r = 0; r < R; ++r) load_channels<KL>(kh + rows.k_of(r), rows.valid >> r & 1, kr[r]);
+    };
+    auto load_v = [&]() {
+#pragma unroll
+        for (int r = 0; r < R; ++r) load_channels<VL>(vh + rows.v_of(r), rows.valid >> r & 1, vr[r]);
+    };
+    rows.next(a, hkv);
+    load_k();
+    load_v();
+    for (int first = lo + warp * R; first < hi; first += kWarps * R) {
+        float s[NV];  // value r HT + h
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int h = 0; h < HT; ++h) {
+                s[r * HT + h] = q[h][0] * kr[r][0];
+#pragma unroll
+                for (int i = 1; i < KL; ++i) s[r * HT + h] = fmaf(q[h][i], kr[r][i], s[r * HT + h]);
+            }
+        const bool in = rows.valid >> (lane % NV / HT) & 1;
+        rows.next(a, hkv);
+        load_k();
+#pragma unroll
+        for (int w = NV / 2; w > 0; w /= 2)
+#pragma unroll
+            for (int i = 0; i < w; ++i) {
+                const float mine = lane & w ? s[i + w] : s[i], other = lane & w ? s[i] : s[i + w];
+                s[i] = mine + __shfl_xor_sync(0xffffffffu, other, w);
+            }
+#pragma unroll
+        for (int w = NV; w < 32; w *= 2) s[0] += __shfl_xor_sync(0xffffffffu, s[0], w);
+        const float score = in ? s[0] * a.scale_log2 : -INFINITY;
+        if (__any_sync(0xffffffffu, score > m + kSlack)) {
+            float top = fmaxf(m, score);
+#pragma unroll
+            for (int w = HT; w < NV; w *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+            const float f = exp2f(m - finite_base(top));
+            m = top;
+            l *= f;
+#pragma unroll
+            for (int h = 0; h < HT; ++h) {
+                const float fh = __shfl_sync(0xffffffffu, f, h);
+#pragma unroll
+                for (int i = 0; i < VL; ++i) acc[h][i] *= fh;
+            }
+        }
+        const float p = exp2f(score - finite_base(m));
+        l += p;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int h = 0; h < HT; ++h) {
+                const float ph = __shfl_sync(0xffffffffu, p, r * HT + h);
+#pragma unroll
+                for (int i = 0; i < VL; ++i) acc[h][i] = fmaf(ph, vr[r][i], acc[h][i]);
+            }
+        load_v();
+    }
+#pragma unroll
+    for (int w = HT; w < NV; w *= 2) l += __shfl_xor_sync(0xffffffffu, l, w);
+    if (lane < HT) {
+        sm[warp][lane] = m;
+        sl[warp][lane] = l;
+    }
+#pragma unroll
+    for (int h = 0; h < HT; ++h)
+#pragma unroll
+        for (int i = 0; i < VL; ++i) sacc[warp][h][lane * VL + i] = acc[h][i];
+    __syncthreads();
+    join_warps<float, V, HT>(a, n, h0, heads, part, used, sm, sl, sacc);
+}
+
+// ------------------------------------------------------------------ launch
+
+// Query heads that a CTA takes together.
+int head_tile(const kda_cache* c, int HQ) {
+    const int group = HQ / c->HKV;
+    if (c->dtype == KDA_DTYPE_BF16) return group <= 8 ? 8 : 16;
+    return group == 1 ? 1 : group <= 4 ? 4 : 8;
+}
+
+// Parts that each sequence's rows are cut into at most.
+int num_parts(const kda_cache* c, int HQ, int N, int max_pages, int window) {
+    const int group = HQ / c->HKV, ht = head_tile(c, HQ);
+    const int64_t units = (int64_t)N * c->HKV * ((group + ht - 1) / ht);
+    int64_t rows = (int64_t)max_pages * c->page_size;
+    if (window > 0 && window < rows) rows = window;
+    const int64_t most = (rows + kPartRows - 1) / kPartRows;
+    const int64_t want = (kWantedCtas + units - 1) / (units > 0 ? units : 1);
+    const int64_t parts = want < most ? want : most;
+    return parts < 1 ? 1 : (int)parts;
+}
+
+template <int K, int V>
+void launch_kv(const AttendArgs& a, int ht, unsigned grid, cudaStream_t st) {
+    const bool bf16 = a.c.dtype == KDA_DTYPE_BF16;
+    if (bf16 && ht == 8) k_attend_mma<K, V, 1><<<grid, kWarps * 32, 0, st>>>(a);
+    if (bf16 && ht == 16) k_attend_mma<K, V, 2><<<grid, kWarps * 32, 0, st>>>(a);
+    if (!bf16 && ht == 1) k_attend_simt<K, V, 1, 8><<<grid, kWarps * 32, 0, st>>>(a);
+    if (!bf16 && ht == 4) k_attend_simt<K, V, 4, 8><<<grid, kWarps * 32, 0, st>>>(a);
+    if (!bf16 && ht == 8) k_attend_simt<K, V, 8, 4><<<grid, kWarps * 32, 0, st>>>(a);
+}
+
+cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
+    const int ht = head_tile(&a.c, a.HQ), group = a.HQ / a.c.HKV;
+    const unsigned grid = (unsigned)((int64_t)a.N * a.c.HKV * ((group + ht - 1) / ht) * a.parts);
     const int K = a.c.K, V = a.c.V;
-    if (K == 128 && V == 128) k_attend<TI, 128, 128><<<grid, kWarps * 32, 0, st>>>(a);
-    if (K == 128 && V == 64) k_attend<TI, 128, 64><<<grid, kWarps * 32, 0, st>>>(a);
-    if (K == 64 && V == 128) k_attend<TI, 64, 128><<<grid, kWarps * 32, 0, st>>>(a);
-    if (K == 64 && V == 64) k_attend<TI, 64, 64><<<grid, kWarps * 32, 0, st>>>(a);
+    if (K == 128 && V == 128) launch_kv<128, 128>(a, ht, grid, st);
+    if (K == 128 && V == 64) launch_kv<128, 64>(a, ht, grid, st);
+    if (K == 64 && V == 128) launch_kv<64, 128>(a, ht, grid, st);
+    if (K == 64 && V == 64) launch_kv<64, 64>(a, ht, grid, st);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    note_launch("cache_attend", st);
+    if (a.parts == 1) return cudaSuccess;
+    const unsigned heads = (unsigned)((int64_t)a.N * a.HQ);
+    if (a.c.dtype == KDA_DTYPE_BF16)
+        V == 128 ? k_attend_join<__nv_bfloat16, 128><<<heads, 128, 0, st>>>(a)
+                 : k_attend_join<__nv_bfloat16, 64><<<heads, 128, 0, st>>>(a);
+    else
+        V == 128 ? k_attend_join<float, 128><<<heads, 128, 0, st>>>(a) : k_attend_join<float, 64><<<heads, 128, 0, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    note_launch("cache_attend_join", st);
+    return cudaSuccess;
 }
 
 kda_status check_sizes(const kda_cache* c, int32_t HQ, int32_t N, int32_t max_pages, int32_t window) {
     const kda_status s = check_cache(c);
     if (s != KDA_OK) return s;
     if (N < 0 || HQ < 1 || HQ % c->HKV != 0 || max_pages < 0 || window < 0) return KDA_ERR_INVALID_ARG;
-    if ((int64_t)N * HQ > INT32_MAX || (int64_t)max_pages * c->page_size > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if ((int64_t)N * HQ > INT32_MAX || (int64_t)max_pages * c->page_size > (1 << 30)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -122,7 +564,9 @@ using namespace kda;
 
 extern "C" size_t kda_cache_attend_workspace_bytes(const kda_cache* c, int32_t HQ, int32_t N, int32_t max_pages,
                                                    int32_t window) {
-    return check_sizes(c, HQ, N, max_pages, window) == KDA_OK ? 256 : 0;
+    if (check_sizes(c, HQ, N, max_pages, window) != KDA_OK) return 0;
+    const int64_t parts = num_parts(c, HQ, N, max_pages, window);
+    return parts == 1 ? 256 : 256 + (size_t)N * HQ * parts * ((size_t)c->V * sizeof(float) + sizeof(float2));
 }
 
 extern "C" kda_status kda_cache_attend(const kda_cache* c, const void* q, int64_t q_stride, int32_t HQ, int32_t N,
@@ -141,15 +585,12 @@ extern "C" kda_status kda_cache_attend(const kda_cache* c, const void* q, int64_
     if (!ws || !aligned16(ws) || ws_bytes < kda_cache_attend_workspace_bytes(c, HQ, N, max_pages, window))
         return KDA_ERR_WORKSPACE;
     AttendArgs a{*c, q, q_stride, table_stride, HQ, N, max_pages, window, page_table, kv_lens, scale * kLog2e, o, lse,
-                 status};
+                 status, num_parts(c, HQ, N, max_pages, window), nullptr, nullptr};
+    a.part_acc = (float*)ws;
+    a.part_ml = (float2*)(a.part_acc + (int64_t)N * HQ * a.parts * c->V);
     cudaStream_t st = (cudaStream_t)stream;
     begin_launches(st);
-    if (c->dtype == KDA_DTYPE_BF16)
-        launch_attend<__nv_bfloat16>(a, st);
-    else
-        launch_attend<float>(a, st);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_attend(a, st);
     if (e != cudaSuccess) return cuda_fail(e);
-    note_launch("cache_attend", st);
     return KDA_OK;
 }
