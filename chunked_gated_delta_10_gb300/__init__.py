@@ -1,7 +1,9 @@
 """GB300 (sm_103a) chunk-parallel Kimi Delta Attention: forward and backward.
 
-Thin Python binding of the C ABI in ``include/kda.h`` and ``include/kda_serve.h``
-(the single-token operators of serving; ``lib/libkda_gb300.so``, built by :func:`build`). This module only marshals arguments: it checks
+Thin Python binding of the C ABI in ``include/kda.h`` and, for the single-token
+operators of serving, ``include/kda_serve.h`` (``lib/libkda_gb300.so``, built by
+:func:`build`). This module only marshals arguments (those of the single-token
+operators in C++, ``lib/_kda_serve.so``, where a call costs less): it checks
 shapes, allocates outputs and the workspace with PyTorch's caching allocator,
 passes raw device pointers and the current CUDA stream, and turns status codes
 into exceptions. Every step of the computation runs in the library's CUDA
@@ -11,17 +13,18 @@ library raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 from typing import Optional
 
 import torch
 
-from .build import LIB, build  # noqa: F401
+from .build import LIB, SERVE, build  # noqa: F401
 
 __all__ = ["build", "load", "Dims", "prepare_chunks", "workspace_bytes", "saved_bytes", "chunk_fwd", "chunk_bwd",
-           "chunk_fwd_save", "chunk_bwd_from_saved", "step", "cache_append", "cache_attend", "new_cache", "KdaError", "STATUS", "DTYPE_BF16", "DTYPE_F32", "PASS_FWD",
-           "PASS_BWD"]
+           "chunk_fwd_save", "chunk_bwd_from_saved", "step", "new_cache", "cache_append", "cache_attend", "KdaError",
+           "STATUS", "DTYPE_BF16", "DTYPE_F32", "PASS_FWD", "PASS_BWD"]
 
 DTYPE_BF16, DTYPE_F32 = 0, 1
 PASS_FWD, PASS_BWD = 0, 1
@@ -326,22 +329,19 @@ def device_status(ws: torch.Tensor) -> int:
 # ------------------------------------------------------------------ single tokens (include/kda_serve.h)
 
 
-def _dtype_code(t, name):
-    if t.dtype == torch.bfloat16:
-        return DTYPE_BF16
-    if t.dtype == torch.float32:
-        return DTYPE_F32
-    raise TypeError(f"unsupported dtype {t.dtype} of {name}")
+_serve_module = None
 
 
-def _like(t, name, shape, dtype, device):
-    """``t`` must be a contiguous CUDA tensor of this shape and type (None stays None)."""
-    if t is None:
-        return None
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
-    return t.data_ptr()
+def _serve():
+    """The compiled binding of these operators (raises if the library has not been built)."""
+    global _serve_module
+    if _serve_module is None:
+        load()
+        spec = importlib.util.spec_from_file_location("_kda_serve", SERVE)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _serve_module = module
+    return _serve_module
 
 
 def step(q, k, v, g, beta, state, scale=None, slots=None, out=None, status=None):
@@ -351,22 +351,10 @@ def step(q, k, v, g, beta, state, scale=None, slots=None, out=None, status=None)
     [slots,HV,K,V] fp32 (:func:`chunk_fwd`'s ht is one). ``slots`` (int32 [N]) names each sequence's state, a
     negative one marks an inactive row; without it sequence n has state[n]. Returns o [N,T,HV,V] (``out``, if
     given). ``status`` (int32 [1], zeroed by the caller) is set where a slot does not exist."""
-    lib = load()
-    if not q.is_cuda or q.dim() != 4 or v.dim() != 4 or state.dim() != 4:
-        raise ValueError("q, v and state must be CUDA tensors of four dimensions")
-    dt, dev = q.dtype, q.device
-    N, T, H, K = q.shape
-    HV, V = v.shape[2], v.shape[3]
-    dims = StepDims(N, T, H, HV, K, V, state.shape[0], _dtype_code(q, "q"), K ** -0.5 if scale is None else scale)
-    shape_v = (N, T, HV, V)
-    ptrs = (_like(q, "q", q.shape, dt, dev), _like(k, "k", q.shape, dt, dev), _like(v, "v", shape_v, dt, dev),
-            _like(g, "g", (N, T, HV, K), torch.float32, dev), _like(beta, "beta", (N, T, HV), dt, dev),
-            _like(state, "state", (state.shape[0], HV, K, V), torch.float32, dev),
-            _like(slots, "slots", (N,), torch.int32, dev))
-    o = torch.empty(shape_v, dtype=dt, device=dev) if out is None else out
-    _check(lib.kda_step(dims, *ptrs, _like(o, "out", shape_v, dt, dev), _like(status, "status", (1,), torch.int32, dev),
-                        _stream()), "kda_step")
-    return o
+    r = (_serve_module or _serve()).step(q, k, v, g, beta, state, scale, slots, out, status)
+    if type(r) is int:
+        raise KdaError(r, "kda_step")
+    return r
 
 
 def new_cache(num_pages, page_size, heads, K, V, dtype=torch.bfloat16, device="cuda"):
@@ -374,40 +362,6 @@ def new_cache(num_pages, page_size, heads, K, V, dtype=torch.bfloat16, device="c
     of a page contiguous: the layout that :func:`cache_attend` reads in the longest runs."""
     return tuple(torch.zeros(num_pages, heads, page_size, d, dtype=dtype, device=device).transpose(1, 2)
                  for d in (K, V))
-
-
-def _cache(k_cache, v_cache):
-    if not k_cache.is_cuda or k_cache.dim() != 4 or v_cache.dim() != 4:
-        raise ValueError("k_cache and v_cache must be CUDA tensors [pages, page_size, heads, channels]")
-    pages, size, heads, K = k_cache.shape
-    if v_cache.shape[:3] != k_cache.shape[:3] or v_cache.dtype != k_cache.dtype or v_cache.device != k_cache.device:
-        raise ValueError(f"v_cache {v_cache.dtype} {tuple(v_cache.shape)} on {v_cache.device} does not go with k_cache "
-                         f"{k_cache.dtype} {tuple(k_cache.shape)} on {k_cache.device}")
-    ks, vs = k_cache.stride(), v_cache.stride()
-    if ks[3] != 1 or vs[3] != 1:
-        raise ValueError("the channels of a cache row must be contiguous")
-    return Cache(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], pages, size, heads, K,
-                 v_cache.shape[3], _dtype_code(k_cache, "k_cache"))
-
-
-def _rows(t, name, rows, heads, channels, dtype, device):
-    """A [rows, heads, channels] tensor whose rows may lie apart: (pointer, row stride)."""
-    s = t.stride()
-    # (the stride of a dimension of one says nothing)
-    if (t.shape != (rows, heads, channels) or t.dtype != dtype or t.device != device or s[2] != 1 or
-            (s[1] != channels and heads > 1)):
-        raise ValueError(f"{name} must be {dtype} of shape {(rows, heads, channels)} on {device} with contiguous rows, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {s}")
-    return t.data_ptr(), (s[0] if rows > 1 else heads * channels)
-
-
-def _table(page_table, kv_lens, device):
-    """(pointer, row stride, max_pages, kv_lens pointer, N)"""
-    if (page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != device or
-            (page_table.stride(1) != 1 and page_table.shape[1] > 1)):
-        raise ValueError("page_table must be int32 [N, max_pages] with contiguous rows, on the cache's device")
-    N, width = page_table.shape
-    return page_table.data_ptr(), page_table.stride(0), width, _like(kv_lens, "kv_lens", (N,), torch.int32, device), N
 
 
 def cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q=None, rope=None, interleaved=False, cu_seqlens=None,
@@ -420,30 +374,11 @@ def cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q=None, rope=None,
     negative: inactive). ``rope`` fp32 [positions, r]: r/2 cosines, then r/2 sines; channel i turns with i + r/2, or,
     ``interleaved``, 2i with 2i+1. Returns the rotated queries (``q_out``, if given), or None without q.
     ``status`` (int32 [1], zeroed by the caller) is set where a page or position does not exist."""
-    lib = load()
-    cache = _cache(k_cache, v_cache)
-    dt, dev, R = k_cache.dtype, k_cache.device, k.shape[0]
-    kp, ks = _rows(k, "k", R, cache.HKV, cache.K, dt, dev)
-    vp, vs = _rows(v, "v", R, cache.HKV, cache.V, dt, dev)
-    table, table_stride, width, lens, N = _table(page_table, kv_lens, dev)
-    qp, qs, HQ, op = None, 0, 0, None
-    if q is not None:
-        HQ = q.shape[1]
-        qp, qs = _rows(q, "q", R, HQ, cache.K, dt, dev)
-        if q_out is None:
-            q_out = torch.empty((R, HQ, cache.K), dtype=dt, device=dev)
-        op = _like(q_out, "q_out", (R, HQ, cache.K), dt, dev)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    rp, positions, turned = None, 0, 0
-    if rope is not None:
-        positions, turned = rope.shape
-        rp = _like(rope, "rope", (positions, turned), torch.float32, dev)
-    _check(lib.kda_cache_append(cache, kp, ks, vp, vs, qp, qs, op, HQ, N, R,
-                                _like(cu_seqlens, "cu_seqlens", (N + 1,), torch.int64, dev), rp, positions, turned,
-                                int(interleaved), table, table_stride, width, lens,
-                                _like(status, "status", (1,), torch.int32, dev), _stream()), "kda_cache_append")
-    return q_out
+    r = (_serve_module or _serve()).append(k, v, k_cache, v_cache, page_table, kv_lens, q, rope, interleaved, cu_seqlens,
+                                           q_out, status)
+    if type(r) is int:
+        raise KdaError(r, "kda_cache_append")
+    return r
 
 
 def cache_attend(q, k_cache, v_cache, page_table, kv_lens, scale=None, window=0, ws=None, out=None, status=None):
@@ -452,20 +387,7 @@ def cache_attend(q, k_cache, v_cache, page_table, kv_lens, scale=None, window=0,
     q [N,HQ,K]; the cache, ``page_table`` and ``status`` as in :func:`cache_append`; ``kv_lens`` int32 [N], the
     rows to attend, the new token's own among them (none: o is 0 and lse -inf). Returns (o [N,HQ,V], lse fp32
     [N,HQ])."""
-    lib = load()
-    cache = _cache(k_cache, v_cache)
-    dt, dev = k_cache.dtype, k_cache.device
-    table, table_stride, width, lens, N = _table(page_table, kv_lens, dev)
-    HQ = q.shape[1]
-    qp, qs = _rows(q, "q", N, HQ, cache.K, dt, dev)
-    o = torch.empty((N, HQ, cache.V), dtype=dt, device=dev) if out is None else out
-    lse = torch.empty((N, HQ), dtype=torch.float32, device=dev)
-    need = lib.kda_cache_attend_workspace_bytes(cache, HQ, N, width, window)
-    if ws is None or ws.numel() < need:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _check(lib.kda_cache_attend(cache, qp, qs, HQ, N, table, table_stride, width, lens, window,
-                                cache.K ** -0.5 if scale is None else scale,
-                                _like(o, "out", (N, HQ, cache.V), dt, dev), lse.data_ptr(),
-                                _like(status, "status", (1,), torch.int32, dev), ws.data_ptr(), ws.numel(), _stream()),
-           "kda_cache_attend")
-    return o, lse
+    r = (_serve_module or _serve()).attend(q, k_cache, v_cache, page_table, kv_lens, scale, window, ws, out, status)
+    if type(r) is int:
+        raise KdaError(r, "kda_cache_attend")
+    return r
