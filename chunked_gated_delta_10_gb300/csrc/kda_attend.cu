@@ -22,9 +22,9 @@ struct AttendArgs {
     void* o;
     float* lse;
     int32_t* status;
-    int parts;        // CTAs over a sequence's rows
-    float* part_acc;  // [N, HQ, parts, V]: each part's weighted sum, relative to its maximum
-    float2* part_ml;  // [N, HQ, parts]: its maximum (log2 units) and its sum of weights
+    int cluster, slices;  // CTAs of a slice, slices of a sequence's rows
+    float* part_acc;      // [N, HQ, slices, V]: each slice's weighted sum, relative to its maximum
+    float2* part_ml;      // [N, HQ, slices]: its maximum (log2 units) and its sum of weights
 };
 
 // The rows [begin, end) that sequence n attends.
@@ -39,22 +39,33 @@ __device__ __forceinline__ void kv_range(const AttendArgs& a, int64_t n, int& be
 // weight there is 2^-inf = 0 and a NaN score stays a NaN.
 __device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
 
+#ifndef WANT
+#define WANT (152 * 12)
+#endif
+#ifndef MAXC
+#define MAXC 8
+#endif
+#ifndef SLICE_ROWS
+#define SLICE_ROWS 512
+#endif
 constexpr int kWarps = 4;
-constexpr int kPartRows = 64;        // a part's rows are a multiple: a tile of 16 for each warp
-constexpr int kWantedCtas = 152 * 3; // parts are cut until there are so many CTAs
+constexpr int kMaxCluster = MAXC;
+constexpr int kPartRows = 64;  // a part's rows are a multiple: a tile of 16 for each warp
 
 // ------------------------------------------------------------------ split
 //
-// The rows of a sequence are cut into equal parts, a CTA each. How many CTAs there are is the host's choice (it knows
-// the sizes but not the lengths); how a sequence's own rows fill them follows from its length on the device.
+// The rows of a sequence are cut into equal parts, a CTA each. `cluster` neighbouring parts are a slice: a cluster of
+// CTAs that join their results in shared memory. Where a sequence has more than one slice in use, each leaves its
+// result in the workspace and a second kernel joins those. How many parts and slices there are is the host's choice (it
+// knows the sizes but not the lengths); how a sequence's own rows fill them follows from its length on the device.
 
 // Rows [lo, hi) of part s, and the number of parts that hold any.
 __device__ __forceinline__ int part_rows(int begin, int end, int parts, int s, int& lo, int& hi) {
     const int len = end - begin;
     int per = (len + parts - 1) / parts;
     per = (max(per, 1) + kPartRows - 1) / kPartRows * kPartRows;
-    lo = min(begin + s * per, end);
-    hi = min(lo + per, end);
+    lo = (int)min(begin + (int64_t)s * per, (int64_t)end);
+    hi = (int)min((int64_t)lo + per, (int64_t)end);
     return max((len + per - 1) / per, 1);
 }
 
@@ -115,55 +126,109 @@ template <int C> __device__ __forceinline__ void load_channels(const float* p, b
 
 // ------------------------------------------------------------------ joins
 
-// The warps' results for `heads` heads (m, l, and acc relative to m) joined, and written as the result or, with more
-// than one part, as this part's.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The value at shared-memory address p of this cluster's CTA `rank`.
+__device__ __forceinline__ float load_of(const float* p, uint32_t rank) {
+    uint32_t at;
+    float x;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at));
+    return x;
+}
+
+// The results of a CTA's warps for HT heads: maxima m, sums of weights l, and weighted sums acc relative to m.
+template <int HT, int V> struct Partial {
+    float m[kWarps][HT], l[kWarps][HT], acc[kWarps][HT][V + 4];
+    float cta_m[HT], cta_l[HT];
+};
+
+// Joins the warps of a CTA, then the CTAs of its cluster, and writes the result for `heads` heads: the operator's, or,
+// where the sequence has more than one slice in use, this slice's. The order of the sums is fixed.
 template <typename TI, int V, int HT>
-__device__ __forceinline__ void join_warps(const AttendArgs& a, int64_t n, int h0, int heads, int part, int used,
-                                           const float (*sm)[HT], const float (*sl)[HT],
-                                           const float (*sacc)[HT][V + 4]) {
+__device__ __forceinline__ void join_slice(const AttendArgs& a, int64_t n, int h0, int heads, int slice, int slices_used,
+                                           Partial<HT, V>& p) {
+    auto write = [&](int h, int d, float m, float l, float x) {
+        const int64_t at = n * a.HQ + h0 + h;
+        if (slices_used == 1) {
+            ((TI*)a.o)[at * V + d] = from_f<TI>(l == 0.f ? 0.f : x / l);
+            if (d == 0 && a.lse) a.lse[at] = (finite_base(m) + log2f(l)) * kLn2;
+        } else {
+            a.part_acc[(at * a.slices + slice) * V + d] = x;
+            if (d == 0) a.part_ml[at * a.slices + slice] = make_float2(m, l);
+        }
+    };
+    __syncthreads();
     for (int i = threadIdx.x; i < heads * V; i += kWarps * 32) {
         const int h = i / V, d = i % V;
-        float m = sm[0][h];
+        float m = p.m[0][h];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sm[w][h]);
+        for (int w = 1; w < kWarps; ++w) m = fmaxf(m, p.m[w][h]);
         const float base = finite_base(m);
         float l = 0.f, x = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float f = exp2f(sm[w][h] - base);
-            l = fmaf(sl[w][h], f, l);
-            x = fmaf(sacc[w][h][d], f, x);
+            const float f = exp2f(p.m[w][h] - base);
+            l = fmaf(p.l[w][h], f, l);
+            x = fmaf(p.acc[w][h][d], f, x);
         }
-        const int64_t at = n * a.HQ + h0 + h;
-        if (used == 1) {
-            ((TI*)a.o)[at * V + d] = from_f<TI>(l == 0.f ? 0.f : x / l);
-            if (d == 0 && a.lse) a.lse[at] = (base + log2f(l)) * kLn2;
+        if (a.cluster == 1) {
+            write(h, d, m, l, x);
         } else {
-            a.part_acc[(at * a.parts + part) * V + d] = x;
-            if (d == 0) a.part_ml[at * a.parts + part] = make_float2(m, l);
+            p.acc[0][h][d] = x;  // read by this thread only, above
+            if (d == 0) {
+                p.cta_m[h] = m;
+                p.cta_l[h] = l;
+            }
         }
     }
+    if (a.cluster == 1) return;
+    cluster_sync();
+    const int rank = blockIdx.x % a.cluster;
+    for (int i = rank * kWarps * 32 + threadIdx.x; i < heads * V; i += a.cluster * kWarps * 32) {
+        const int h = i / V, d = i % V;
+        float mc[kMaxCluster], m = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            mc[c] = c < a.cluster ? load_of(&p.cta_m[h], c) : -INFINITY;
+            m = fmaxf(m, mc[c]);
+        }
+        const float base = finite_base(m);
+        float l = 0.f, x = 0.f;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            if (c < a.cluster) {
+                const float f = exp2f(mc[c] - base);
+                l = fmaf(load_of(&p.cta_l[h], c), f, l);
+                x = fmaf(load_of(&p.acc[0][h][d], c), f, x);
+            }
+        }
+        write(h, d, m, l, x);
+    }
+    cluster_sync();  // the others may still read this CTA's shared memory
 }
 
-// The parts of one query head, joined in order.
+// The slices of one query head, joined in order.
 template <typename TI, int V>
 __global__ void __launch_bounds__(128) k_attend_join(AttendArgs a) {
     constexpr int G = 128 / (V / 4);  // groups of threads, each taking every G-th part
     __shared__ float4 sx[G][V / 4];
     __shared__ float sl[G];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t at = blockIdx.x, n = at / a.HQ;
     int begin, end, lo, hi;
     kv_range(a, n, begin, end);
-    const int used = part_rows(begin, end, a.parts, 0, lo, hi);
+    const int used = (part_rows(begin, end, a.cluster * a.slices, 0, lo, hi) + a.cluster - 1) / a.cluster;
     if (used == 1) return;
-    const float2* ml = a.part_ml + at * a.parts;
+    const float2* ml = a.part_ml + at * a.slices;
     float m = -INFINITY;
     for (int s = threadIdx.x % 32; s < used; s += 32) m = fmaxf(m, ml[s].x);
 #pragma unroll
     for (int w = 16; w > 0; w /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
     const float base = finite_base(m);
     const int g = threadIdx.x / (V / 4), c = threadIdx.x % (V / 4);
-    const float4* acc = (const float4*)(a.part_acc + at * a.parts * V) + c;
+    const float4* acc = (const float4*)(a.part_acc + at * a.slices * V) + c;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
 #pragma unroll 4
@@ -234,19 +299,21 @@ constexpr float kSlack = 8.f;
 // A tensor core of the fifth generation wants its operands in shared memory and 128 rows in a product; with at most 16
 // query heads against it, the memory's time would cover none of that traffic.
 template <int K, int V, int NT>
-__global__ void __launch_bounds__(kWarps * 32) k_attend_mma(AttendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) k_attend_mma(AttendArgs a) {
     using TI = __nv_bfloat16;
     constexpr int KI = K / 32, VC = V / 64, VJ = V / 16, HT = 8 * NT;
-    __shared__ float sm[kWarps][HT], sl[kWarps][HT], sacc[kWarps][HT][V + 4];
-    const int part = blockIdx.x % a.parts, group = a.HQ / a.c.HKV, tiles = (group + HT - 1) / HT;
-    const int64_t unit = blockIdx.x / a.parts, n = unit / (a.c.HKV * tiles);
+    __shared__ Partial<HT, V> sm;
+    const int parts = a.cluster * a.slices, part = blockIdx.x % parts, slice = part / a.cluster;
+    const int group = a.HQ / a.c.HKV, tiles = (group + HT - 1) / HT;
+    const int64_t unit = blockIdx.x / parts, n = unit / (a.c.HKV * tiles);
     const int hkv = (int)(unit / tiles % a.c.HKV), qt = (int)(unit % tiles);
     const int h0 = hkv * group + qt * HT, heads = min(HT, group - qt * HT);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     int begin, end, lo, hi;
     kv_range(a, n, begin, end);
-    const int used = part_rows(begin, end, a.parts, part, lo, hi);
-    if (part >= used) return;
+    const int used = part_rows(begin, end, parts, part, lo, hi);
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (slice * a.cluster >= used) return;  // so does the whole cluster
 
     uint4 q[NT][KI];
 #pragma unroll
@@ -372,10 +439,10 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend_mma(AttendArgs a) {
 #pragma unroll
             for (int w = 4; w < 32; w *= 2) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], w);
             if (g == 0) {
-                sm[warp][h] = m[j][e];
-                sl[warp][h] = l[j][e];
+                sm.m[warp][h] = m[j][e];
+                sm.l[warp][h] = l[j][e];
             }
-            float* row = &sacc[warp][h][8 * g];
+            float* row = &sm.acc[warp][h][8 * g];
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -384,8 +451,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend_mma(AttendArgs a) {
                         make_float4(acc[j][i][e + 2 * r], acc[j][i + 1][e + 2 * r], acc[j][i + 2][e + 2 * r],
                                     acc[j][i + 3][e + 2 * r]);
         }
-    __syncthreads();
-    join_warps<TI, V, HT>(a, n, h0, heads, part, used, sm, sl, sacc);
+    join_slice<TI, V, HT>(a, n, h0, heads, slice, (used + a.cluster - 1) / a.cluster, sm);
 }
 
 // ------------------------------------------------------------------ fp32
@@ -396,16 +462,18 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend_mma(AttendArgs a) {
 template <int K, int V, int HT, int R>
 __global__ void __launch_bounds__(kWarps * 32) k_attend_simt(AttendArgs a) {
     constexpr int KL = K / 32, VL = V / 32, NV = R * HT;
-    __shared__ float sm[kWarps][HT], sl[kWarps][HT], sacc[kWarps][HT][V + 4];
-    const int part = blockIdx.x % a.parts, group = a.HQ / a.c.HKV, tiles = (group + HT - 1) / HT;
-    const int64_t unit = blockIdx.x / a.parts, n = unit / (a.c.HKV * tiles);
+    __shared__ Partial<HT, V> sm;
+    const int parts = a.cluster * a.slices, part = blockIdx.x % parts, slice = part / a.cluster;
+    const int group = a.HQ / a.c.HKV, tiles = (group + HT - 1) / HT;
+    const int64_t unit = blockIdx.x / parts, n = unit / (a.c.HKV * tiles);
     const int hkv = (int)(unit / tiles % a.c.HKV), qt = (int)(unit % tiles);
     const int h0 = hkv * group + qt * HT, heads = min(HT, group - qt * HT);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     int begin, end, lo, hi;
     kv_range(a, n, begin, end);
-    const int used = part_rows(begin, end, a.parts, part, lo, hi);
-    if (part >= used) return;
+    const int used = part_rows(begin, end, parts, part, lo, hi);
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (slice * a.cluster >= used) return;  // so does the whole cluster
 
     float q[HT][KL], acc[HT][VL];
 #pragma unroll
@@ -484,15 +552,14 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend_simt(AttendArgs a) {
 #pragma unroll
     for (int w = HT; w < NV; w *= 2) l += __shfl_xor_sync(0xffffffffu, l, w);
     if (lane < HT) {
-        sm[warp][lane] = m;
-        sl[warp][lane] = l;
+        sm.m[warp][lane] = m;
+        sm.l[warp][lane] = l;
     }
 #pragma unroll
     for (int h = 0; h < HT; ++h)
 #pragma unroll
-        for (int i = 0; i < VL; ++i) sacc[warp][h][lane * VL + i] = acc[h][i];
-    __syncthreads();
-    join_warps<float, V, HT>(a, n, h0, heads, part, used, sm, sl, sacc);
+        for (int i = 0; i < VL; ++i) sm.acc[warp][h][lane * VL + i] = acc[h][i];
+    join_slice<float, V, HT>(a, n, h0, heads, slice, (used + a.cluster - 1) / a.cluster, sm);
 }
 
 // ------------------------------------------------------------------ launch
@@ -504,47 +571,71 @@ int head_tile(const kda_cache* c, int HQ) {
     return group == 1 ? 1 : group <= 4 ? 4 : 8;
 }
 
-// Parts that each sequence's rows are cut into at most.
-int num_parts(const kda_cache* c, int HQ, int N, int max_pages, int window) {
+// The split of each sequence's rows: CTAs to a cluster, and clusters.
+struct Plan {
+    int cluster, slices;
+};
+Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window) {
     const int group = HQ / c->HKV, ht = head_tile(c, HQ);
-    const int64_t units = (int64_t)N * c->HKV * ((group + ht - 1) / ht);
+    const int64_t units = (int64_t)(N > 0 ? N : 1) * c->HKV * ((group + ht - 1) / ht);
     int64_t rows = (int64_t)max_pages * c->page_size;
     if (window > 0 && window < rows) rows = window;
-    const int64_t most = (rows + kPartRows - 1) / kPartRows;
-    const int64_t want = (kWantedCtas + units - 1) / (units > 0 ? units : 1);
-    const int64_t parts = want < most ? want : most;
-    return parts < 1 ? 1 : (int)parts;
+    const int64_t most = (rows + kPartRows - 1) / kPartRows, want = (WANT + units - 1) / units;
+    Plan p{1, 1};
+    while (p.cluster < kMaxCluster && p.cluster < want && p.cluster < most) p.cluster *= 2;
+    int64_t slices = want / p.cluster;
+    const int64_t fill = rows / ((int64_t)p.cluster * SLICE_ROWS);
+    if (slices > fill) slices = fill;
+    if (slices > 1) p.slices = (int)slices;
+    return p;
 }
 
-template <int K, int V>
-void launch_kv(const AttendArgs& a, int ht, unsigned grid, cudaStream_t st) {
-    const bool bf16 = a.c.dtype == KDA_DTYPE_BF16;
-    if (bf16 && ht == 8) k_attend_mma<K, V, 1><<<grid, kWarps * 32, 0, st>>>(a);
-    if (bf16 && ht == 16) k_attend_mma<K, V, 2><<<grid, kWarps * 32, 0, st>>>(a);
-    if (!bf16 && ht == 1) k_attend_simt<K, V, 1, 8><<<grid, kWarps * 32, 0, st>>>(a);
-    if (!bf16 && ht == 4) k_attend_simt<K, V, 4, 8><<<grid, kWarps * 32, 0, st>>>(a);
-    if (!bf16 && ht == 8) k_attend_simt<K, V, 8, 4><<<grid, kWarps * 32, 0, st>>>(a);
+cudaError_t launch_in(void (*kernel)(AttendArgs), const AttendArgs& a, unsigned grid, int cluster, bool after,
+                      cudaStream_t st) {
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    if (cluster > 1) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = cluster;
+        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
+    if (after) {  // may be set up while the kernel before it runs; it waits for that one's end itself
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++cfg.numAttrs;
+    }
+    if (cluster > 8) {
+        const cudaError_t e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+typedef void (*Kernel)(AttendArgs);
+
+template <int K, int V> Kernel kernel_of(bool bf16, int ht) {
+    if (bf16) return ht == 8 ? k_attend_mma<K, V, 1> : k_attend_mma<K, V, 2>;
+    return ht == 1 ? k_attend_simt<K, V, 1, 8> : ht == 4 ? k_attend_simt<K, V, 4, 8> : k_attend_simt<K, V, 8, 4>;
 }
 
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
-    const int ht = head_tile(&a.c, a.HQ), group = a.HQ / a.c.HKV;
-    const unsigned grid = (unsigned)((int64_t)a.N * a.c.HKV * ((group + ht - 1) / ht) * a.parts);
-    const int K = a.c.K, V = a.c.V;
-    if (K == 128 && V == 128) launch_kv<128, 128>(a, ht, grid, st);
-    if (K == 128 && V == 64) launch_kv<128, 64>(a, ht, grid, st);
-    if (K == 64 && V == 128) launch_kv<64, 128>(a, ht, grid, st);
-    if (K == 64 && V == 64) launch_kv<64, 64>(a, ht, grid, st);
-    cudaError_t e = cudaGetLastError();
+    const bool bf16 = a.c.dtype == KDA_DTYPE_BF16;
+    const int ht = head_tile(&a.c, a.HQ), group = a.HQ / a.c.HKV, K = a.c.K, V = a.c.V;
+    const unsigned grid = (unsigned)((int64_t)a.N * a.c.HKV * ((group + ht - 1) / ht) * a.cluster * a.slices);
+    const Kernel kernel = K == 128 ? (V == 128 ? kernel_of<128, 128>(bf16, ht) : kernel_of<128, 64>(bf16, ht))
+                                   : (V == 128 ? kernel_of<64, 128>(bf16, ht) : kernel_of<64, 64>(bf16, ht));
+    cudaError_t e = launch_in(kernel, a, grid, a.cluster, false, st);
     if (e != cudaSuccess) return e;
     note_launch("cache_attend", st);
-    if (a.parts == 1) return cudaSuccess;
-    const unsigned heads = (unsigned)((int64_t)a.N * a.HQ);
-    if (a.c.dtype == KDA_DTYPE_BF16)
-        V == 128 ? k_attend_join<__nv_bfloat16, 128><<<heads, 128, 0, st>>>(a)
-                 : k_attend_join<__nv_bfloat16, 64><<<heads, 128, 0, st>>>(a);
-    else
-        V == 128 ? k_attend_join<float, 128><<<heads, 128, 0, st>>>(a) : k_attend_join<float, 64><<<heads, 128, 0, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (a.slices == 1) return cudaSuccess;
+    const Kernel join = bf16 ? (V == 128 ? k_attend_join<__nv_bfloat16, 128> : k_attend_join<__nv_bfloat16, 64>)
+                             : (V == 128 ? k_attend_join<float, 128> : k_attend_join<float, 64>);
+    if ((e = launch_in(join, a, (unsigned)((int64_t)a.N * a.HQ), 1, true, st)) != cudaSuccess) return e;
     note_launch("cache_attend_join", st);
     return cudaSuccess;
 }
@@ -565,8 +656,8 @@ using namespace kda;
 extern "C" size_t kda_cache_attend_workspace_bytes(const kda_cache* c, int32_t HQ, int32_t N, int32_t max_pages,
                                                    int32_t window) {
     if (check_sizes(c, HQ, N, max_pages, window) != KDA_OK) return 0;
-    const int64_t parts = num_parts(c, HQ, N, max_pages, window);
-    return parts == 1 ? 256 : 256 + (size_t)N * HQ * parts * ((size_t)c->V * sizeof(float) + sizeof(float2));
+    const int64_t slices = plan_of(c, HQ, N, max_pages, window).slices;
+    return slices == 1 ? 256 : 256 + (size_t)N * HQ * slices * ((size_t)c->V * sizeof(float) + sizeof(float2));
 }
 
 extern "C" kda_status kda_cache_attend(const kda_cache* c, const void* q, int64_t q_stride, int32_t HQ, int32_t N,
@@ -584,10 +675,11 @@ extern "C" kda_status kda_cache_attend(const kda_cache* c, const void* q, int64_
         return KDA_ERR_INVALID_ARG;
     if (!ws || !aligned16(ws) || ws_bytes < kda_cache_attend_workspace_bytes(c, HQ, N, max_pages, window))
         return KDA_ERR_WORKSPACE;
+    const Plan plan = plan_of(c, HQ, N, max_pages, window);
     AttendArgs a{*c, q, q_stride, table_stride, HQ, N, max_pages, window, page_table, kv_lens, scale * kLog2e, o, lse,
-                 status, num_parts(c, HQ, N, max_pages, window), nullptr, nullptr};
+                 status, plan.cluster, plan.slices, nullptr, nullptr};
     a.part_acc = (float*)ws;
-    a.part_ml = (float2*)(a.part_acc + (int64_t)N * HQ * a.parts * c->V);
+    a.part_ml = (float2*)(a.part_acc + (int64_t)N * HQ * a.slices * c->V);
     cudaStream_t st = (cudaStream_t)stream;
     begin_launches(st);
     const cudaError_t e = launch_attend(a, st);
