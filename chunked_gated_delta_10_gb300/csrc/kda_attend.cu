@@ -9,6 +9,9 @@
 // Bound: the cached keys and values are read once.
 #include "kda_cache.cuh"
 
+#ifdef TUNE
+#include <stdlib.h>
+#endif
 namespace kda {
 namespace {
 
@@ -22,9 +25,11 @@ struct AttendArgs {
     void* o;
     float* lse;
     int32_t* status;
-    int cluster, slices;  // CTAs of a slice, slices of a sequence's rows
-    float* part_acc;      // [N, HQ, slices, V]: each slice's weighted sum, relative to its maximum
-    float2* part_ml;      // [N, HQ, slices]: its maximum (log2 units) and its sum of weights
+    int parts;        // CTAs over a sequence's rows
+    int cluster;      // whether the parts of a sequence are a cluster of CTAs, which joins them
+    int turn;         // rows that a CTA takes at a time
+    float* part_acc;  // [N, HQ, parts, V]: each part's weighted sum, relative to its maximum
+    float2* part_ml;  // [N, HQ, parts]: its maximum (log2 units) and its sum of weights
 };
 
 // The rows [begin, end) that sequence n attends.
@@ -39,34 +44,19 @@ __device__ __forceinline__ void kv_range(const AttendArgs& a, int64_t n, int& be
 // weight there is 2^-inf = 0 and a NaN score stays a NaN.
 __device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
 
-#ifndef WANT
-#define WANT (152 * 12)
-#endif
-#ifndef MAXC
-#define MAXC 8
-#endif
-#ifndef SLICE_ROWS
-#define SLICE_ROWS 512
-#endif
-constexpr int kWarps = 4;
-constexpr int kMaxCluster = MAXC;
-constexpr int kPartRows = 64;  // a part's rows are a multiple: a tile of 16 for each warp
-
 // ------------------------------------------------------------------ split
 //
-// The rows of a sequence are cut into equal parts, a CTA each. `cluster` neighbouring parts are a slice: a cluster of
-// CTAs that join their results in shared memory. Where a sequence has more than one slice in use, each leaves its
-// result in the workspace and a second kernel joins those. How many parts and slices there are is the host's choice (it
-// knows the sizes but not the lengths); how a sequence's own rows fill them follows from its length on the device.
+// A CTA takes W R rows at a time, R for each of its W warps, and the CTAs of a sequence, its parts, take them in turn:
+// CTA i the turns i, i + parts, .. So parts are equal whatever the length, and the first rows of a CTA do not depend on
+// it: their pages are looked up while the length is on its way. Where a sequence has more than one part in use, each
+// leaves its result in the workspace and a second kernel joins those. How many parts there are is the host's choice (it
+// knows the sizes but not the lengths).
 
-// Rows [lo, hi) of part s, and the number of parts that hold any.
-__device__ __forceinline__ int part_rows(int begin, int end, int parts, int s, int& lo, int& hi) {
-    const int len = end - begin;
-    int per = (len + parts - 1) / parts;
-    per = (max(per, 1) + kPartRows - 1) / kPartRows * kPartRows;
-    lo = (int)min(begin + (int64_t)s * per, (int64_t)end);
-    hi = (int)min((int64_t)lo + per, (int64_t)end);
-    return max((len + per - 1) / per, 1);
+constexpr int kMaxCluster = 16;
+
+// The parts of a sequence that hold any rows (one at least, which writes the result of a sequence without).
+__device__ __forceinline__ int parts_used(const AttendArgs& a, int rows, int turn) {
+    return max(1, min(a.parts, (rows + turn - 1) / turn));
 }
 
 // ------------------------------------------------------------------ rows of a tile
@@ -75,21 +65,24 @@ __device__ __forceinline__ int part_rows(int begin, int end, int parts, int s, i
 // of the next tile's pages is in flight while a tile is computed.
 template <int R> struct Rows {
     const int32_t* table;
-    int hi, row, pg, off, page;      // the next tile's row of this lane
+    int end, row, pg, off, page;     // the next tile's row of this lane
     int step_pg, step_off, step;
     int64_t k_off, v_off;            // this tile's row of this lane
     unsigned valid;                  // bit r: row r is in range and its page exists
 
-    __device__ __forceinline__ Rows(const AttendArgs& a, int64_t n, int lo, int hi_, int stride)
-        : table(a.table + n * a.table_stride), hi(hi_), row(lo + threadIdx.x % 32 % R), step(stride) {
-        pg = row / a.c.page_size;
+    // Rows from `first` on, `stride` apart; without a window neither depends on the sequence's length.
+    __device__ __forceinline__ void start(const AttendArgs& a, int64_t n, int first, int stride) {
+        table = a.table + n * a.table_stride;
+        row = first + threadIdx.x % 32 % R;
+        step = stride;
+        pg = (unsigned)row / (unsigned)a.c.page_size;
         off = row - pg * a.c.page_size;
-        step_pg = stride / a.c.page_size;
+        step_pg = (unsigned)stride / (unsigned)a.c.page_size;
         step_off = stride - step_pg * a.c.page_size;
-        page = row < hi ? table[pg] : -1;
+        page = pg < a.max_pages ? __ldg(table + pg) : -1;
     }
-    __device__ __forceinline__ void next(const AttendArgs& a, int hkv) {
-        const bool in = row < hi, ok = (unsigned)page < (unsigned)a.c.num_pages;
+    __device__ __forceinline__ void next(const AttendArgs& a) {
+        const bool in = row < end, ok = in && (unsigned)page < (unsigned)a.c.num_pages;
         if (in && !ok && a.status) *a.status = KDA_ERR_INVALID_ARG;
         valid = __ballot_sync(0xffffffffu, ok);
         const int64_t p = ok ? page : 0;
@@ -102,10 +95,40 @@ template <int R> struct Rows {
             off -= a.c.page_size;
             ++pg;
         }
-        page = row < hi ? table[pg] : -1;
+        page = row < end ? __ldg(table + pg) : -1;
     }
     __device__ __forceinline__ int64_t k_of(int r) const { return __shfl_sync(0xffffffffu, k_off, r); }
     __device__ __forceinline__ int64_t v_of(int r) const { return __shfl_sync(0xffffffffu, v_off, r); }
+};
+
+// What a CTA works on, and the rows of this warp: the first lookup is issued before the length is read.
+template <int W, int R, int HT> struct Work {
+    int64_t n;
+    int hkv, h0, heads, part, used, warp, first, end;
+    Rows<R> rows;
+
+    __device__ __forceinline__ bool start(const AttendArgs& a) {
+        const unsigned parts = a.parts, unit = blockIdx.x / parts;
+        const unsigned group = (unsigned)a.HQ / a.c.HKV, tiles = (group + HT - 1) / HT, per = a.c.HKV * tiles;
+        const unsigned qt = unit % tiles;
+        n = unit / per;
+        hkv = unit / tiles % a.c.HKV;
+        h0 = hkv * group + qt * HT;
+        heads = min(HT, (int)(group - qt * HT));
+        part = blockIdx.x % parts;
+        warp = threadIdx.x / 32;
+        first = (part * W + warp) * R;
+        rows.start(a, n, first, parts * W * R);
+        int begin;
+        kv_range(a, n, begin, end);
+        if (begin > 0) {
+            first += begin;
+            rows.start(a, n, first, parts * W * R);
+        }
+        rows.end = end;
+        used = parts_used(a, end - begin, W * R);
+        return part < used;
+    }
 };
 
 __device__ __forceinline__ uint4 load16(const void* p, bool ok) {
@@ -126,136 +149,176 @@ template <int C> __device__ __forceinline__ void load_channels(const float* p, b
 
 // ------------------------------------------------------------------ joins
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The value at shared-memory address p of this cluster's CTA `rank`.
-__device__ __forceinline__ float load_of(const float* p, uint32_t rank) {
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// The address in the cluster's CTA `rank` of what has address p here.
+__device__ __forceinline__ uint32_t cluster_address(const void* p, uint32_t rank) {
     uint32_t at;
-    float x;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at));
-    return x;
+    return at;
+}
+__device__ __forceinline__ void push(float4* p, uint32_t rank, float4 x) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_address(p, rank)), "f"(x.x), "f"(x.y),
+                 "f"(x.z), "f"(x.w)
+                 : "memory");
+}
+__device__ __forceinline__ void push(float2* p, uint32_t rank, float2 x) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_address(p, rank)), "f"(x.x), "f"(x.y) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void add_scaled(float4& x, const float4& y, float f) {
+    x.x = fmaf(y.x, f, x.x);
+    x.y = fmaf(y.y, f, x.y);
+    x.z = fmaf(y.z, f, x.z);
+    x.w = fmaf(y.w, f, x.w);
+}
+// Channels d .. d + 3 of a query head's result.
+template <typename TI> __device__ __forceinline__ void write_result(const AttendArgs& a, int64_t at, int V, int d, float m,
+                                                                    float l, float4 x) {
+    const float f = l == 0.f ? 0.f : 1.f / l;  // nothing attended: x is 0
+    TI* o = (TI*)a.o + at * V + d;
+    if constexpr (sizeof(TI) == 2) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x * f, x.y * f), hi = __floats2bfloat162_rn(x.z * f, x.w * f);
+        *(uint2*)o = make_uint2(*(const uint32_t*)&lo, *(const uint32_t*)&hi);
+    } else {
+        *(float4*)o = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+    }
+    if (d == 0 && a.lse) a.lse[at] = (finite_base(m) + log2f(l)) * kLn2;
 }
 
-// The results of a CTA's warps for HT heads: maxima m, sums of weights l, and weighted sums acc relative to m.
-template <int HT, int V> struct Partial {
-    float m[kWarps][HT], l[kWarps][HT], acc[kWarps][HT][V + 4];
-    float cta_m[HT], cta_l[HT];
+// The results of a CTA's warps for HT heads: maxima m, sums of weights l, and weighted sums acc relative to m. In a
+// cluster: what its CTAs send of the channels that this one joins, and of every head their m and l.
+template <int W, int HT, int V> struct Partial {
+    float m[W][HT], l[W][HT];
+    float4 acc[W][HT][V / 4 + 1];
+    float4 in_acc[HT * V / 4 + kMaxCluster];
+    float2 in_ml[kMaxCluster][HT];
 };
 
-// Joins the warps of a CTA, then the CTAs of its cluster, and writes the result for `heads` heads: the operator's, or,
-// where the sequence has more than one slice in use, this slice's. The order of the sums is fixed.
-template <typename TI, int V, int HT>
-__device__ __forceinline__ void join_slice(const AttendArgs& a, int64_t n, int h0, int heads, int slice, int slices_used,
-                                           Partial<HT, V>& p) {
-    auto write = [&](int h, int d, float m, float l, float x) {
-        const int64_t at = n * a.HQ + h0 + h;
-        if (slices_used == 1) {
-            ((TI*)a.o)[at * V + d] = from_f<TI>(l == 0.f ? 0.f : x / l);
-            if (d == 0 && a.lse) a.lse[at] = (finite_base(m) + log2f(l)) * kLn2;
-        } else {
-            a.part_acc[(at * a.slices + slice) * V + d] = x;
-            if (d == 0) a.part_ml[at * a.slices + slice] = make_float2(m, l);
-        }
-    };
+// Joins the warps of a CTA and, where the parts of a sequence are a cluster, its CTAs, and writes the result for the
+// heads: the operator's, or, where a second kernel is to join the parts, this part's. The order of the sums is fixed.
+template <typename TI, int V, int W, int HT, typename Wk>
+__device__ __forceinline__ void join(const AttendArgs& a, const Wk& wk, Partial<W, HT, V>& p) {
+    const int units = wk.heads * (V / 4), share = (units + a.parts - 1) / a.parts;  // of a CTA of the cluster
+    if (a.cluster) cluster_wait();  // for the others to have started
     __syncthreads();
-    for (int i = threadIdx.x; i < heads * V; i += kWarps * 32) {
-        const int h = i / V, d = i % V;
+    for (int i = threadIdx.x; i < units; i += W * 32) {
+        const int h = i / (V / 4), u = i % (V / 4);
         float m = p.m[0][h];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) m = fmaxf(m, p.m[w][h]);
+        for (int w = 1; w < W; ++w) m = fmaxf(m, p.m[w][h]);
         const float base = finite_base(m);
-        float l = 0.f, x = 0.f;
+        float l = 0.f;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = exp2f(p.m[w][h] - base);
+        for (int w = 0; w < W; ++w) {
+            const float f = ex2(p.m[w][h] - base);
             l = fmaf(p.l[w][h], f, l);
-            x = fmaf(p.acc[w][h][d], f, x);
+            add_scaled(x, p.acc[w][h][u], f);
         }
-        if (a.cluster == 1) {
-            write(h, d, m, l, x);
+        const int64_t at = wk.n * a.HQ + wk.h0 + h;
+        if (a.cluster) {
+            push(&p.in_acc[wk.part * share + i % share], i / share, x);
+            if (u < a.parts) push(&p.in_ml[wk.part][h], u, make_float2(m, l));
+        } else if (wk.used == 1) {
+            write_result<TI>(a, at, V, 4 * u, m, l, x);
         } else {
-            p.acc[0][h][d] = x;  // read by this thread only, above
-            if (d == 0) {
-                p.cta_m[h] = m;
-                p.cta_l[h] = l;
-            }
+            ((float4*)a.part_acc)[(at * a.parts + wk.part) * (V / 4) + u] = x;
+            if (u == 0) a.part_ml[at * a.parts + wk.part] = make_float2(m, l);
         }
     }
-    if (a.cluster == 1) return;
-    cluster_sync();
-    const int rank = blockIdx.x % a.cluster;
-    for (int i = rank * kWarps * 32 + threadIdx.x; i < heads * V; i += a.cluster * kWarps * 32) {
-        const int h = i / V, d = i % V;
-        float mc[kMaxCluster], m = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) {
-            mc[c] = c < a.cluster ? load_of(&p.cta_m[h], c) : -INFINITY;
-            m = fmaxf(m, mc[c]);
-        }
+    if (!a.cluster) return;
+    cluster_arrive();
+    cluster_wait();
+    for (int j = threadIdx.x; j < share && wk.part * share + j < units; j += W * 32) {
+        const int i = wk.part * share + j, h = i / (V / 4), u = i % (V / 4);
+        float m = p.in_ml[0][h].x;
+        for (int c = 1; c < a.parts; ++c) m = fmaxf(m, p.in_ml[c][h].x);
         const float base = finite_base(m);
-        float l = 0.f, x = 0.f;
-#pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) {
-            if (c < a.cluster) {
-                const float f = exp2f(mc[c] - base);
-                l = fmaf(load_of(&p.cta_l[h], c), f, l);
-                x = fmaf(load_of(&p.acc[0][h][d], c), f, x);
-            }
+        float l = 0.f;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int c = 0; c < a.parts; ++c) {
+            const float f = ex2(p.in_ml[c][h].x - base);
+            l = fmaf(p.in_ml[c][h].y, f, l);
+            add_scaled(x, p.in_acc[c * share + j], f);
         }
-        write(h, d, m, l, x);
+        write_result<TI>(a, wk.n * a.HQ + wk.h0 + h, V, 4 * u, m, l, x);
     }
-    cluster_sync();  // the others may still read this CTA's shared memory
 }
 
-// The slices of one query head, joined in order.
+// The parts of one query head, joined in an order that goes by their number alone: group g of the threads takes parts
+// g, g + G, .., eight of them at a time, and the groups are joined in shared memory. The length, which says how many
+// parts there are to join, is on its way together with the first of them.
+constexpr int kJoinThreads = 512, kJoinBatch = 8;
 template <typename TI, int V>
-__global__ void __launch_bounds__(128) k_attend_join(AttendArgs a) {
-    constexpr int G = 128 / (V / 4);  // groups of threads, each taking every G-th part
-    __shared__ float4 sx[G][V / 4];
-    __shared__ float sl[G];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t at = blockIdx.x, n = at / a.HQ;
-    int begin, end, lo, hi;
-    kv_range(a, n, begin, end);
-    const int used = (part_rows(begin, end, a.cluster * a.slices, 0, lo, hi) + a.cluster - 1) / a.cluster;
-    if (used == 1) return;
-    const float2* ml = a.part_ml + at * a.slices;
-    float m = -INFINITY;
-    for (int s = threadIdx.x % 32; s < used; s += 32) m = fmaxf(m, ml[s].x);
-#pragma unroll
-    for (int w = 16; w > 0; w /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-    const float base = finite_base(m);
-    const int g = threadIdx.x / (V / 4), c = threadIdx.x % (V / 4);
-    const float4* acc = (const float4*)(a.part_acc + at * a.slices * V) + c;
+__global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendArgs a) {
+    constexpr int U = V / 4, G = kJoinThreads / U;
+    __shared__ float4 sx[G][U];
+    __shared__ float2 sml[G];
+    const unsigned at = blockIdx.x, n = at / a.HQ;
+    const int g = threadIdx.x / U, u = threadIdx.x % U;
+    after_previous();
+    const float2* ml = a.part_ml + (int64_t)at * a.parts;
+    const float4* acc = (const float4*)a.part_acc + (int64_t)at * a.parts * U + u;
+    float m = -INFINITY, l = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int s = g; s < used; s += G) {
-        const float2 e = ml[s];
-        const float4 y = acc[s * (V / 4)];
-        const float f = exp2f(e.x - base);
-        l = fmaf(e.y, f, l);
-        x.x = fmaf(y.x, f, x.x);
-        x.y = fmaf(y.y, f, x.y);
-        x.z = fmaf(y.z, f, x.z);
-        x.w = fmaf(y.w, f, x.w);
-    }
-    sx[g][c] = x;
-    if (c == 0) sl[g] = l;
-    __syncthreads();
-    if (threadIdx.x < V) {
-        const int d = threadIdx.x;
-        float total = 0.f, y = 0.f;
+    int used = a.parts, s = g;
+    do {
+        float2 e[kJoinBatch];
+        float4 y[kJoinBatch];
 #pragma unroll
-        for (int i = 0; i < G; ++i) {
-            total += sl[i];
-            y += ((const float*)&sx[i][d / 4])[d % 4];
+        for (int i = 0; i < kJoinBatch; ++i) {
+            const bool in = s + i * G < used;
+            e[i] = in ? ml[s + i * G] : make_float2(-INFINITY, 0.f);
+            y[i] = in ? acc[(s + i * G) * U] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        ((TI*)a.o)[at * V + d] = from_f<TI>(total == 0.f ? 0.f : y / total);
-        if (d == 0 && a.lse) a.lse[at] = (base + log2f(total)) * kLn2;
+        if (s == g) {
+            int begin, end;
+            kv_range(a, n, begin, end);
+            used = parts_used(a, end - begin, a.turn);
+        }
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i) {
+            if (s + i * G >= used) {  // what lies there was not written
+                e[i] = make_float2(-INFINITY, 0.f);
+                y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            top = fmaxf(top, e[i].x);
+        }
+        const float base = finite_base(top), keep = ex2(m - base);
+        l *= keep;
+        x = make_float4(x.x * keep, x.y * keep, x.z * keep, x.w * keep);
+        m = top;
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i) {
+            const float f = ex2(e[i].x - base);
+            l = fmaf(e[i].y, f, l);
+            add_scaled(x, y[i], f);
+        }
+        s += G * kJoinBatch;
+    } while (s < used);
+    if (used == 1) return;  // the one part has written the result
+    sx[g][u] = x;
+    if (u == 0) sml[g] = make_float2(m, l);
+    __syncthreads();
+    if (g > 0) return;
+    for (int i = 1; i < G; ++i) m = fmaxf(m, sml[i].x);
+    const float base = finite_base(m);
+    l = 0.f;
+    x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+        const float f = ex2(sml[i].x - base);
+        l = fmaf(sml[i].y, f, l);
+        add_scaled(x, sx[i][u], f);
     }
+    write_result<TI>(a, at, V, 4 * u, m, l, x);
 }
 
 // ------------------------------------------------------------------ bf16
@@ -276,12 +339,6 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *(const uint32_t*)&b;
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // How far above the running maximum a score may lie (log2 units) before acc and l are rescaled: up to 2^8 is no loss
 // in fp32 or in a pair of bf16 values, and most tiles then only ask whether any score is higher.
 constexpr float kSlack = 8.f;
@@ -298,29 +355,24 @@ constexpr float kSlack = 8.f;
 //   - P^T comes from S^T by an 8 x 8 transposition in registers; it is split into a pair of bf16 values (2^-16).
 // A tensor core of the fifth generation wants its operands in shared memory and 128 rows in a product; with at most 16
 // query heads against it, the memory's time would cover none of that traffic.
-template <int K, int V, int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) k_attend_mma(AttendArgs a) {
+template <int K, int V, int NT, int W>
+__global__ void __launch_bounds__(W * 32, W == 8 ? 1 : NT == 1 ? 3 : 2) k_attend_mma(AttendArgs a) {
     using TI = __nv_bfloat16;
     constexpr int KI = K / 32, VC = V / 64, VJ = V / 16, HT = 8 * NT;
-    __shared__ Partial<HT, V> sm;
-    const int parts = a.cluster * a.slices, part = blockIdx.x % parts, slice = part / a.cluster;
-    const int group = a.HQ / a.c.HKV, tiles = (group + HT - 1) / HT;
-    const int64_t unit = blockIdx.x / parts, n = unit / (a.c.HKV * tiles);
-    const int hkv = (int)(unit / tiles % a.c.HKV), qt = (int)(unit % tiles);
-    const int h0 = hkv * group + qt * HT, heads = min(HT, group - qt * HT);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-    int begin, end, lo, hi;
-    kv_range(a, n, begin, end);
-    const int used = part_rows(begin, end, parts, part, lo, hi);
-    asm volatile("griddepcontrol.launch_dependents;");
-    if (slice * a.cluster >= used) return;  // so does the whole cluster
-
+    __shared__ Partial<W, HT, V> sm;
+    const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    Work<W, 16, HT> wk;
+    if (a.cluster) cluster_arrive();
+    after_previous();
+    if (!wk.start(a) && !a.cluster) return;
+    const int h0 = wk.h0, heads = wk.heads, warp = wk.warp;
+    Rows<16>& rows = wk.rows;
     uint4 q[NT][KI];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int i = 0; i < KI; ++i)
-            q[j][i] = load16((const TI*)a.q + n * a.q_stride + (h0 + 8 * j + g) * K + (4 * i + t) * 8, 8 * j + g < heads);
+            q[j][i] = load16((const TI*)a.q + wk.n * a.q_stride + (h0 + 8 * j + g) * K + (4 * i + t) * 8, 8 * j + g < heads);
     float acc[NT][VJ][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -331,10 +383,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) k_attend_mma(Att
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[j][i][e] = 0.f;
     }
-    const TI* kh = (const TI*)a.c.k + hkv * a.c.k_head + t * 8;
-    const TI* vh = (const TI*)a.c.v + hkv * a.c.v_head + g * 8;
+    const TI* kh = (const TI*)a.c.k + wk.hkv * a.c.k_head + t * 8;
+    const TI* vh = (const TI*)a.c.v + wk.hkv * a.c.v_head + g * 8;
     uint4 kr[2][KI], vr[4][VC];
-    Rows<16> rows(a, n, lo + warp * 16, hi, kWarps * 16);
     auto load_k = [&]() {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -354,10 +405,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) k_attend_mma(Att
             for (int i = 0; i < VC; ++i) vr[r][i] = load16(p + 64 * i, ok);
         }
     };
-    rows.next(a, hkv);
+    rows.next(a);
     load_k();
     load_v();
-    for (int first = lo + warp * 16; first < hi; first += kWarps * 16) {
+    for (int first = wk.first; first < wk.end; first += rows.step) {
         float s[NT][4];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -369,7 +420,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) k_attend_mma(Att
             }
         }
         const bool in0 = rows.valid >> g & 1, in1 = rows.valid >> (g + 8) & 1;
-        rows.next(a, hkv);
+        rows.next(a);
         load_k();
         bool higher = false;
 #pragma unroll
@@ -442,7 +493,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) k_attend_mma(Att
                 sm.m[warp][h] = m[j][e];
                 sm.l[warp][h] = l[j][e];
             }
-            float* row = &sm.acc[warp][h][8 * g];
+            float* row = (float*)sm.acc[warp][h] + 8 * g;
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -451,7 +502,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) k_attend_mma(Att
                         make_float4(acc[j][i][e + 2 * r], acc[j][i + 1][e + 2 * r], acc[j][i + 2][e + 2 * r],
                                     acc[j][i + 3][e + 2 * r]);
         }
-    join_slice<TI, V, HT>(a, n, h0, heads, slice, (used + a.cluster - 1) / a.cluster, sm);
+    join<TI>(a, wk, sm);
 }
 
 // ------------------------------------------------------------------ fp32
@@ -459,36 +510,30 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) k_attend_mma(Att
 // FFMA kernel: one CTA per (part, up to HT query heads of one cache head, sequence), each warp R rows at a time, a
 // lane holding K / 32 and V / 32 channels of each row and of every head. The R HT scores are sums over the lanes: a
 // butterfly that halves the values with the lanes leaves value i, summed, in the lanes l with l % (R HT) == i.
-template <int K, int V, int HT, int R>
-__global__ void __launch_bounds__(kWarps * 32) k_attend_simt(AttendArgs a) {
+template <int K, int V, int HT, int R, int W>
+__global__ void __launch_bounds__(W * 32) k_attend_simt(AttendArgs a) {
     constexpr int KL = K / 32, VL = V / 32, NV = R * HT;
-    __shared__ Partial<HT, V> sm;
-    const int parts = a.cluster * a.slices, part = blockIdx.x % parts, slice = part / a.cluster;
-    const int group = a.HQ / a.c.HKV, tiles = (group + HT - 1) / HT;
-    const int64_t unit = blockIdx.x / parts, n = unit / (a.c.HKV * tiles);
-    const int hkv = (int)(unit / tiles % a.c.HKV), qt = (int)(unit % tiles);
-    const int h0 = hkv * group + qt * HT, heads = min(HT, group - qt * HT);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    int begin, end, lo, hi;
-    kv_range(a, n, begin, end);
-    const int used = part_rows(begin, end, parts, part, lo, hi);
-    asm volatile("griddepcontrol.launch_dependents;");
-    if (slice * a.cluster >= used) return;  // so does the whole cluster
-
+    __shared__ Partial<W, HT, V> sm;
+    const int lane = threadIdx.x % 32;
+    Work<W, R, HT> wk;
+    if (a.cluster) cluster_arrive();
+    after_previous();
+    if (!wk.start(a) && !a.cluster) return;
+    const int h0 = wk.h0, heads = wk.heads, warp = wk.warp;
+    Rows<R>& rows = wk.rows;
     float q[HT][KL], acc[HT][VL];
 #pragma unroll
     for (int h = 0; h < HT; ++h) {
 #pragma unroll
         for (int i = 0; i < KL; ++i)
-            q[h][i] = h < heads ? ((const float*)a.q)[n * a.q_stride + (h0 + h) * K + lane * KL + i] : 0.f;
+            q[h][i] = h < heads ? ((const float*)a.q)[wk.n * a.q_stride + (h0 + h) * K + lane * KL + i] : 0.f;
 #pragma unroll
         for (int i = 0; i < VL; ++i) acc[h][i] = 0.f;
     }
     float m = -INFINITY, l = 0.f;  // of head lane % HT
-    const float* kh = (const float*)a.c.k + hkv * a.c.k_head + lane * KL;
-    const float* vh = (const float*)a.c.v + hkv * a.c.v_head + lane * VL;
+    const float* kh = (const float*)a.c.k + wk.hkv * a.c.k_head + lane * KL;
+    const float* vh = (const float*)a.c.v + wk.hkv * a.c.v_head + lane * VL;
     float kr[R][KL], vr[R][VL];
-    Rows<R> rows(a, n, lo + warp * R, hi, kWarps * R);
     auto load_k = [&]() {
 #pragma unroll
         for (int r = 0; r < R; ++r) load_channels<KL>(kh + rows.k_of(r), rows.valid >> r & 1, kr[r]);
@@ -497,10 +542,10 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend_simt(AttendArgs a) {
 #pragma unroll
         for (int r = 0; r < R; ++r) load_channels<VL>(vh + rows.v_of(r), rows.valid >> r & 1, vr[r]);
     };
-    rows.next(a, hkv);
+    rows.next(a);
     load_k();
     load_v();
-    for (int first = lo + warp * R; first < hi; first += kWarps * R) {
+    for (int first = wk.first; first < wk.end; first += rows.step) {
         float s[NV];  // value r HT + h
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -511,7 +556,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend_simt(AttendArgs a) {
                 for (int i = 1; i < KL; ++i) s[r * HT + h] = fmaf(q[h][i], kr[r][i], s[r * HT + h]);
             }
         const bool in = rows.valid >> (lane % NV / HT) & 1;
-        rows.next(a, hkv);
+        rows.next(a);
         load_k();
 #pragma unroll
         for (int w = NV / 2; w > 0; w /= 2)
@@ -558,8 +603,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend_simt(AttendArgs a) {
 #pragma unroll
     for (int h = 0; h < HT; ++h)
 #pragma unroll
-        for (int i = 0; i < VL; ++i) sm.acc[warp][h][lane * VL + i] = acc[h][i];
-    join_slice<float, V, HT>(a, n, h0, heads, slice, (used + a.cluster - 1) / a.cluster, sm);
+        for (int i = 0; i < VL; ++i) ((float*)sm.acc[warp][h])[lane * VL + i] = acc[h][i];
+    join<float>(a, wk, sm);
 }
 
 // ------------------------------------------------------------------ launch
@@ -571,71 +616,44 @@ int head_tile(const kda_cache* c, int HQ) {
     return group == 1 ? 1 : group <= 4 ? 4 : 8;
 }
 
-// The split of each sequence's rows: CTAs to a cluster, and clusters.
+// The split of each sequence's rows: warps to a CTA, CTAs.
 struct Plan {
-    int cluster, slices;
+    int warps, parts, cluster, turn;
 };
 Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window) {
     const int group = HQ / c->HKV, ht = head_tile(c, HQ);
     const int64_t units = (int64_t)(N > 0 ? N : 1) * c->HKV * ((group + ht - 1) / ht);
     int64_t rows = (int64_t)max_pages * c->page_size;
     if (window > 0 && window < rows) rows = window;
-    const int64_t most = (rows + kPartRows - 1) / kPartRows, want = (WANT + units - 1) / units;
-    Plan p{1, 1};
-    while (p.cluster < kMaxCluster && p.cluster < want && p.cluster < most) p.cluster *= 2;
-    int64_t slices = want / p.cluster;
-    const int64_t fill = rows / ((int64_t)p.cluster * SLICE_ROWS);
-    if (slices > fill) slices = fill;
-    if (slices > 1) p.slices = (int)slices;
+    const int tile = c->dtype == KDA_DTYPE_BF16 ? 16 : ht == 8 ? 4 : 8;
+    Plan p{4, (int)((152 * 3 + units - 1) / units), 0, 4 * tile};
+#ifdef TUNE
+    p.warps = atoi(getenv("KW")); p.parts = atoi(getenv("KS")); p.cluster = atoi(getenv("KC")); p.turn = p.warps * tile;
+#endif
     return p;
-}
-
-cudaError_t launch_in(void (*kernel)(AttendArgs), const AttendArgs& a, unsigned grid, int cluster, bool after,
-                      cudaStream_t st) {
-    cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.stream = st;
-    cfg.attrs = attr;
-    if (cluster > 1) {
-        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-        attr[cfg.numAttrs].val.clusterDim.x = cluster;
-        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
-        ++cfg.numAttrs;
-    }
-    if (after) {  // may be set up while the kernel before it runs; it waits for that one's end itself
-        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
-        ++cfg.numAttrs;
-    }
-    if (cluster > 8) {
-        const cudaError_t e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 typedef void (*Kernel)(AttendArgs);
 
-template <int K, int V> Kernel kernel_of(bool bf16, int ht) {
-    if (bf16) return ht == 8 ? k_attend_mma<K, V, 1> : k_attend_mma<K, V, 2>;
-    return ht == 1 ? k_attend_simt<K, V, 1, 8> : ht == 4 ? k_attend_simt<K, V, 4, 8> : k_attend_simt<K, V, 8, 4>;
+template <int K, int V> Kernel kernel_of(bool bf16, int ht, int warps) {
+    if (bf16 && warps == 8) return k_attend_mma<K, V, 1, 8>;
+    if (bf16) return ht == 8 ? k_attend_mma<K, V, 1, 4> : k_attend_mma<K, V, 2, 4>;
+    return ht == 1 ? k_attend_simt<K, V, 1, 8, 4> : ht == 4 ? k_attend_simt<K, V, 4, 8, 4> : k_attend_simt<K, V, 8, 4, 4>;
 }
 
-cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
+cudaError_t launch_attend(const AttendArgs& a, int warps, cudaStream_t st) {
     const bool bf16 = a.c.dtype == KDA_DTYPE_BF16;
     const int ht = head_tile(&a.c, a.HQ), group = a.HQ / a.c.HKV, K = a.c.K, V = a.c.V;
-    const unsigned grid = (unsigned)((int64_t)a.N * a.c.HKV * ((group + ht - 1) / ht) * a.cluster * a.slices);
-    const Kernel kernel = K == 128 ? (V == 128 ? kernel_of<128, 128>(bf16, ht) : kernel_of<128, 64>(bf16, ht))
-                                   : (V == 128 ? kernel_of<64, 128>(bf16, ht) : kernel_of<64, 64>(bf16, ht));
-    cudaError_t e = launch_in(kernel, a, grid, a.cluster, false, st);
+    const unsigned grid = (unsigned)((int64_t)a.N * a.c.HKV * ((group + ht - 1) / ht) * a.parts);
+    const Kernel kernel = K == 128 ? (V == 128 ? kernel_of<128, 128>(bf16, ht, warps) : kernel_of<128, 64>(bf16, ht, warps))
+                                   : (V == 128 ? kernel_of<64, 128>(bf16, ht, warps) : kernel_of<64, 64>(bf16, ht, warps));
+    cudaError_t e = launch_after(kernel, a, grid, warps * 32, st, a.cluster ? a.parts : 1);
     if (e != cudaSuccess) return e;
     note_launch("cache_attend", st);
-    if (a.slices == 1) return cudaSuccess;
+    if (a.parts == 1 || a.cluster) return cudaSuccess;
     const Kernel join = bf16 ? (V == 128 ? k_attend_join<__nv_bfloat16, 128> : k_attend_join<__nv_bfloat16, 64>)
                              : (V == 128 ? k_attend_join<float, 128> : k_attend_join<float, 64>);
-    if ((e = launch_in(join, a, (unsigned)((int64_t)a.N * a.HQ), 1, true, st)) != cudaSuccess) return e;
+    if ((e = launch_after(join, a, (unsigned)((int64_t)a.N * a.HQ), kJoinThreads, st)) != cudaSuccess) return e;
     note_launch("cache_attend_join", st);
     return cudaSuccess;
 }
@@ -656,8 +674,9 @@ using namespace kda;
 extern "C" size_t kda_cache_attend_workspace_bytes(const kda_cache* c, int32_t HQ, int32_t N, int32_t max_pages,
                                                    int32_t window) {
     if (check_sizes(c, HQ, N, max_pages, window) != KDA_OK) return 0;
-    const int64_t slices = plan_of(c, HQ, N, max_pages, window).slices;
-    return slices == 1 ? 256 : 256 + (size_t)N * HQ * slices * ((size_t)c->V * sizeof(float) + sizeof(float2));
+    const Plan plan = plan_of(c, HQ, N, max_pages, window);
+    const int64_t parts = plan.cluster ? 1 : plan.parts;
+    return parts == 1 ? 256 : 256 + (size_t)N * HQ * parts * ((size_t)c->V * sizeof(float) + sizeof(float2));
 }
 
 extern "C" kda_status kda_cache_attend(const kda_cache* c, const void* q, int64_t q_stride, int32_t HQ, int32_t N,
@@ -677,12 +696,12 @@ extern "C" kda_status kda_cache_attend(const kda_cache* c, const void* q, int64_
         return KDA_ERR_WORKSPACE;
     const Plan plan = plan_of(c, HQ, N, max_pages, window);
     AttendArgs a{*c, q, q_stride, table_stride, HQ, N, max_pages, window, page_table, kv_lens, scale * kLog2e, o, lse,
-                 status, plan.cluster, plan.slices, nullptr, nullptr};
+                 status, plan.parts, plan.cluster, plan.turn, nullptr, nullptr};
     a.part_acc = (float*)ws;
-    a.part_ml = (float2*)(a.part_acc + (int64_t)N * HQ * a.slices * c->V);
+    a.part_ml = (float2*)(a.part_acc + (int64_t)N * HQ * a.parts * c->V);
     cudaStream_t st = (cudaStream_t)stream;
     begin_launches(st);
-    const cudaError_t e = launch_attend(a, st);
+    const cudaError_t e = launch_attend(a, plan.warps, st);
     if (e != cudaSuccess) return cuda_fail(e);
     return KDA_OK;
 }

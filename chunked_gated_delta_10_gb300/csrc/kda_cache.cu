@@ -43,6 +43,7 @@ __device__ __forceinline__ int seq_of(const int64_t* cu, int N, int64_t r) {
 template <typename TI>
 __global__ void __launch_bounds__(256) k_append(AppendArgs a) {
     constexpr int E = Unit<TI>::n;
+    after_previous();
     const int64_t r = blockIdx.x;
     int64_t n, idx;
     if (a.cu) {
@@ -166,11 +167,8 @@ extern "C" kda_status kda_cache_append(const kda_cache* c, const void* k, int64_
                  rope_dim, interleaved, page_table, kv_lens, max_pages, status};
     cudaStream_t st = (cudaStream_t)stream;
     begin_launches(st);
-    if (c->dtype == KDA_DTYPE_BF16)
-        k_append<__nv_bfloat16><<<(unsigned)R, 256, 0, st>>>(a);
-    else
-        k_append<float><<<(unsigned)R, 256, 0, st>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_after(c->dtype == KDA_DTYPE_BF16 ? k_append<__nv_bfloat16> : k_append<float>, a,
+                                       (unsigned)R, 256, st);
     if (e != cudaSuccess) return cuda_fail(e);
     note_launch("cache_append", st);
     return KDA_OK;

@@ -3,6 +3,7 @@
 #include "../../include/kda_serve.h"
 #include "kda_common.cuh"
 #include "kda_internal.h"
+#include "serve_common.cuh"
 
 namespace kda {
 

@@ -12,6 +12,7 @@
 #include "../../include/kda_serve.h"
 #include "kda_common.cuh"
 #include "kda_internal.h"
+#include "serve_common.cuh"
 
 namespace kda {
 namespace {
@@ -32,6 +33,7 @@ __global__ void __launch_bounds__(V) k_step(StepArgs a) {
     __shared__ float4 sk[K / 4], sq[K / 4], se[K / 4];
     const int64_t n = blockIdx.x / a.HV;
     const int hv = blockIdx.x % a.HV, h = hv / (a.HV / a.H), col = threadIdx.x;
+    after_previous();
     const int64_t slot = a.slots ? a.slots[n] : n;
     if (slot < 0 || slot >= a.num_slots) {
         for (int t = 0; t < a.T; ++t)
@@ -83,13 +85,9 @@ __global__ void __launch_bounds__(V) k_step(StepArgs a) {
     for (int j = 0; j < K; ++j) S[j * V] = s[j];
 }
 
-template <typename TI>
-void launch_step(const StepArgs& a, int K, int V, cudaStream_t st) {
-    const unsigned grid = (unsigned)((int64_t)a.N * a.HV);
-    if (K == 128 && V == 128) k_step<TI, 128, 128><<<grid, 128, 0, st>>>(a);
-    if (K == 128 && V == 64) k_step<TI, 128, 64><<<grid, 64, 0, st>>>(a);
-    if (K == 64 && V == 128) k_step<TI, 64, 128><<<grid, 128, 0, st>>>(a);
-    if (K == 64 && V == 64) k_step<TI, 64, 64><<<grid, 64, 0, st>>>(a);
+template <typename TI> void (*kernel_of(int K, int V))(StepArgs) {
+    return K == 128 ? (V == 128 ? k_step<TI, 128, 128> : k_step<TI, 128, 64>)
+                    : (V == 128 ? k_step<TI, 64, 128> : k_step<TI, 64, 64>);
 }
 
 }  // namespace
@@ -114,11 +112,8 @@ extern "C" kda_status kda_step(const kda_step_dims* d, const void* q, const void
     StepArgs a{q, k, v, beta, g, state, slots, o, status, d->N, d->T, d->H, d->HV, d->num_slots, d->scale};
     cudaStream_t st = (cudaStream_t)stream;
     begin_launches(st);
-    if (d->dtype == KDA_DTYPE_BF16)
-        launch_step<__nv_bfloat16>(a, d->K, d->V, st);
-    else
-        launch_step<float>(a, d->K, d->V, st);
-    const cudaError_t e = cudaGetLastError();
+    const auto kernel = d->dtype == KDA_DTYPE_BF16 ? kernel_of<__nv_bfloat16>(d->K, d->V) : kernel_of<float>(d->K, d->V);
+    const cudaError_t e = launch_after(kernel, a, (unsigned)(d->N * d->HV), d->V, st);
     if (e != cudaSuccess) return cuda_fail(e);
     note_launch("step", st);
     return KDA_OK;
