@@ -65,7 +65,7 @@ def _serve_commands(nvcc, obj):
     compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
                 *[x for d in include for x in ("-isystem", d)], "-c", SERVE_SRC, "-o", obj]
     link = [cxx, "-shared", obj, LIB, "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(top, "lib"), "-ltorch_python", "-ltorch",
-            "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+            "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10"]
     return compile_, link
 
 

@@ -15,6 +15,9 @@
 namespace kda {
 namespace {
 
+// How the rows are given to CTAs (see Work).
+enum Split { kWhole, kCluster, kShares };
+
 struct AttendArgs {
     kda_cache c;
     const void* q;
@@ -25,11 +28,13 @@ struct AttendArgs {
     void* o;
     float* lse;
     int32_t* status;
-    int parts;        // CTAs over a sequence's rows
-    int cluster;      // whether the parts of a sequence are a cluster of CTAs, which joins them
-    int turn;         // rows that a CTA takes at a time
-    float* part_acc;  // [N, HQ, parts, V]: each part's weighted sum, relative to its maximum
-    float2* part_ml;  // [N, HQ, parts]: its maximum (log2 units) and its sum of weights
+    int split, parts;  // parts: kCluster: CTAs of a cluster; kShares: CTAs in all; kWhole: 1
+    // kShares: what a CTA has of a unit that it ends (0) or begins (1) but does not have whole, head by head: the
+    // weighted sum relative to its maximum [parts, 2, HT, V], and its maximum (log2 units) and sum of weights
+    // [parts, 2, HT]; and of each unit the first and last CTA that have some of it.
+    float4* part_acc;
+    float2* part_ml;
+    int2* unit_parts;
 };
 
 // The rows [begin, end) that sequence n attends.
@@ -44,19 +49,10 @@ __device__ __forceinline__ void kv_range(const AttendArgs& a, int64_t n, int& be
 // weight there is 2^-inf = 0 and a NaN score stays a NaN.
 __device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
 
-// ------------------------------------------------------------------ split
-//
-// A CTA takes W R rows at a time, R for each of its W warps, and the CTAs of a sequence, its parts, take them in turn:
-// CTA i the turns i, i + parts, .. So parts are equal whatever the length, and the first rows of a CTA do not depend on
-// it: their pages are looked up while the length is on its way. Where a sequence has more than one part in use, each
-// leaves its result in the workspace and a second kernel joins those. How many parts there are is the host's choice (it
-// knows the sizes but not the lengths).
-
-constexpr int kMaxCluster = 16;
-
-// The parts of a sequence that hold any rows (one at least, which writes the result of a sequence without).
-__device__ __forceinline__ int parts_used(const AttendArgs& a, int rows, int turn) {
-    return max(1, min(a.parts, (rows + turn - 1) / turn));
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // ------------------------------------------------------------------ rows of a tile
@@ -70,7 +66,7 @@ template <int R> struct Rows {
     int64_t k_off, v_off;            // this tile's row of this lane
     unsigned valid;                  // bit r: row r is in range and its page exists
 
-    // Rows from `first` on, `stride` apart; without a window neither depends on the sequence's length.
+    // Rows from `first` on, `stride` apart; `end` is set by the caller, later where the length is still on its way.
     __device__ __forceinline__ void start(const AttendArgs& a, int64_t n, int first, int stride) {
         table = a.table + n * a.table_stride;
         row = first + threadIdx.x % 32 % R;
@@ -101,36 +97,6 @@ template <int R> struct Rows {
     __device__ __forceinline__ int64_t v_of(int r) const { return __shfl_sync(0xffffffffu, v_off, r); }
 };
 
-// What a CTA works on, and the rows of this warp: the first lookup is issued before the length is read.
-template <int W, int R, int HT> struct Work {
-    int64_t n;
-    int hkv, h0, heads, part, used, warp, first, end;
-    Rows<R> rows;
-
-    __device__ __forceinline__ bool start(const AttendArgs& a) {
-        const unsigned parts = a.parts, unit = blockIdx.x / parts;
-        const unsigned group = (unsigned)a.HQ / a.c.HKV, tiles = (group + HT - 1) / HT, per = a.c.HKV * tiles;
-        const unsigned qt = unit % tiles;
-        n = unit / per;
-        hkv = unit / tiles % a.c.HKV;
-        h0 = hkv * group + qt * HT;
-        heads = min(HT, (int)(group - qt * HT));
-        part = blockIdx.x % parts;
-        warp = threadIdx.x / 32;
-        first = (part * W + warp) * R;
-        rows.start(a, n, first, parts * W * R);
-        int begin;
-        kv_range(a, n, begin, end);
-        if (begin > 0) {
-            first += begin;
-            rows.start(a, n, first, parts * W * R);
-        }
-        rows.end = end;
-        used = parts_used(a, end - begin, W * R);
-        return part < used;
-    }
-};
-
 __device__ __forceinline__ uint4 load16(const void* p, bool ok) {
     uint4 x = make_uint4(0, 0, 0, 0);
     if (ok) x = __ldcs((const uint4*)p);
@@ -146,6 +112,166 @@ template <int C> __device__ __forceinline__ void load_channels(const float* p, b
         x[0] = y.x, x[1] = y.y;
     }
 }
+
+// ------------------------------------------------------------------ split
+//
+// A unit is a sequence, a cache head and up to HT of its query heads. A CTA takes W R rows at a time, R for each of its
+// W warps: a turn. The host knows the sizes but not the lengths, which lie on the device. It chooses between
+//   kWhole    a CTA per unit: for units of few turns, or very many units;
+//   kCluster  a cluster of CTAs per unit, which take its turns one after the other (so the first rows of a CTA do not
+//             depend on the length, and their pages are looked up while it is on its way) and join their results in
+//             shared memory: for few units of some turns, where latency counts;
+//   kShares   as many CTAs as the GPU holds at once, each with an equal share of all turns in the order of the units,
+//             whatever the lengths are: every CTA adds up the lengths to find its share. A unit that falls to several
+//             CTAs is joined by a second kernel.
+constexpr int kWarps = 4;
+constexpr int kMaxCluster = 16;
+
+template <int R, int HT> struct Work {
+    static constexpr int W = kWarps, kTurn = W * R;
+    int n, hkv, h0, heads, warp, first, end;
+    int odd;  // kShares: which of the share's two states is the next
+    Rows<R> rows;
+
+    // What a CTA keeps in shared memory (a barrier lies between two units).
+    struct Share {
+        // the unit, for the join: whole, if the CTA or its cluster has all of it; part: kCluster: the CTA's rank;
+        // kShares: where it leaves its part
+        int64_t head;
+        int heads, whole, part;
+        // kShares: the turns [at, stop) of `total` are still to be done, from sequence n on, whose first turn is `seq`
+        int sums[W], stop, total;
+        struct {
+            int at, n, seq;
+        } state[2];
+    };
+
+    __device__ __forceinline__ static int turns_of(int begin, int end) {
+        return max(1, (end - begin + kTurn - 1) / kTurn);  // one at least, which writes the result of no rows
+    }
+    // Unit u of sequence n.
+    __device__ __forceinline__ void set_unit(const AttendArgs& a, unsigned u, bool whole, int part, Share& share) {
+        const unsigned group = (unsigned)a.HQ / a.c.HKV, tiles = (group + HT - 1) / HT, qt = u % tiles;
+        hkv = u / tiles;
+        h0 = hkv * group + qt * HT;
+        heads = min(HT, (int)(group - qt * HT));
+        if (threadIdx.x == 0) {
+            share.head = (int64_t)n * a.HQ + h0;
+            share.heads = heads;
+            share.whole = whole;
+            share.part = part;
+        }
+    }
+    // The CTA's first unit; false if it has none.
+    __device__ __forceinline__ static unsigned units_of(const AttendArgs& a) {  // of a sequence
+        return a.c.HKV * (((unsigned)a.HQ / a.c.HKV + HT - 1) / HT);
+    }
+    __device__ __forceinline__ bool start(const AttendArgs& a, Share& share) {
+        const unsigned units = units_of(a);
+        warp = threadIdx.x / 32;
+        odd = 0;
+        if (a.split == kShares) {
+            find_share(a, units, share);
+            return next(a, share);
+        }
+        const unsigned x = blockIdx.x / (unsigned)a.parts;
+        const int part = blockIdx.x % (unsigned)a.parts;
+        n = x / units;
+        set_unit(a, x % units, true, part, share);
+        first = (part * W + warp) * R;
+        rows.start(a, n, first, a.parts * kTurn);
+        int begin;
+        kv_range(a, n, begin, end);
+        if (a.window > 0) {
+            first += begin;
+            rows.start(a, n, first, a.parts * kTurn);
+        }
+        rows.end = end;
+        return true;
+    }
+    // kShares: the CTA's share, and the sequence that it begins in.
+    __device__ __forceinline__ void find_share(const AttendArgs& a, int units, Share& share) {
+        if (a.N == 1) {
+            if (threadIdx.x == 0) {
+                int begin, last;
+                kv_range(a, 0, begin, last);
+                const int total = turns_of(begin, last) * units, ctas = min(a.parts, total);
+                const int x = min((int)blockIdx.x, ctas);
+                share.state[0] = {(int)((int64_t)x * total / ctas), 0, 0};
+                share.stop = x == ctas ? 0 : (int)((int64_t)(x + 1) * total / ctas);
+                share.total = total;
+            }
+            __syncthreads();
+            return;
+        }
+        const int per = (a.N + W * 32 - 1) / (W * 32), lane = threadIdx.x % 32;
+        const int n0 = min((int)threadIdx.x * per, a.N), n1 = min(n0 + per, a.N);
+        int mine = 0, begin, last;
+        for (int i = n0; i < n1; ++i) {
+            kv_range(a, i, begin, last);
+            mine += turns_of(begin, last) * units;
+        }
+        int before = mine;
+#pragma unroll
+        for (int w = 1; w < 32; w *= 2) {
+            const int y = __shfl_up_sync(0xffffffffu, before, w);
+            if (lane >= w) before += y;
+        }
+        if (lane == 31) share.sums[warp] = before;
+        __syncthreads();
+        before -= mine;
+        int total = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            if (w < warp) before += share.sums[w];
+            total += share.sums[w];
+        }
+        const int ctas = min(a.parts, total);  // with fewer turns than CTAs, those that have one
+        const int at = (int)((int64_t)min((int)blockIdx.x, ctas) * total / ctas);
+        if (blockIdx.x >= ctas && threadIdx.x == 0) share.state[0].at = share.stop = 0;
+        if (at >= before && at < before + mine) {
+            int i = n0;
+            for (;; ++i) {
+                kv_range(a, i, begin, last);
+                const int turns = turns_of(begin, last) * units;
+                if (at < before + turns) break;
+                before += turns;
+            }
+            share.stop = (int)((int64_t)(blockIdx.x + 1) * total / ctas);
+            share.total = total;
+            share.state[0] = {at, i, before};
+        }
+        __syncthreads();
+    }
+    // kShares: the next unit, or part of one, of the CTA's share; false if there is none.
+    __device__ __forceinline__ bool next(const AttendArgs& a, Share& share) {
+        const int at = share.state[odd].at, stop = share.stop, units = units_of(a);
+        if (at >= stop) return false;
+        int begin, last, turns, seq = share.state[odd].seq;
+        for (n = share.state[odd].n;; ++n) {
+            kv_range(a, n, begin, last);
+            turns = turns_of(begin, last);
+            if (at < seq + turns * units) break;
+            seq += turns * units;
+        }
+        const unsigned u = (unsigned)(at - seq) / (unsigned)turns;
+        const int t0 = at - seq - u * turns, t1 = min(turns, t0 + stop - at);
+        set_unit(a, u, t0 == 0 && t1 == turns, 2 * blockIdx.x + (t0 == 0), share);
+        odd ^= 1;
+        if (threadIdx.x == 0) {
+            share.state[odd] = {at + t1 - t0, n, seq};
+            if (t0 == 0) {
+                const int64_t behind = (int64_t)at + turns;  // the turn behind the unit's last, which CTA `to` has
+                const int to = (int)((behind * min(a.parts, share.total) - 1) / share.total);
+                a.unit_parts[(int64_t)n * units + u] = make_int2(blockIdx.x, to);
+            }
+        }
+        first = begin + (t0 * W + warp) * R;
+        rows.start(a, n, first, kTurn);
+        rows.end = end = min(last, begin + t1 * kTurn);
+        return true;
+    }
+};
 
 // ------------------------------------------------------------------ joins
 
@@ -165,20 +291,15 @@ __device__ __forceinline__ void push(float4* p, uint32_t rank, float4 x) {
 __device__ __forceinline__ void push(float2* p, uint32_t rank, float2 x) {
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_address(p, rank)), "f"(x.x), "f"(x.y) : "memory");
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ void add_scaled(float4& x, const float4& y, float f) {
     x.x = fmaf(y.x, f, x.x);
     x.y = fmaf(y.y, f, x.y);
     x.z = fmaf(y.z, f, x.z);
     x.w = fmaf(y.w, f, x.w);
 }
-// Channels d .. d + 3 of a query head's result.
-template <typename TI> __device__ __forceinline__ void write_result(const AttendArgs& a, int64_t at, int V, int d, float m,
-                                                                    float l, float4 x) {
+// Channels d .. d + 3 of the result of query head `at`.
+template <typename TI>
+__device__ __forceinline__ void write_result(const AttendArgs& a, int64_t at, int V, int d, float m, float l, float4 x) {
     const float f = l == 0.f ? 0.f : 1.f / l;  // nothing attended: x is 0
     TI* o = (TI*)a.o + at * V + d;
     if constexpr (sizeof(TI) == 2) {
@@ -192,50 +313,53 @@ template <typename TI> __device__ __forceinline__ void write_result(const Attend
 
 // The results of a CTA's warps for HT heads: maxima m, sums of weights l, and weighted sums acc relative to m. In a
 // cluster: what its CTAs send of the channels that this one joins, and of every head their m and l.
-template <int W, int HT, int V> struct Partial {
-    float m[W][HT], l[W][HT];
-    float4 acc[W][HT][V / 4 + 1];
+template <int HT, int V> struct Partial {
+    float m[kWarps][HT], l[kWarps][HT];
+    float4 acc[kWarps][HT][V / 4 + 1];
     float4 in_acc[HT * V / 4 + kMaxCluster];
     float2 in_ml[kMaxCluster][HT];
 };
 
-// Joins the warps of a CTA and, where the parts of a sequence are a cluster, its CTAs, and writes the result for the
-// heads: the operator's, or, where a second kernel is to join the parts, this part's. The order of the sums is fixed.
-template <typename TI, int V, int W, int HT, typename Wk>
-__device__ __forceinline__ void join(const AttendArgs& a, const Wk& wk, Partial<W, HT, V>& p) {
-    const int units = wk.heads * (V / 4), share = (units + a.parts - 1) / a.parts;  // of a CTA of the cluster
-    if (a.cluster) cluster_wait();  // for the others to have started
+// Joins the warps of a CTA and, in a cluster, its CTAs, and writes the unit's result, or, where the CTA does not have
+// all of the unit, its part. The order of the sums is fixed.
+template <typename TI, int V, int HT, typename Share>
+__device__ __forceinline__ void join(const AttendArgs& a, const Share& unit, Partial<HT, V>& p) {
+    const bool cluster = a.split == kCluster;
+    if (cluster) cluster_wait();  // for the others to have started
     __syncthreads();
-    for (int i = threadIdx.x; i < units; i += W * 32) {
+    const int items = unit.heads * (V / 4), share = (items + a.parts - 1) / a.parts;  // share: of a CTA of the cluster
+    const int part = unit.part;
+    const int64_t head = unit.head;
+    for (int i = threadIdx.x; i < items; i += kWarps * 32) {
         const int h = i / (V / 4), u = i % (V / 4);
         float m = p.m[0][h];
 #pragma unroll
-        for (int w = 1; w < W; ++w) m = fmaxf(m, p.m[w][h]);
+        for (int w = 1; w < kWarps; ++w) m = fmaxf(m, p.m[w][h]);
         const float base = finite_base(m);
         float l = 0.f;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             const float f = ex2(p.m[w][h] - base);
             l = fmaf(p.l[w][h], f, l);
             add_scaled(x, p.acc[w][h][u], f);
         }
-        const int64_t at = wk.n * a.HQ + wk.h0 + h;
-        if (a.cluster) {
-            push(&p.in_acc[wk.part * share + i % share], i / share, x);
-            if (u < a.parts) push(&p.in_ml[wk.part][h], u, make_float2(m, l));
-        } else if (wk.used == 1) {
-            write_result<TI>(a, at, V, 4 * u, m, l, x);
+        if (cluster) {
+            push(&p.in_acc[part * share + i % share], i / share, x);
+            if (u < a.parts) push(&p.in_ml[part][h], u, make_float2(m, l));
+        } else if (unit.whole) {
+            write_result<TI>(a, head + h, V, 4 * u, m, l, x);
         } else {
-            ((float4*)a.part_acc)[(at * a.parts + wk.part) * (V / 4) + u] = x;
-            if (u == 0) a.part_ml[at * a.parts + wk.part] = make_float2(m, l);
+            const int64_t to = (int64_t)part * HT + h;
+            a.part_acc[to * (V / 4) + u] = x;
+            if (u == 0) a.part_ml[to] = make_float2(m, l);
         }
     }
-    if (!a.cluster) return;
+    if (!cluster) return;
     cluster_arrive();
     cluster_wait();
-    for (int j = threadIdx.x; j < share && wk.part * share + j < units; j += W * 32) {
-        const int i = wk.part * share + j, h = i / (V / 4), u = i % (V / 4);
+    for (int j = threadIdx.x; j < share && part * share + j < items; j += kWarps * 32) {
+        const int i = part * share + j, h = i / (V / 4), u = i % (V / 4);
         float m = p.in_ml[0][h].x;
         for (int c = 1; c < a.parts; ++c) m = fmaxf(m, p.in_ml[c][h].x);
         const float base = finite_base(m);
@@ -247,78 +371,72 @@ __device__ __forceinline__ void join(const AttendArgs& a, const Wk& wk, Partial<
             l = fmaf(p.in_ml[c][h].y, f, l);
             add_scaled(x, p.in_acc[c * share + j], f);
         }
-        write_result<TI>(a, wk.n * a.HQ + wk.h0 + h, V, 4 * u, m, l, x);
+        write_result<TI>(a, head + h, V, 4 * u, m, l, x);
     }
 }
 
-// The parts of one query head, joined in an order that goes by their number alone: group g of the threads takes parts
-// g, g + G, .., eight of them at a time, and the groups are joined in shared memory. The length, which says how many
-// parts there are to join, is on its way together with the first of them.
-constexpr int kJoinThreads = 512, kJoinBatch = 8;
-template <typename TI, int V>
-__global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendArgs a) {
-    constexpr int U = V / 4, G = kJoinThreads / U;
-    __shared__ float4 sx[G][U];
-    __shared__ float2 sml[G];
-    const unsigned at = blockIdx.x, n = at / a.HQ;
-    const int g = threadIdx.x / U, u = threadIdx.x % U;
+// kShares: the parts of one query head, joined in an order that goes by their number alone. Group g of G groups of
+// V / 4 threads takes parts g, g + G, .., a batch of them at a time; the groups are joined in shared memory.
+constexpr int kJoinBatch = 8, kJoinThreads = 128;
+template <typename TI, int V, int HT, int G>
+__global__ void __launch_bounds__(G * V / 4 > kJoinThreads ? G * V / 4 : kJoinThreads) k_attend_join(AttendArgs a) {
+    constexpr int U = V / 4, HB = G * U > kJoinThreads ? 1 : kJoinThreads / (G * U);  // query heads of a CTA
+    __shared__ float4 sx[HB][G][U];
+    __shared__ float2 sml[HB][G];
+    const unsigned mine = threadIdx.x / (G * U), head = min(blockIdx.x * HB + mine, (unsigned)(a.N * a.HQ - 1));
+    const int g = threadIdx.x / U % G, u = threadIdx.x % U;
+    const unsigned group = (unsigned)a.HQ / a.c.HKV, tiles = (group + HT - 1) / HT;
+    const unsigned n = head / a.HQ, hq = head % a.HQ, hkv = hq / group, qt = hq % group / HT, h = hq % group % HT;
     after_previous();
-    const float2* ml = a.part_ml + (int64_t)at * a.parts;
-    const float4* acc = (const float4*)a.part_acc + (int64_t)at * a.parts * U + u;
+    const int2 range = a.unit_parts[(n * a.c.HKV + hkv) * tiles + qt];
+    const int count = range.y - range.x + 1;
     float m = -INFINITY, l = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    int used = a.parts, s = g;
-    do {
-        float2 e[kJoinBatch];
-        float4 y[kJoinBatch];
+    if (count > 1) {
+        for (int s = g; s < count; s += G * kJoinBatch) {
+            float2 e[kJoinBatch];
+            float4 y[kJoinBatch];
+            float top = m;
 #pragma unroll
-        for (int i = 0; i < kJoinBatch; ++i) {
-            const bool in = s + i * G < used;
-            e[i] = in ? ml[s + i * G] : make_float2(-INFINITY, 0.f);
-            y[i] = in ? acc[(s + i * G) * U] : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        if (s == g) {
-            int begin, end;
-            kv_range(a, n, begin, end);
-            used = parts_used(a, end - begin, a.turn);
-        }
-        float top = m;
-#pragma unroll
-        for (int i = 0; i < kJoinBatch; ++i) {
-            if (s + i * G >= used) {  // what lies there was not written
-                e[i] = make_float2(-INFINITY, 0.f);
-                y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < kJoinBatch; ++i) {
+                const int c = s + i * G;
+                const int64_t from = (int64_t)(2 * (range.x + c) + (c == 0)) * HT + h;
+                e[i] = c < count ? a.part_ml[from] : make_float2(-INFINITY, 0.f);
+                y[i] = c < count ? a.part_acc[from * U + u] : make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            top = fmaxf(top, e[i].x);
-        }
-        const float base = finite_base(top), keep = ex2(m - base);
-        l *= keep;
-        x = make_float4(x.x * keep, x.y * keep, x.z * keep, x.w * keep);
-        m = top;
 #pragma unroll
-        for (int i = 0; i < kJoinBatch; ++i) {
-            const float f = ex2(e[i].x - base);
-            l = fmaf(e[i].y, f, l);
-            add_scaled(x, y[i], f);
-        }
-        s += G * kJoinBatch;
-    } while (s < used);
-    if (used == 1) return;  // the one part has written the result
-    sx[g][u] = x;
-    if (u == 0) sml[g] = make_float2(m, l);
-    __syncthreads();
-    if (g > 0) return;
-    for (int i = 1; i < G; ++i) m = fmaxf(m, sml[i].x);
-    const float base = finite_base(m);
-    l = 0.f;
-    x = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < kJoinBatch; ++i) top = fmaxf(top, e[i].x);
+            const float base = finite_base(top), keep = ex2(m - base);
+            l *= keep;
+            x = make_float4(x.x * keep, x.y * keep, x.z * keep, x.w * keep);
+            m = top;
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-        const float f = ex2(sml[i].x - base);
-        l = fmaf(sml[i].y, f, l);
-        add_scaled(x, sx[i][u], f);
+            for (int i = 0; i < kJoinBatch; ++i) {
+                const float f = ex2(e[i].x - base);
+                l = fmaf(e[i].y, f, l);
+                add_scaled(x, y[i], f);
+            }
+        }
     }
-    write_result<TI>(a, at, V, 4 * u, m, l, x);
+    if constexpr (G > 1) {
+        sx[mine][g][u] = x;
+        if (u == 0) sml[mine][g] = make_float2(m, l);
+        __syncthreads();
+        if (g > 0) return;
+#pragma unroll
+        for (int i = 1; i < G; ++i) m = fmaxf(m, sml[mine][i].x);
+        const float base = finite_base(m);
+        l = 0.f;
+        x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            const float f = ex2(sml[mine][i].x - base);
+            l = fmaf(sml[mine][i].y, f, l);
+            add_scaled(x, sx[mine][i][u], f);
+        }
+    }
+    // (one part alone has written the result; the last CTA's spare threads have the last head once more)
+    if (count > 1 && blockIdx.x * HB + mine == head) write_result<TI>(a, head, V, 4 * u, m, l, x);
 }
 
 // ------------------------------------------------------------------ bf16
@@ -355,154 +473,162 @@ constexpr float kSlack = 8.f;
 //   - P^T comes from S^T by an 8 x 8 transposition in registers; it is split into a pair of bf16 values (2^-16).
 // A tensor core of the fifth generation wants its operands in shared memory and 128 rows in a product; with at most 16
 // query heads against it, the memory's time would cover none of that traffic.
-template <int K, int V, int NT, int W>
-__global__ void __launch_bounds__(W * 32, W == 8 ? 1 : NT == 1 ? 3 : 2) k_attend_mma(AttendArgs a) {
+template <int K, int V, int NT>
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) k_attend_mma(AttendArgs a) {
     using TI = __nv_bfloat16;
     constexpr int KI = K / 32, VC = V / 64, VJ = V / 16, HT = 8 * NT;
-    __shared__ Partial<W, HT, V> sm;
+    __shared__ Partial<HT, V> sm;
     const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-    Work<W, 16, HT> wk;
-    if (a.cluster) cluster_arrive();
+    if (a.split == kCluster) cluster_arrive();
     after_previous();
-    if (!wk.start(a) && !a.cluster) return;
-    const int h0 = wk.h0, heads = wk.heads, warp = wk.warp;
-    Rows<16>& rows = wk.rows;
-    uint4 q[NT][KI];
+    Work<16, HT> wk;
+    __shared__ typename Work<16, HT>::Share share;
+    for (bool more = wk.start(a, share); more; more = wk.next(a, share)) {
+        const int h0 = wk.h0, heads = wk.heads, warp = wk.warp;
+        Rows<16>& rows = wk.rows;
+        uint4 q[NT][KI];
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int i = 0; i < KI; ++i)
-            q[j][i] = load16((const TI*)a.q + wk.n * a.q_stride + (h0 + 8 * j + g) * K + (4 * i + t) * 8, 8 * j + g < heads);
-    float acc[NT][VJ][4], m[NT][2], l[NT][2];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        m[j][0] = m[j][1] = -INFINITY;
-        l[j][0] = l[j][1] = 0.f;
-#pragma unroll
-        for (int i = 0; i < VJ; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][i][e] = 0.f;
-    }
-    const TI* kh = (const TI*)a.c.k + wk.hkv * a.c.k_head + t * 8;
-    const TI* vh = (const TI*)a.c.v + wk.hkv * a.c.v_head + g * 8;
-    uint4 kr[2][KI], vr[4][VC];
-    auto load_k = [&]() {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const TI* p = kh + rows.k_of(g + 8 * r);
-            const bool ok = rows.valid >> (g + 8 * r) & 1;
-#pragma unroll
-            for (int i = 0; i < KI; ++i) kr[r][i] = load16(p + 32 * i, ok);
-        }
-    };
-    auto load_v = [&]() {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int at = 2 * t + (r & 1) + 4 * (r & 2);
-            const TI* p = vh + rows.v_of(at);
-            const bool ok = rows.valid >> at & 1;
-#pragma unroll
-            for (int i = 0; i < VC; ++i) vr[r][i] = load16(p + 64 * i, ok);
-        }
-    };
-    rows.next(a);
-    load_k();
-    load_v();
-    for (int first = wk.first; first < wk.end; first += rows.step) {
-        float s[NT][4];
+            for (int i = 0; i < KI; ++i)
+                q[j][i] =
+                    load16((const TI*)a.q + (int64_t)wk.n * a.q_stride + (h0 + 8 * j + g) * K + (4 * i + t) * 8, 8 * j + g < heads);
+        float acc[NT][VJ][4], m[NT][2], l[NT][2];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+            m[j][0] = m[j][1] = -INFINITY;
+            l[j][0] = l[j][1] = 0.f;
 #pragma unroll
-            for (int i = 0; i < KI; ++i) {
-                mma(s[j], kr[0][i].x, kr[1][i].x, kr[0][i].y, kr[1][i].y, q[j][i].x, q[j][i].y);
-                mma(s[j], kr[0][i].z, kr[1][i].z, kr[0][i].w, kr[1][i].w, q[j][i].z, q[j][i].w);
-            }
+            for (int i = 0; i < VJ; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[j][i][e] = 0.f;
         }
-        const bool in0 = rows.valid >> g & 1, in1 = rows.valid >> (g + 8) & 1;
-        rows.next(a);
-        load_k();
-        bool higher = false;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[j][e] = (e < 2 ? in0 : in1) ? s[j][e] * a.scale_log2 : -INFINITY;
-                higher |= s[j][e] > m[j][e & 1] + kSlack;
-            }
-        }
-        if (__any_sync(0xffffffffu, higher)) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float top = fmaxf(m[j][e], fmaxf(s[j][e], s[j][e + 2]));
-#pragma unroll
-                    for (int w = 4; w < 32; w *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-                    const float f = ex2(m[j][e] - finite_base(top));
-                    m[j][e] = top;
-                    l[j][e] *= f;
-#pragma unroll
-                    for (int i = 0; i < VJ; ++i) {
-                        acc[j][i][e] *= f;
-                        acc[j][i][e + 2] *= f;
-                    }
-                }
-        }
-        uint32_t hi_p[NT][2], lo_p[NT][2];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const float b0 = finite_base(m[j][0]), b1 = finite_base(m[j][1]);
+        const TI* kh = (const TI*)a.c.k + wk.hkv * a.c.k_head + t * 8;
+        const TI* vh = (const TI*)a.c.v + wk.hkv * a.c.v_head + g * 8;
+        uint4 kr[2][KI], vr[4][VC];
+        auto load_k = [&]() {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const float p0 = ex2(s[j][2 * r] - b0), p1 = ex2(s[j][2 * r + 1] - b1);
-                l[j][0] += p0;
-                l[j][1] += p1;
-                const uint32_t h = pack(p0, p1);
-                hi_p[j][r] = transpose8(h);
-                lo_p[j][r] = transpose8(pack(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u)));
-            }
-        }
+                const TI* p = kh + rows.k_of(g + 8 * r);
+                const bool ok = rows.valid >> (g + 8 * r) & 1;
 #pragma unroll
-        for (int i = 0; i < VJ; ++i) {
-            // product i: rows 0-7 are channels 8 g + i (V = 64: 8 g + i), rows 8-15 channels 64 + 8 g + i (8 g + i + 4)
-            uint32_t x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = VC == 2 ? e & 1 : 0, j = VC == 2 ? i : i + 4 * (e & 1), r = e & 2;
-                const uint32_t* even = (const uint32_t*)&vr[r][c];
-                const uint32_t* odd = (const uint32_t*)&vr[r + 1][c];
-                x[e] = __byte_perm(even[j / 2], odd[j / 2], j % 2 ? 0x7632 : 0x5410);
+                for (int i = 0; i < KI; ++i) kr[r][i] = load16(p + 32 * i, ok);
             }
+        };
+        auto load_v = [&]() {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int at = 2 * t + (r & 1) + 4 * (r & 2);
+                const TI* p = vh + rows.v_of(at);
+                const bool ok = rows.valid >> at & 1;
+#pragma unroll
+                for (int i = 0; i < VC; ++i) vr[r][i] = load16(p + 64 * i, ok);
+            }
+        };
+        rows.next(a);
+        load_k();
+        load_v();
+        for (int first = wk.first; first < wk.end; first += rows.step) {
+            float s[NT][4];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                mma(acc[j][i], x[0], x[1], x[2], x[3], hi_p[j][0], hi_p[j][1]);
-                mma(acc[j][i], x[0], x[1], x[2], x[3], lo_p[j][0], lo_p[j][1]);
+                float s1[4] = {0.f, 0.f, 0.f, 0.f};  // two chains of products
+                s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+#pragma unroll
+                for (int i = 0; i < KI; ++i) {
+                    mma(s[j], kr[0][i].x, kr[1][i].x, kr[0][i].y, kr[1][i].y, q[j][i].x, q[j][i].y);
+                    mma(s1, kr[0][i].z, kr[1][i].z, kr[0][i].w, kr[1][i].w, q[j][i].z, q[j][i].w);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[j][e] += s1[e];
             }
+            const bool in0 = rows.valid >> g & 1, in1 = rows.valid >> (g + 8) & 1;
+            rows.next(a);
+            load_k();
+            bool higher = false;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[j][e] = (e < 2 ? in0 : in1) ? s[j][e] * a.scale_log2 : -INFINITY;
+                    higher |= s[j][e] > m[j][e & 1] + kSlack;
+                }
+            }
+            if (__any_sync(0xffffffffu, higher)) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float top = fmaxf(m[j][e], fmaxf(s[j][e], s[j][e + 2]));
+#pragma unroll
+                        for (int w = 4; w < 32; w *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+                        const float f = ex2(m[j][e] - finite_base(top));
+                        m[j][e] = top;
+                        l[j][e] *= f;
+#pragma unroll
+                        for (int i = 0; i < VJ; ++i) {
+                            acc[j][i][e] *= f;
+                            acc[j][i][e + 2] *= f;
+                        }
+                    }
+            }
+            uint32_t hi_p[NT][2], lo_p[NT][2];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const float b0 = finite_base(m[j][0]), b1 = finite_base(m[j][1]);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float p0 = ex2(s[j][2 * r] - b0), p1 = ex2(s[j][2 * r + 1] - b1);
+                    l[j][0] += p0;
+                    l[j][1] += p1;
+                    const uint32_t h = pack(p0, p1);
+                    hi_p[j][r] = transpose8(h);
+                    lo_p[j][r] = transpose8(pack(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u)));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < VJ; ++i) {
+                // product i: rows 0-7 are channels 8 g + i (V = 64: 8 g + i), rows 8-15 channels 64 + 8 g + i (8 g + i + 4)
+                uint32_t x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = VC == 2 ? e & 1 : 0, j = VC == 2 ? i : i + 4 * (e & 1), r = e & 2;
+                    const uint32_t* even = (const uint32_t*)&vr[r][c];
+                    const uint32_t* odd = (const uint32_t*)&vr[r + 1][c];
+                    x[e] = __byte_perm(even[j / 2], odd[j / 2], j % 2 ? 0x7632 : 0x5410);
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    mma(acc[j][i], x[0], x[1], x[2], x[3], hi_p[j][0], hi_p[j][1]);
+                    mma(acc[j][i], x[0], x[1], x[2], x[3], lo_p[j][0], lo_p[j][1]);
+                }
+            }
+            load_v();
         }
-        load_v();
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int h = 8 * j + 2 * t + e;
+#pragma unroll
+                for (int w = 4; w < 32; w *= 2) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], w);
+                if (g == 0) {
+                    sm.m[warp][h] = m[j][e];
+                    sm.l[warp][h] = l[j][e];
+                }
+                float* row = (float*)sm.acc[warp][h] + 8 * g;
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int i = 0; i < VJ; i += 4)
+                        *(float4*)(row + (VC == 2 ? 64 : 4) * r + i) =
+                            make_float4(acc[j][i][e + 2 * r], acc[j][i + 1][e + 2 * r], acc[j][i + 2][e + 2 * r],
+                                        acc[j][i + 3][e + 2 * r]);
+            }
+        join<TI>(a, share, sm);
+        if (a.split != kShares) return;
+        __syncthreads();  // the shared memory is free for the next unit
     }
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int h = 8 * j + 2 * t + e;
-#pragma unroll
-            for (int w = 4; w < 32; w *= 2) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], w);
-            if (g == 0) {
-                sm.m[warp][h] = m[j][e];
-                sm.l[warp][h] = l[j][e];
-            }
-            float* row = (float*)sm.acc[warp][h] + 8 * g;
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int i = 0; i < VJ; i += 4)
-                    *(float4*)(row + (VC == 2 ? 64 : 4) * r + i) =
-                        make_float4(acc[j][i][e + 2 * r], acc[j][i + 1][e + 2 * r], acc[j][i + 2][e + 2 * r],
-                                    acc[j][i + 3][e + 2 * r]);
-        }
-    join<TI>(a, wk, sm);
 }
 
 // ------------------------------------------------------------------ fp32
@@ -510,101 +636,105 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 1 : NT == 1 ? 3 : 2) k_attend
 // FFMA kernel: one CTA per (part, up to HT query heads of one cache head, sequence), each warp R rows at a time, a
 // lane holding K / 32 and V / 32 channels of each row and of every head. The R HT scores are sums over the lanes: a
 // butterfly that halves the values with the lanes leaves value i, summed, in the lanes l with l % (R HT) == i.
-template <int K, int V, int HT, int R, int W>
-__global__ void __launch_bounds__(W * 32) k_attend_simt(AttendArgs a) {
+template <int K, int V, int HT, int R>
+__global__ void __launch_bounds__(kWarps * 32, 3) k_attend_simt(AttendArgs a) {
     constexpr int KL = K / 32, VL = V / 32, NV = R * HT;
-    __shared__ Partial<W, HT, V> sm;
+    __shared__ Partial<HT, V> sm;
     const int lane = threadIdx.x % 32;
-    Work<W, R, HT> wk;
-    if (a.cluster) cluster_arrive();
+    if (a.split == kCluster) cluster_arrive();
     after_previous();
-    if (!wk.start(a) && !a.cluster) return;
-    const int h0 = wk.h0, heads = wk.heads, warp = wk.warp;
-    Rows<R>& rows = wk.rows;
-    float q[HT][KL], acc[HT][VL];
+    Work<R, HT> wk;
+    __shared__ typename Work<R, HT>::Share share;
+    for (bool more = wk.start(a, share); more; more = wk.next(a, share)) {
+        const int h0 = wk.h0, heads = wk.heads, warp = wk.warp;
+        Rows<R>& rows = wk.rows;
+        float q[HT][KL], acc[HT][VL];
 #pragma unroll
-    for (int h = 0; h < HT; ++h) {
+        for (int h = 0; h < HT; ++h) {
 #pragma unroll
-        for (int i = 0; i < KL; ++i)
-            q[h][i] = h < heads ? ((const float*)a.q)[wk.n * a.q_stride + (h0 + h) * K + lane * KL + i] : 0.f;
+            for (int i = 0; i < KL; ++i)
+                q[h][i] = h < heads ? ((const float*)a.q)[(int64_t)wk.n * a.q_stride + (h0 + h) * K + lane * KL + i] : 0.f;
 #pragma unroll
-        for (int i = 0; i < VL; ++i) acc[h][i] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;  // of head lane % HT
-    const float* kh = (const float*)a.c.k + wk.hkv * a.c.k_head + lane * KL;
-    const float* vh = (const float*)a.c.v + wk.hkv * a.c.v_head + lane * VL;
-    float kr[R][KL], vr[R][VL];
-    auto load_k = [&]() {
+            for (int i = 0; i < VL; ++i) acc[h][i] = 0.f;
+        }
+        float m = -INFINITY, l = 0.f;  // of head lane % HT
+        const float* kh = (const float*)a.c.k + wk.hkv * a.c.k_head + lane * KL;
+        const float* vh = (const float*)a.c.v + wk.hkv * a.c.v_head + lane * VL;
+        float kr[R][KL], vr[R][VL];
+        auto load_k = [&]() {
 #pragma unroll
-        for (int r = 0; r < R; ++r) load_channels<KL>(kh + rows.k_of(r), rows.valid >> r & 1, kr[r]);
-    };
-    auto load_v = [&]() {
+            for (int r = 0; r < R; ++r) load_channels<KL>(kh + rows.k_of(r), rows.valid >> r & 1, kr[r]);
+        };
+        auto load_v = [&]() {
 #pragma unroll
-        for (int r = 0; r < R; ++r) load_channels<VL>(vh + rows.v_of(r), rows.valid >> r & 1, vr[r]);
-    };
-    rows.next(a);
-    load_k();
-    load_v();
-    for (int first = wk.first; first < wk.end; first += rows.step) {
-        float s[NV];  // value r HT + h
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int h = 0; h < HT; ++h) {
-                s[r * HT + h] = q[h][0] * kr[r][0];
-#pragma unroll
-                for (int i = 1; i < KL; ++i) s[r * HT + h] = fmaf(q[h][i], kr[r][i], s[r * HT + h]);
-            }
-        const bool in = rows.valid >> (lane % NV / HT) & 1;
+            for (int r = 0; r < R; ++r) load_channels<VL>(vh + rows.v_of(r), rows.valid >> r & 1, vr[r]);
+        };
         rows.next(a);
         load_k();
-#pragma unroll
-        for (int w = NV / 2; w > 0; w /= 2)
-#pragma unroll
-            for (int i = 0; i < w; ++i) {
-                const float mine = lane & w ? s[i + w] : s[i], other = lane & w ? s[i] : s[i + w];
-                s[i] = mine + __shfl_xor_sync(0xffffffffu, other, w);
-            }
-#pragma unroll
-        for (int w = NV; w < 32; w *= 2) s[0] += __shfl_xor_sync(0xffffffffu, s[0], w);
-        const float score = in ? s[0] * a.scale_log2 : -INFINITY;
-        if (__any_sync(0xffffffffu, score > m + kSlack)) {
-            float top = fmaxf(m, score);
-#pragma unroll
-            for (int w = HT; w < NV; w *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-            const float f = exp2f(m - finite_base(top));
-            m = top;
-            l *= f;
-#pragma unroll
-            for (int h = 0; h < HT; ++h) {
-                const float fh = __shfl_sync(0xffffffffu, f, h);
-#pragma unroll
-                for (int i = 0; i < VL; ++i) acc[h][i] *= fh;
-            }
-        }
-        const float p = exp2f(score - finite_base(m));
-        l += p;
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int h = 0; h < HT; ++h) {
-                const float ph = __shfl_sync(0xffffffffu, p, r * HT + h);
-#pragma unroll
-                for (int i = 0; i < VL; ++i) acc[h][i] = fmaf(ph, vr[r][i], acc[h][i]);
-            }
         load_v();
+        for (int first = wk.first; first < wk.end; first += rows.step) {
+            float s[NV];  // value r HT + h
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int h = 0; h < HT; ++h) {
+                    s[r * HT + h] = q[h][0] * kr[r][0];
+#pragma unroll
+                    for (int i = 1; i < KL; ++i) s[r * HT + h] = fmaf(q[h][i], kr[r][i], s[r * HT + h]);
+                }
+            const bool in = rows.valid >> (lane % NV / HT) & 1;
+            rows.next(a);
+            load_k();
+#pragma unroll
+            for (int w = NV / 2; w > 0; w /= 2)
+#pragma unroll
+                for (int i = 0; i < w; ++i) {
+                    const float mine = lane & w ? s[i + w] : s[i], other = lane & w ? s[i] : s[i + w];
+                    s[i] = mine + __shfl_xor_sync(0xffffffffu, other, w);
+                }
+#pragma unroll
+            for (int w = NV; w < 32; w *= 2) s[0] += __shfl_xor_sync(0xffffffffu, s[0], w);
+            const float score = in ? s[0] * a.scale_log2 : -INFINITY;
+            if (__any_sync(0xffffffffu, score > m + kSlack)) {
+                float top = fmaxf(m, score);
+#pragma unroll
+                for (int w = HT; w < NV; w *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+                const float f = exp2f(m - finite_base(top));
+                m = top;
+                l *= f;
+#pragma unroll
+                for (int h = 0; h < HT; ++h) {
+                    const float fh = __shfl_sync(0xffffffffu, f, h);
+#pragma unroll
+                    for (int i = 0; i < VL; ++i) acc[h][i] *= fh;
+                }
+            }
+            const float p = exp2f(score - finite_base(m));
+            l += p;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int h = 0; h < HT; ++h) {
+                    const float ph = __shfl_sync(0xffffffffu, p, r * HT + h);
+#pragma unroll
+                    for (int i = 0; i < VL; ++i) acc[h][i] = fmaf(ph, vr[r][i], acc[h][i]);
+                }
+            load_v();
+        }
+#pragma unroll
+        for (int w = HT; w < NV; w *= 2) l += __shfl_xor_sync(0xffffffffu, l, w);
+        if (lane < HT) {
+            sm.m[warp][lane] = m;
+            sm.l[warp][lane] = l;
+        }
+#pragma unroll
+        for (int h = 0; h < HT; ++h)
+#pragma unroll
+            for (int i = 0; i < VL; ++i) ((float*)sm.acc[warp][h])[lane * VL + i] = acc[h][i];
+        join<float>(a, share, sm);
+        if (a.split != kShares) return;
+        __syncthreads();  // the shared memory is free for the next unit
     }
-#pragma unroll
-    for (int w = HT; w < NV; w *= 2) l += __shfl_xor_sync(0xffffffffu, l, w);
-    if (lane < HT) {
-        sm.m[warp][lane] = m;
-        sm.l[warp][lane] = l;
-    }
-#pragma unroll
-    for (int h = 0; h < HT; ++h)
-#pragma unroll
-        for (int i = 0; i < VL; ++i) ((float*)sm.acc[warp][h])[lane * VL + i] = acc[h][i];
-    join<float>(a, wk, sm);
 }
 
 // ------------------------------------------------------------------ launch
@@ -616,44 +746,82 @@ int head_tile(const kda_cache* c, int HQ) {
     return group == 1 ? 1 : group <= 4 ? 4 : 8;
 }
 
-// The split of each sequence's rows: warps to a CTA, CTAs.
 struct Plan {
-    int warps, parts, cluster, turn;
+    Split split;
+    int parts, ht, units;
+    unsigned grid;
+    size_t acc_bytes, ml_bytes, ws_bytes;  // of the workspace
 };
 Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window) {
-    const int group = HQ / c->HKV, ht = head_tile(c, HQ);
-    const int64_t units = (int64_t)(N > 0 ? N : 1) * c->HKV * ((group + ht - 1) / ht);
+    const bool bf16 = c->dtype == KDA_DTYPE_BF16;
+    const int group = HQ / c->HKV, ht = head_tile(c, HQ), units = c->HKV * ((group + ht - 1) / ht);
+    const int turn = kWarps * (bf16 ? 16 : ht == 8 ? 4 : 8);
     int64_t rows = (int64_t)max_pages * c->page_size;
     if (window > 0 && window < rows) rows = window;
-    const int tile = c->dtype == KDA_DTYPE_BF16 ? 16 : ht == 8 ? 4 : 8;
-    Plan p{4, (int)((152 * 3 + units - 1) / units), 0, 4 * tile};
+    const int64_t turns = rows > turn ? (rows + turn - 1) / turn : 1, all = (int64_t)N * units;  // of a unit; units
+    const int slots = 152 * (bf16 && ht == 16 ? 2 : 3);
+    Plan p{kWhole, 1, ht, units};
+    if (turns > 1 && all * 2 <= slots && turns <= 2 * kMaxCluster) {
+        p.split = kCluster;
+        p.parts = 2;
+        while (p.parts < kMaxCluster && p.parts < turns && all * p.parts * 2 <= slots) p.parts *= 2;
+    } else if (turns > 2 && turns * all < INT32_MAX) {
+        p.split = kShares;
+        p.parts = (int)(turns * all < slots ? turns * all : slots);
+    }
 #ifdef TUNE
-    p.warps = atoi(getenv("KW")); p.parts = atoi(getenv("KS")); p.cluster = atoi(getenv("KC")); p.turn = p.warps * tile;
+    if (getenv("KM")) {
+        p.split = (Split)atoi(getenv("KM"));
+        p.parts = p.split == kWhole ? 1 : atoi(getenv("KS"));
+    }
 #endif
+    p.grid = (unsigned)(p.split == kShares ? p.parts : all * p.parts);
+    p.ws_bytes = 256;
+    if (p.split == kShares) {
+        p.acc_bytes = (size_t)p.parts * 2 * ht * c->V * sizeof(float);
+        p.ml_bytes = (size_t)p.parts * 2 * ht * sizeof(float2);
+        p.ws_bytes += p.acc_bytes + p.ml_bytes + (size_t)all * sizeof(int2);
+    }
     return p;
 }
 
 typedef void (*Kernel)(AttendArgs);
 
-template <int K, int V> Kernel kernel_of(bool bf16, int ht, int warps) {
-    if (bf16 && warps == 8) return k_attend_mma<K, V, 1, 8>;
-    if (bf16) return ht == 8 ? k_attend_mma<K, V, 1, 4> : k_attend_mma<K, V, 2, 4>;
-    return ht == 1 ? k_attend_simt<K, V, 1, 8, 4> : ht == 4 ? k_attend_simt<K, V, 4, 8, 4> : k_attend_simt<K, V, 8, 4, 4>;
+template <int K, int V> Kernel kernel_of(bool bf16, int ht) {
+    if (bf16) return ht == 8 ? k_attend_mma<K, V, 1> : k_attend_mma<K, V, 2>;
+    return ht == 1 ? k_attend_simt<K, V, 1, 8> : ht == 4 ? k_attend_simt<K, V, 4, 8> : k_attend_simt<K, V, 8, 4>;
+}
+template <typename TI, int V, int HT> cudaError_t launch_join(const AttendArgs& a, int64_t parts, cudaStream_t st) {
+    const int64_t heads = (int64_t)a.N * a.HQ;
+    constexpr int U = V / 4;
+    if (parts <= kJoinBatch)
+        return launch_after(k_attend_join<TI, V, HT, 1>, a, (unsigned)((heads * U + kJoinThreads - 1) / kJoinThreads),
+                            kJoinThreads, st);
+    if (parts <= 4 * kJoinBatch)
+        return launch_after(k_attend_join<TI, V, HT, 4>, a, (unsigned)((heads * 4 * U + kJoinThreads - 1) / kJoinThreads),
+                            kJoinThreads, st);
+    return launch_after(k_attend_join<TI, V, HT, 16>, a, (unsigned)heads, 16 * U, st);
+}
+template <int V> cudaError_t launch_join(const AttendArgs& a, bool bf16, int ht, int64_t parts, cudaStream_t st) {
+    if (bf16)
+        return ht == 8 ? launch_join<__nv_bfloat16, V, 8>(a, parts, st) : launch_join<__nv_bfloat16, V, 16>(a, parts, st);
+    return ht == 1   ? launch_join<float, V, 1>(a, parts, st)
+           : ht == 4 ? launch_join<float, V, 4>(a, parts, st)
+                     : launch_join<float, V, 8>(a, parts, st);
 }
 
-cudaError_t launch_attend(const AttendArgs& a, int warps, cudaStream_t st) {
+cudaError_t launch_attend(const AttendArgs& a, const Plan& p, cudaStream_t st) {
     const bool bf16 = a.c.dtype == KDA_DTYPE_BF16;
-    const int ht = head_tile(&a.c, a.HQ), group = a.HQ / a.c.HKV, K = a.c.K, V = a.c.V;
-    const unsigned grid = (unsigned)((int64_t)a.N * a.c.HKV * ((group + ht - 1) / ht) * a.parts);
-    const Kernel kernel = K == 128 ? (V == 128 ? kernel_of<128, 128>(bf16, ht, warps) : kernel_of<128, 64>(bf16, ht, warps))
-                                   : (V == 128 ? kernel_of<64, 128>(bf16, ht, warps) : kernel_of<64, 64>(bf16, ht, warps));
-    cudaError_t e = launch_after(kernel, a, grid, warps * 32, st, a.cluster ? a.parts : 1);
+    const int K = a.c.K, V = a.c.V;
+    const Kernel kernel = K == 128 ? (V == 128 ? kernel_of<128, 128>(bf16, p.ht) : kernel_of<128, 64>(bf16, p.ht))
+                                   : (V == 128 ? kernel_of<64, 128>(bf16, p.ht) : kernel_of<64, 64>(bf16, p.ht));
+    cudaError_t e = launch_after(kernel, a, p.grid, kWarps * 32, st, p.split == kCluster ? p.parts : 1);
     if (e != cudaSuccess) return e;
     note_launch("cache_attend", st);
-    if (a.parts == 1 || a.cluster) return cudaSuccess;
-    const Kernel join = bf16 ? (V == 128 ? k_attend_join<__nv_bfloat16, 128> : k_attend_join<__nv_bfloat16, 64>)
-                             : (V == 128 ? k_attend_join<float, 128> : k_attend_join<float, 64>);
-    if ((e = launch_after(join, a, (unsigned)((int64_t)a.N * a.HQ), kJoinThreads, st)) != cudaSuccess) return e;
+    if (p.split != kShares) return cudaSuccess;
+    const int64_t parts = p.parts / ((int64_t)a.N * p.units) + 2;  // of a unit, with equal lengths
+    e = V == 128 ? launch_join<128>(a, bf16, p.ht, parts, st) : launch_join<64>(a, bf16, p.ht, parts, st);
+    if (e != cudaSuccess) return e;
     note_launch("cache_attend_join", st);
     return cudaSuccess;
 }
@@ -674,9 +842,7 @@ using namespace kda;
 extern "C" size_t kda_cache_attend_workspace_bytes(const kda_cache* c, int32_t HQ, int32_t N, int32_t max_pages,
                                                    int32_t window) {
     if (check_sizes(c, HQ, N, max_pages, window) != KDA_OK) return 0;
-    const Plan plan = plan_of(c, HQ, N, max_pages, window);
-    const int64_t parts = plan.cluster ? 1 : plan.parts;
-    return parts == 1 ? 256 : 256 + (size_t)N * HQ * parts * ((size_t)c->V * sizeof(float) + sizeof(float2));
+    return plan_of(c, HQ, N, max_pages, window).ws_bytes;
 }
 
 extern "C" kda_status kda_cache_attend(const kda_cache* c, const void* q, int64_t q_stride, int32_t HQ, int32_t N,
@@ -692,16 +858,15 @@ extern "C" kda_status kda_cache_attend(const kda_cache* c, const void* q, int64_
     if (!aligned16(q) || !aligned16(o) || ((uintptr_t)lse & 3u) || ((uintptr_t)page_table & 3u) ||
         ((uintptr_t)kv_lens & 3u) || ((uintptr_t)status & 3u))
         return KDA_ERR_INVALID_ARG;
-    if (!ws || !aligned16(ws) || ws_bytes < kda_cache_attend_workspace_bytes(c, HQ, N, max_pages, window))
-        return KDA_ERR_WORKSPACE;
     const Plan plan = plan_of(c, HQ, N, max_pages, window);
-    AttendArgs a{*c, q, q_stride, table_stride, HQ, N, max_pages, window, page_table, kv_lens, scale * kLog2e, o, lse,
-                 status, plan.parts, plan.cluster, plan.turn, nullptr, nullptr};
-    a.part_acc = (float*)ws;
-    a.part_ml = (float2*)(a.part_acc + (int64_t)N * HQ * a.parts * c->V);
+    if (!ws || !aligned16(ws) || ws_bytes < plan.ws_bytes) return KDA_ERR_WORKSPACE;
+    char* w = (char*)ws;
+    const AttendArgs a{*c, q, q_stride, table_stride, HQ, N, max_pages, window, page_table, kv_lens, scale * kLog2e, o,
+                       lse, status, plan.split, plan.parts, (float4*)w, (float2*)(w + plan.acc_bytes),
+                       (int2*)(w + plan.acc_bytes + plan.ml_bytes)};
     cudaStream_t st = (cudaStream_t)stream;
     begin_launches(st);
-    const cudaError_t e = launch_attend(a, plan.warps, st);
+    const cudaError_t e = launch_attend(a, plan, st);
     if (e != cudaSuccess) return cuda_fail(e);
     return KDA_OK;
 }
