@@ -28,6 +28,7 @@ struct AttendArgs {
     void* o;
     float* lse;
     int32_t* status;
+    int step, step_pg, step_off;  // rows from a warp's tile to its next, in pages and rows
     int split, parts;  // parts: kCluster: CTAs of a cluster; kShares: CTAs in all; kWhole: 1
     // kShares: what a CTA has of a unit that it ends (0) or begins (1) but does not have whole, head by head: the
     // weighted sum relative to its maximum [parts, 2, HT, V], and its maximum (log2 units) and sum of weights
@@ -61,37 +62,36 @@ __device__ __forceinline__ float ex2(float x) {
 // of the next tile's pages is in flight while a tile is computed.
 template <int R> struct Rows {
     const int32_t* table;
-    int end, row, pg, off, page;     // the next tile's row of this lane
-    int step_pg, step_off, step;
-    int64_t k_off, v_off;            // this tile's row of this lane
-    unsigned valid;                  // bit r: row r is in range and its page exists
+    int left;           // rows from the next tile's row of this lane to the end
+    int pg, off, page;  // that row's place
+    int64_t k_off, v_off;  // this tile's row of this lane
+    unsigned valid;        // bit r: row r is in range and its page exists
 
-    // Rows from `first` on, `stride` apart; `end` is set by the caller, later where the length is still on its way.
-    __device__ __forceinline__ void start(const AttendArgs& a, int64_t n, int first, int stride) {
+    // Rows from `first` on, of a warp whose tiles are a.step rows apart.
+    __device__ __forceinline__ void start(const AttendArgs& a, int64_t n, int first) {
+        const int row = first + threadIdx.x % 32 % R;
         table = a.table + n * a.table_stride;
-        row = first + threadIdx.x % 32 % R;
-        step = stride;
         pg = (unsigned)row / (unsigned)a.c.page_size;
         off = row - pg * a.c.page_size;
-        step_pg = (unsigned)stride / (unsigned)a.c.page_size;
-        step_off = stride - step_pg * a.c.page_size;
         page = pg < a.max_pages ? __ldg(table + pg) : -1;
     }
+    // The end of the rows, which may be known later than their beginning.
+    __device__ __forceinline__ void until(int first, int end) { left = end - first - (int)(threadIdx.x % 32 % R); }
     __device__ __forceinline__ void next(const AttendArgs& a) {
-        const bool in = row < end, ok = in && (unsigned)page < (unsigned)a.c.num_pages;
+        const bool in = left > 0, ok = in && (unsigned)page < (unsigned)a.c.num_pages;
         if (in && !ok && a.status) *a.status = KDA_ERR_INVALID_ARG;
         valid = __ballot_sync(0xffffffffu, ok);
         const int64_t p = ok ? page : 0;
         k_off = p * a.c.k_page + off * a.c.k_row;
         v_off = p * a.c.v_page + off * a.c.v_row;
-        row += step;
-        pg += step_pg;
-        off += step_off;
+        left -= a.step;
+        pg += a.step_pg;
+        off += a.step_off;
         if (off >= a.c.page_size) {
             off -= a.c.page_size;
             ++pg;
         }
-        page = row < end ? __ldg(table + pg) : -1;
+        page = left > 0 ? __ldg(table + pg) : -1;
     }
     __device__ __forceinline__ int64_t k_of(int r) const { return __shfl_sync(0xffffffffu, k_off, r); }
     __device__ __forceinline__ int64_t v_of(int r) const { return __shfl_sync(0xffffffffu, v_off, r); }
@@ -127,9 +127,10 @@ template <int C> __device__ __forceinline__ void load_channels(const float* p, b
 constexpr int kWarps = 4;
 constexpr int kMaxCluster = 16;
 
-template <int R, int HT> struct Work {
+template <int R, int HT, bool SHARES> struct Work {
     static constexpr int W = kWarps, kTurn = W * R;
-    int n, hkv, h0, heads, warp, first, end;
+    int n, hkv, h0, heads, warp;
+    int left;  // rows from the warp's first one to the end
     int odd;  // kShares: which of the share's two states is the next
     Rows<R> rows;
 
@@ -170,7 +171,7 @@ template <int R, int HT> struct Work {
         const unsigned units = units_of(a);
         warp = threadIdx.x / 32;
         odd = 0;
-        if (a.split == kShares) {
+        if constexpr (SHARES) {
             find_share(a, units, share);
             return next(a, share);
         }
@@ -178,16 +179,25 @@ template <int R, int HT> struct Work {
         const int part = blockIdx.x % (unsigned)a.parts;
         n = x / units;
         set_unit(a, x % units, true, part, share);
-        first = (part * W + warp) * R;
-        rows.start(a, n, first, a.parts * kTurn);
-        int begin;
+        int first = (part * W + warp) * R, begin, end;
+        rows.start(a, n, first);
         kv_range(a, n, begin, end);
         if (a.window > 0) {
             first += begin;
-            rows.start(a, n, first, a.parts * kTurn);
+            rows.start(a, n, first);
         }
-        rows.end = end;
+        left = end - first;
+        rows.until(first, end);
         return true;
+    }
+    // kShares: turns are dealt out evenly, one more to each of the first total % ctas CTAs: the first turn of CTA x, and
+    // the CTA that has turn y.
+    __device__ __forceinline__ static int first_turn(int x, int total, int ctas) {
+        return x * (total / ctas) + min(x, total % ctas);
+    }
+    __device__ __forceinline__ static int cta_of(int y, int total, int ctas) {
+        const int each = total / ctas, more = total % ctas, both = more * (each + 1);
+        return y < both ? y / (each + 1) : more + (y - both) / each;
     }
     // kShares: the CTA's share, and the sequence that it begins in.
     __device__ __forceinline__ void find_share(const AttendArgs& a, int units, Share& share) {
@@ -195,10 +205,9 @@ template <int R, int HT> struct Work {
             if (threadIdx.x == 0) {
                 int begin, last;
                 kv_range(a, 0, begin, last);
-                const int total = turns_of(begin, last) * units, ctas = min(a.parts, total);
-                const int x = min((int)blockIdx.x, ctas);
-                share.state[0] = {(int)((int64_t)x * total / ctas), 0, 0};
-                share.stop = x == ctas ? 0 : (int)((int64_t)(x + 1) * total / ctas);
+                const int total = turns_of(begin, last) * units, ctas = min(a.parts, total), x = min((int)blockIdx.x, ctas);
+                share.state[0] = {first_turn(x, total, ctas), 0, 0};
+                share.stop = x == ctas ? 0 : first_turn(x + 1, total, ctas);
                 share.total = total;
             }
             __syncthreads();
@@ -227,7 +236,7 @@ template <int R, int HT> struct Work {
             total += share.sums[w];
         }
         const int ctas = min(a.parts, total);  // with fewer turns than CTAs, those that have one
-        const int at = (int)((int64_t)min((int)blockIdx.x, ctas) * total / ctas);
+        const int at = first_turn(min((int)blockIdx.x, ctas), total, ctas);
         if (blockIdx.x >= ctas && threadIdx.x == 0) share.state[0].at = share.stop = 0;
         if (at >= before && at < before + mine) {
             int i = n0;
@@ -237,7 +246,7 @@ template <int R, int HT> struct Work {
                 if (at < before + turns) break;
                 before += turns;
             }
-            share.stop = (int)((int64_t)(blockIdx.x + 1) * total / ctas);
+            share.stop = first_turn(blockIdx.x + 1, total, ctas);
             share.total = total;
             share.state[0] = {at, i, before};
         }
@@ -261,14 +270,14 @@ template <int R, int HT> struct Work {
         if (threadIdx.x == 0) {
             share.state[odd] = {at + t1 - t0, n, seq};
             if (t0 == 0) {
-                const int64_t behind = (int64_t)at + turns;  // the turn behind the unit's last, which CTA `to` has
-                const int to = (int)((behind * min(a.parts, share.total) - 1) / share.total);
+                const int to = cta_of(at + turns - 1, share.total, min(a.parts, share.total));
                 a.unit_parts[(int64_t)n * units + u] = make_int2(blockIdx.x, to);
             }
         }
-        first = begin + (t0 * W + warp) * R;
-        rows.start(a, n, first, kTurn);
-        rows.end = end = min(last, begin + t1 * kTurn);
+        const int first = begin + (t0 * W + warp) * R, end = min(last, begin + t1 * kTurn);
+        rows.start(a, n, first);
+        left = end - first;
+        rows.until(first, end);
         return true;
     }
 };
@@ -322,9 +331,9 @@ template <int HT, int V> struct Partial {
 
 // Joins the warps of a CTA and, in a cluster, its CTAs, and writes the unit's result, or, where the CTA does not have
 // all of the unit, its part. The order of the sums is fixed.
-template <typename TI, int V, int HT, typename Share>
+template <typename TI, int V, int HT, bool SHARES, typename Share>
 __device__ __forceinline__ void join(const AttendArgs& a, const Share& unit, Partial<HT, V>& p) {
-    const bool cluster = a.split == kCluster;
+    const bool cluster = !SHARES && a.split == kCluster;
     if (cluster) cluster_wait();  // for the others to have started
     __syncthreads();
     const int items = unit.heads * (V / 4), share = (items + a.parts - 1) / a.parts;  // share: of a CTA of the cluster
@@ -347,7 +356,7 @@ __device__ __forceinline__ void join(const AttendArgs& a, const Share& unit, Par
         if (cluster) {
             push(&p.in_acc[part * share + i % share], i / share, x);
             if (u < a.parts) push(&p.in_ml[part][h], u, make_float2(m, l));
-        } else if (unit.whole) {
+        } else if (!SHARES || unit.whole) {
             write_result<TI>(a, head + h, V, 4 * u, m, l, x);
         } else {
             const int64_t to = (int64_t)part * HT + h;
@@ -375,16 +384,18 @@ __device__ __forceinline__ void join(const AttendArgs& a, const Share& unit, Par
     }
 }
 
-// kShares: the parts of one query head, joined in an order that goes by their number alone. Group g of G groups of
-// V / 4 threads takes parts g, g + G, .., a batch of them at a time; the groups are joined in shared memory.
-constexpr int kJoinBatch = 8, kJoinThreads = 128;
-template <typename TI, int V, int HT, int G>
-__global__ void __launch_bounds__(G * V / 4 > kJoinThreads ? G * V / 4 : kJoinThreads) k_attend_join(AttendArgs a) {
-    constexpr int U = V / 4, HB = G * U > kJoinThreads ? 1 : kJoinThreads / (G * U);  // query heads of a CTA
+// kShares: the parts of one query head and VS of its channels, joined in an order that goes by their number alone.
+// Group g of G groups of VS / 4 threads takes parts g, g + G, .., a batch of them at a time; the groups are joined in
+// shared memory.
+constexpr int kJoinBatch = 8;
+template <typename TI, int V, int HT, int VS, int G, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_attend_join(AttendArgs a) {
+    constexpr int U = VS / 4, S = V / VS, HB = THREADS / (G * U);  // slices of a head; (head, slice) pairs of a CTA
     __shared__ float4 sx[HB][G][U];
     __shared__ float2 sml[HB][G];
-    const unsigned mine = threadIdx.x / (G * U), head = min(blockIdx.x * HB + mine, (unsigned)(a.N * a.HQ - 1));
-    const int g = threadIdx.x / U % G, u = threadIdx.x % U;
+    const unsigned mine = threadIdx.x / (G * U), at = blockIdx.x * HB + mine, last = (unsigned)(a.N * a.HQ) * S - 1;
+    const unsigned head = min(at, last) / S, u = min(at, last) % S * U + threadIdx.x % U;
+    const int g = threadIdx.x / U % G;
     const unsigned group = (unsigned)a.HQ / a.c.HKV, tiles = (group + HT - 1) / HT;
     const unsigned n = head / a.HQ, hq = head % a.HQ, hkv = hq / group, qt = hq % group / HT, h = hq % group % HT;
     after_previous();
@@ -402,7 +413,7 @@ __global__ void __launch_bounds__(G * V / 4 > kJoinThreads ? G * V / 4 : kJoinTh
                 const int c = s + i * G;
                 const int64_t from = (int64_t)(2 * (range.x + c) + (c == 0)) * HT + h;
                 e[i] = c < count ? a.part_ml[from] : make_float2(-INFINITY, 0.f);
-                y[i] = c < count ? a.part_acc[from * U + u] : make_float4(0.f, 0.f, 0.f, 0.f);
+                y[i] = c < count ? a.part_acc[from * (V / 4) + u] : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
             for (int i = 0; i < kJoinBatch; ++i) top = fmaxf(top, e[i].x);
@@ -419,8 +430,8 @@ __global__ void __launch_bounds__(G * V / 4 > kJoinThreads ? G * V / 4 : kJoinTh
         }
     }
     if constexpr (G > 1) {
-        sx[mine][g][u] = x;
-        if (u == 0) sml[mine][g] = make_float2(m, l);
+        sx[mine][g][threadIdx.x % U] = x;
+        if (threadIdx.x % U == 0) sml[mine][g] = make_float2(m, l);
         __syncthreads();
         if (g > 0) return;
 #pragma unroll
@@ -432,11 +443,11 @@ __global__ void __launch_bounds__(G * V / 4 > kJoinThreads ? G * V / 4 : kJoinTh
         for (int i = 0; i < G; ++i) {
             const float f = ex2(sml[mine][i].x - base);
             l = fmaf(sml[mine][i].y, f, l);
-            add_scaled(x, sx[mine][i][u], f);
+            add_scaled(x, sx[mine][i][threadIdx.x % U], f);
         }
     }
-    // (one part alone has written the result; the last CTA's spare threads have the last head once more)
-    if (count > 1 && blockIdx.x * HB + mine == head) write_result<TI>(a, head, V, 4 * u, m, l, x);
+    // (one part alone has written the result; the last CTA's spare threads have the last pair once more)
+    if (count > 1 && at <= last) write_result<TI>(a, head, V, 4 * u, m, l, x);
 }
 
 // ------------------------------------------------------------------ bf16
@@ -473,16 +484,17 @@ constexpr float kSlack = 8.f;
 //   - P^T comes from S^T by an 8 x 8 transposition in registers; it is split into a pair of bf16 values (2^-16).
 // A tensor core of the fifth generation wants its operands in shared memory and 128 rows in a product; with at most 16
 // query heads against it, the memory's time would cover none of that traffic.
-template <int K, int V, int NT>
+template <int K, int V, int NT, bool SHARES>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) k_attend_mma(AttendArgs a) {
     using TI = __nv_bfloat16;
     constexpr int KI = K / 32, VC = V / 64, VJ = V / 16, HT = 8 * NT;
     __shared__ Partial<HT, V> sm;
     const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-    if (a.split == kCluster) cluster_arrive();
+    if (!SHARES && a.split == kCluster) cluster_arrive();
     after_previous();
-    Work<16, HT> wk;
-    __shared__ typename Work<16, HT>::Share share;
+    Work<16, HT, SHARES> wk;
+    __shared__ typename Work<16, HT, SHARES>::Share share;
+#pragma unroll 1
     for (bool more = wk.start(a, share); more; more = wk.next(a, share)) {
         const int h0 = wk.h0, heads = wk.heads, warp = wk.warp;
         Rows<16>& rows = wk.rows;
@@ -528,7 +540,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) k_attend_mma(Att
         rows.next(a);
         load_k();
         load_v();
-        for (int first = wk.first; first < wk.end; first += rows.step) {
+#pragma unroll 1
+        for (int left = wk.left; left > 0; left -= a.step) {
             float s[NT][4];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -625,26 +638,31 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) k_attend_mma(Att
                             make_float4(acc[j][i][e + 2 * r], acc[j][i + 1][e + 2 * r], acc[j][i + 2][e + 2 * r],
                                         acc[j][i + 3][e + 2 * r]);
             }
-        join<TI>(a, share, sm);
-        if (a.split != kShares) return;
+        join<TI, V, HT, SHARES>(a, share, sm);
+        if constexpr (!SHARES) return;
         __syncthreads();  // the shared memory is free for the next unit
     }
 }
 
 // ------------------------------------------------------------------ fp32
 
+// CTAs of k_attend_simt to an SM, and rows of a warp's tile.
+constexpr int simt_ctas(int ht) { return ht == 1 ? 4 : 3; }
+constexpr int simt_rows(int ht) { return ht == 8 ? 4 : 8; }
+
 // FFMA kernel: one CTA per (part, up to HT query heads of one cache head, sequence), each warp R rows at a time, a
 // lane holding K / 32 and V / 32 channels of each row and of every head. The R HT scores are sums over the lanes: a
 // butterfly that halves the values with the lanes leaves value i, summed, in the lanes l with l % (R HT) == i.
-template <int K, int V, int HT, int R>
-__global__ void __launch_bounds__(kWarps * 32, 3) k_attend_simt(AttendArgs a) {
+template <int K, int V, int HT, int R, bool SHARES>
+__global__ void __launch_bounds__(kWarps * 32, SHARES ? simt_ctas(HT) : 1) k_attend_simt(AttendArgs a) {
     constexpr int KL = K / 32, VL = V / 32, NV = R * HT;
     __shared__ Partial<HT, V> sm;
     const int lane = threadIdx.x % 32;
-    if (a.split == kCluster) cluster_arrive();
+    if (!SHARES && a.split == kCluster) cluster_arrive();
     after_previous();
-    Work<R, HT> wk;
-    __shared__ typename Work<R, HT>::Share share;
+    Work<R, HT, SHARES> wk;
+    __shared__ typename Work<R, HT, SHARES>::Share share;
+#pragma unroll 1
     for (bool more = wk.start(a, share); more; more = wk.next(a, share)) {
         const int h0 = wk.h0, heads = wk.heads, warp = wk.warp;
         Rows<R>& rows = wk.rows;
@@ -672,7 +690,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) k_attend_simt(AttendArgs a) {
         rows.next(a);
         load_k();
         load_v();
-        for (int first = wk.first; first < wk.end; first += rows.step) {
+#pragma unroll 1
+        for (int left = wk.left; left > 0; left -= a.step) {
             float s[NV];  // value r HT + h
 #pragma unroll
             for (int r = 0; r < R; ++r)
@@ -731,8 +750,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) k_attend_simt(AttendArgs a) {
         for (int h = 0; h < HT; ++h)
 #pragma unroll
             for (int i = 0; i < VL; ++i) ((float*)sm.acc[warp][h])[lane * VL + i] = acc[h][i];
-        join<float>(a, share, sm);
-        if (a.split != kShares) return;
+        join<float, V, HT, SHARES>(a, share, sm);
+        if constexpr (!SHARES) return;
         __syncthreads();  // the shared memory is free for the next unit
     }
 }
@@ -748,26 +767,36 @@ int head_tile(const kda_cache* c, int HQ) {
 
 struct Plan {
     Split split;
-    int parts, ht, units;
+    int parts, ht, units, turn;
     unsigned grid;
     size_t acc_bytes, ml_bytes, ws_bytes;  // of the workspace
 };
 Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window) {
     const bool bf16 = c->dtype == KDA_DTYPE_BF16;
     const int group = HQ / c->HKV, ht = head_tile(c, HQ), units = c->HKV * ((group + ht - 1) / ht);
-    const int turn = kWarps * (bf16 ? 16 : ht == 8 ? 4 : 8);
+    const int turn = kWarps * (bf16 ? 16 : simt_rows(ht));
     int64_t rows = (int64_t)max_pages * c->page_size;
     if (window > 0 && window < rows) rows = window;
     const int64_t turns = rows > turn ? (rows + turn - 1) / turn : 1, all = (int64_t)N * units;  // of a unit; units
-    const int slots = 152 * (bf16 && ht == 16 ? 2 : 3);
-    Plan p{kWhole, 1, ht, units};
-    if (turns > 1 && all * 2 <= slots && turns <= 2 * kMaxCluster) {
+    const int slots = 152 * (!bf16 ? simt_ctas(ht) : ht == 8 ? 3 : 2);
+    const int slots_alone = !bf16 && ht == 1 && c->K + c->V == 128 ? 152 * 5 : slots;  // without kShares' registers
+    Plan p{kWhole, 1, ht, units, turn};
+    // What each costs, in turns (about 1.1 us): a cluster's own cost over a CTA alone is about one turn; that of shares
+    // (the lengths to add up first, the second kernel, its launch) four. Lengths are taken as three quarters of the
+    // longest that fits where there are several.
+    int cluster = 1;
+    while (cluster < kMaxCluster && cluster < turns &&
+           (all * cluster * 2 <= slots_alone || (all * cluster * 16 <= slots_alone * 9 && turns >= 8 * cluster)))
+        cluster *= 2;
+    const auto waves = [&](int64_t ctas) { return ctas > slots_alone ? (double)ctas / slots_alone : 1.0; };
+    const double whole = turns * waves(all), clusters = 1 + (double)turns / cluster * waves(all * cluster);
+    const double shares = 4 + (double)turns * all * (N > 1 ? 0.75 : 1.0) / slots;
+    if (cluster > 1 && clusters < whole && clusters <= shares) {
         p.split = kCluster;
-        p.parts = 2;
-        while (p.parts < kMaxCluster && p.parts < turns && all * p.parts * 2 <= slots) p.parts *= 2;
-    } else if (turns > 2 && turns * all < INT32_MAX) {
+        p.parts = cluster;
+    } else if (shares < whole && turns * all < INT32_MAX) {
         p.split = kShares;
-        p.parts = (int)(turns * all < slots ? turns * all : slots);
+        p.parts = turns * all < 64 * slots ? slots : 2 * slots;
     }
 #ifdef TUNE
     if (getenv("KM")) {
@@ -787,20 +816,26 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window) {
 
 typedef void (*Kernel)(AttendArgs);
 
-template <int K, int V> Kernel kernel_of(bool bf16, int ht) {
-    if (bf16) return ht == 8 ? k_attend_mma<K, V, 1> : k_attend_mma<K, V, 2>;
-    return ht == 1 ? k_attend_simt<K, V, 1, 8> : ht == 4 ? k_attend_simt<K, V, 4, 8> : k_attend_simt<K, V, 8, 4>;
+template <int K, int V, bool SHARES> Kernel kernel_of(bool bf16, int ht) {
+    if (bf16) return ht == 8 ? k_attend_mma<K, V, 1, SHARES> : k_attend_mma<K, V, 2, SHARES>;
+    return ht == 1   ? k_attend_simt<K, V, 1, simt_rows(1), SHARES>
+           : ht == 4 ? k_attend_simt<K, V, 4, simt_rows(4), SHARES>
+                     : k_attend_simt<K, V, 8, simt_rows(8), SHARES>;
 }
+template <int K, int V> Kernel kernel_of(bool bf16, int ht, Split split) {
+    return split == kShares ? kernel_of<K, V, true>(bf16, ht) : kernel_of<K, V, false>(bf16, ht);
+}
+template <typename TI, int V, int HT, int VS, int G, int THREADS>
+cudaError_t launch_join(const AttendArgs& a, cudaStream_t st) {
+    const int64_t threads = (int64_t)a.N * a.HQ * (V / 4) * G;
+    return launch_after(k_attend_join<TI, V, HT, VS, G, THREADS>, a, (unsigned)((threads + THREADS - 1) / THREADS),
+                        THREADS, st);
+}
+// `parts`: of a unit, with equal lengths. A batch of loads is to cover them.
 template <typename TI, int V, int HT> cudaError_t launch_join(const AttendArgs& a, int64_t parts, cudaStream_t st) {
-    const int64_t heads = (int64_t)a.N * a.HQ;
-    constexpr int U = V / 4;
-    if (parts <= kJoinBatch)
-        return launch_after(k_attend_join<TI, V, HT, 1>, a, (unsigned)((heads * U + kJoinThreads - 1) / kJoinThreads),
-                            kJoinThreads, st);
-    if (parts <= 4 * kJoinBatch)
-        return launch_after(k_attend_join<TI, V, HT, 4>, a, (unsigned)((heads * 4 * U + kJoinThreads - 1) / kJoinThreads),
-                            kJoinThreads, st);
-    return launch_after(k_attend_join<TI, V, HT, 16>, a, (unsigned)heads, 16 * U, st);
+    if (parts <= kJoinBatch) return launch_join<TI, V, HT, V, 1, 128>(a, st);
+    if (parts <= 4 * kJoinBatch) return launch_join<TI, V, HT, V, 4, 128>(a, st);
+    return launch_join<TI, V, HT, 32, 32, 256>(a, st);
 }
 template <int V> cudaError_t launch_join(const AttendArgs& a, bool bf16, int ht, int64_t parts, cudaStream_t st) {
     if (bf16)
@@ -813,8 +848,9 @@ template <int V> cudaError_t launch_join(const AttendArgs& a, bool bf16, int ht,
 cudaError_t launch_attend(const AttendArgs& a, const Plan& p, cudaStream_t st) {
     const bool bf16 = a.c.dtype == KDA_DTYPE_BF16;
     const int K = a.c.K, V = a.c.V;
-    const Kernel kernel = K == 128 ? (V == 128 ? kernel_of<128, 128>(bf16, p.ht) : kernel_of<128, 64>(bf16, p.ht))
-                                   : (V == 128 ? kernel_of<64, 128>(bf16, p.ht) : kernel_of<64, 64>(bf16, p.ht));
+    const Kernel kernel =
+        K == 128 ? (V == 128 ? kernel_of<128, 128>(bf16, p.ht, p.split) : kernel_of<128, 64>(bf16, p.ht, p.split))
+                 : (V == 128 ? kernel_of<64, 128>(bf16, p.ht, p.split) : kernel_of<64, 64>(bf16, p.ht, p.split));
     cudaError_t e = launch_after(kernel, a, p.grid, kWarps * 32, st, p.split == kCluster ? p.parts : 1);
     if (e != cudaSuccess) return e;
     note_launch("cache_attend", st);
@@ -861,8 +897,9 @@ extern "C" kda_status kda_cache_attend(const kda_cache* c, const void* q, int64_
     const Plan plan = plan_of(c, HQ, N, max_pages, window);
     if (!ws || !aligned16(ws) || ws_bytes < plan.ws_bytes) return KDA_ERR_WORKSPACE;
     char* w = (char*)ws;
+    const int step = plan.turn * (plan.split == kCluster ? plan.parts : 1);
     const AttendArgs a{*c, q, q_stride, table_stride, HQ, N, max_pages, window, page_table, kv_lens, scale * kLog2e, o,
-                       lse, status, plan.split, plan.parts, (float4*)w, (float2*)(w + plan.acc_bytes),
+                       lse, status, step, step / c->page_size, step % c->page_size, plan.split, plan.parts, (float4*)w, (float2*)(w + plan.acc_bytes),
                        (int2*)(w + plan.acc_bytes + plan.ml_bytes)};
     cudaStream_t st = (cudaStream_t)stream;
     begin_launches(st);
