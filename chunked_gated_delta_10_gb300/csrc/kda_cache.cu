@@ -7,7 +7,18 @@
 // that turns channel i with channel i + rope_dim / 2 takes the unit of each.
 //
 // Bound: every new row is read once and written once; for one token a sequence
-// it is the latency of a launch.
+// it is the latency of a launch. A CTA has one row, so that its sequence, page
+// and angles are found by uniform instructions; what is left of it is loads and
+// stores, and the CTA's size decides how many rows an SM has under way:
+//   from 1024 rows on, 64 threads. 16 packed prompts of U[1,4096] tokens, 32
+//     query and 8 cache heads of 128, bf16 (822 MB): 122 us, 6.74 TB/s, the rate
+//     of a plain copy; with 128 threads 124 us, 256: 131, 512: 236.
+//   below, up to 512 threads, one unit each: one token 2.1 us (64 threads: 4.2),
+//     128 tokens 3.0 us (7.2).
+//   rows of 64 units or fewer share a CTA of 256 threads: 33,000 rows of two
+//     heads of 64 take 10.2 us, and 33.5 us with a CTA each (1 ns a CTA).
+// Several rows to a thread, their loads ahead of their sums, was slower (150 to
+// 226 us for the prompts): the angles take the registers that more CTAs need.
 #include "kda_cache.cuh"
 
 namespace kda {
@@ -17,18 +28,20 @@ struct AppendArgs {
     kda_cache c;
     const void *k, *v, *q;
     void* q_out;
-    int64_t k_stride, v_stride, q_stride, R, table_stride;
+    int64_t k_stride, v_stride, q_stride, table_stride;
     int HQ, N;
+    unsigned R, per;  // new rows; of a sequence, where there is no cu
     const int64_t* cu;
     const float* rope;
     int rope_len, rope_dim, interleaved;
     const int32_t *table, *kv_lens;
     int max_pages;
     int32_t* status;
+    unsigned lanes, rows;  // short rows: threads of a row, rows of a CTA
 };
 
 // The sequence of new row r: the last n with cu[n] <= r.
-__device__ __forceinline__ int seq_of(const int64_t* cu, int N, int64_t r) {
+__device__ __forceinline__ int seq_of(const int64_t* cu, int N, unsigned r) {
     int lo = 0, hi = N - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
@@ -40,45 +53,50 @@ __device__ __forceinline__ int seq_of(const int64_t* cu, int N, int64_t r) {
     return lo;
 }
 
-template <typename TI>
-__global__ void __launch_bounds__(256) k_append(AppendArgs a) {
+template <typename TI, bool SHORT, int MOST>
+__global__ void __launch_bounds__(MOST) k_append(AppendArgs a) {
     constexpr int E = Unit<TI>::n;
     after_previous();
-    const int64_t r = blockIdx.x;
-    int64_t n, idx;
+    unsigned r = blockIdx.x;
+    int lane = threadIdx.x;
+    if constexpr (SHORT) {
+        const unsigned in = lane / a.lanes;
+        r = r * a.rows + in;
+        lane -= in * a.lanes;
+        if (in >= a.rows || r >= a.R) return;
+    }
+    unsigned n, idx;
+    bool ok = true;
     if (a.cu) {
         n = seq_of(a.cu, a.N, r);
-        idx = r - a.cu[n];
+        const int64_t first = a.cu[n];
+        ok = first <= r;
+        idx = r - (unsigned)first;
     } else {
-        const int64_t per = a.R / a.N;
-        n = r / per;
-        idx = r % per;
+        n = r / a.per;
+        idx = r - n * a.per;
     }
-    const int32_t len = a.kv_lens[n];
-    const int64_t pos = len + idx, pg = pos / a.c.page_size;
-    int64_t page = -1;
+    const int len = a.kv_lens[n];
+    const unsigned pos = (unsigned)len + idx, pg = pos / (unsigned)a.c.page_size, row = pos - pg * a.c.page_size;
+    int page = -1;
     if (len >= 0) {
-        bool ok = idx >= 0 && pg < a.max_pages && (!a.rope || pos < a.rope_len);
-        if (ok) {
-            page = a.table[n * a.table_stride + pg];
-            ok = page >= 0 && page < a.c.num_pages;
-        }
-        if (!ok) {
+        ok = ok && pg < (unsigned)a.max_pages && (!a.rope || pos < (unsigned)a.rope_len);
+        if (ok) page = a.table[n * a.table_stride + pg];
+        if (page < 0 || page >= a.c.num_pages) {
             page = -1;
-            if (a.status && threadIdx.x == 0) *a.status = KDA_ERR_INVALID_ARG;
+            if (a.status && lane == 0) *a.status = KDA_ERR_INVALID_ARG;
         }
     }
-    const int64_t row = pos % a.c.page_size;
     // units of a head: the pairs of units that turn together, then the rest
     const int half = a.interleaved ? 0 : a.rope_dim / 2 / E;
     const int uk = a.c.K / E - half, uv = a.c.V / E;
     const int units_q = a.HQ * uk, units_k = a.c.HKV * uk, units = units_q + units_k + a.c.HKV * uv;
-    for (int i = threadIdx.x; i < units; i += blockDim.x) {
+    for (int i = lane; i < units; i += SHORT ? a.lanes : blockDim.x) {
         if (i >= units_q + units_k) {
             const int j = i - units_q - units_k, h = j / uv, u = j % uv;
             if (page >= 0) {
-                const TI* src = (const TI*)a.v + r * a.v_stride + h * a.c.V + u * E;
-                TI* dst = (TI*)a.c.v + page * a.c.v_page + row * a.c.v_row + h * a.c.v_head + u * E;
+                const TI* src = (const TI*)a.v + (int64_t)r * a.v_stride + h * a.c.V + u * E;
+                TI* dst = (TI*)a.c.v + (int64_t)page * a.c.v_page + row * a.c.v_row + h * a.c.v_head + u * E;
                 *(uint4*)dst = *(const uint4*)src;
             }
             continue;
@@ -86,9 +104,9 @@ __global__ void __launch_bounds__(256) k_append(AppendArgs a) {
         const bool is_q = i < units_q;
         const int j = is_q ? i : i - units_q, h = j / uk, u = j % uk;
         if (!is_q && page < 0) continue;
-        const TI* src = is_q ? (const TI*)a.q + r * a.q_stride + h * a.c.K : (const TI*)a.k + r * a.k_stride + h * a.c.K;
-        TI* dst = is_q ? (TI*)a.q_out + (r * a.HQ + h) * a.c.K
-                       : (TI*)a.c.k + page * a.c.k_page + row * a.c.k_row + h * a.c.k_head;
+        const TI* src = is_q ? (const TI*)a.q + (int64_t)r * a.q_stride + h * a.c.K : (const TI*)a.k + (int64_t)r * a.k_stride + h * a.c.K;
+        TI* dst = is_q ? (TI*)a.q_out + ((int64_t)r * a.HQ + h) * a.c.K
+                       : (TI*)a.c.k + (int64_t)page * a.c.k_page + row * a.c.k_row + h * a.c.k_head;
         float x[E], y[E];
         if (page < 0) {  // a query row of a dropped or inactive token
 #pragma unroll
@@ -97,7 +115,7 @@ __global__ void __launch_bounds__(256) k_append(AppendArgs a) {
             Unit<TI>::store(dst + (u + half) * E, x);
             continue;
         }
-        const float* cs = a.rope + pos * a.rope_dim;
+        const float* cs = a.rope + (int64_t)pos * a.rope_dim;
         if (u < half) {
             Unit<TI>::load(src + u * E, x);
             Unit<TI>::load(src + (u + half) * E, y);
@@ -129,6 +147,10 @@ __global__ void __launch_bounds__(256) k_append(AppendArgs a) {
         }
         Unit<TI>::store(dst + at, x);
     }
+}
+
+template <typename TI> void (*kernel_of(bool few, bool many))(AppendArgs) {
+    return few ? k_append<TI, true, 256> : many ? k_append<TI, false, 64> : k_append<TI, false, 512>;
 }
 
 }  // namespace
@@ -163,12 +185,19 @@ extern "C" kda_status kda_cache_append(const kda_cache* c, const void* k, int64_
         ((uintptr_t)cu_seqlens & 7u))
         return KDA_ERR_INVALID_ARG;
     if (R > INT32_MAX || ((int64_t)HQ + 2 * (int64_t)c->HKV) * 32 > INT32_MAX) return KDA_ERR_UNSUPPORTED;
-    AppendArgs a{*c, k, v, q, q_out, k_stride, v_stride, q_stride, R, table_stride, HQ, N, cu_seqlens, rope, rope_len,
-                 rope_dim, interleaved, page_table, kv_lens, max_pages, status};
+    const int64_t uk = (c->K - (interleaved ? 0 : rope_dim / 2)) / unit, units = (HQ + c->HKV) * uk + c->HKV * (c->V / unit);
+    const bool few = units <= 64, many = R >= 1024;  // (measured: see the top of this file)
+    const int most = few ? 256 : many ? 64 : 512;
+    const int64_t turns = (units + most - 1) / most;
+    const int lanes = (int)((units + turns - 1) / turns), rows = few ? most / lanes : 1;
+    const int threads = (lanes * rows + 31) / 32 * 32;
+    const AppendArgs a{*c, k, v, q, q_out, k_stride, v_stride, q_stride, table_stride, HQ, N, (unsigned)R, (unsigned)(R / N), cu_seqlens, rope, rope_len,
+                 rope_dim, interleaved, page_table, kv_lens, max_pages, status, (unsigned)lanes, (unsigned)rows};
     cudaStream_t st = (cudaStream_t)stream;
     begin_launches(st);
-    const cudaError_t e = launch_after(c->dtype == KDA_DTYPE_BF16 ? k_append<__nv_bfloat16> : k_append<float>, a,
-                                       (unsigned)R, 256, st);
+    void (*const kernel)(AppendArgs) =
+        c->dtype == KDA_DTYPE_BF16 ? kernel_of<__nv_bfloat16>(few, many) : kernel_of<float>(few, many);
+    const cudaError_t e = launch_after(kernel, a, (unsigned)((R + rows - 1) / rows), threads, st);
     if (e != cudaSuccess) return cuda_fail(e);
     note_launch("cache_append", st);
     return KDA_OK;
