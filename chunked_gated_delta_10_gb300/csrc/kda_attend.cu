@@ -15,6 +15,19 @@
 namespace kda {
 namespace {
 
+// Division of numbers below 2^31 by an invariant d (Granlund and Montgomery, 1994): with 2^s >= d, floor(n / d) =
+// floor(n ceil(2^(31 + s) / d) / 2^(31 + s)).
+struct Divisor {
+    unsigned factor, shift;
+    __host__ explicit Divisor(unsigned d) : shift(31) {
+        while (1ull << (shift - 31) < d) ++shift;
+        factor = (unsigned)(((1ull << shift) + d - 1) / d);
+    }
+    __device__ __forceinline__ unsigned operator()(unsigned n) const {
+        return (unsigned)((uint64_t)n * factor >> shift);
+    }
+};
+
 // How the rows are given to CTAs (see Work).
 enum Split { kWhole, kCluster, kShares };
 
@@ -28,6 +41,8 @@ struct AttendArgs {
     void* o;
     float* lse;
     int32_t* status;
+    int group, tiles, units;      // query heads of a cache head, in tiles of HT; units of a sequence (HKV tiles)
+    Divisor page;                 // by c.page_size
     int step, step_pg, step_off;  // rows from a warp's tile to its next, in pages and rows
     int split, parts;  // parts: kCluster: CTAs of a cluster; kShares: CTAs in all; kWhole: 1
     // kShares: what a CTA has of a unit that it ends (0) or begins (1) but does not have whole, head by head: the
@@ -71,7 +86,7 @@ template <int R> struct Rows {
     __device__ __forceinline__ void start(const AttendArgs& a, int64_t n, int first) {
         const int row = first + threadIdx.x % 32 % R;
         table = a.table + n * a.table_stride;
-        pg = (unsigned)row / (unsigned)a.c.page_size;
+        pg = a.page(row);
         off = row - pg * a.c.page_size;
         page = pg < a.max_pages ? __ldg(table + pg) : -1;
     }
@@ -140,6 +155,9 @@ template <int R, int HT, bool SHARES> struct Work {
         // kShares: where it leaves its part
         int64_t head;
         int heads, whole, part;
+        // kShares: the unit's number, if it begins here, and its last turn
+        int64_t unit;
+        int last_turn;
         // kShares: the turns [at, stop) of `total` are still to be done, from sequence n on, whose first turn is `seq`
         int sums[W], stop, total;
         struct {
@@ -152,10 +170,14 @@ template <int R, int HT, bool SHARES> struct Work {
     }
     // Unit u of sequence n.
     __device__ __forceinline__ void set_unit(const AttendArgs& a, unsigned u, bool whole, int part, Share& share) {
-        const unsigned group = (unsigned)a.HQ / a.c.HKV, tiles = (group + HT - 1) / HT, qt = u % tiles;
-        hkv = u / tiles;
-        h0 = hkv * group + qt * HT;
-        heads = min(HT, (int)(group - qt * HT));
+        unsigned qt = 0;
+        hkv = u;
+        if (a.tiles > 1) {
+            hkv = u / (unsigned)a.tiles;
+            qt = u - hkv * a.tiles;
+        }
+        h0 = hkv * a.group + qt * HT;
+        heads = min(HT, (int)(a.group - qt * HT));
         if (threadIdx.x == 0) {
             share.head = (int64_t)n * a.HQ + h0;
             share.heads = heads;
@@ -164,21 +186,17 @@ template <int R, int HT, bool SHARES> struct Work {
         }
     }
     // The CTA's first unit; false if it has none.
-    __device__ __forceinline__ static unsigned units_of(const AttendArgs& a) {  // of a sequence
-        return a.c.HKV * (((unsigned)a.HQ / a.c.HKV + HT - 1) / HT);
-    }
     __device__ __forceinline__ bool start(const AttendArgs& a, Share& share) {
-        const unsigned units = units_of(a);
         warp = threadIdx.x / 32;
         odd = 0;
         if constexpr (SHARES) {
-            find_share(a, units, share);
+            find_share(a, share);
             return next(a, share);
         }
-        const unsigned x = blockIdx.x / (unsigned)a.parts;
-        const int part = blockIdx.x % (unsigned)a.parts;
-        n = x / units;
-        set_unit(a, x % units, true, part, share);
+        // (a cluster has 2^i CTAs; the units of a sequence, which share its pages, come one after the other)
+        const int part = blockIdx.x & (a.parts - 1);
+        n = blockIdx.y;
+        set_unit(a, blockIdx.x >> (31 - __clz(a.parts)), true, part, share);
         int first = (part * W + warp) * R, begin, end;
         rows.start(a, n, first);
         kv_range(a, n, begin, end);
@@ -200,7 +218,8 @@ template <int R, int HT, bool SHARES> struct Work {
         return y < both ? y / (each + 1) : more + (y - both) / each;
     }
     // kShares: the CTA's share, and the sequence that it begins in.
-    __device__ __forceinline__ void find_share(const AttendArgs& a, int units, Share& share) {
+    __device__ __forceinline__ void find_share(const AttendArgs& a, Share& share) {
+        const int units = a.units;
         if (a.N == 1) {
             if (threadIdx.x == 0) {
                 int begin, last;
@@ -254,7 +273,7 @@ template <int R, int HT, bool SHARES> struct Work {
     }
     // kShares: the next unit, or part of one, of the CTA's share; false if there is none.
     __device__ __forceinline__ bool next(const AttendArgs& a, Share& share) {
-        const int at = share.state[odd].at, stop = share.stop, units = units_of(a);
+        const int at = share.state[odd].at, stop = share.stop, units = a.units;
         if (at >= stop) return false;
         int begin, last, turns, seq = share.state[odd].seq;
         for (n = share.state[odd].n;; ++n) {
@@ -269,10 +288,8 @@ template <int R, int HT, bool SHARES> struct Work {
         odd ^= 1;
         if (threadIdx.x == 0) {
             share.state[odd] = {at + t1 - t0, n, seq};
-            if (t0 == 0) {
-                const int to = cta_of(at + turns - 1, share.total, min(a.parts, share.total));
-                a.unit_parts[(int64_t)n * units + u] = make_int2(blockIdx.x, to);
-            }
+            share.unit = t0 == 0 ? (int64_t)n * units + u : -1;
+            share.last_turn = at + turns - 1;
         }
         const int first = begin + (t0 * W + warp) * R, end = min(last, begin + t1 * kTurn);
         rows.start(a, n, first);
@@ -331,14 +348,19 @@ template <int HT, int V> struct Partial {
 
 // Joins the warps of a CTA and, in a cluster, its CTAs, and writes the unit's result, or, where the CTA does not have
 // all of the unit, its part. The order of the sums is fixed.
-template <typename TI, int V, int HT, bool SHARES, typename Share>
-__device__ __forceinline__ void join(const AttendArgs& a, const Share& unit, Partial<HT, V>& p) {
+template <typename TI, int V, int HT, bool SHARES, typename Wk>
+__device__ __forceinline__ void join(const AttendArgs& a, const typename Wk::Share& unit, Partial<HT, V>& p) {
     const bool cluster = !SHARES && a.split == kCluster;
     if (cluster) cluster_wait();  // for the others to have started
     __syncthreads();
     const int items = unit.heads * (V / 4), share = (items + a.parts - 1) / a.parts;  // share: of a CTA of the cluster
     const int part = unit.part;
     const int64_t head = unit.head;
+    if constexpr (SHARES) {
+        if (threadIdx.x == kWarps * 32 - 1 && unit.unit >= 0)
+            a.unit_parts[unit.unit] =
+                make_int2(blockIdx.x, Wk::cta_of(unit.last_turn, unit.total, min(a.parts, unit.total)));
+    }
     for (int i = threadIdx.x; i < items; i += kWarps * 32) {
         const int h = i / (V / 4), u = i % (V / 4);
         float m = p.m[0][h];
@@ -391,15 +413,16 @@ constexpr int kJoinBatch = 8;
 template <typename TI, int V, int HT, int VS, int G, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_attend_join(AttendArgs a) {
     constexpr int U = VS / 4, S = V / VS, HB = THREADS / (G * U);  // slices of a head; (head, slice) pairs of a CTA
-    __shared__ float4 sx[HB][G][U];
-    __shared__ float2 sml[HB][G];
+    constexpr int GW = U < 32 && G > 1 ? 32 / U : 1;  // groups of a warp
+    static_assert(G % GW == 0, "a warp has groups of one pair");
+    __shared__ float4 sx[HB][G / GW][U];
+    __shared__ float2 sml[HB][G / GW];
     const unsigned mine = threadIdx.x / (G * U), at = blockIdx.x * HB + mine, last = (unsigned)(a.N * a.HQ) * S - 1;
     const unsigned head = min(at, last) / S, u = min(at, last) % S * U + threadIdx.x % U;
     const int g = threadIdx.x / U % G;
-    const unsigned group = (unsigned)a.HQ / a.c.HKV, tiles = (group + HT - 1) / HT;
-    const unsigned n = head / a.HQ, hq = head % a.HQ, hkv = hq / group, qt = hq % group / HT, h = hq % group % HT;
+    const unsigned n = head / a.HQ, hq = head % a.HQ, hkv = hq / a.group, qt = hq % a.group / HT, h = hq % a.group % HT;
     after_previous();
-    const int2 range = a.unit_parts[(n * a.c.HKV + hkv) * tiles + qt];
+    const int2 range = a.unit_parts[(int64_t)n * a.units + hkv * a.tiles + qt];
     const int count = range.y - range.x + 1;
     float m = -INFINITY, l = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -430,17 +453,30 @@ __global__ void __launch_bounds__(THREADS) k_attend_join(AttendArgs a) {
         }
     }
     if constexpr (G > 1) {
-        sx[mine][g][threadIdx.x % U] = x;
-        if (threadIdx.x % U == 0) sml[mine][g] = make_float2(m, l);
+        // the groups of a warp, then the warps
+#pragma unroll
+        for (int w = U; w < 32; w *= 2) {
+            const float m1 = __shfl_xor_sync(0xffffffffu, m, w), l1 = __shfl_xor_sync(0xffffffffu, l, w);
+            const float4 x1 = make_float4(__shfl_xor_sync(0xffffffffu, x.x, w), __shfl_xor_sync(0xffffffffu, x.y, w),
+                                          __shfl_xor_sync(0xffffffffu, x.z, w), __shfl_xor_sync(0xffffffffu, x.w, w));
+            const float top = fmaxf(m, m1), base = finite_base(top), f = ex2(m - base), f1 = ex2(m1 - base);
+            m = top;
+            l = l * f + l1 * f1;
+            x = make_float4(x.x * f + x1.x * f1, x.y * f + x1.y * f1, x.z * f + x1.z * f1, x.w * f + x1.w * f1);
+        }
+        if (threadIdx.x % 32 < U) {
+            sx[mine][g / GW][threadIdx.x % U] = x;
+            if (threadIdx.x % U == 0) sml[mine][g / GW] = make_float2(m, l);
+        }
         __syncthreads();
         if (g > 0) return;
 #pragma unroll
-        for (int i = 1; i < G; ++i) m = fmaxf(m, sml[mine][i].x);
+        for (int i = 1; i < G / GW; ++i) m = fmaxf(m, sml[mine][i].x);
         const float base = finite_base(m);
         l = 0.f;
         x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < G; ++i) {
+        for (int i = 0; i < G / GW; ++i) {
             const float f = ex2(sml[mine][i].x - base);
             l = fmaf(sml[mine][i].y, f, l);
             add_scaled(x, sx[mine][i][threadIdx.x % U], f);
@@ -638,7 +674,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) k_attend_mma(Att
                             make_float4(acc[j][i][e + 2 * r], acc[j][i + 1][e + 2 * r], acc[j][i + 2][e + 2 * r],
                                         acc[j][i + 3][e + 2 * r]);
             }
-        join<TI, V, HT, SHARES>(a, share, sm);
+        join<TI, V, HT, SHARES, Work<16, HT, SHARES>>(a, share, sm);
         if constexpr (!SHARES) return;
         __syncthreads();  // the shared memory is free for the next unit
     }
@@ -750,7 +786,7 @@ __global__ void __launch_bounds__(kWarps * 32, SHARES ? simt_ctas(HT) : 1) k_att
         for (int h = 0; h < HT; ++h)
 #pragma unroll
             for (int i = 0; i < VL; ++i) ((float*)sm.acc[warp][h])[lane * VL + i] = acc[h][i];
-        join<float, V, HT, SHARES>(a, share, sm);
+        join<float, V, HT, SHARES, Work<R, HT, SHARES>>(a, share, sm);
         if constexpr (!SHARES) return;
         __syncthreads();  // the shared memory is free for the next unit
     }
@@ -768,7 +804,7 @@ int head_tile(const kda_cache* c, int HQ) {
 struct Plan {
     Split split;
     int parts, ht, units, turn;
-    unsigned grid;
+    dim3 grid;
     size_t acc_bytes, ml_bytes, ws_bytes;  // of the workspace
 };
 Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window) {
@@ -804,7 +840,7 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window) {
         p.parts = p.split == kWhole ? 1 : atoi(getenv("KS"));
     }
 #endif
-    p.grid = (unsigned)(p.split == kShares ? p.parts : all * p.parts);
+    p.grid = p.split == kShares ? dim3(p.parts) : dim3(units * p.parts, N);
     p.ws_bytes = 256;
     if (p.split == kShares) {
         p.acc_bytes = (size_t)p.parts * 2 * ht * c->V * sizeof(float);
@@ -866,7 +902,7 @@ kda_status check_sizes(const kda_cache* c, int32_t HQ, int32_t N, int32_t max_pa
     const kda_status s = check_cache(c);
     if (s != KDA_OK) return s;
     if (N < 0 || HQ < 1 || HQ % c->HKV != 0 || max_pages < 0 || window < 0) return KDA_ERR_INVALID_ARG;
-    if ((int64_t)N * HQ > INT32_MAX || (int64_t)max_pages * c->page_size > (1 << 30)) return KDA_ERR_UNSUPPORTED;
+    if (N > 65535 || HQ > 65535 || (int64_t)max_pages * c->page_size > (1 << 30)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -899,7 +935,7 @@ extern "C" kda_status kda_cache_attend(const kda_cache* c, const void* q, int64_
     char* w = (char*)ws;
     const int step = plan.turn * (plan.split == kCluster ? plan.parts : 1);
     const AttendArgs a{*c, q, q_stride, table_stride, HQ, N, max_pages, window, page_table, kv_lens, scale * kLog2e, o,
-                       lse, status, step, step / c->page_size, step % c->page_size, plan.split, plan.parts, (float4*)w, (float2*)(w + plan.acc_bytes),
+                       lse, status, HQ / c->HKV, plan.units / c->HKV, plan.units, Divisor(c->page_size), step, step / c->page_size, step % c->page_size, plan.split, plan.parts, (float4*)w, (float2*)(w + plan.acc_bytes),
                        (int2*)(w + plan.acc_bytes + plan.ml_bytes)};
     cudaStream_t st = (cudaStream_t)stream;
     begin_launches(st);

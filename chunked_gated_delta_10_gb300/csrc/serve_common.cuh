@@ -19,13 +19,13 @@ __device__ __forceinline__ void after_previous() {
 }
 
 template <typename Args>
-cudaError_t launch_after(void (*kernel)(Args), const Args& a, unsigned grid, int threads, cudaStream_t st,
+cudaError_t launch_after(void (*kernel)(Args), const Args& a, dim3 grid, int threads, cudaStream_t st,
                          int cluster = 1) {
     cudaLaunchAttribute attr[2] = {};
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.stream = st;
     cfg.attrs = attr;
