@@ -29,7 +29,7 @@ struct Divisor {
 };
 
 // How the rows are given to CTAs (see Work).
-enum Split { kWhole, kCluster, kShares };
+enum Split { kWhole, kCluster, kParts, kShares };
 
 struct AttendArgs {
     kda_cache c;
@@ -44,10 +44,13 @@ struct AttendArgs {
     int group, tiles, units;      // query heads of a cache head, in tiles of HT; units of a sequence (HKV tiles)
     Divisor page;                 // by c.page_size
     int step, step_pg, step_off;  // rows from a warp's tile to its next, in pages and rows
-    int split, parts;  // parts: kCluster: CTAs of a cluster; kShares: CTAs in all; kWhole: 1
-    // kShares: what a CTA has of a unit that it ends (0) or begins (1) but does not have whole, head by head: the
-    // weighted sum relative to its maximum [parts, 2, HT, V], and its maximum (log2 units) and sum of weights
-    // [parts, 2, HT]; and of each unit the first and last CTA that have some of it.
+    int split, parts;  // parts: kCluster, kParts: CTAs of a unit; kShares: CTAs in all; kWhole: 1
+    Divisor by_parts;
+    int turn;  // rows that a CTA takes at a time
+    // What a CTA has of a unit that it does not have whole, head by head: the weighted sum relative to its maximum, and
+    // its maximum (log2 units) and sum of weights. kParts: [units, parts, HT, V] and [units, parts, HT]; kShares: of the
+    // unit that it ends (0) and of the one that it begins (1), [parts, 2, HT, V] and [parts, 2, HT], and of each unit the
+    // first and last CTA that have some of it.
     float4* part_acc;
     float2* part_ml;
     int2* unit_parts;
@@ -136,6 +139,7 @@ template <int C> __device__ __forceinline__ void load_channels(const float* p, b
 //   kCluster  a cluster of CTAs per unit, which take its turns one after the other (so the first rows of a CTA do not
 //             depend on the length, and their pages are looked up while it is on its way) and join their results in
 //             shared memory: for few units of some turns, where latency counts;
+//   kParts    the same with more CTAs than a cluster has, joined by a second kernel: for few units of many turns;
 //   kShares   as many CTAs as the GPU holds at once, each with an equal share of all turns in the order of the units,
 //             whatever the lengths are: every CTA adds up the lengths to find its share. A unit that falls to several
 //             CTAs is joined by a second kernel.
@@ -152,7 +156,7 @@ template <int R, int HT, bool SHARES> struct Work {
     // What a CTA keeps in shared memory (a barrier lies between two units).
     struct Share {
         // the unit, for the join: whole, if the CTA or its cluster has all of it; part: kCluster: the CTA's rank;
-        // kShares: where it leaves its part
+        // kParts, kShares: where it leaves its part
         int64_t head;
         int heads, whole, part;
         // kShares: the unit's number, if it begins here, and its last turn
@@ -193,10 +197,9 @@ template <int R, int HT, bool SHARES> struct Work {
             find_share(a, share);
             return next(a, share);
         }
-        // (a cluster has 2^i CTAs; the units of a sequence, which share its pages, come one after the other)
-        const int part = blockIdx.x & (a.parts - 1);
+        // (the units of a sequence, which share its pages, come one after the other)
+        const int unit = a.by_parts(blockIdx.x), part = blockIdx.x - unit * a.parts;
         n = blockIdx.y;
-        set_unit(a, blockIdx.x >> (31 - __clz(a.parts)), true, part, share);
         int first = (part * W + warp) * R, begin, end;
         rows.start(a, n, first);
         kv_range(a, n, begin, end);
@@ -206,7 +209,9 @@ template <int R, int HT, bool SHARES> struct Work {
         }
         left = end - first;
         rows.until(first, end);
-        return true;
+        const bool alone = a.split != kParts || end - begin <= a.turn;
+        set_unit(a, unit, alone, a.split == kParts ? (n * a.units + unit) * a.parts + part : part, share);
+        return a.split != kParts || part < turns_of(begin, end);
     }
     // kShares: turns are dealt out evenly, one more to each of the first total % ctas CTAs: the first turn of CTA x, and
     // the CTA that has turn y.
@@ -378,7 +383,7 @@ __device__ __forceinline__ void join(const AttendArgs& a, const typename Wk::Sha
         if (cluster) {
             push(&p.in_acc[part * share + i % share], i / share, x);
             if (u < a.parts) push(&p.in_ml[part][h], u, make_float2(m, l));
-        } else if (!SHARES || unit.whole) {
+        } else if (unit.whole) {
             write_result<TI>(a, head + h, V, 4 * u, m, l, x);
         } else {
             const int64_t to = (int64_t)part * HT + h;
@@ -406,11 +411,11 @@ __device__ __forceinline__ void join(const AttendArgs& a, const typename Wk::Sha
     }
 }
 
-// kShares: the parts of one query head and VS of its channels, joined in an order that goes by their number alone.
+// kParts, kShares: the parts of one query head and VS of its channels, joined in an order that goes by their number alone.
 // Group g of G groups of VS / 4 threads takes parts g, g + G, .., a batch of them at a time; the groups are joined in
 // shared memory.
 constexpr int kJoinBatch = 8;
-template <typename TI, int V, int HT, int VS, int G, int THREADS>
+template <typename TI, int V, int HT, int VS, int G, int THREADS, bool SHARES>
 __global__ void __launch_bounds__(THREADS) k_attend_join(AttendArgs a) {
     constexpr int U = VS / 4, S = V / VS, HB = THREADS / (G * U);  // slices of a head; (head, slice) pairs of a CTA
     constexpr int GW = U < 32 && G > 1 ? 32 / U : 1;  // groups of a warp
@@ -422,21 +427,45 @@ __global__ void __launch_bounds__(THREADS) k_attend_join(AttendArgs a) {
     const int g = threadIdx.x / U % G;
     const unsigned n = head / a.HQ, hq = head % a.HQ, hkv = hq / a.group, qt = hq % a.group / HT, h = hq % a.group % HT;
     after_previous();
-    const int2 range = a.unit_parts[(int64_t)n * a.units + hkv * a.tiles + qt];
-    const int count = range.y - range.x + 1;
+    // parts first .. first + count - 1 (with kParts the length says how many there are, and is on its way together with
+    // the first of them)
+    const int64_t unit = (int64_t)n * a.units + hkv * a.tiles + qt;
+    int64_t first;
+    int count;
+    if constexpr (SHARES) {
+        const int2 range = a.unit_parts[unit];
+        first = 2 * (int64_t)range.x;
+        count = range.y - range.x + 1;
+    } else {
+        first = unit * a.parts;
+        count = a.parts;
+    }
     float m = -INFINITY, l = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    int s = g;
     if (count > 1) {
-        for (int s = g; s < count; s += G * kJoinBatch) {
+        do {
             float2 e[kJoinBatch];
             float4 y[kJoinBatch];
             float top = m;
 #pragma unroll
             for (int i = 0; i < kJoinBatch; ++i) {
                 const int c = s + i * G;
-                const int64_t from = (int64_t)(2 * (range.x + c) + (c == 0)) * HT + h;
+                const int64_t from = (first + (SHARES ? 2 * c + (c == 0) : c)) * HT + h;
                 e[i] = c < count ? a.part_ml[from] : make_float2(-INFINITY, 0.f);
                 y[i] = c < count ? a.part_acc[from * (V / 4) + u] : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            if (!SHARES && s == g) {
+                int begin, end;
+                kv_range(a, n, begin, end);
+                count = max(1, min(count, (end - begin + a.turn - 1) / a.turn));
+#pragma unroll
+                for (int i = 0; i < kJoinBatch; ++i) {
+                    if (s + i * G >= count) {  // what lies there was not written
+                        e[i] = make_float2(-INFINITY, 0.f);
+                        y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                }
             }
 #pragma unroll
             for (int i = 0; i < kJoinBatch; ++i) top = fmaxf(top, e[i].x);
@@ -450,7 +479,8 @@ __global__ void __launch_bounds__(THREADS) k_attend_join(AttendArgs a) {
                 l = fmaf(e[i].y, f, l);
                 add_scaled(x, y[i], f);
             }
-        }
+            s += G * kJoinBatch;
+        } while (s < count);
     }
     if constexpr (G > 1) {
         // the groups of a warp, then the warps
@@ -817,34 +847,39 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window) {
     const int slots = 152 * (!bf16 ? simt_ctas(ht) : ht == 8 ? 3 : 2);
     const int slots_alone = !bf16 && ht == 1 && c->K + c->V == 128 ? 152 * 5 : slots;  // without kShares' registers
     Plan p{kWhole, 1, ht, units, turn};
-    // What each costs, in turns (about 1.1 us): a cluster's own cost over a CTA alone is about one turn; that of shares
-    // (the lengths to add up first, the second kernel, its launch) four. Lengths are taken as three quarters of the
-    // longest that fits where there are several.
+    // What each costs, in turns (about 1.1 us). Over a CTA alone a cluster's join costs about one, the second kernel
+    // with its launch 2.2, and with kShares the lengths that are added up first and the ends of units within a share
+    // another 3.3. Clusters that do not all fit at once wait for room for a whole one. Where there are several sequences,
+    // shares are taken to be three quarters of what the longest that fits would give.
     int cluster = 1;
     while (cluster < kMaxCluster && cluster < turns &&
            (all * cluster * 2 <= slots_alone || (all * cluster * 16 <= slots_alone * 9 && turns >= 8 * cluster)))
         cluster *= 2;
     const auto waves = [&](int64_t ctas) { return ctas > slots_alone ? (double)ctas / slots_alone : 1.0; };
-    const double whole = turns * waves(all), clusters = 1 + (double)turns / cluster * waves(all * cluster);
-    const double shares = 4 + (double)turns * all * (N > 1 ? 0.75 : 1.0) / slots;
-    if (cluster > 1 && clusters < whole && clusters <= shares) {
+    const double whole = turns * waves(all), clusters = 1 + (double)turns / cluster * (all * cluster > slots_alone ? 1.4 : 1.0);
+    const double shares = 5.5 + (double)turns * all * (N > 1 ? 0.75 : 1.0) / slots;
+    const int64_t parts = all <= slots ? (slots / all < turns ? slots / all : turns) : 1;
+    const double cut = parts > 1 ? 2.2 + (double)turns / parts : whole;
+    const double least = cut < shares ? cut : shares;
+    if (cluster > 1 && clusters < whole && clusters <= least) {
         p.split = kCluster;
         p.parts = cluster;
-    } else if (shares < whole && turns * all < INT32_MAX) {
-        p.split = kShares;
-        p.parts = turns * all < 64 * slots ? slots : 2 * slots;
+    } else if (least < whole && turns * all < INT32_MAX) {
+        p.split = cut < shares ? kParts : kShares;
+        p.parts = p.split == kParts ? (int)parts : turns * all < 64 * slots ? slots : 2 * slots;
     }
 #ifdef TUNE
-    if (getenv("KM")) {
+    if (getenv("KM") && atoi(getenv("KM")) >= 0) {
         p.split = (Split)atoi(getenv("KM"));
         p.parts = p.split == kWhole ? 1 : atoi(getenv("KS"));
     }
 #endif
     p.grid = p.split == kShares ? dim3(p.parts) : dim3(units * p.parts, N);
     p.ws_bytes = 256;
-    if (p.split == kShares) {
-        p.acc_bytes = (size_t)p.parts * 2 * ht * c->V * sizeof(float);
-        p.ml_bytes = (size_t)p.parts * 2 * ht * sizeof(float2);
+    if (p.split >= kParts) {
+        const size_t held = p.split == kParts ? (size_t)all * p.parts : (size_t)p.parts * 2;
+        p.acc_bytes = held * ht * c->V * sizeof(float);
+        p.ml_bytes = held * ht * sizeof(float2);
         p.ws_bytes += p.acc_bytes + p.ml_bytes + (size_t)all * sizeof(int2);
     }
     return p;
@@ -864,8 +899,9 @@ template <int K, int V> Kernel kernel_of(bool bf16, int ht, Split split) {
 template <typename TI, int V, int HT, int VS, int G, int THREADS>
 cudaError_t launch_join(const AttendArgs& a, cudaStream_t st) {
     const int64_t threads = (int64_t)a.N * a.HQ * (V / 4) * G;
-    return launch_after(k_attend_join<TI, V, HT, VS, G, THREADS>, a, (unsigned)((threads + THREADS - 1) / THREADS),
-                        THREADS, st);
+    return launch_after(a.split == kShares ? k_attend_join<TI, V, HT, VS, G, THREADS, true>
+                                           : k_attend_join<TI, V, HT, VS, G, THREADS, false>,
+                        a, (unsigned)((threads + THREADS - 1) / THREADS), THREADS, st);
 }
 // `parts`: of a unit, with equal lengths. A batch of loads is to cover them.
 template <typename TI, int V, int HT> cudaError_t launch_join(const AttendArgs& a, int64_t parts, cudaStream_t st) {
@@ -890,8 +926,8 @@ cudaError_t launch_attend(const AttendArgs& a, const Plan& p, cudaStream_t st) {
     cudaError_t e = launch_after(kernel, a, p.grid, kWarps * 32, st, p.split == kCluster ? p.parts : 1);
     if (e != cudaSuccess) return e;
     note_launch("cache_attend", st);
-    if (p.split != kShares) return cudaSuccess;
-    const int64_t parts = p.parts / ((int64_t)a.N * p.units) + 2;  // of a unit, with equal lengths
+    if (p.split < kParts) return cudaSuccess;
+    const int64_t parts = p.split == kParts ? p.parts : p.parts / ((int64_t)a.N * p.units) + 2;  // of a unit, with equal lengths
     e = V == 128 ? launch_join<128>(a, bf16, p.ht, parts, st) : launch_join<64>(a, bf16, p.ht, parts, st);
     if (e != cudaSuccess) return e;
     note_launch("cache_attend_join", st);
@@ -933,9 +969,9 @@ extern "C" kda_status kda_cache_attend(const kda_cache* c, const void* q, int64_
     const Plan plan = plan_of(c, HQ, N, max_pages, window);
     if (!ws || !aligned16(ws) || ws_bytes < plan.ws_bytes) return KDA_ERR_WORKSPACE;
     char* w = (char*)ws;
-    const int step = plan.turn * (plan.split == kCluster ? plan.parts : 1);
+    const int step = plan.turn * (plan.split == kShares ? 1 : plan.parts);
     const AttendArgs a{*c, q, q_stride, table_stride, HQ, N, max_pages, window, page_table, kv_lens, scale * kLog2e, o,
-                       lse, status, HQ / c->HKV, plan.units / c->HKV, plan.units, Divisor(c->page_size), step, step / c->page_size, step % c->page_size, plan.split, plan.parts, (float4*)w, (float2*)(w + plan.acc_bytes),
+                       lse, status, HQ / c->HKV, plan.units / c->HKV, plan.units, Divisor(c->page_size), step, step / c->page_size, step % c->page_size, plan.split, plan.parts, Divisor(plan.parts), plan.turn, (float4*)w, (float2*)(w + plan.acc_bytes),
                        (int2*)(w + plan.acc_bytes + plan.ml_bytes)};
     cudaStream_t st = (cudaStream_t)stream;
     begin_launches(st);
