@@ -5,20 +5,28 @@
 // delta) and once for the output after the update, but
 //   o = scale (S' + k d^T)^T q = scale (S'^T q + (q . k) d),
 // so both products come from one sweep over S', and the columns of S are
-// independent of one another. A CTA holds 32 columns of one state in registers
-// for all T tokens: the state is read once and written once.
+// independent of one another. A CTA holds 64 (or 32) columns of one state in
+// registers for all T tokens: the state is read once and written once.
 //
 // Bound: 8 K V bytes of state traffic per (sequence, value head), 128 KB at
-// K = V = 128. What the split is for: a CTA's loads, sums and stores follow one
-// another, so an SM needs many of them at different points of their way. With
-// 32 columns eight CTAs fit an SM, each with 16 KB under way. Measured at N = 256,
-// HV = 32, K = V = 128, bf16: 159.5 us (6.81 TB/s, the rate of a plain copy);
-// with 64 columns and four CTAs 158 us, but small batches take 0.3 to 0.5 us
-// longer (N = 1: 2.0 -> 2.3 us); with 16 columns 187 us; with a column per
-// thread, a whole state per CTA, 248 us.
-// With several tokens the sums bound it (two barriers and about 200
-// instructions a warp and token): N = 16, T = 4, HV = 32 takes 19.4 us where
-// the states' traffic takes 10.3.
+// K = V = 128. A CTA's loads, sums and stores follow one another, so an SM needs
+// several at different points of their way: four CTAs of 32 KB (64 columns) fit.
+// Measured, bf16, K = V = 128:
+//   N = 256, HV = 32: 157.3 us, 6.91 TB/s, a little above the rate of a plain
+//     copy; with 32 columns (seven CTAs) 159.4; a column of a whole state per
+//     thread 248.
+//   N = 1, HV = 16: 1.9 us with 32 columns, 2.2 with 64: where 64 would leave SMs
+//     without a CTA, 32 are taken.
+//   N = 16, T = 4, HV = 32: 17.1 us (the states' traffic alone: 10.3); N = 64,
+//     T = 7: 73 us (42). Tokens after the first cost sums alone, and what bounds
+//     those is the shared memory's return path: the factors of a row (k, q, e^g,
+//     and k again) come back 32 times, for every lane. So a lane takes two columns
+//     (N = 64, T = 7 with one: 95 to 115 us). Eight columns of all rows to a warp,
+//     without shared memory and barriers, took 100 us: each warp then forms the
+//     factors for itself.
+// Two rows are a pair of fp32 values (one instruction for both); the rows of a
+// column are summed in the same order whatever T and the split are, so several
+// tokens at once give the bits of one after the other.
 #include "../../include/kda_serve.h"
 #include "kda_common.cuh"
 #include "kda_internal.h"
@@ -38,7 +46,7 @@ struct StepArgs {
     float scale;
 };
 
-constexpr int kThreads = 128, kCols = 32;
+constexpr int kThreads = 128;
 
 // Two fp32 values in a 64-bit register: one instruction multiplies or adds both.
 using Pair = uint64_t;
@@ -67,11 +75,25 @@ __device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(a), "l"(b), "l"(c));
     return p;
 }
-__device__ __forceinline__ Pair shuffle_xor(Pair p, int w) { return __shfl_xor_sync(0xffffffffu, p, w); }
 
-// A token's inputs as a thread reads them: one channel of k, q and g, its four columns of v, and beta.
-template <typename TI> struct Token {
-    TI k, q, v[4], beta;
+template <int C> __device__ __forceinline__ void load_columns(const float* p, float (&x)[C]) {
+    if constexpr (C == 2) {
+        const float2 y = *(const float2*)p;
+        x[0] = y.x, x[1] = y.y;
+    } else {
+        x[0] = *p;
+    }
+}
+template <int C> __device__ __forceinline__ void store_columns(float* p, const float (&x)[C]) {
+    if constexpr (C == 2)
+        *(float2*)p = make_float2(x[0], x[1]);
+    else
+        *p = x[0];
+}
+
+// A token's inputs as a thread reads them: one channel of k, q and g, its columns of v, and beta.
+template <typename TI, int C> struct Token {
+    TI k, q, v[C], beta;
     float g;
     template <int K, int V> __device__ __forceinline__ void load(const StepArgs& a, int64_t row, int h, int hv, int col) {
         if (threadIdx.x < K) {
@@ -79,124 +101,151 @@ template <typename TI> struct Token {
             q = ((const TI*)a.q)[(row * a.H + h) * K + threadIdx.x];
             g = a.g[(row * a.HV + hv) * K + threadIdx.x];
         }
-        const TI* p = (const TI*)a.v + (row * a.HV + hv) * V + col;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = p[i];
+        for (int c = 0; c < C; ++c) v[c] = ((const TI*)a.v)[(row * a.HV + hv) * V + col + c];
         beta = ((const TI*)a.beta)[row * a.HV + hv];
     }
 };
 
-// One CTA per (sequence, value head, slice of kCols columns). A row of the slice is kCols / 4 threads with four columns
-// each; a thread has every (4 kThreads / kCols)-th row. The next token's inputs are loaded while a token is computed.
-template <typename TI, int K, int V, bool MANY>
-__global__ void __launch_bounds__(kThreads, MANY ? 7 : 8) k_step(StepArgs a) {
-    constexpr int LR = kCols / 4, RP = kThreads / LR, P = K / RP, W = kThreads / 32;  // threads of a row, rows of a pass, passes
-    __shared__ float factors[MANY ? 2 : 1][3][K];  // k, q and e^g of a token; the next token has the other buffer
-    __shared__ ulonglong2 sum_k[W][LR], sum_q[W][LR];
-    __shared__ float sum_qk[W];
+// One CTA per (sequence, value head, slice of 32 C columns): a lane has C columns, a warp K / 4 rows, two rows to a
+// pair. The next token's inputs are loaded while a token is computed.
+constexpr int ctas(bool many, int C) { return C == 2 ? 4 : many ? 5 : 7; }  // to an SM
+template <typename TI, int K, int V, bool MANY, int C>
+__global__ void __launch_bounds__(kThreads, ctas(MANY, C)) k_step(StepArgs a) {
+    constexpr int W = kThreads / 32, P = K / W, COLS = 32 * C;  // warps, rows of a warp, columns
+    __shared__ __align__(16) float factors[MANY ? 2 : 1][3][K];  // k, q and e^g of a token; the next token has the other
+    __shared__ float sum_k[W][COLS], sum_q[W][COLS], sum_qk[W];
     after_previous();
-    const unsigned slice = blockIdx.x % (V / kCols), nh = blockIdx.x / (V / kCols);
+    const unsigned slice = blockIdx.x % (V / COLS), nh = blockIdx.x / (V / COLS);
     const int64_t n = nh / (unsigned)a.HV;
     const int hv = nh % (unsigned)a.HV, h = hv / (a.HV / a.H);
-    const int warp = threadIdx.x / 32, c = threadIdx.x % LR, r0 = threadIdx.x / LR, col = slice * kCols + 4 * c;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r0 = warp * P, col = slice * COLS + lane * C;
     const int64_t slot = a.slots ? a.slots[n] : n;
     if (slot < 0 || slot >= a.num_slots) {
         for (int t = 0; t < a.T; ++t)
-            if (threadIdx.x < kCols)
-                ((TI*)a.o)[((n * a.T + t) * a.HV + hv) * V + slice * kCols + threadIdx.x] = from_f<TI>(0.f);
+            if (warp == 0)
+#pragma unroll
+                for (int c = 0; c < C; ++c) ((TI*)a.o)[((n * a.T + t) * a.HV + hv) * V + col + c] = from_f<TI>(0.f);
         if (slot >= 0 && a.status && threadIdx.x == 0) *a.status = KDA_ERR_INVALID_ARG;
         return;
     }
-    Token<TI> in;
+    Token<TI, C> in;
     in.template load<K, V>(a, n * a.T, h, hv, col);
     float* S = a.state + (slot * a.HV + hv) * K * V + r0 * V + col;
-    ulonglong2 s[P];
+    Pair s[P / 2][C];
 #pragma unroll
-    for (int i = 0; i < P; ++i) s[i] = *(const ulonglong2*)(S + i * RP * V);
+    for (int i = 0; i < P / 2; ++i) {
+        float x[C], y[C];
+        load_columns(S + 2 * i * V, x);
+        load_columns(S + (2 * i + 1) * V, y);
+#pragma unroll
+        for (int c = 0; c < C; ++c) s[i][c] = pair(x[c], y[c]);
+    }
     for (int t = 0; t < (MANY ? a.T : 1); ++t) {
-        const auto& f = factors[MANY ? t % 2 : 0];
+        float(*f)[K] = factors[MANY ? t % 2 : 0];
         if (threadIdx.x < K) {
-            float(*to)[K] = factors[MANY ? t % 2 : 0];
-            to[0][threadIdx.x] = to_f(in.k);
-            to[1][threadIdx.x] = to_f(in.q);
-            to[2][threadIdx.x] = exp2f(in.g * kLog2e);
+            f[0][threadIdx.x] = to_f(in.k);
+            f[1][threadIdx.x] = to_f(in.q);
+            f[2][threadIdx.x] = exp2f(in.g * kLog2e);
         }
-        const Pair v0 = pair(to_f(in.v[0]), to_f(in.v[1])), v1 = pair(to_f(in.v[2]), to_f(in.v[3]));
+        float v[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[c] = to_f(in.v[c]);
         const float beta = to_f(in.beta);
         __syncthreads();
         if (MANY && t + 1 < a.T) in.template load<K, V>(a, n * a.T + t + 1, h, hv, col);
-        Pair k0 = 0, k1 = 0, q0 = 0, q1 = 0;  // sums of k S' and q S' (0 is a pair of zeros)
-        float qk = 0.f;
+        float qk = lane < P ? f[0][r0 + lane] * f[1][r0 + lane] : 0.f;
+        Pair xk[2][C], xq[2][C];  // sums of k S' and q S'
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const int j = i * RP + r0;
-            const Pair k = pair(f[0][j], f[0][j]), q = pair(f[1][j], f[1][j]), e = pair(f[2][j], f[2][j]);
-            s[i].x = mul(s[i].x, e);
-            s[i].y = mul(s[i].y, e);
-            k0 = fma(k, s[i].x, k0);
-            k1 = fma(k, s[i].y, k1);
-            q0 = fma(q, s[i].x, q0);
-            q1 = fma(q, s[i].y, q1);
-            qk = fmaf(f[1][j], f[0][j], qk);
+        for (int c = 0; c < C; ++c) xk[0][c] = xk[1][c] = xq[0][c] = xq[1][c] = 0;  // a pair of zeros
+#pragma unroll
+        for (int i = 0; i < P; i += 4) {
+            const ulonglong2 k = *(const ulonglong2*)&f[0][r0 + i], q = *(const ulonglong2*)&f[1][r0 + i];
+            const ulonglong2 e = *(const ulonglong2*)&f[2][r0 + i];
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                s[i / 2][c] = mul(s[i / 2][c], e.x);
+                s[i / 2 + 1][c] = mul(s[i / 2 + 1][c], e.y);
+                xk[0][c] = fma(k.x, s[i / 2][c], xk[0][c]);
+                xk[1][c] = fma(k.y, s[i / 2 + 1][c], xk[1][c]);
+                xq[0][c] = fma(q.x, s[i / 2][c], xq[0][c]);
+                xq[1][c] = fma(q.y, s[i / 2 + 1][c], xq[1][c]);
+            }
         }
 #pragma unroll
-        for (int w = LR; w < 32; w *= 2) {
-            k0 = add(k0, shuffle_xor(k0, w));
-            k1 = add(k1, shuffle_xor(k1, w));
-            q0 = add(q0, shuffle_xor(q0, w));
-            q1 = add(q1, shuffle_xor(q1, w));
-            qk += __shfl_xor_sync(0xffffffffu, qk, w);
+        for (int w = 16; w > 0; w /= 2) qk += __shfl_xor_sync(0xffffffffu, qk, w);
+        float zk[C], zq[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const float2 yk = values(add(xk[0][c], xk[1][c])), yq = values(add(xq[0][c], xq[1][c]));
+            zk[c] = yk.x + yk.y;
+            zq[c] = yq.x + yq.y;
         }
-        if (threadIdx.x % 32 < LR) {
-            sum_k[warp][c] = make_ulonglong2(k0, k1);
-            sum_q[warp][c] = make_ulonglong2(q0, q1);
-            if (c == 0) sum_qk[warp] = qk;
-        }
+        store_columns(&sum_k[warp][lane * C], zk);
+        store_columns(&sum_q[warp][lane * C], zq);
+        if (lane == 0) sum_qk[warp] = qk;
         __syncthreads();
-        k0 = sum_k[0][c].x;
-        k1 = sum_k[0][c].y;
+        float d[C];
+        load_columns(&sum_k[0][lane * C], zk);
 #pragma unroll
         for (int w = 1; w < W; ++w) {
-            k0 = add(k0, sum_k[w][c].x);
-            k1 = add(k1, sum_k[w][c].y);
-        }
-        const Pair b = pair(beta, beta), minus = pair(-1.f, -1.f);
-        const Pair d0 = mul(b, fma(minus, k0, v0)), d1 = mul(b, fma(minus, k1, v1));
+            float y[C];
+            load_columns(&sum_k[w][lane * C], y);
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const Pair k = pair(f[0][i * RP + r0], f[0][i * RP + r0]);
-            s[i].x = fma(k, d0, s[i].x);
-            s[i].y = fma(k, d1, s[i].y);
+            for (int c = 0; c < C; ++c) zk[c] += y[c];
         }
-        if (r0 == 0) {
-            q0 = sum_q[0][c].x;
-            q1 = sum_q[0][c].y;
-            qk = sum_qk[0];
+        Pair dd[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            d[c] = beta * (v[c] - zk[c]);
+            dd[c] = pair(d[c], d[c]);
+        }
+#pragma unroll
+        for (int i = 0; i < P; i += 4) {
+            const ulonglong2 k = *(const ulonglong2*)&f[0][r0 + i];
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                s[i / 2][c] = fma(k.x, dd[c], s[i / 2][c]);
+                s[i / 2 + 1][c] = fma(k.y, dd[c], s[i / 2 + 1][c]);
+            }
+        }
+        if (warp == 0) {
+            float z = sum_qk[0];
+            load_columns(&sum_q[0][lane * C], zq);
 #pragma unroll
             for (int w = 1; w < W; ++w) {
-                q0 = add(q0, sum_q[w][c].x);
-                q1 = add(q1, sum_q[w][c].y);
-                qk += sum_qk[w];
+                float y[C];
+                load_columns(&sum_q[w][lane * C], y);
+#pragma unroll
+                for (int c = 0; c < C; ++c) zq[c] += y[c];
+                z += sum_qk[w];
             }
-            const Pair x = pair(qk, qk);
-            const float2 lo = values(fma(x, d0, q0)), hi = values(fma(x, d1, q1));
-            TI* op = (TI*)a.o + ((n * a.T + t) * a.HV + hv) * V + col;
-            op[0] = from_f<TI>(a.scale * lo.x);
-            op[1] = from_f<TI>(a.scale * lo.y);
-            op[2] = from_f<TI>(a.scale * hi.x);
-            op[3] = from_f<TI>(a.scale * hi.y);
+            TI* o = (TI*)a.o + ((n * a.T + t) * a.HV + hv) * V + col;
+#pragma unroll
+            for (int c = 0; c < C; ++c) o[c] = from_f<TI>(a.scale * fmaf(z, d[c], zq[c]));
         }
     }
 #pragma unroll
-    for (int i = 0; i < P; ++i) *(ulonglong2*)(S + i * RP * V) = s[i];
+    for (int i = 0; i < P / 2; ++i) {
+        float x[C], y[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const float2 z = values(s[i][c]);
+            x[c] = z.x;
+            y[c] = z.y;
+        }
+        store_columns(S + 2 * i * V, x);
+        store_columns(S + (2 * i + 1) * V, y);
+    }
 }
 
-template <typename TI, bool MANY> void (*kernel_of(int K, int V))(StepArgs) {
-    return K == 128 ? (V == 128 ? k_step<TI, 128, 128, MANY> : k_step<TI, 128, 64, MANY>)
-                    : (V == 128 ? k_step<TI, 64, 128, MANY> : k_step<TI, 64, 64, MANY>);
+template <typename TI, bool MANY, int C> void (*kernel_of(int K, int V))(StepArgs) {
+    return K == 128 ? (V == 128 ? k_step<TI, 128, 128, MANY, C> : k_step<TI, 128, 64, MANY, C>)
+                    : (V == 128 ? k_step<TI, 64, 128, MANY, C> : k_step<TI, 64, 64, MANY, C>);
 }
-template <typename TI> void (*kernel_of(int K, int V, int T))(StepArgs) {
-    return T > 1 ? kernel_of<TI, true>(K, V) : kernel_of<TI, false>(K, V);
+template <typename TI> void (*kernel_of(int K, int V, int T, int C))(StepArgs) {
+    return T > 1 ? (C == 2 ? kernel_of<TI, true, 2>(K, V) : kernel_of<TI, true, 1>(K, V))
+                 : (C == 2 ? kernel_of<TI, false, 2>(K, V) : kernel_of<TI, false, 1>(K, V));
 }
 
 }  // namespace
@@ -221,9 +270,10 @@ extern "C" kda_status kda_step(const kda_step_dims* d, const void* q, const void
     StepArgs a{q, k, v, beta, g, state, slots, o, status, d->N, d->T, d->H, d->HV, d->num_slots, d->scale};
     cudaStream_t st = (cudaStream_t)stream;
     begin_launches(st);
-    const auto kernel = d->dtype == KDA_DTYPE_BF16 ? kernel_of<__nv_bfloat16>(d->K, d->V, d->T)
-                                                     : kernel_of<float>(d->K, d->V, d->T);
-    const cudaError_t e = launch_after(kernel, a, (unsigned)(d->N * d->HV * (d->V / kCols)), kThreads, st);
+    const int C = (int64_t)d->N * d->HV * (d->V / 64) >= 152 ? 2 : 1;
+    const auto kernel = d->dtype == KDA_DTYPE_BF16 ? kernel_of<__nv_bfloat16>(d->K, d->V, d->T, C)
+                                                   : kernel_of<float>(d->K, d->V, d->T, C);
+    const cudaError_t e = launch_after(kernel, a, (unsigned)(d->N * d->HV * (d->V / (32 * C))), kThreads, st);
     if (e != cudaSuccess) return cuda_fail(e);
     note_launch("step", st);
     return KDA_OK;
