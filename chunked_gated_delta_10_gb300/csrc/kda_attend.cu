@@ -9,9 +9,6 @@
 // Bound: the cached keys and values are read once.
 #include "kda_cache.cuh"
 
-#ifdef TUNE
-#include <stdlib.h>
-#endif
 namespace kda {
 namespace {
 
@@ -60,8 +57,8 @@ struct AttendArgs {
 __device__ __forceinline__ void kv_range(const AttendArgs& a, int64_t n, int& begin, int& end) {
     const int64_t len = a.kv_lens[n], room = (int64_t)a.max_pages * a.c.page_size;
     if (len > room && a.status && threadIdx.x == 0) *a.status = KDA_ERR_INVALID_ARG;
-    begin = a.window > 0 && len > a.window ? (int)(len - a.window) : 0;
     end = (int)max(min(len, room), (int64_t)0);
+    begin = a.window > 0 && len > a.window ? (int)min(len - a.window, (int64_t)end) : 0;
 }
 
 // The value that exponents are taken relative to: the maximum, or 0 where no score is above -inf, so that a
@@ -868,12 +865,6 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window) {
         p.split = cut < shares ? kParts : kShares;
         p.parts = p.split == kParts ? (int)parts : turns * all < 64 * slots ? slots : 2 * slots;
     }
-#ifdef TUNE
-    if (getenv("KM") && atoi(getenv("KM")) >= 0) {
-        p.split = (Split)atoi(getenv("KM"));
-        p.parts = p.split == kWhole ? 1 : atoi(getenv("KS"));
-    }
-#endif
     p.grid = p.split == kShares ? dim3(p.parts) : dim3(units * p.parts, N);
     p.ws_bytes = 256;
     if (p.split >= kParts) {
@@ -925,7 +916,8 @@ cudaError_t launch_attend(const AttendArgs& a, const Plan& p, cudaStream_t st) {
                  : (V == 128 ? kernel_of<64, 128>(bf16, p.ht, p.split) : kernel_of<64, 64>(bf16, p.ht, p.split));
     cudaError_t e = launch_after(kernel, a, p.grid, kWarps * 32, st, p.split == kCluster ? p.parts : 1);
     if (e != cudaSuccess) return e;
-    note_launch("cache_attend", st);
+    static const char* const names[] = {"cache_attend", "cache_attend_cluster", "cache_attend_parts", "cache_attend_shares"};
+    note_launch(names[p.split], st);
     if (p.split < kParts) return cudaSuccess;
     const int64_t parts = p.split == kParts ? p.parts : p.parts / ((int64_t)a.N * p.units) + 2;  // of a unit, with equal lengths
     e = V == 128 ? launch_join<128>(a, bf16, p.ht, parts, st) : launch_join<64>(a, bf16, p.ht, parts, st);
@@ -938,7 +930,7 @@ kda_status check_sizes(const kda_cache* c, int32_t HQ, int32_t N, int32_t max_pa
     const kda_status s = check_cache(c);
     if (s != KDA_OK) return s;
     if (N < 0 || HQ < 1 || HQ % c->HKV != 0 || max_pages < 0 || window < 0) return KDA_ERR_INVALID_ARG;
-    if (N > 65535 || HQ > 65535 || (int64_t)max_pages * c->page_size > (1 << 30)) return KDA_ERR_UNSUPPORTED;
+    if (N > 65535 || HQ > 65535 || (int64_t)N * HQ > (1 << 24) || (int64_t)max_pages * c->page_size > (1 << 30)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 

@@ -5,9 +5,6 @@
 // before it still runs, and each thread then waits for that one's end (and its writes) before it touches memory.
 #pragma once
 #include <cuda_runtime.h>
-#ifdef TUNE
-#include <stdlib.h>
-#endif
 
 namespace kda {
 
@@ -40,9 +37,6 @@ cudaError_t launch_after(void (*kernel)(Args), const Args& a, dim3 grid, int thr
         const cudaError_t e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
     }
-#ifdef TUNE
-    if (getenv("KP") && getenv("KP")[0] == '0') cfg.numAttrs = 0;
-#endif
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 

@@ -129,8 +129,8 @@ kda_status kda_cache_append(const kda_cache* cache, const void* k, int64_t k_str
  *   ws / ws_bytes: device workspace of at least
  *     kda_cache_attend_workspace_bytes; its contents do not matter. Calls
  *     that overlap on the GPU with the same workspace race.
- * N == 0 is KDA_OK and launches nothing. N and HQ are at most 65535, and
- * max_pages * page_size at most 2^30.
+ * N == 0 is KDA_OK and launches nothing. N and HQ are at most 65535, N * HQ at
+ * most 2^24 and max_pages * page_size at most 2^30 (else KDA_ERR_UNSUPPORTED).
  * Errors: KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_WORKSPACE before
  * any launch; KDA_ERR_CUDA if a launch fails.
  */
