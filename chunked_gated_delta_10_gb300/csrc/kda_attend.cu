@@ -6,7 +6,21 @@
 //   l <- l 2^(m - m') + 2^(s - m'),   acc <- acc 2^(m - m') + 2^(s - m') V.
 // Partial results over disjoint rows join by the same rule.
 //
-// Bound: the cached keys and values are read once.
+// Bound: the cached keys and values are read once. Measured on one GB300 (time of
+// a call among others; GB/s of the cached rows), bf16, K = V = 128:
+//   64 sequences of U[1,8192] rows, 32 query heads on 8: 157.6 to 159.7 us,
+//     6.7 to 6.8 TB/s, the rate of a plain copy;
+//   one of 65536 rows, 16 heads on 2: 15.7 us (9.9 at that rate): the length, the
+//     pages and the first rows are read one after the other before the stream is
+//     full (1.5 us), its end is uneven (4 or 5 turns a CTA), and the second kernel
+//     takes 2 us;
+//   one of 2048 rows, 32 heads on 8: 5.4 us, all of it latency (1.2 us of rows).
+// What was tried and is slower: two tiles under way in a warp's registers (two CTAs
+// an SM instead of three: 180 us for the first of these); joins of the parts by
+// reading the other CTAs' shared memory instead of pushing to it (1.5 us more);
+// clusters for large batches (169 to 180 us: a cluster waits for room for all of its
+// CTAs); the sequences of a batch side by side instead of a sequence's heads, which
+// share its pages (fp32, 12 sequences: 15.7 against 13.6 us).
 #include "kda_cache.cuh"
 
 namespace kda {
@@ -88,7 +102,7 @@ template <int R> struct Rows {
         table = a.table + n * a.table_stride;
         pg = a.page(row);
         off = row - pg * a.c.page_size;
-        page = pg < a.max_pages ? __ldg(table + pg) : -1;
+        page = pg < a.max_pages ? table[pg] : -1;
     }
     // The end of the rows, which may be known later than their beginning.
     __device__ __forceinline__ void until(int first, int end) { left = end - first - (int)(threadIdx.x % 32 % R); }
@@ -106,7 +120,7 @@ template <int R> struct Rows {
             off -= a.c.page_size;
             ++pg;
         }
-        page = left > 0 ? __ldg(table + pg) : -1;
+        page = left > 0 ? table[pg] : -1;
     }
     __device__ __forceinline__ int64_t k_of(int r) const { return __shfl_sync(0xffffffffu, k_off, r); }
     __device__ __forceinline__ int64_t v_of(int r) const { return __shfl_sync(0xffffffffu, v_off, r); }
@@ -222,18 +236,6 @@ template <int R, int HT, bool SHARES> struct Work {
     // kShares: the CTA's share, and the sequence that it begins in.
     __device__ __forceinline__ void find_share(const AttendArgs& a, Share& share) {
         const int units = a.units;
-        if (a.N == 1) {
-            if (threadIdx.x == 0) {
-                int begin, last;
-                kv_range(a, 0, begin, last);
-                const int total = turns_of(begin, last) * units, ctas = min(a.parts, total), x = min((int)blockIdx.x, ctas);
-                share.state[0] = {first_turn(x, total, ctas), 0, 0};
-                share.stop = x == ctas ? 0 : first_turn(x + 1, total, ctas);
-                share.total = total;
-            }
-            __syncthreads();
-            return;
-        }
         const int per = (a.N + W * 32 - 1) / (W * 32), lane = threadIdx.x % 32;
         const int n0 = min((int)threadIdx.x * per, a.N), n1 = min(n0 + per, a.N);
         int mine = 0, begin, last;
@@ -304,6 +306,9 @@ template <int R, int HT, bool SHARES> struct Work {
 // ------------------------------------------------------------------ joins
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_started() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // The address in the cluster's CTA `rank` of what has address p here.
 __device__ __forceinline__ uint32_t cluster_address(const void* p, uint32_t rank) {
@@ -328,7 +333,8 @@ __device__ __forceinline__ void add_scaled(float4& x, const float4& y, float f) 
 // Channels d .. d + 3 of the result of query head `at`.
 template <typename TI>
 __device__ __forceinline__ void write_result(const AttendArgs& a, int64_t at, int V, int d, float m, float l, float4 x) {
-    const float f = l == 0.f ? 0.f : 1.f / l;  // nothing attended: x is 0
+    if (l == 0.f) x = make_float4(0.f, 0.f, 0.f, 0.f);  // nothing attended
+    const float f = l == 0.f ? 0.f : 1.f / l;
     TI* o = (TI*)a.o + at * V + d;
     if constexpr (sizeof(TI) == 2) {
         const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x * f, x.y * f), hi = __floats2bfloat162_rn(x.z * f, x.w * f);
@@ -535,8 +541,7 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 // in fp32 or in a pair of bf16 values, and most tiles then only ask whether any score is higher.
 constexpr float kSlack = 8.f;
 
-// Tensor-core kernel: one CTA per (part, up to 8 NT query heads of one cache head, sequence), each warp a tile of 16
-// rows at a time. The products are taken transposed,
+// Tensor-core kernel: a unit has up to 8 NT query heads, each warp a tile of 16 rows at a time. The products are taken transposed,
 //   S^T [16 rows x 8 heads] = K Q^T,     O^T [V x 8 heads] += V^T P^T,
 // so that the rows of the cache are the 16-row operand and a group's few heads the 8 columns. The cache goes from
 // memory straight to the registers in which mma.sync wants it, with no copy in shared memory:
@@ -545,15 +550,17 @@ constexpr float kSlack = 8.f;
 //   - of V it loads unit g (and g + 8) of rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9; a byte permutation pairs the rows, and
 //     row i of the product is channel 8 (i % 8) + j of the j-th product.
 //   - P^T comes from S^T by an 8 x 8 transposition in registers; it is split into a pair of bf16 values (2^-16).
-// A tensor core of the fifth generation wants its operands in shared memory and 128 rows in a product; with at most 16
-// query heads against it, the memory's time would cover none of that traffic.
+// Groups of 9 to 16 heads take two such columns of heads (NT = 2) at two CTAs an SM: reading the rows twice instead
+// takes 80 us where this takes 50 (64 sequences of 8000 rows, 16 heads on one).
+// A tensor core of the fifth generation wants its operands in shared memory and 128 rows in a product; here 8 to 16
+// columns of the product are of use, and with the memory at its rate the tensor cores are busy 14 % of the time as it is.
 template <int K, int V, int NT, bool SHARES>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) k_attend_mma(AttendArgs a) {
     using TI = __nv_bfloat16;
     constexpr int KI = K / 32, VC = V / 64, VJ = V / 16, HT = 8 * NT;
     __shared__ Partial<HT, V> sm;
     const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-    if (!SHARES && a.split == kCluster) cluster_arrive();
+    if (!SHARES && a.split == kCluster) cluster_started();
     after_previous();
     Work<16, HT, SHARES> wk;
     __shared__ typename Work<16, HT, SHARES>::Share share;
@@ -713,15 +720,17 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) k_attend_mma(Att
 constexpr int simt_ctas(int ht) { return ht == 1 ? 4 : 3; }
 constexpr int simt_rows(int ht) { return ht == 8 ? 4 : 8; }
 
-// FFMA kernel: one CTA per (part, up to HT query heads of one cache head, sequence), each warp R rows at a time, a
+// FFMA kernel (fp32): a unit has up to HT query heads, each warp R rows at a time, a
 // lane holding K / 32 and V / 32 channels of each row and of every head. The R HT scores are sums over the lanes: a
 // butterfly that halves the values with the lanes leaves value i, summed, in the lanes l with l % (R HT) == i.
+// 8 sequences of U[1,8000] rows, K = V = 128: 16 heads on 16 108 us (102 at a plain copy's rate), on 4 38 us (25), 32 on 4
+// 49 us (25): with four and eight heads the registers leave 48 KB of rows under way on an SM, too few.
 template <int K, int V, int HT, int R, bool SHARES>
 __global__ void __launch_bounds__(kWarps * 32, SHARES ? simt_ctas(HT) : 1) k_attend_simt(AttendArgs a) {
     constexpr int KL = K / 32, VL = V / 32, NV = R * HT;
     __shared__ Partial<HT, V> sm;
     const int lane = threadIdx.x % 32;
-    if (!SHARES && a.split == kCluster) cluster_arrive();
+    if (!SHARES && a.split == kCluster) cluster_started();
     after_previous();
     Work<R, HT, SHARES> wk;
     __shared__ typename Work<R, HT, SHARES>::Share share;
@@ -840,7 +849,7 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window) {
     const int turn = kWarps * (bf16 ? 16 : simt_rows(ht));
     int64_t rows = (int64_t)max_pages * c->page_size;
     if (window > 0 && window < rows) rows = window;
-    const int64_t turns = rows > turn ? (rows + turn - 1) / turn : 1, all = (int64_t)N * units;  // of a unit; units
+    const int64_t turns = rows > turn ? (rows + turn - 1) / turn : 1, all = (int64_t)(N > 0 ? N : 1) * units;  // of a unit; units
     const int slots = 152 * (!bf16 ? simt_ctas(ht) : ht == 8 ? 3 : 2);
     const int slots_alone = !bf16 && ht == 1 && c->K + c->V == 128 ? 152 * 5 : slots;  // without kShares' registers
     Plan p{kWhole, 1, ht, units, turn};

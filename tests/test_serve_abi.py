@@ -113,6 +113,7 @@ def test_attend_refuses(lib, bad, code):
 def test_attend_of_nothing(lib):
     assert _attend(lib, N=0, q=None, o=None) == 0
     assert lib.kda_cache_attend_workspace_bytes(_cache(), 16, 2, 5, 0) > 0
+    assert lib.kda_cache_attend_workspace_bytes(_cache(), 16, 0, 5, 0) > 0
     assert lib.kda_cache_attend_workspace_bytes(None, 16, 2, 5, 0) == 0
 
 
