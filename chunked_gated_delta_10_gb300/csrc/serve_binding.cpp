@@ -263,21 +263,23 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if ((size_t)t.numel() >= need) ws = t;
     }
     // o, lse and a small workspace are one allocation (three cost 2 us more)
-    const int64_t shape[3] = {x.N, HQ, x.c.V}, heads = (int64_t)x.N * HQ;
-    const int64_t o_bytes = a[8] == Py_None ? heads * x.c.V * (int64_t)c10::elementSize(x.type) : 0;
+    const int64_t shape[3] = {x.N, HQ, x.c.V}, heads = (int64_t)x.N * HQ, size = (int64_t)c10::elementSize(x.type);
+    const int64_t o_bytes = a[8] == Py_None ? heads * x.c.V * size : 0;
     const int64_t lse_bytes = (heads * (int64_t)sizeof(float) + 15) / 16 * 16, ws_bytes = need <= 256 ? 256 : 0;
-    const Tensor all = make({o_bytes + lse_bytes + ws_bytes}, at::kByte, x.dev);
+    Tensor all = make({(o_bytes + lse_bytes + ws_bytes) / size}, x.type, x.dev);
     char* base = (char*)all.data_ptr();
     THPObjectPtr out, lse;
+    lse = THPVariable_Wrap(part_of(all, o_bytes, {shape, 2}, at::kFloat));
+    void* op = base;
     if (a[8] == Py_None) {
-        out = THPVariable_Wrap(part_of(all, 0, shape, x.type));
+        all.unsafeGetTensorImpl()->set_sizes_contiguous(shape);  // o is the allocation's beginning
+        out = THPVariable_Wrap(std::move(all));
     } else {
+        op = like(a[8], "out", shape, x.type, x.dev);
         Py_INCREF(a[8]);
         out = a[8];
     }
-    lse = THPVariable_Wrap(part_of(all, o_bytes, {shape, 2}, at::kFloat));
     if (!out || !lse) throw python_error();
-    void* op = a[8] == Py_None ? base : like(out.get(), "out", shape, x.type, x.dev);
     void* wp = base + o_bytes + lse_bytes;
     size_t room = ws_bytes;
     if (ws.defined() || !ws_bytes) {

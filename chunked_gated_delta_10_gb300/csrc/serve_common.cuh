@@ -33,9 +33,18 @@ cudaError_t launch_after(void (*kernel)(Args), const Args& a, dim3 grid, int thr
         attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
         cfg.numAttrs = 2;
     }
-    if (cluster > 8) {
-        const cudaError_t e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (cluster > 8) {  // (the attribute stays with the kernel on its device: set it again only where that may differ)
+        thread_local const void* set_for = nullptr;
+        thread_local int set_on = -1;
+        int device;
+        cudaError_t e = cudaGetDevice(&device);
         if (e != cudaSuccess) return e;
+        if (set_for != (const void*)kernel || set_on != device) {
+            e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+            set_for = (const void*)kernel;
+            set_on = device;
+        }
     }
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
