@@ -16,11 +16,12 @@
 //     takes 2 us;
 //   one of 2048 rows, 32 heads on 8: 5.4 us, all of it latency (1.2 us of rows).
 // What was tried and is slower: two tiles under way in a warp's registers (two CTAs
-// an SM instead of three: 180 us for the first of these); joins of the parts by
-// reading the other CTAs' shared memory instead of pushing to it (1.5 us more);
-// clusters for large batches (169 to 180 us: a cluster waits for room for all of its
-// CTAs); the sequences of a batch side by side instead of a sequence's heads, which
-// share its pages (fp32, 12 sequences: 15.7 against 13.6 us).
+// an SM instead of three: 180 us for the first of these); the tile after the next
+// asked into L2 (166 us; fp32 with eight heads alone gains, 48 -> 44 us); joins of
+// the parts by reading the other CTAs' shared memory instead of pushing to it (1.5
+// us more); clusters for large batches (169 to 180 us: a cluster waits for room for
+// all of its CTAs); the sequences of a batch side by side instead of a sequence's
+// heads, which share its pages (fp32, 12 sequences: 15.7 against 13.6 us).
 #include "kda_cache.cuh"
 
 namespace kda {
