@@ -31,6 +31,7 @@ namespace {
 // floor(n ceil(2^(31 + s) / d) / 2^(31 + s)).
 struct Divisor {
     unsigned factor, shift;
+    Divisor() = default;
     __host__ explicit Divisor(unsigned d) : shift(31) {
         while (1ull << (shift - 31) < d) ++shift;
         factor = (unsigned)(((1ull << shift) + d - 1) / d);
@@ -542,7 +543,8 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 // in fp32 or in a pair of bf16 values, and most tiles then only ask whether any score is higher.
 constexpr float kSlack = 8.f;
 
-// Tensor-core kernel: a unit has up to 8 NT query heads, each warp a tile of 16 rows at a time. The products are taken transposed,
+// Tensor-core kernel: a unit has up to 8 NT query heads, each warp a tile of 16 rows at a time. The products are taken
+// transposed,
 //   S^T [16 rows x 8 heads] = K Q^T,     O^T [V x 8 heads] += V^T P^T,
 // so that the rows of the cache are the 16-row operand and a group's few heads the 8 columns. The cache goes from
 // memory straight to the registers in which mma.sync wants it, with no copy in shared memory:
@@ -574,8 +576,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) k_attend_mma(Att
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int i = 0; i < KI; ++i)
-                q[j][i] =
-                    load16((const TI*)a.q + (int64_t)wk.n * a.q_stride + (h0 + 8 * j + g) * K + (4 * i + t) * 8, 8 * j + g < heads);
+                q[j][i] = load16((const TI*)a.q + (int64_t)wk.n * a.q_stride + (h0 + 8 * j + g) * K + (4 * i + t) * 8,
+                                 8 * j + g < heads);
         float acc[NT][VJ][4], m[NT][2], l[NT][2];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -850,7 +852,8 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window) {
     const int turn = kWarps * (bf16 ? 16 : simt_rows(ht));
     int64_t rows = (int64_t)max_pages * c->page_size;
     if (window > 0 && window < rows) rows = window;
-    const int64_t turns = rows > turn ? (rows + turn - 1) / turn : 1, all = (int64_t)(N > 0 ? N : 1) * units;  // of a unit; units
+    const int64_t turns = rows > turn ? (rows + turn - 1) / turn : 1;  // of a unit
+    const int64_t all = (int64_t)(N > 0 ? N : 1) * units;              // units
     const int slots = 152 * (!bf16 ? simt_ctas(ht) : ht == 8 ? 3 : 2);
     const int slots_alone = !bf16 && ht == 1 && c->K + c->V == 128 ? 152 * 5 : slots;  // without kShares' registers
     Plan p{kWhole, 1, ht, units, turn};
@@ -863,7 +866,8 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window) {
            (all * cluster * 2 <= slots_alone || (all * cluster * 16 <= slots_alone * 9 && turns >= 8 * cluster)))
         cluster *= 2;
     const auto waves = [&](int64_t ctas) { return ctas > slots_alone ? (double)ctas / slots_alone : 1.0; };
-    const double whole = turns * waves(all), clusters = 1 + (double)turns / cluster * (all * cluster > slots_alone ? 1.4 : 1.0);
+    const double whole = turns * waves(all);
+    const double clusters = 1 + (double)turns / cluster * (all * cluster > slots_alone ? 1.4 : 1.0);
     const double shares = 5.5 + (double)turns * all * (N > 1 ? 0.75 : 1.0) / slots;
     const int64_t parts = all <= slots ? (slots / all < turns ? slots / all : turns) : 1;
     const double cut = parts > 1 ? 2.2 + (double)turns / parts : whole;
@@ -926,10 +930,12 @@ cudaError_t launch_attend(const AttendArgs& a, const Plan& p, cudaStream_t st) {
                  : (V == 128 ? kernel_of<64, 128>(bf16, p.ht, p.split) : kernel_of<64, 64>(bf16, p.ht, p.split));
     cudaError_t e = launch_after(kernel, a, p.grid, kWarps * 32, st, p.split == kCluster ? p.parts : 1);
     if (e != cudaSuccess) return e;
-    static const char* const names[] = {"cache_attend", "cache_attend_cluster", "cache_attend_parts", "cache_attend_shares"};
+    static const char* const names[] = {"cache_attend", "cache_attend_cluster", "cache_attend_parts",
+                                        "cache_attend_shares"};
     note_launch(names[p.split], st);
     if (p.split < kParts) return cudaSuccess;
-    const int64_t parts = p.split == kParts ? p.parts : p.parts / ((int64_t)a.N * p.units) + 2;  // of a unit, with equal lengths
+    // of a unit, with equal lengths
+    const int64_t parts = p.split == kParts ? p.parts : p.parts / ((int64_t)a.N * p.units) + 2;
     e = V == 128 ? launch_join<128>(a, bf16, p.ht, parts, st) : launch_join<64>(a, bf16, p.ht, parts, st);
     if (e != cudaSuccess) return e;
     note_launch("cache_attend_join", st);
@@ -940,7 +946,8 @@ kda_status check_sizes(const kda_cache* c, int32_t HQ, int32_t N, int32_t max_pa
     const kda_status s = check_cache(c);
     if (s != KDA_OK) return s;
     if (N < 0 || HQ < 1 || HQ % c->HKV != 0 || max_pages < 0 || window < 0) return KDA_ERR_INVALID_ARG;
-    if (N > 65535 || HQ > 65535 || (int64_t)N * HQ > (1 << 24) || (int64_t)max_pages * c->page_size > (1 << 30)) return KDA_ERR_UNSUPPORTED;
+    if (N > 65535 || HQ > 65535 || (int64_t)N * HQ > (1 << 24) || (int64_t)max_pages * c->page_size > (1 << 30))
+        return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -972,9 +979,35 @@ extern "C" kda_status kda_cache_attend(const kda_cache* c, const void* q, int64_
     if (!ws || !aligned16(ws) || ws_bytes < plan.ws_bytes) return KDA_ERR_WORKSPACE;
     char* w = (char*)ws;
     const int step = plan.turn * (plan.split == kShares ? 1 : plan.parts);
-    const AttendArgs a{*c, q, q_stride, table_stride, HQ, N, max_pages, window, page_table, kv_lens, scale * kLog2e, o,
-                       lse, status, HQ / c->HKV, plan.units / c->HKV, plan.units, Divisor(c->page_size), step, step / c->page_size, step % c->page_size, plan.split, plan.parts, Divisor(plan.parts), plan.turn, (float4*)w, (float2*)(w + plan.acc_bytes),
-                       (int2*)(w + plan.acc_bytes + plan.ml_bytes)};
+    AttendArgs a;
+    a.c = *c;
+    a.q = q;
+    a.q_stride = q_stride;
+    a.table_stride = table_stride;
+    a.HQ = HQ;
+    a.N = N;
+    a.max_pages = max_pages;
+    a.window = window;
+    a.table = page_table;
+    a.kv_lens = kv_lens;
+    a.scale_log2 = scale * kLog2e;
+    a.o = o;
+    a.lse = lse;
+    a.status = status;
+    a.group = HQ / c->HKV;
+    a.tiles = plan.units / c->HKV;
+    a.units = plan.units;
+    a.page = Divisor(c->page_size);
+    a.step = step;
+    a.step_pg = step / c->page_size;
+    a.step_off = step % c->page_size;
+    a.split = plan.split;
+    a.parts = plan.parts;
+    a.by_parts = Divisor(plan.parts);
+    a.turn = plan.turn;
+    a.part_acc = (float4*)w;
+    a.part_ml = (float2*)(w + plan.acc_bytes);
+    a.unit_parts = (int2*)(w + plan.acc_bytes + plan.ml_bytes);
     cudaStream_t st = (cudaStream_t)stream;
     begin_launches(st);
     const cudaError_t e = launch_attend(a, plan, st);

@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(MOST) k_append(AppendArgs a) {
         const bool is_q = i < units_q;
         const int j = is_q ? i : i - units_q, h = j / uk, u = j % uk;
         if (!is_q && page < 0) continue;
-        const TI* src = is_q ? (const TI*)a.q + (int64_t)r * a.q_stride + h * a.c.K : (const TI*)a.k + (int64_t)r * a.k_stride + h * a.c.K;
+        const TI* src = is_q ? (const TI*)a.q + (int64_t)r * a.q_stride + h * a.c.K
+                             : (const TI*)a.k + (int64_t)r * a.k_stride + h * a.c.K;
         TI* dst = is_q ? (TI*)a.q_out + ((int64_t)r * a.HQ + h) * a.c.K
                        : (TI*)a.c.k + (int64_t)page * a.c.k_page + row * a.c.k_row + h * a.c.k_head;
         float x[E], y[E];
@@ -185,14 +186,16 @@ extern "C" kda_status kda_cache_append(const kda_cache* c, const void* k, int64_
         ((uintptr_t)cu_seqlens & 7u))
         return KDA_ERR_INVALID_ARG;
     if (R > INT32_MAX || ((int64_t)HQ + 2 * (int64_t)c->HKV) * 32 > INT32_MAX) return KDA_ERR_UNSUPPORTED;
-    const int64_t uk = (c->K - (interleaved ? 0 : rope_dim / 2)) / unit, units = (HQ + c->HKV) * uk + c->HKV * (c->V / unit);
+    const int64_t uk = (c->K - (interleaved ? 0 : rope_dim / 2)) / unit;
+    const int64_t units = (HQ + c->HKV) * uk + c->HKV * (c->V / unit);  // of a row
     const bool few = units <= 64, many = R >= 1024;  // (measured: see the top of this file)
     const int most = few ? 256 : many ? 64 : 512;
     const int64_t turns = (units + most - 1) / most;
     const int lanes = (int)((units + turns - 1) / turns), rows = few ? most / lanes : 1;
     const int threads = (lanes * rows + 31) / 32 * 32;
-    const AppendArgs a{*c, k, v, q, q_out, k_stride, v_stride, q_stride, table_stride, HQ, N, (unsigned)R, (unsigned)(R / N), cu_seqlens, rope, rope_len,
-                 rope_dim, interleaved, page_table, kv_lens, max_pages, status, (unsigned)lanes, (unsigned)rows};
+    const AppendArgs a{*c, k, v, q, q_out, k_stride, v_stride, q_stride, table_stride, HQ, N, (unsigned)R,
+                       (unsigned)(R / N), cu_seqlens, rope, rope_len, rope_dim, interleaved, page_table, kv_lens, max_pages,
+                       status, (unsigned)lanes, (unsigned)rows};
     cudaStream_t st = (cudaStream_t)stream;
     begin_launches(st);
     void (*const kernel)(AppendArgs) =

@@ -9,6 +9,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -256,6 +257,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const c10::cuda::CUDAGuard guard(x.dev);
     const size_t need = kda_cache_attend_workspace_bytes(&x.c, HQ, x.N, x.width, window);
     Tensor ws;
+    c10::DataPtr scratch;
     if (a[7] != Py_None) {
         const Tensor& t = tensor(a[7], "ws");
         if (t.scalar_type() != at::kByte || t.device() != x.dev || !t.is_contiguous())
@@ -282,10 +284,13 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!out || !lse) throw python_error();
     void* wp = base + o_bytes + lse_bytes;
     size_t room = ws_bytes;
-    if (ws.defined() || !ws_bytes) {
-        if (!ws.defined()) ws = make({(int64_t)need}, at::kByte, x.dev);
+    if (ws.defined()) {
         wp = ws.data_ptr();
         room = ws.numel();
+    } else if (!ws_bytes) {  // (its memory is free again for what follows on this stream)
+        scratch = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+        wp = scratch.get();
+        room = need;
     }
     const kda_status s = kda_cache_attend(&x.c, q.p, q.stride, HQ, x.N, x.table, x.table_stride, x.width, x.lens, window,
                                           scale, op, (float*)(base + o_bytes), (int32_t*)status, wp, room,
