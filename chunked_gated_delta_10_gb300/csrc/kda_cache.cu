@@ -10,11 +10,13 @@
 // it is the latency of a launch. A CTA has one row, so that its sequence, page
 // and angles are found by uniform instructions; what is left of it is loads and
 // stores, and the CTA's size decides how many rows an SM has under way:
-//   from 1024 rows on, 64 threads. 16 packed prompts of U[1,4096] tokens, 32
-//     query and 8 cache heads of 128, bf16 (822 MB): 122 us, 6.74 TB/s, the rate
-//     of a plain copy; with 128 threads 124 us, 256: 131, 512: 236.
-//   below, up to 512 threads, one unit each: one token 2.1 us (64 threads: 4.2),
-//     128 tokens 3.0 us (7.2).
+//   many rows: the fewest threads, from 64 on, that fill the SMs. 16 packed prompts
+//     of U[1,4096] tokens, 32 query and 8 cache heads of 128, bf16 (822 MB): 64
+//     threads, 122 us, 6.74 TB/s, the rate of a plain copy; with 128 threads 124
+//     us, 256: 131, 512: 236. 3000 rows of 128 and 16 heads: 128 threads, 21.7 us;
+//     with 64, which leave SMs half empty, 33.6.
+//   up to two rows an SM: 512 threads, one unit each. One token 2.1 us (64 threads:
+//     4.2), 128 tokens 3.0 us (7.2); 512 tokens already 4.5 (256 threads: 4.0).
 //   rows of 64 units or fewer share a CTA of 256 threads: 33,000 rows of two
 //     heads of 64 take 10.2 us, and 33.5 us with a CTA each (1 ns a CTA).
 // Several rows to a thread, their loads ahead of their sums, was slower (150 to
@@ -150,8 +152,8 @@ __global__ void __launch_bounds__(MOST) k_append(AppendArgs a) {
     }
 }
 
-template <typename TI> void (*kernel_of(bool few, bool many))(AppendArgs) {
-    return few ? k_append<TI, true, 256> : many ? k_append<TI, false, 64> : k_append<TI, false, 512>;
+template <typename TI> void (*kernel_of(bool few, int most))(AppendArgs) {
+    return few ? k_append<TI, true, 256> : most == 64 ? k_append<TI, false, 64> : k_append<TI, false, 512>;
 }
 
 }  // namespace
@@ -188,8 +190,9 @@ extern "C" kda_status kda_cache_append(const kda_cache* c, const void* k, int64_
     if (R > INT32_MAX || ((int64_t)HQ + 2 * (int64_t)c->HKV) * 32 > INT32_MAX) return KDA_ERR_UNSUPPORTED;
     const int64_t uk = (c->K - (interleaved ? 0 : rope_dim / 2)) / unit;
     const int64_t units = (HQ + c->HKV) * uk + c->HKV * (c->V / unit);  // of a row
-    const bool few = units <= 64, many = R >= 1024;  // (measured: see the top of this file)
-    const int most = few ? 256 : many ? 64 : 512;
+    const bool few = units <= 64;
+    int most = few ? 256 : R <= 2 * 152 ? 512 : 64;  // threads of a CTA; measured: see the top of this file
+    while (most < 256 && R * most < 152 * 2048) most *= 2;
     const int64_t turns = (units + most - 1) / most;
     const int lanes = (int)((units + turns - 1) / turns), rows = few ? most / lanes : 1;
     const int threads = (lanes * rows + 31) / 32 * 32;
@@ -199,7 +202,7 @@ extern "C" kda_status kda_cache_append(const kda_cache* c, const void* k, int64_
     cudaStream_t st = (cudaStream_t)stream;
     begin_launches(st);
     void (*const kernel)(AppendArgs) =
-        c->dtype == KDA_DTYPE_BF16 ? kernel_of<__nv_bfloat16>(few, many) : kernel_of<float>(few, many);
+        c->dtype == KDA_DTYPE_BF16 ? kernel_of<__nv_bfloat16>(few, most) : kernel_of<float>(few, most);
     const cudaError_t e = launch_after(kernel, a, (unsigned)((R + rows - 1) / rows), threads, st);
     if (e != cudaSuccess) return cuda_fail(e);
     note_launch("cache_append", st);
