@@ -543,6 +543,9 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 // in fp32 or in a pair of bf16 values, and most tiles then only ask whether any score is higher.
 constexpr float kSlack = 8.f;
 
+// CTAs of k_attend_mma to an SM.
+constexpr int mma_ctas(int NT, int K, int V) { return (K + V == 128 ? 5 : 3) - (NT - 1); }
+
 // Tensor-core kernel: a unit has up to 8 NT query heads, each warp a tile of 16 rows at a time. The products are taken
 // transposed,
 //   S^T [16 rows x 8 heads] = K Q^T,     O^T [V x 8 heads] += V^T P^T,
@@ -554,11 +557,12 @@ constexpr float kSlack = 8.f;
 //     row i of the product is channel 8 (i % 8) + j of the j-th product.
 //   - P^T comes from S^T by an 8 x 8 transposition in registers; it is split into a pair of bf16 values (2^-16).
 // Groups of 9 to 16 heads take two such columns of heads (NT = 2) at two CTAs an SM: reading the rows twice instead
-// takes 80 us where this takes 50 (64 sequences of 8000 rows, 16 heads on one).
+// takes 80 us where this takes 50 (64 sequences of 8000 rows, 16 heads on one). K = V = 64 leaves registers for five CTAs
+// (40 sequences of U[1,8000] rows, 16 heads on 16: 111.6 us; with three, whose rows under way are too few, 120).
 // A tensor core of the fifth generation wants its operands in shared memory and 128 rows in a product; here 8 to 16
 // columns of the product are of use, and with the memory at its rate the tensor cores are busy 14 % of the time as it is.
 template <int K, int V, int NT, bool SHARES>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) k_attend_mma(AttendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, mma_ctas(NT, K, V)) k_attend_mma(AttendArgs a) {
     using TI = __nv_bfloat16;
     constexpr int KI = K / 32, VC = V / 64, VJ = V / 16, HT = 8 * NT;
     __shared__ Partial<HT, V> sm;
@@ -854,7 +858,7 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window) {
     if (window > 0 && window < rows) rows = window;
     const int64_t turns = rows > turn ? (rows + turn - 1) / turn : 1;  // of a unit
     const int64_t all = (int64_t)(N > 0 ? N : 1) * units;              // units
-    const int slots = 152 * (!bf16 ? simt_ctas(ht) : ht == 8 ? 3 : 2);
+    const int slots = 152 * (bf16 ? mma_ctas(ht / 8, c->K, c->V) : simt_ctas(ht));
     const int slots_alone = !bf16 && ht == 1 && c->K + c->V == 128 ? 152 * 5 : slots;  // without kShares' registers
     Plan p{kWhole, 1, ht, units, turn};
     // What each costs, in turns (about 1.1 us). Over a CTA alone a cluster's join costs about one, the second kernel
