@@ -13,12 +13,15 @@
 //   many rows: the fewest threads, from 64 on, that fill the SMs. 16 packed prompts
 //     of U[1,4096] tokens, 32 query and 8 cache heads of 128, bf16 (822 MB): 64
 //     threads, 122 us, 6.74 TB/s, the rate of a plain copy; with 128 threads 124
-//     us, 256: 131, 512: 236. 3000 rows of 128 and 16 heads: 128 threads, 21.7 us;
-//     with 64, which leave SMs half empty, 33.6.
+//     us, 256: 131, 512: 236. 3000 rows of 128 and 16 heads: 128 threads, 17.2 us;
+//     64 leave SMs half empty, and took half as long again.
 //   up to two rows an SM: 512 threads, one unit each. One token 2.1 us (64 threads:
 //     4.2), 128 tokens 3.0 us (7.2); 512 tokens already 4.5 (256 threads: 4.0).
 //   rows of 64 units or fewer share a CTA of 256 threads: 33,000 rows of two
 //     heads of 64 take 10.2 us, and 33.5 us with a CTA each (1 ns a CTA).
+// Units that turn and units that are copied are separate loops, the copies two at a
+// time (the prompts without a rotation 139 -> 120 us, with half of each head turned
+// 169 -> 124); 24 CTAs of 64 threads fit an SM (40 registers; with 47: 126 us).
 // Several rows to a thread, their loads ahead of their sums, was slower (150 to
 // 226 us for the prompts): the angles take the registers that more CTAs need.
 #include "kda_cache.cuh"
@@ -56,10 +59,10 @@ __device__ __forceinline__ int seq_of(const int64_t* cu, int N, unsigned r) {
 }
 
 template <typename TI, bool SHORT, int MOST>
-__global__ void __launch_bounds__(MOST) k_append(AppendArgs a) {
-    constexpr int E = Unit<TI>::n;
+__global__ void __launch_bounds__(MOST, SHORT ? 6 : MOST == 64 ? 24 : 2) k_append(AppendArgs a) {
+    constexpr int E = Unit<TI>::n, kBatch = SHORT ? 1 : 2;  // units of a row; copies that a thread has under way
     after_previous();
-    unsigned r = blockIdx.x;
+    int64_t r = blockIdx.x;
     int lane = threadIdx.x;
     if constexpr (SHORT) {
         const unsigned in = lane / a.lanes;
@@ -70,17 +73,18 @@ __global__ void __launch_bounds__(MOST) k_append(AppendArgs a) {
     unsigned n, idx;
     bool ok = true;
     if (a.cu) {
-        n = seq_of(a.cu, a.N, r);
-        const int64_t first = a.cu[n];
-        ok = first <= r;
-        idx = r - (unsigned)first;
+        n = seq_of(a.cu, a.N, (unsigned)r);
+        const int64_t begin = a.cu[n];
+        ok = begin <= r;
+        idx = (unsigned)(r - begin);
     } else {
-        n = r / a.per;
-        idx = r - n * a.per;
+        n = (unsigned)r / a.per;
+        idx = (unsigned)r - n * a.per;
     }
     const int len = a.kv_lens[n];
-    const unsigned pos = (unsigned)len + idx, pg = pos / (unsigned)a.c.page_size, row = pos - pg * a.c.page_size;
-    int page = -1;
+    const unsigned at_pos = (unsigned)len + idx, pg = at_pos / (unsigned)a.c.page_size;
+    const int64_t pos = at_pos, row = at_pos - pg * a.c.page_size;
+    int64_t page = -1;
     if (len >= 0) {
         ok = ok && pg < (unsigned)a.max_pages && (!a.rope || pos < (unsigned)a.rope_len);
         if (ok) page = a.table[n * a.table_stride + pg];
@@ -89,44 +93,48 @@ __global__ void __launch_bounds__(MOST) k_append(AppendArgs a) {
             if (a.status && lane == 0) *a.status = KDA_ERR_INVALID_ARG;
         }
     }
-    // units of a head: the pairs of units that turn together, then the rest
-    const int half = a.interleaved ? 0 : a.rope_dim / 2 / E;
-    const int uk = a.c.K / E - half, uv = a.c.V / E;
-    const int units_q = a.HQ * uk, units_k = a.c.HKV * uk, units = units_q + units_k + a.c.HKV * uv;
-    for (int i = lane; i < units; i += SHORT ? a.lanes : blockDim.x) {
-        if (i >= units_q + units_k) {
-            const int j = i - units_q - units_k, h = j / uv, u = j % uv;
-            if (page >= 0) {
-                const TI* src = (const TI*)a.v + (int64_t)r * a.v_stride + h * a.c.V + u * E;
-                TI* dst = (TI*)a.c.v + (int64_t)page * a.c.v_page + row * a.c.v_row + h * a.c.v_head + u * E;
-                *(uint4*)dst = *(const uint4*)src;
-            }
-            continue;
-        }
-        const bool is_q = i < units_q;
-        const int j = is_q ? i : i - units_q, h = j / uk, u = j % uk;
-        if (!is_q && page < 0) continue;
-        const TI* src = is_q ? (const TI*)a.q + (int64_t)r * a.q_stride + h * a.c.K
-                             : (const TI*)a.k + (int64_t)r * a.k_stride + h * a.c.K;
-        TI* dst = is_q ? (TI*)a.q_out + ((int64_t)r * a.HQ + h) * a.c.K
-                       : (TI*)a.c.k + (int64_t)page * a.c.k_page + row * a.c.k_row + h * a.c.k_head;
+    const int lanes = SHORT ? a.lanes : blockDim.x;
+    const int heads = a.HQ + a.c.HKV, rot = a.rope_dim / E;  // query heads, then key heads; a head's units that turn
+    // row r of head h, from channel `at` on: where it is, and where it goes (null: it is dropped)
+    const auto from = [&](int h, int at) {
+        return h < a.HQ ? (const TI*)a.q + r * a.q_stride + h * a.c.K + at
+                        : (const TI*)a.k + r * a.k_stride + (h - a.HQ) * a.c.K + at;
+    };
+    const auto to = [&](int h, int at) -> TI* {
+        if (h < a.HQ) return (TI*)a.q_out + (r * a.HQ + h) * a.c.K + at;
+        if (page < 0) return nullptr;
+        return (TI*)a.c.k + page * a.c.k_page + row * a.c.k_row + (h - a.HQ) * a.c.k_head + at;
+    };
+    // the units that turn: two of them, half of rope_dim apart, or one with its channels in pairs
+    const int per = a.interleaved ? rot : rot / 2, turning = heads * per;
+    const float* cs = a.rope + pos * a.rope_dim;
+    for (int i = lane; i < turning; i += lanes) {
+        const int h = i / per, at = (i - h * per) * E, other = at + a.rope_dim / 2;
+        TI* dst = to(h, at);
+        if (!dst) continue;
         float x[E], y[E];
         if (page < 0) {  // a query row of a dropped or inactive token
 #pragma unroll
             for (int e = 0; e < E; ++e) x[e] = 0.f;
-            if (u < half) Unit<TI>::store(dst + u * E, x);
-            Unit<TI>::store(dst + (u + half) * E, x);
-            continue;
-        }
-        const float* cs = a.rope + (int64_t)pos * a.rope_dim;
-        if (u < half) {
-            Unit<TI>::load(src + u * E, x);
-            Unit<TI>::load(src + (u + half) * E, y);
+            Unit<TI>::store(dst, x);
+            if (!a.interleaved) Unit<TI>::store(dst + a.rope_dim / 2, x);
+        } else if (a.interleaved) {
+            Unit<TI>::load(from(h, at), x);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float co = cs[(at + e) / 2], si = cs[(a.rope_dim + at + e) / 2], t = x[e];
+                x[e] = t * co - x[e + 1] * si;
+                x[e + 1] = x[e + 1] * co + t * si;
+            }
+            Unit<TI>::store(dst, x);
+        } else {
+            Unit<TI>::load(from(h, at), x);
+            Unit<TI>::load(from(h, other), y);
             float co[E], si[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                co[e] = cs[u * E + e];
-                si[e] = cs[a.rope_dim / 2 + u * E + e];
+                co[e] = cs[at + e];
+                si[e] = cs[other + e];
             }
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -134,21 +142,34 @@ __global__ void __launch_bounds__(MOST) k_append(AppendArgs a) {
                 x[e] = t * co[e] - y[e] * si[e];
                 y[e] = y[e] * co[e] + t * si[e];
             }
-            Unit<TI>::store(dst + u * E, x);
-            Unit<TI>::store(dst + (u + half) * E, y);
-            continue;
+            Unit<TI>::store(dst, x);
+            Unit<TI>::store(dst + a.rope_dim / 2, y);
         }
-        const int at = (u + half) * E;
-        Unit<TI>::load(src + at, x);
-        if (a.interleaved && at < a.rope_dim) {
+    }
+    // the units that are copied, some at a time; the threads that had the fewest to turn begin
+    const int rest = a.c.K / E - rot, uv = a.c.V / E, of_heads = heads * rest, copied = of_heads + a.c.HKV * uv;
+    int first = lane - turning % lanes;
+    if (first < 0) first += lanes;
+    for (int i = first; i < copied; i += kBatch * lanes) {
+        uint4 x[kBatch];
+        TI* dst[kBatch];
 #pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const float co = cs[(at + e) / 2], si = cs[a.rope_dim / 2 + (at + e) / 2], t = x[e];
-                x[e] = t * co - x[e + 1] * si;
-                x[e + 1] = x[e + 1] * co + t * si;
+        for (int b = 0; b < kBatch; ++b) {
+            const int j = i + b * lanes;
+            dst[b] = nullptr;
+            if (j < of_heads) {
+                const int h = j / rest, at = (rot + j - h * rest) * E;
+                dst[b] = to(h, at);
+                x[b] = page < 0 ? make_uint4(0, 0, 0, 0) : *(const uint4*)from(h, at);
+            } else if (j < copied && page >= 0) {
+                const int h = (j - of_heads) / uv, at = (j - of_heads - h * uv) * E;
+                dst[b] = (TI*)a.c.v + page * a.c.v_page + row * a.c.v_row + h * a.c.v_head + at;
+                x[b] = *(const uint4*)((const TI*)a.v + r * a.v_stride + h * a.c.V + at);
             }
         }
-        Unit<TI>::store(dst + at, x);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            if (dst[b]) *(uint4*)dst[b] = x[b];
     }
 }
 
