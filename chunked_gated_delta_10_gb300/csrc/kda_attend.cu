@@ -8,9 +8,9 @@
 //
 // Bound: the cached keys and values are read once. Measured on one GB300 (time of
 // a call among others; GB/s of the cached rows), bf16, K = V = 128:
-//   64 sequences of U[1,8192] rows, 32 query heads on 8: 157.6 to 159.7 us,
-//     6.7 to 6.8 TB/s, the rate of a plain copy;
-//   one of 65536 rows, 16 heads on 2: 15.7 us (9.9 at that rate): the length, the
+//   64 sequences of U[1,8192] rows, 32 query heads on 8: 154.4 to 156.3 us,
+//     6.8 to 6.9 TB/s, a little above a plain copy's rate;
+//   one of 65536 rows, 16 heads on 2: 15.9 us (9.9 at that rate): the length, the
 //     pages and the first rows are read one after the other before the stream is
 //     full (1.5 us), its end is uneven (4 or 5 turns a CTA), and the second kernel
 //     takes 2 us;
@@ -20,8 +20,9 @@
 // asked into L2 (166 us; fp32 with eight heads alone gains, 48 -> 44 us); joins of
 // the parts by reading the other CTAs' shared memory instead of pushing to it (1.5
 // us more); clusters for large batches (169 to 180 us: a cluster waits for room for
-// all of its CTAs); the sequences of a batch side by side instead of a sequence's
-// heads, which share its pages (fp32, 12 sequences: 15.7 against 13.6 us).
+// all of its CTAs); shares of the rows alone, without a weight for a unit's ends
+// (160 us for the first of these); the sequences of a batch side by side instead of
+// a sequence's heads, which share its pages (fp32, 12 sequences: 15.7 against 13.6).
 #include "kda_cache.cuh"
 
 namespace kda {
@@ -152,10 +153,14 @@ template <int C> __device__ __forceinline__ void load_channels(const float* p, b
 //   kCluster  a cluster of CTAs per unit, which take its turns one after the other (so the first rows of a CTA do not
 //             depend on the length, and their pages are looked up while it is on its way) and join their results in
 //             shared memory: for few units of some turns, where latency counts;
-//   kParts    the same with more CTAs than a cluster has, joined by a second kernel: for few units of many turns;
-//   kShares   as many CTAs as the GPU holds at once, each with an equal share of all turns in the order of the units,
-//             whatever the lengths are: every CTA adds up the lengths to find its share. A unit that falls to several
-//             CTAs is joined by a second kernel.
+//   kParts    the same with more CTAs than a cluster has, joined by a second kernel: for few units of many turns, and
+//             with fp32 for all of many rows;
+//   kShares   (bf16) as many CTAs as the GPU holds at once, each with an equal share of all turns in the order of the
+//             units, whatever the lengths are: every CTA adds up the lengths to find its share. A unit counts for
+//             kUnitTurns more than it has, about what it costs to begin and end one; else the CTAs with many short units
+//             would be the last (64 sequences of U[1,8192] rows, 32 heads on 8: 160 -> 154 us; 11 of U[1,4240], 256
+//             heads on 16: 42 -> 28 us). A unit that falls to several CTAs is joined by a second kernel.
+constexpr int kUnitTurns = 2;
 constexpr int kWarps = 4;
 constexpr int kMaxCluster = 16;
 
@@ -243,7 +248,7 @@ template <int R, int HT, bool SHARES> struct Work {
         int mine = 0, begin, last;
         for (int i = n0; i < n1; ++i) {
             kv_range(a, i, begin, last);
-            mine += turns_of(begin, last) * units;
+            mine += (turns_of(begin, last) + kUnitTurns) * units;
         }
         int before = mine;
 #pragma unroll
@@ -267,7 +272,7 @@ template <int R, int HT, bool SHARES> struct Work {
             int i = n0;
             for (;; ++i) {
                 kv_range(a, i, begin, last);
-                const int turns = turns_of(begin, last) * units;
+                const int turns = (turns_of(begin, last) + kUnitTurns) * units;
                 if (at < before + turns) break;
                 before += turns;
             }
@@ -279,21 +284,28 @@ template <int R, int HT, bool SHARES> struct Work {
     }
     // kShares: the next unit, or part of one, of the CTA's share; false if there is none.
     __device__ __forceinline__ bool next(const AttendArgs& a, Share& share) {
-        const int at = share.state[odd].at, stop = share.stop, units = a.units;
-        if (at >= stop) return false;
-        int begin, last, turns, seq = share.state[odd].seq;
-        for (n = share.state[odd].n;; ++n) {
-            kv_range(a, n, begin, last);
-            turns = turns_of(begin, last);
-            if (at < seq + turns * units) break;
-            seq += turns * units;
+        const int stop = share.stop, units = a.units;
+        int at = share.state[odd].at, begin, last, turns, each, t0, seq = share.state[odd].seq;
+        unsigned u;
+        n = share.state[odd].n;
+        for (;; at += each - t0) {  // (a share may begin behind a unit's rows)
+            if (at >= stop) return false;
+            for (;; ++n) {
+                kv_range(a, n, begin, last);
+                turns = turns_of(begin, last);
+                each = turns + kUnitTurns;
+                if (at < seq + each * units) break;
+                seq += each * units;
+            }
+            u = (unsigned)(at - seq) / (unsigned)each;
+            t0 = at - seq - u * each;
+            if (t0 < turns) break;
         }
-        const unsigned u = (unsigned)(at - seq) / (unsigned)turns;
-        const int t0 = at - seq - u * turns, t1 = min(turns, t0 + stop - at);
+        const int t1 = min(turns, t0 + stop - at);
         set_unit(a, u, t0 == 0 && t1 == turns, 2 * blockIdx.x + (t0 == 0), share);
         odd ^= 1;
         if (threadIdx.x == 0) {
-            share.state[odd] = {at + t1 - t0, n, seq};
+            share.state[odd] = {at + (t1 < turns ? t1 : each) - t0, n, seq};
             share.unit = t0 == 0 ? (int64_t)n * units + u : -1;
             share.last_turn = at + turns - 1;
         }
@@ -724,115 +736,113 @@ __global__ void __launch_bounds__(kWarps * 32, mma_ctas(NT, K, V)) k_attend_mma(
 // ------------------------------------------------------------------ fp32
 
 // CTAs of k_attend_simt to an SM, and rows of a warp's tile.
-constexpr int simt_ctas(int ht) { return ht == 1 ? 4 : 3; }
+constexpr int simt_ctas(int HT, int K, int V) { return (HT == 1 ? 4 : 3) + (HT == 4 ? K + V < 256 : V == 64); }
 constexpr int simt_rows(int ht) { return ht == 8 ? 4 : 8; }
 
 // FFMA kernel (fp32): a unit has up to HT query heads, each warp R rows at a time, a
 // lane holding K / 32 and V / 32 channels of each row and of every head. The R HT scores are sums over the lanes: a
 // butterfly that halves the values with the lanes leaves value i, summed, in the lanes l with l % (R HT) == i.
-// 8 sequences of U[1,8000] rows, K = V = 128: 16 heads on 16 108 us (102 at a plain copy's rate), on 4 38 us (25), 32 on 4
-// 49 us (25): with four and eight heads the registers leave 48 KB of rows under way on an SM, too few.
-template <int K, int V, int HT, int R, bool SHARES>
-__global__ void __launch_bounds__(kWarps * 32, SHARES ? simt_ctas(HT) : 1) k_attend_simt(AttendArgs a) {
+// 8 sequences of U[1,8000] rows, K = V = 128: 16 heads on 16 99 us (102 at a plain copy's rate), on 4 32 us (25), 32 on
+// 4 49 us (25): with eight heads the scores' sums over the lanes take as many issue slots as the products, and 48 KB of
+// rows under way on an SM are too few to hide them.
+template <int K, int V, int HT, int R>
+__global__ void __launch_bounds__(kWarps * 32, simt_ctas(HT, K, V)) k_attend_simt(AttendArgs a) {
     constexpr int KL = K / 32, VL = V / 32, NV = R * HT;
     __shared__ Partial<HT, V> sm;
     const int lane = threadIdx.x % 32;
-    if (!SHARES && a.split == kCluster) cluster_started();
+    if (a.split == kCluster) cluster_started();
     after_previous();
-    Work<R, HT, SHARES> wk;
-    __shared__ typename Work<R, HT, SHARES>::Share share;
+    typedef Work<R, HT, false> Wk;
+    Wk wk;
+    __shared__ typename Wk::Share share;
+    if (!wk.start(a, share)) return;
+    const int h0 = wk.h0, heads = wk.heads, warp = wk.warp;
+    Rows<R>& rows = wk.rows;
+    float q[HT][KL], acc[HT][VL];
+#pragma unroll
+    for (int h = 0; h < HT; ++h) {
+#pragma unroll
+        for (int i = 0; i < KL; ++i)
+            q[h][i] = h < heads ? ((const float*)a.q)[(int64_t)wk.n * a.q_stride + (h0 + h) * K + lane * KL + i] : 0.f;
+#pragma unroll
+        for (int i = 0; i < VL; ++i) acc[h][i] = 0.f;
+    }
+    float m = -INFINITY, l = 0.f;  // of head lane % HT
+    const float* kh = (const float*)a.c.k + wk.hkv * a.c.k_head + lane * KL;
+    const float* vh = (const float*)a.c.v + wk.hkv * a.c.v_head + lane * VL;
+    float kr[R][KL], vr[R][VL];
+    auto load_k = [&]() {
+#pragma unroll
+        for (int r = 0; r < R; ++r) load_channels<KL>(kh + rows.k_of(r), rows.valid >> r & 1, kr[r]);
+    };
+    auto load_v = [&]() {
+#pragma unroll
+        for (int r = 0; r < R; ++r) load_channels<VL>(vh + rows.v_of(r), rows.valid >> r & 1, vr[r]);
+    };
+    rows.next(a);
+    load_k();
+    load_v();
 #pragma unroll 1
-    for (bool more = wk.start(a, share); more; more = wk.next(a, share)) {
-        const int h0 = wk.h0, heads = wk.heads, warp = wk.warp;
-        Rows<R>& rows = wk.rows;
-        float q[HT][KL], acc[HT][VL];
+    for (int left = wk.left; left > 0; left -= a.step) {
+        float s[NV];  // value r HT + h
 #pragma unroll
-        for (int h = 0; h < HT; ++h) {
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int i = 0; i < KL; ++i)
-                q[h][i] = h < heads ? ((const float*)a.q)[(int64_t)wk.n * a.q_stride + (h0 + h) * K + lane * KL + i] : 0.f;
+            for (int h = 0; h < HT; ++h) {
+                s[r * HT + h] = q[h][0] * kr[r][0];
 #pragma unroll
-            for (int i = 0; i < VL; ++i) acc[h][i] = 0.f;
-        }
-        float m = -INFINITY, l = 0.f;  // of head lane % HT
-        const float* kh = (const float*)a.c.k + wk.hkv * a.c.k_head + lane * KL;
-        const float* vh = (const float*)a.c.v + wk.hkv * a.c.v_head + lane * VL;
-        float kr[R][KL], vr[R][VL];
-        auto load_k = [&]() {
-#pragma unroll
-            for (int r = 0; r < R; ++r) load_channels<KL>(kh + rows.k_of(r), rows.valid >> r & 1, kr[r]);
-        };
-        auto load_v = [&]() {
-#pragma unroll
-            for (int r = 0; r < R; ++r) load_channels<VL>(vh + rows.v_of(r), rows.valid >> r & 1, vr[r]);
-        };
+                for (int i = 1; i < KL; ++i) s[r * HT + h] = fmaf(q[h][i], kr[r][i], s[r * HT + h]);
+            }
+        const bool in = rows.valid >> (lane % NV / HT) & 1;
         rows.next(a);
         load_k();
-        load_v();
-#pragma unroll 1
-        for (int left = wk.left; left > 0; left -= a.step) {
-            float s[NV];  // value r HT + h
 #pragma unroll
-            for (int r = 0; r < R; ++r)
+        for (int w = NV / 2; w > 0; w /= 2)
 #pragma unroll
-                for (int h = 0; h < HT; ++h) {
-                    s[r * HT + h] = q[h][0] * kr[r][0];
-#pragma unroll
-                    for (int i = 1; i < KL; ++i) s[r * HT + h] = fmaf(q[h][i], kr[r][i], s[r * HT + h]);
-                }
-            const bool in = rows.valid >> (lane % NV / HT) & 1;
-            rows.next(a);
-            load_k();
-#pragma unroll
-            for (int w = NV / 2; w > 0; w /= 2)
-#pragma unroll
-                for (int i = 0; i < w; ++i) {
-                    const float mine = lane & w ? s[i + w] : s[i], other = lane & w ? s[i] : s[i + w];
-                    s[i] = mine + __shfl_xor_sync(0xffffffffu, other, w);
-                }
-#pragma unroll
-            for (int w = NV; w < 32; w *= 2) s[0] += __shfl_xor_sync(0xffffffffu, s[0], w);
-            const float score = in ? s[0] * a.scale_log2 : -INFINITY;
-            if (__any_sync(0xffffffffu, score > m + kSlack)) {
-                float top = fmaxf(m, score);
-#pragma unroll
-                for (int w = HT; w < NV; w *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-                const float f = exp2f(m - finite_base(top));
-                m = top;
-                l *= f;
-#pragma unroll
-                for (int h = 0; h < HT; ++h) {
-                    const float fh = __shfl_sync(0xffffffffu, f, h);
-#pragma unroll
-                    for (int i = 0; i < VL; ++i) acc[h][i] *= fh;
-                }
+            for (int i = 0; i < w; ++i) {
+                const float mine = lane & w ? s[i + w] : s[i], other = lane & w ? s[i] : s[i + w];
+                s[i] = mine + __shfl_xor_sync(0xffffffffu, other, w);
             }
-            const float p = exp2f(score - finite_base(m));
-            l += p;
 #pragma unroll
-            for (int r = 0; r < R; ++r)
+        for (int w = NV; w < 32; w *= 2) s[0] += __shfl_xor_sync(0xffffffffu, s[0], w);
+        const float score = in ? s[0] * a.scale_log2 : -INFINITY;
+        if (__any_sync(0xffffffffu, score > m + kSlack)) {
+            float top = fmaxf(m, score);
 #pragma unroll
-                for (int h = 0; h < HT; ++h) {
-                    const float ph = __shfl_sync(0xffffffffu, p, r * HT + h);
+            for (int w = HT; w < NV; w *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+            const float f = exp2f(m - finite_base(top));
+            m = top;
+            l *= f;
 #pragma unroll
-                    for (int i = 0; i < VL; ++i) acc[h][i] = fmaf(ph, vr[r][i], acc[h][i]);
-                }
-            load_v();
+            for (int h = 0; h < HT; ++h) {
+                const float fh = __shfl_sync(0xffffffffu, f, h);
+#pragma unroll
+                for (int i = 0; i < VL; ++i) acc[h][i] *= fh;
+            }
         }
+        const float p = exp2f(score - finite_base(m));
+        l += p;
 #pragma unroll
-        for (int w = HT; w < NV; w *= 2) l += __shfl_xor_sync(0xffffffffu, l, w);
-        if (lane < HT) {
-            sm.m[warp][lane] = m;
-            sm.l[warp][lane] = l;
-        }
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int h = 0; h < HT; ++h)
+            for (int h = 0; h < HT; ++h) {
+                const float ph = __shfl_sync(0xffffffffu, p, r * HT + h);
 #pragma unroll
-            for (int i = 0; i < VL; ++i) ((float*)sm.acc[warp][h])[lane * VL + i] = acc[h][i];
-        join<float, V, HT, SHARES, Work<R, HT, SHARES>>(a, share, sm);
-        if constexpr (!SHARES) return;
-        __syncthreads();  // the shared memory is free for the next unit
+                for (int i = 0; i < VL; ++i) acc[h][i] = fmaf(ph, vr[r][i], acc[h][i]);
+            }
+        load_v();
     }
+#pragma unroll
+    for (int w = HT; w < NV; w *= 2) l += __shfl_xor_sync(0xffffffffu, l, w);
+    if (lane < HT) {
+        sm.m[warp][lane] = m;
+        sm.l[warp][lane] = l;
+    }
+#pragma unroll
+    for (int h = 0; h < HT; ++h)
+#pragma unroll
+        for (int i = 0; i < VL; ++i) ((float*)sm.acc[warp][h])[lane * VL + i] = acc[h][i];
+    join<float, V, HT, false, Wk>(a, share, sm);
 }
 
 // ------------------------------------------------------------------ launch
@@ -858,30 +868,58 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window) {
     if (window > 0 && window < rows) rows = window;
     const int64_t turns = rows > turn ? (rows + turn - 1) / turn : 1;  // of a unit
     const int64_t all = (int64_t)(N > 0 ? N : 1) * units;              // units
-    const int slots = 152 * (bf16 ? mma_ctas(ht / 8, c->K, c->V) : simt_ctas(ht));
-    const int slots_alone = !bf16 && ht == 1 && c->K + c->V == 128 ? 152 * 5 : slots;  // without kShares' registers
+    const int slots = 152 * (bf16 ? mma_ctas(ht / 8, c->K, c->V) : simt_ctas(ht, c->K, c->V));
     Plan p{kWhole, 1, ht, units, turn};
-    // What each costs, in turns (about 1.1 us). Over a CTA alone a cluster's join costs about one, the second kernel
-    // with its launch 2.2, and with kShares the lengths that are added up first and the ends of units within a share
-    // another 3.3. Clusters that do not all fit at once wait for room for a whole one. Where there are several sequences,
-    // shares are taken to be three quarters of what the longest that fits would give.
-    int cluster = 1;
-    while (cluster < kMaxCluster && cluster < turns &&
-           (all * cluster * 2 <= slots_alone || (all * cluster * 16 <= slots_alone * 9 && turns >= 8 * cluster)))
-        cluster *= 2;
-    const auto waves = [&](int64_t ctas) { return ctas > slots_alone ? (double)ctas / slots_alone : 1.0; };
-    const double whole = turns * waves(all);
-    const double clusters = 1 + (double)turns / cluster * (all * cluster > slots_alone ? 1.4 : 1.0);
-    const double shares = 5.5 + (double)turns * all * (N > 1 ? 0.75 : 1.0) / slots;
-    const int64_t parts = all <= slots ? (slots / all < turns ? slots / all : turns) : 1;
-    const double cut = parts > 1 ? 2.2 + (double)turns / parts : whole;
-    const double least = cut < shares ? cut : shares;
-    if (cluster > 1 && clusters < whole && clusters <= least) {
+    // What each split costs, in turns (0.6 to 0.9 us) of a CTA that takes all of its rows in turn: fitted to 1600 times
+    // of all splits. The CTAs of an SM start one after the other. Those that do not fit take the places of others that
+    // end: with lengths that differ, the sequences of a batch have about 0.7 of the rows of all as long as the longest
+    // that fits; with equal lengths the last wave takes almost as long as a full one. The cost is the mean of the two.
+    const double mean = N > 1 ? 0.7 : 1.0;
+    const auto begin = [&](int64_t ctas) { return (double)(ctas < slots ? ctas : slots) / 152; };
+    const auto queue = [&](int64_t ctas) {
+        const double x = (double)ctas / slots;
+        return x > 1 ? (1 + mean) / 2 * x + (1 - mean) / 2 + 0.4 * (ceil(x) - x) : 1.0;
+    };
+    double least = turns * queue(all) + begin(all);
+    // Clusters need room for all of their CTAs in one part of the GPU: of the SMs' room, clusters of 16 find 74 % (21 of
+    // 28 clusters; the next one waits for the others' end, 7.0 -> 11.3 us), of 8 89 %, of 4 96 %. (Few clusters of 4 may
+    // wait: a few per cent are gained with lengths that differ, 17.1 -> 15.5 us, and a quarter lost with equal ones.)
+    constexpr struct {
+        int ctas, room;
+        double join;
+    } clusters[] = {{2, 100, 1.2}, {4, 102, 1.2}, {8, 89, 1.7}, {16, 73, 2.4}};
+    for (const auto& x : clusters) {
+        if (all * x.ctas * 100 > (int64_t)slots * x.room || x.ctas >= 2 * turns) continue;
+        const double cost = x.join + (turns + x.ctas - 1) / x.ctas + begin(all * x.ctas);
+        if (cost >= least) continue;
+        least = cost;
         p.split = kCluster;
-        p.parts = cluster;
-    } else if (least < whole && turns * all < INT32_MAX) {
-        p.split = cut < shares ? kParts : kShares;
-        p.parts = p.split == kParts ? (int)parts : turns * all < 64 * slots ? slots : 2 * slots;
+        p.parts = x.ctas;
+    }
+    // Parts, and the second kernel: as many as fit. fp32, sequences of several lengths: `times` as many, so that others
+    // take the places of those that end early, which evens them out: T turns of a CTA become T (mean + (1 - mean) /
+    // times), and each time costs a start of 0.9. (152 sequences of U[1,16000], K = V = 128, five heads: 414 -> 266 us;
+    // of 16000: 465 -> 480.)
+    const double each_fit = (double)turns * all / slots;
+    const int times = bf16 || N <= 1 || each_fit < 12 ? 1 : each_fit > 192 ? 8 : (int)sqrt(each_fit / 3);
+    int64_t parts = (int64_t)slots * times / all;
+    if (parts > turns) parts = turns;
+    if (parts > 1) {
+        const int64_t each = (turns + parts - 1) / parts;
+        parts = (turns + each - 1) / each;
+        const double cost = 3.6 + each * queue(all * parts) + begin(all * parts);
+        if (cost < least) {
+            least = cost;
+            p.split = kParts;
+            p.parts = (int)parts;
+        }
+    }
+    // Shares add up the lengths first, and have the ends of units within them. With fp32 the loop over units costs
+    // registers, and 20 to 50 % of the time.
+    const double shares = 6.0 + mean * (turns + kUnitTurns) * all / slots + begin(slots);
+    if (bf16 && (turns + kUnitTurns) * all < INT32_MAX && shares < least) {
+        p.split = kShares;
+        p.parts = slots;
     }
     p.grid = p.split == kShares ? dim3(p.parts) : dim3(units * p.parts, N);
     p.ws_bytes = 256;
@@ -896,21 +934,20 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window) {
 
 typedef void (*Kernel)(AttendArgs);
 
-template <int K, int V, bool SHARES> Kernel kernel_of(bool bf16, int ht) {
-    if (bf16) return ht == 8 ? k_attend_mma<K, V, 1, SHARES> : k_attend_mma<K, V, 2, SHARES>;
-    return ht == 1   ? k_attend_simt<K, V, 1, simt_rows(1), SHARES>
-           : ht == 4 ? k_attend_simt<K, V, 4, simt_rows(4), SHARES>
-                     : k_attend_simt<K, V, 8, simt_rows(8), SHARES>;
-}
 template <int K, int V> Kernel kernel_of(bool bf16, int ht, Split split) {
-    return split == kShares ? kernel_of<K, V, true>(bf16, ht) : kernel_of<K, V, false>(bf16, ht);
+    if (bf16 && split == kShares) return ht == 8 ? k_attend_mma<K, V, 1, true> : k_attend_mma<K, V, 2, true>;
+    if (bf16) return ht == 8 ? k_attend_mma<K, V, 1, false> : k_attend_mma<K, V, 2, false>;
+    return ht == 1   ? k_attend_simt<K, V, 1, simt_rows(1)>
+           : ht == 4 ? k_attend_simt<K, V, 4, simt_rows(4)>
+                     : k_attend_simt<K, V, 8, simt_rows(8)>;
 }
 template <typename TI, int V, int HT, int VS, int G, int THREADS>
 cudaError_t launch_join(const AttendArgs& a, cudaStream_t st) {
     const int64_t threads = (int64_t)a.N * a.HQ * (V / 4) * G;
-    return launch_after(a.split == kShares ? k_attend_join<TI, V, HT, VS, G, THREADS, true>
-                                           : k_attend_join<TI, V, HT, VS, G, THREADS, false>,
-                        a, (unsigned)((threads + THREADS - 1) / THREADS), THREADS, st);
+    const unsigned grid = (unsigned)((threads + THREADS - 1) / THREADS);
+    if constexpr (sizeof(TI) == 2)
+        if (a.split == kShares) return launch_after(k_attend_join<TI, V, HT, VS, G, THREADS, true>, a, grid, THREADS, st);
+    return launch_after(k_attend_join<TI, V, HT, VS, G, THREADS, false>, a, grid, THREADS, st);
 }
 // `parts`: of a unit, with equal lengths. A batch of loads is to cover them.
 template <typename TI, int V, int HT> cudaError_t launch_join(const AttendArgs& a, int64_t parts, cudaStream_t st) {

@@ -16,9 +16,9 @@
 //     us, 256: 131, 512: 236. 3000 rows of 128 and 16 heads: 128 threads, 17.2 us;
 //     64 leave SMs half empty, and took half as long again.
 //   up to two rows an SM: 512 threads, one unit each. One token 2.1 us (64 threads:
-//     4.2), 128 tokens 3.0 us (7.2); 512 tokens already 4.5 (256 threads: 4.0).
+//     4.2), 128 tokens 2.6 us (7.2); 512 tokens already 4.5 (256 threads: 4.0).
 //   rows of 64 units or fewer share a CTA of 256 threads: 33,000 rows of two
-//     heads of 64 take 10.2 us, and 33.5 us with a CTA each (1 ns a CTA).
+//     heads of 64 take 11.9 us, and 33.5 us with a CTA each (1 ns a CTA).
 // Units that turn and units that are copied are separate loops, the copies two at a
 // time (the prompts without a rotation 139 -> 120 us, with half of each head turned
 // 169 -> 124); 24 CTAs of 64 threads fit an SM (40 registers; with 47: 126 us).
@@ -218,8 +218,8 @@ extern "C" kda_status kda_cache_append(const kda_cache* c, const void* k, int64_
     const int lanes = (int)((units + turns - 1) / turns), rows = few ? most / lanes : 1;
     const int threads = (lanes * rows + 31) / 32 * 32;
     const AppendArgs a{*c, k, v, q, q_out, k_stride, v_stride, q_stride, table_stride, HQ, N, (unsigned)R,
-                       (unsigned)(R / N), cu_seqlens, rope, rope_len, rope_dim, interleaved, page_table, kv_lens, max_pages,
-                       status, (unsigned)lanes, (unsigned)rows};
+                       (unsigned)(R / N), cu_seqlens, rope, rope_len, rope_dim, interleaved, page_table, kv_lens,
+                       max_pages, status, (unsigned)lanes, (unsigned)rows};
     cudaStream_t st = (cudaStream_t)stream;
     begin_launches(st);
     void (*const kernel)(AppendArgs) =

@@ -19,6 +19,8 @@ def lengths(gen, kind, N, longest):
         return [longest] * N
     if kind == "one long":
         return [longest if n == N // 2 else n % 3 for n in range(N)]
+    if kind == "mostly short":
+        return [longest if n % 20 == 7 else some[n] % 70 for n in range(N)]
     if kind == "empty":
         return [0] * N
     return [some[n] if n % 4 else 0 for n in range(N)]  # "gaps"
@@ -43,6 +45,8 @@ CASES = [
     ("cache_attend_shares", 130, 1500, "gaps", 16, 4, 128, 128, 13, 1400),
     ("cache_attend_shares", 64, 3000, "equal", 16, 4, 64, 64, 64, 0),
     ("cache_attend_shares", 90, 2500, "ragged", 32, 2, 128, 128, 32, 0),
+    ("cache_attend_shares", 200, 3000, "mostly short", 16, 4, 128, 128, 64, 0),
+    ("cache_attend_shares", 160, 4000, "mostly short", 40, 4, 64, 64, 20, 0),
 ]
 
 
