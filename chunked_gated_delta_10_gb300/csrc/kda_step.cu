@@ -21,7 +21,8 @@
 //     T = 7: 73 us (42). Tokens after the first cost sums alone, and what bounds
 //     those is the shared memory's return path: the factors of a row (k, q, e^g,
 //     and k again) come back 32 times, for every lane. So a lane takes two columns
-//     (N = 64, T = 7 with one: 95 to 115 us). Eight columns of all rows to a warp,
+//     (N = 64, T = 7 with one: 95 to 115 us; with four, two CTAs of 128 or 256
+//     threads an SM, 87 and 118: too few warps). Eight columns of all rows to a warp,
 //     without shared memory and barriers, took 100 us: each warp then forms the
 //     factors for itself.
 // Two rows are a pair of fp32 values (one instruction for both); the rows of a
