@@ -18,13 +18,15 @@
 //   N = 1, HV = 16: 1.9 us with 32 columns, 2.2 with 64: where 64 would leave SMs
 //     without a CTA, 32 are taken.
 //   N = 16, T = 4, HV = 32: 17.1 us (the states' traffic alone: 10.3); N = 64,
-//     T = 7: 73 us (42). Tokens after the first cost sums alone, and what bounds
-//     those is the shared memory's return path: the factors of a row (k, q, e^g,
-//     and k again) come back 32 times, for every lane. So a lane takes two columns
-//     (N = 64, T = 7 with one: 95 to 115 us; with four, two CTAs of 128 or 256
-//     threads an SM, 87 and 118: too few warps). Eight columns of all rows to a warp,
-//     without shared memory and barriers, took 100 us: each warp then forms the
-//     factors for itself.
+//     T = 7: 73 us (42). Tokens after the first cost sums alone: four operations
+//     for each element of a state, 3.6 us a token of the fp32 pipes for N = 64,
+//     where a token takes 4.7. With one column a lane the shared memory's return
+//     path came first (95 to 115 us): the factors of a row (k, q, e^g, and k
+//     again) come back 32 times, for every lane, so a lane takes two columns.
+//     Tried: four columns, two CTAs of 128 or 256 threads an SM, 87 and 118 us;
+//     eight columns of all rows to a warp, without shared memory and barriers, 100
+//     (each warp then forms the factors for itself); one barrier a token instead
+//     of two, with three sets of factors, 77 (T = 2: 48 against 50).
 // Two rows are a pair of fp32 values (one instruction for both); the rows of a
 // column are summed in the same order whatever T and the split are, so several
 // tokens at once give the bits of one after the other.
