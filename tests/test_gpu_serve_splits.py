@@ -19,6 +19,8 @@ def lengths(gen, kind, N, longest):
         return [longest] * N
     if kind == "one long":
         return [longest if n == N // 2 else n % 3 for n in range(N)]
+    if kind == "short":  # fewer turns in all than CTAs
+        return [x % 70 for x in some]
     if kind == "mostly short":
         return [longest if n % 20 == 7 else some[n] % 70 for n in range(N)]
     if kind == "empty":
@@ -47,6 +49,8 @@ CASES = [
     ("cache_attend_shares", 90, 2500, "ragged", 32, 2, 128, 128, 32, 0),
     ("cache_attend_shares", 200, 3000, "mostly short", 16, 4, 128, 128, 64, 0),
     ("cache_attend_shares", 160, 4000, "mostly short", 40, 4, 64, 64, 20, 0),
+    ("cache_attend_shares", 20, 16000, "short", 8, 2, 128, 128, 64, 0),
+    ("cache_attend_shares", 30, 20032, "short", 16, 1, 64, 64, 32, 0),
 ]
 
 
