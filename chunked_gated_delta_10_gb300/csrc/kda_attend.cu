@@ -552,7 +552,7 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     return *(const uint32_t*)&b;
 }
 // How far above the running maximum a score may lie (log2 units) before acc and l are rescaled: up to 2^8 is no loss
-// in fp32 or in a pair of bf16 values, and most tiles then only ask whether any score is higher.
+// in fp32 or in three bf16 values, and most tiles then only ask whether any score is higher.
 constexpr float kSlack = 8.f;
 
 // CTAs of k_attend_mma to an SM.
@@ -567,7 +567,11 @@ constexpr int mma_ctas(int NT, int K, int V) { return (K + V == 128 ? 5 : 3) - (
 //     contraction is free as long as Q has the same.
 //   - of V it loads unit g (and g + 8) of rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9; a byte permutation pairs the rows, and
 //     row i of the product is channel 8 (i % 8) + j of the j-th product.
-//   - P^T comes from S^T by an 8 x 8 transposition in registers; it is split into a pair of bf16 values (2^-16).
+//   - P^T comes from S^T by an 8 x 8 transposition in registers; it is split into three bf16 values, which hold the 24
+//     bits of fp32. (With two of them, 16 to 18 bits, 646 of the 262144 outputs of 64 sequences of U[1,8192] rows were not
+//     the exact result's rounding; with three 349, of elementary operations in fp32 225. The third product costs 0 to 3 %
+//     where memory is the bound, 10 % where a CTA's few turns are, 4000 rows 8.3 -> 9.1 us, and 12 % with 9 to 16 heads
+//     of K = V = 64.)
 // Groups of 9 to 16 heads take two such columns of heads (NT = 2) at two CTAs an SM: reading the rows twice instead
 // takes 80 us where this takes 50 (64 sequences of 8000 rows, 16 heads on one). K = V = 64 leaves registers for five CTAs
 // (40 sequences of U[1,8000] rows, 16 heads on 16: 111.6 us; with three, whose rows under way are too few, 120).
@@ -674,18 +678,22 @@ __global__ void __launch_bounds__(kWarps * 32, mma_ctas(NT, K, V)) k_attend_mma(
                         }
                     }
             }
-            uint32_t hi_p[NT][2], lo_p[NT][2];
+            uint32_t pt[NT][3][2];  // the parts of P^T
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const float b0 = finite_base(m[j][0]), b1 = finite_base(m[j][1]);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const float p0 = ex2(s[j][2 * r] - b0), p1 = ex2(s[j][2 * r + 1] - b1);
+                    float p0 = ex2(s[j][2 * r] - b0), p1 = ex2(s[j][2 * r + 1] - b1);
                     l[j][0] += p0;
                     l[j][1] += p1;
-                    const uint32_t h = pack(p0, p1);
-                    hi_p[j][r] = transpose8(h);
-                    lo_p[j][r] = transpose8(pack(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u)));
+#pragma unroll
+                    for (int c = 0; c < 3; ++c) {
+                        const uint32_t x = pack(p0, p1);
+                        pt[j][c][r] = transpose8(x);
+                        p0 -= __uint_as_float(x << 16);
+                        p1 -= __uint_as_float(x & 0xffff0000u);
+                    }
                 }
             }
 #pragma unroll
@@ -701,8 +709,8 @@ __global__ void __launch_bounds__(kWarps * 32, mma_ctas(NT, K, V)) k_attend_mma(
                 }
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    mma(acc[j][i], x[0], x[1], x[2], x[3], hi_p[j][0], hi_p[j][1]);
-                    mma(acc[j][i], x[0], x[1], x[2], x[3], lo_p[j][0], lo_p[j][1]);
+#pragma unroll
+                    for (int c = 0; c < 3; ++c) mma(acc[j][i], x[0], x[1], x[2], x[3], pt[j][c][0], pt[j][c][1]);
                 }
             }
             load_v();

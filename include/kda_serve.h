@@ -122,7 +122,9 @@ kda_status kda_cache_append(const kda_cache* cache, const void* k, int64_t k_str
  *   lse  fp32 [N, HQ], nullable: the natural log of the softmax's denominator
  * Where nothing is left to attend (kv_lens[n] <= 0, or every score is -inf)
  * o is 0 and lse is -inf. Rows outside the range are never read, whatever
- * they hold. Softmax statistics, products and sums are held in fp32 or better.
+ * they hold. Softmax statistics, weights and sums are held in fp32 (with a bf16
+ * cache the weights enter the products as three bf16 values that add up to
+ * them within 2^-22), and each output is rounded once.
  *   status  nullable: set where kv_lens[n] needs more than max_pages pages
  *     (only the rows of the table are attended) or a page is outside
  *     [0, num_pages) (its rows are left out).
