@@ -554,6 +554,10 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 // How far above the running maximum a score may lie (log2 units) before acc and l are rescaled: up to 2^8 is no loss
 // in fp32 or in three bf16 values, and most tiles then only ask whether any score is higher.
 constexpr float kSlack = 8.f;
+// The three parts of a weight above 0 are all above 0: the first two are cut off a little below what is left, not rounded.
+// A part of 0, or one of the other sign, would make a NaN of an infinite value of V. What is left for the third part
+// is less than 2^-13.8 of the weight, so rounding it loses 2^-22.8 at most.
+constexpr float kBelow = 1.f - 0x1p-12f;
 
 // CTAs of k_attend_mma to an SM.
 constexpr int mma_ctas(int NT, int K, int V) { return (K + V == 128 ? 5 : 3) - (NT - 1); }
@@ -688,12 +692,13 @@ __global__ void __launch_bounds__(kWarps * 32, mma_ctas(NT, K, V)) k_attend_mma(
                     l[j][0] += p0;
                     l[j][1] += p1;
 #pragma unroll
-                    for (int c = 0; c < 3; ++c) {
-                        const uint32_t x = pack(p0, p1);
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t x = __byte_perm(__float_as_uint(p0 * kBelow), __float_as_uint(p1 * kBelow), 0x7632);
                         pt[j][c][r] = transpose8(x);
                         p0 -= __uint_as_float(x << 16);
                         p1 -= __uint_as_float(x & 0xffff0000u);
                     }
+                    pt[j][2][r] = transpose8(pack(p0, p1));
                 }
             }
 #pragma unroll

@@ -1,4 +1,6 @@
-"""What attention of one token does with particular values: weights as precise as the sums."""
+"""What attention of one token does with particular values: weights as precise as the sums, infinite values."""
+import math
+
 import pytest
 import torch
 
@@ -31,3 +33,52 @@ def test_weights_are_as_precise_as_the_sums(kda, dtype):  # noqa: F811
     want, size = p1 * b - (1 - p1) * a, p1 * b + (1 - p1) * a
     rounding = (2.0 ** -8 if dtype == "bf16" else U) * want.abs()
     assert ((o.double().cpu() - want).abs() <= 2.0 ** -20 * size + 1.01 * rounding).all()
+
+
+def same_kind(got, ref, bound):
+    """Equal infinities and NaNs, and the finite values within the bound."""
+    got = got.double().cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    assert torch.equal(torch.isinf(got), torch.isinf(ref)) and torch.equal(got[torch.isinf(ref)], ref[torch.isinf(ref)])
+    some = torch.isfinite(ref)
+    assert ((got - ref).abs() <= bound)[some].all()
+
+
+# split of the bf16 kernel, N, rows, heads
+SPLITS = [("cache_attend", 300, 60, 4), ("cache_attend_cluster", 2, 900, 4), ("cache_attend_parts", 1, 9000, 2),
+          ("cache_attend_shares", 48, 3000, 8)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("split, N, L, H", SPLITS)
+def test_values_that_are_not_finite(kda, split, N, L, H, D, dtype):  # noqa: F811
+    """An infinite value makes its channel infinite, two of opposite sign or a NaN make it NaN, and the other channels
+    are what they are without them; at the row of the greatest weight as at the others."""
+    gen, dt = _gen(32), DT[dtype]
+    size, some = 20, 3
+    width = -(-L // size)
+    kc, vc = (torch.randn(some * width, size, H, D, generator=gen).to(dt) for _ in range(2))
+    table = (torch.arange(N)[:, None] % some * width + torch.arange(width)).to(torch.int32)
+    q = torch.randn(some, H, D, generator=gen).to(dt)
+    flat_k, flat_v = (t.view(some, width * size, H, D)[:, :L] for t in (kc, vc))
+    scores = torch.einsum("nhd,nthd->nht", q.double(), flat_k.double()) * D ** -0.5
+    top = scores.argmax(-1)
+    n, h = torch.meshgrid(torch.arange(some), torch.arange(H), indexing="ij")
+    flat_v[n, top, h, 3] = math.inf
+    flat_v[n, top, h, 5] = -math.inf
+    flat_v[n, (top + 7) % L, h, 17] = math.inf
+    flat_v[n, (top + L // 2) % L, h, D - 1] = -math.inf
+    flat_v[n, (top + 1) % L, h, 33] = math.nan
+    flat_v[n, top, h, 40], flat_v[n, (top + 3) % L, h, 40] = math.inf, -math.inf
+    got, _ = run_attend(kda, q[torch.arange(N) % some], kc, vc, table, [L] * N)
+    if dtype == "bf16":
+        assert kda.load().kda_launch_name(0).decode() == split
+    p = torch.softmax(scores, -1)
+    ref = torch.einsum("nht,nthd->nhd", p, flat_v.double())
+    # scores err by (K + 4) 2u sum |q k| scale, at most 24 here; the sums by 2 (L + 16) u
+    bound = (2 * 24 * (D + 4) * 2 * U + 2.0 ** -20 + 2 * (L + 16) * U) * torch.einsum(
+        "nht,nthd->nhd", p, flat_v.double().abs()) + 1.01 * (2.0 ** -8 if dtype == "bf16" else U) * ref.abs()
+    for i in range(min(N, 6)):
+        same_kind(got[i], ref[i % some], bound[i % some])
+    assert torch.equal(got[-1].isnan(), got[(N - 1) % some].isnan())
