@@ -78,6 +78,12 @@ __device__ __forceinline__ void kv_range(const AttendArgs& a, int64_t n, int& be
     begin = a.window > 0 && len > a.window ? (int)min(len - a.window, (int64_t)end) : 0;
 }
 
+// How far above the running maximum a score may lie (log2 units) before acc and l are rescaled, so that most tiles only
+// ask whether any score is higher. Weights, and sums of them, are held as 2^-8 of what they are relative to the maximum:
+// none is above one, so sums over large values overflow no earlier than relative to the true maximum. (A power of two
+// rounds nothing.)
+constexpr float kSlack = 8.f, kAtMostOne = 0x1p-8f;
+
 // The value that exponents are taken relative to: the maximum, or 0 where no score is above -inf, so that a
 // weight there is 2^-inf = 0 and a NaN score stays a NaN.
 __device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
@@ -356,7 +362,7 @@ __device__ __forceinline__ void write_result(const AttendArgs& a, int64_t at, in
     } else {
         *(float4*)o = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
     }
-    if (d == 0 && a.lse) a.lse[at] = (finite_base(m) + log2f(l)) * kLn2;
+    if (d == 0 && a.lse) a.lse[at] = (finite_base(m) + log2f(l / kAtMostOne)) * kLn2;
 }
 
 // The results of a CTA's warps for HT heads: maxima m, sums of weights l, and weighted sums acc relative to m. In a
@@ -551,9 +557,6 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *(const uint32_t*)&b;
 }
-// How far above the running maximum a score may lie (log2 units) before acc and l are rescaled: up to 2^8 is no loss
-// in fp32 or in three bf16 values, and most tiles then only ask whether any score is higher.
-constexpr float kSlack = 8.f;
 // The three parts of a weight above 0 are all above 0: the first two are cut off a little below what is left, not rounded.
 // A part of 0, or one of the other sign, would make a NaN of an infinite value of V. What is left for the third part
 // is less than 2^-13.8 of the weight, so rounding it loses 2^-22.8 at most.
@@ -688,7 +691,7 @@ __global__ void __launch_bounds__(kWarps * 32, mma_ctas(NT, K, V)) k_attend_mma(
                 const float b0 = finite_base(m[j][0]), b1 = finite_base(m[j][1]);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    float p0 = ex2(s[j][2 * r] - b0), p1 = ex2(s[j][2 * r + 1] - b1);
+                    float p0 = ex2(s[j][2 * r] - b0) * kAtMostOne, p1 = ex2(s[j][2 * r + 1] - b1) * kAtMostOne;
                     l[j][0] += p0;
                     l[j][1] += p1;
 #pragma unroll
@@ -833,7 +836,7 @@ __global__ void __launch_bounds__(kWarps * 32, simt_ctas(HT, K, V)) k_attend_sim
                 for (int i = 0; i < VL; ++i) acc[h][i] *= fh;
             }
         }
-        const float p = exp2f(score - finite_base(m));
+        const float p = ex2(score - finite_base(m)) * kAtMostOne;
         l += p;
 #pragma unroll
         for (int r = 0; r < R; ++r)

@@ -1,4 +1,4 @@
-"""What attention of one token does with particular values: weights as precise as the sums, infinite values."""
+"""What attention of one token does with particular values: weights as precise as the sums, infinite and very large values."""
 import math
 
 import pytest
@@ -82,3 +82,29 @@ def test_values_that_are_not_finite(kda, split, N, L, H, D, dtype):  # noqa: F81
     for i in range(min(N, 6)):
         same_kind(got[i], ref[i % some], bound[i % some])
     assert torch.equal(got[-1].isnan(), got[(N - 1) % some].isnan())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("split, N, L, H", SPLITS)
+def test_very_large_values(kda, split, N, L, H, dtype):  # noqa: F811
+    """Values of 2^127 whose row has the greatest weight, with scores that rise along the rows: the weighted mean is
+    finite and so is every sum of weights of at most one times them."""
+    gen, dt, D, size = _gen(33), DT[dtype], 64, 20
+    width = -(-L // size)
+    kc, vc = (torch.zeros(width, size, 1, D, dtype=dt) for _ in range(2))
+    flat_k, flat_v = (t.view(width * size, D)[:L] for t in (kc, vc))
+    flat_k[:, 0] = (torch.arange(L) / L * 5.0).to(dt)  # up to 7.2 in log2 units
+    q = torch.zeros(N, H, D, dtype=dt)
+    q[..., 0] = 1.0
+    s = flat_k[:, 0].double()
+    flat_v[int(s.argmax()), : D // 2] = 2.0 ** 127
+    flat_v[:, D // 2:] = torch.randn(L, D // 2, generator=gen).to(dt)
+    one = lambda t: t.expand(-1, -1, H, -1).contiguous()  # noqa: E731
+    o, lse = run_attend(kda, q, one(kc), one(vc), torch.arange(width, dtype=torch.int32).expand(N, -1), [L] * N, scale=1.0)
+    p = torch.softmax(s, 0)
+    want, mag = p @ flat_v.double(), p @ flat_v.double().abs()
+    w = 2 * 5 * 68 * 2 * U + 2.0 ** -20 + 2 * (L + 16) * U
+    o = o.double().cpu()
+    assert torch.isfinite(o).all()
+    assert ((o - want).abs() <= w * mag + 1.01 * (2.0 ** -8 if dtype == "bf16" else U) * want.abs()).all()
+    assert ((lse.double().cpu() - torch.logsumexp(s, 0)).abs() <= w + 4 * U * 15).all()
