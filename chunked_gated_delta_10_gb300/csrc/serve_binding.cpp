@@ -100,14 +100,6 @@ void* stream_of(at::Device dev) { return c10::cuda::getCurrentCUDAStream(dev.ind
 Tensor make(at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
     return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
-// A tensor on part of another's memory, `offset` bytes from its start.
-Tensor part_of(const Tensor& base, int64_t offset, at::IntArrayRef shape, at::ScalarType type) {
-    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(base.storage()), base.key_set(),
-                                                        c10::scalarTypeToTypeMeta(type));
-    t.unsafeGetTensorImpl()->set_storage_offset(offset / (int64_t)c10::elementSize(type));
-    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
-    return t;
-}
 
 // ------------------------------------------------------------------ kda_step
 
@@ -264,36 +256,30 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
             refuse("ws", "a contiguous uint8 tensor on the cache's device", &t);
         if ((size_t)t.numel() >= need) ws = t;
     }
-    // o, lse and a small workspace are one allocation (three cost 2 us more)
-    const int64_t shape[3] = {x.N, HQ, x.c.V}, heads = (int64_t)x.N * HQ, size = (int64_t)c10::elementSize(x.type);
-    const int64_t o_bytes = a[8] == Py_None ? heads * x.c.V * size : 0;
-    const int64_t lse_bytes = (heads * (int64_t)sizeof(float) + 15) / 16 * 16, ws_bytes = need <= 256 ? 256 : 0;
-    Tensor all = make({(o_bytes + lse_bytes + ws_bytes) / size}, x.type, x.dev);
-    char* base = (char*)all.data_ptr();
+    const int64_t shape[3] = {x.N, HQ, x.c.V};
     THPObjectPtr out, lse;
-    lse = THPVariable_Wrap(part_of(all, o_bytes, {shape, 2}, at::kFloat));
-    void* op = base;
     if (a[8] == Py_None) {
-        all.unsafeGetTensorImpl()->set_sizes_contiguous(shape);  // o is the allocation's beginning
-        out = THPVariable_Wrap(std::move(all));
+        out = THPVariable_Wrap(make(shape, x.type, x.dev));
     } else {
-        op = like(a[8], "out", shape, x.type, x.dev);
         Py_INCREF(a[8]);
         out = a[8];
     }
+    const Tensor sums = make({shape, 2}, at::kFloat, x.dev);
+    lse = THPVariable_Wrap(sums);
     if (!out || !lse) throw python_error();
-    void* wp = base + o_bytes + lse_bytes;
-    size_t room = ws_bytes;
+    void* op = like(out.get(), "out", shape, x.type, x.dev);
+    void* wp;
+    size_t room;
     if (ws.defined()) {
         wp = ws.data_ptr();
         room = ws.numel();
-    } else if (!ws_bytes) {  // (its memory is free again for what follows on this stream)
+    } else {  // (its memory is free again for what follows on this stream)
         scratch = c10::cuda::CUDACachingAllocator::get()->allocate(need);
         wp = scratch.get();
         room = need;
     }
     const kda_status s = kda_cache_attend(&x.c, q.p, q.stride, HQ, x.N, x.table, x.table_stride, x.width, x.lens, window,
-                                          scale, op, (float*)(base + o_bytes), (int32_t*)status, wp, room,
+                                          scale, op, (float*)sums.data_ptr(), (int32_t*)status, wp, room,
                                           stream_of(x.dev));
     return finish(s, PyTuple_Pack(2, out.get(), lse.get()));
     END_HANDLE_TH_ERRORS

@@ -1,0 +1,31 @@
+"""What the single-token calls return: tensors of their own, that live, are saved and are freed apart from each other."""
+import io
+
+import pytest
+import torch
+
+from tests.test_gpu_serve import _gen, kda  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("N, L", [(2, 50), (1, 9000)])  # without a workspace of the kernels' own, and with one
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_attend_outputs_are_tensors_of_their_own(kda, N, L, dtype):  # noqa: F811
+    gen = _gen(41)
+    width = -(-L // 16)
+    kc, vc = kda.new_cache(N * width, 16, 2, 64, 64, dtype=dtype)
+    table = torch.arange(N * width, dtype=torch.int32, device="cuda").view(N, width)
+    q = torch.randn(N, 4, 64, generator=gen).to(dtype).cuda()
+    lens = torch.full((N,), L, dtype=torch.int32, device="cuda")
+    own = torch.empty(N, 4, 64, dtype=dtype, device="cuda")
+    for out in (None, own):
+        o, lse = kda.cache_attend(q, kc, vc, table, lens, out=out)
+        assert o.untyped_storage().data_ptr() != lse.untyped_storage().data_ptr()
+        for t in (o, lse):
+            assert t.storage_offset() == 0 and t.untyped_storage().nbytes() == t.numel() * t.element_size()
+        file = io.BytesIO()
+        torch.save((o, lse), file)
+        file.seek(0)
+        again = torch.load(file)
+        assert torch.equal(again[0], o) and torch.equal(again[1], lse)
