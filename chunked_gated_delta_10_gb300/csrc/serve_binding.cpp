@@ -101,6 +101,15 @@ Tensor make(at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
     return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
 
+// Other Python threads run while this lives: allocations and launches may wait (for memory, for room in the queue of
+// launches), and what they wait for may need the interpreter.
+struct WithoutGil {
+    PyThreadState* state = PyEval_SaveThread();
+    WithoutGil() = default;
+    WithoutGil(const WithoutGil&) = delete;
+    ~WithoutGil() { PyEval_RestoreThread(state); }
+};
+
 // ------------------------------------------------------------------ kda_step
 
 // step(q, k, v, g, beta, state, scale, slots, out, status)
@@ -124,17 +133,20 @@ PyObject* step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* slots = like(a[7], "slots", {sv, 1}, at::kInt, dev, true);
     void* status = like(a[9], "status", {1}, at::kInt, dev, true);
     const c10::cuda::CUDAGuard guard(dev);
-    PyObject* out = a[8];
-    if (out == Py_None)
-        out = THPVariable_Wrap(make({sv, 4}, type, dev));
-    else
-        Py_INCREF(out);
-    if (!out) throw python_error();
-    THPObjectPtr held(out);
-    void* op = like(out, "out", sv, type, dev);
-    const kda_status s = kda_step(&d, qp, kp, vp, (const float*)gp, bp, (float*)sp, (const int32_t*)slots, op,
-                                  (int32_t*)status, stream_of(dev));
-    return finish(s, held.release());
+    const bool given = a[8] != Py_None;
+    void* op = given ? like(a[8], "out", sv, type, dev) : nullptr;
+    Tensor made;
+    kda_status s;
+    {
+        const WithoutGil others;
+        if (!given) {
+            made = make({sv, 4}, type, dev);
+            op = made.data_ptr();
+        }
+        s = kda_step(&d, qp, kp, vp, (const float*)gp, bp, (float*)sp, (const int32_t*)slots, op, (int32_t*)status,
+                     stream_of(dev));
+    }
+    return finish(s, given ? Py_NewRef(a[8]) : THPVariable_Wrap(std::move(made)));
     END_HANDLE_TH_ERRORS
 }
 
@@ -210,29 +222,30 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Rows q{nullptr, 0};
     int32_t HQ = 0;
     void* op = nullptr;
-    THPObjectPtr held;
+    const bool given = a[10] != Py_None;
+    int64_t shape[3] = {R, 0, x.c.K};
     if (a[6] != Py_None) {
         const Tensor& t = cuda_tensor(a[6], "q", 3);
         HQ = int32_of(t.size(1), "the number of query heads");
         q = rows_of(a[6], "q", R, HQ, x.c.K, x);
-        const int64_t shape[3] = {R, HQ, x.c.K};
-        if (a[10] == Py_None) {
-            held = THPVariable_Wrap(make(shape, x.type, x.dev));
-        } else {
-            Py_INCREF(a[10]);
-            held = a[10];
-        }
-        if (!held) throw python_error();
-        op = like(held.get(), "q_out", shape, x.type, x.dev);
-    } else {
-        if (a[10] != Py_None) refuse("q_out", "None where q is", nullptr);
-        Py_INCREF(Py_None);
-        held = Py_None;
+        shape[1] = HQ;
+        if (given) op = like(a[10], "q_out", shape, x.type, x.dev);
+    } else if (given) {
+        refuse("q_out", "None where q is", nullptr);
     }
-    const kda_status s = kda_cache_append(&x.c, k.p, k.stride, v.p, v.stride, q.p, q.stride, op, HQ, x.N, R,
-                                          (const int64_t*)cu, rope, positions, turned, inter, x.table, x.table_stride,
-                                          x.width, x.lens, (int32_t*)status, stream_of(x.dev));
-    return finish(s, held.release());
+    Tensor made;
+    kda_status s;
+    {
+        const WithoutGil others;
+        if (a[6] != Py_None && !given) {
+            made = make(shape, x.type, x.dev);
+            op = made.data_ptr();
+        }
+        s = kda_cache_append(&x.c, k.p, k.stride, v.p, v.stride, q.p, q.stride, op, HQ, x.N, R, (const int64_t*)cu, rope,
+                             positions, turned, inter, x.table, x.table_stride, x.width, x.lens, (int32_t*)status,
+                             stream_of(x.dev));
+    }
+    return finish(s, made.defined() ? THPVariable_Wrap(std::move(made)) : Py_NewRef(a[10]));  // (None without q)
     END_HANDLE_TH_ERRORS
 }
 
@@ -248,40 +261,41 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* status = like(a[9], "status", {1}, at::kInt, x.dev, true);
     const c10::cuda::CUDAGuard guard(x.dev);
     const size_t need = kda_cache_attend_workspace_bytes(&x.c, HQ, x.N, x.width, window);
-    Tensor ws;
-    c10::DataPtr scratch;
+    void* wp = nullptr;
+    size_t room = 0;
     if (a[7] != Py_None) {
         const Tensor& t = tensor(a[7], "ws");
         if (t.scalar_type() != at::kByte || t.device() != x.dev || !t.is_contiguous())
             refuse("ws", "a contiguous uint8 tensor on the cache's device", &t);
-        if ((size_t)t.numel() >= need) ws = t;
+        if ((size_t)t.numel() >= need) {
+            wp = t.data_ptr();
+            room = t.numel();
+        }
     }
     const int64_t shape[3] = {x.N, HQ, x.c.V};
-    THPObjectPtr out, lse;
-    if (a[8] == Py_None) {
-        out = THPVariable_Wrap(make(shape, x.type, x.dev));
-    } else {
-        Py_INCREF(a[8]);
-        out = a[8];
+    const bool given = a[8] != Py_None;
+    void* op = given ? like(a[8], "out", shape, x.type, x.dev) : nullptr;
+    Tensor made, lse;
+    kda_status s;
+    {
+        const WithoutGil others;
+        if (!given) {
+            made = make(shape, x.type, x.dev);
+            op = made.data_ptr();
+        }
+        lse = make({shape, 2}, at::kFloat, x.dev);
+        c10::DataPtr scratch;  // (its memory is free again for what follows on this stream)
+        if (!wp) {
+            scratch = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+            wp = scratch.get();
+            room = need;
+        }
+        s = kda_cache_attend(&x.c, q.p, q.stride, HQ, x.N, x.table, x.table_stride, x.width, x.lens, window, scale, op,
+                             (float*)lse.data_ptr(), (int32_t*)status, wp, room, stream_of(x.dev));
     }
-    const Tensor sums = make({shape, 2}, at::kFloat, x.dev);
-    lse = THPVariable_Wrap(sums);
-    if (!out || !lse) throw python_error();
-    void* op = like(out.get(), "out", shape, x.type, x.dev);
-    void* wp;
-    size_t room;
-    if (ws.defined()) {
-        wp = ws.data_ptr();
-        room = ws.numel();
-    } else {  // (its memory is free again for what follows on this stream)
-        scratch = c10::cuda::CUDACachingAllocator::get()->allocate(need);
-        wp = scratch.get();
-        room = need;
-    }
-    const kda_status s = kda_cache_attend(&x.c, q.p, q.stride, HQ, x.N, x.table, x.table_stride, x.width, x.lens, window,
-                                          scale, op, (float*)sums.data_ptr(), (int32_t*)status, wp, room,
-                                          stream_of(x.dev));
-    return finish(s, PyTuple_Pack(2, out.get(), lse.get()));
+    THPObjectPtr first(given ? Py_NewRef(a[8]) : THPVariable_Wrap(std::move(made))), second(THPVariable_Wrap(std::move(lse)));
+    if (!first || !second) throw python_error();
+    return finish(s, PyTuple_Pack(2, first.get(), second.get()));
     END_HANDLE_TH_ERRORS
 }
 
