@@ -97,8 +97,8 @@ __global__ void __launch_bounds__(MOST, SHORT ? 6 : MOST == 64 ? 24 : 2) k_appen
     const int heads = a.HQ + a.c.HKV, rot = a.rope_dim / E;  // query heads, then key heads; a head's units that turn
     // row r of head h, from channel `at` on: where it is, and where it goes (null: it is dropped)
     const auto from = [&](int h, int at) {
-        return h < a.HQ ? (const TI*)a.q + r * a.q_stride + h * a.c.K + at
-                        : (const TI*)a.k + r * a.k_stride + (h - a.HQ) * a.c.K + at;
+        return h < a.HQ ? (const TI*)a.q + r * a.q_stride + (int64_t)h * a.c.K + at
+                        : (const TI*)a.k + r * a.k_stride + (int64_t)(h - a.HQ) * a.c.K + at;
     };
     const auto to = [&](int h, int at) -> TI* {
         if (h < a.HQ) return (TI*)a.q_out + (r * a.HQ + h) * a.c.K + at;
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(MOST, SHORT ? 6 : MOST == 64 ? 24 : 2) k_appen
             } else if (j < copied && page >= 0) {
                 const int h = (j - of_heads) / uv, at = (j - of_heads - h * uv) * E;
                 dst[b] = (TI*)a.c.v + page * a.c.v_page + row * a.c.v_row + h * a.c.v_head + at;
-                x[b] = *(const uint4*)((const TI*)a.v + r * a.v_stride + h * a.c.V + at);
+                x[b] = *(const uint4*)((const TI*)a.v + r * a.v_stride + (int64_t)h * a.c.V + at);
             }
         }
 #pragma unroll
@@ -208,7 +208,8 @@ extern "C" kda_status kda_cache_append(const kda_cache* c, const void* k, int64_
     if (((uintptr_t)page_table & 3u) || ((uintptr_t)kv_lens & 3u) || ((uintptr_t)status & 3u) ||
         ((uintptr_t)cu_seqlens & 7u))
         return KDA_ERR_INVALID_ARG;
-    if (R > INT32_MAX || ((int64_t)HQ + 2 * (int64_t)c->HKV) * 32 > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    // (a row's units are counted in 32 bits, in steps of 1024 at most)
+    if (R > INT32_MAX || ((int64_t)HQ + 2 * (int64_t)c->HKV) * 32 > INT32_MAX - 1024) return KDA_ERR_UNSUPPORTED;
     const int64_t uk = (c->K - (interleaved ? 0 : rope_dim / 2)) / unit;
     const int64_t units = (HQ + c->HKV) * uk + c->HKV * (c->V / unit);  // of a row
     const bool few = units <= 64;

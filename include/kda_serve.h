@@ -101,7 +101,8 @@ typedef struct {
  *   status      nullable: set where a position needs a page beyond max_pages,
  *     a page outside [0, num_pages) or a rope row beyond rope_len; such a row
  *     is not appended and its q_out row is 0.
- * R == 0 is KDA_OK and launches nothing.
+ * R == 0 is KDA_OK and launches nothing. R is at most 2^31 - 1 and HQ + 2 HKV
+ * less than 2^26 - 32 (else KDA_ERR_UNSUPPORTED).
  * Errors: KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED before any launch;
  * KDA_ERR_CUDA if the launch fails.
  */
