@@ -23,6 +23,7 @@
 // all of its CTAs); shares of the rows alone, without a weight for a unit's ends
 // (160 us for the first of these); the sequences of a batch side by side instead of
 // a sequence's heads, which share its pages (fp32, 12 sequences: 15.7 against 13.6).
+#include "../../include/kda_selftest.h"
 #include "kda_cache.cuh"
 
 namespace kda {
@@ -898,12 +899,14 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window) {
     };
     double least = turns * queue(all) + begin(all);
     // Clusters need room for all of their CTAs in one part of the GPU: of the SMs' room, clusters of 16 find 74 % (21 of
-    // 28 clusters; the next one waits for the others' end, 7.0 -> 11.3 us), of 8 89 %, of 4 96 %. (Few clusters of 4 may
-    // wait: a few per cent are gained with lengths that differ, 17.1 -> 15.5 us, and a quarter lost with equal ones.)
+    // 28 clusters; the next one waits for the others' end, 7.0 -> 11.3 us), of 8 89 %, of 4 96 % (109 clusters in 456
+    // places; 110 take 26.0 instead of 22.9 us, 111 31.5, where parts take 24.1. In 608 and 760 places 97 % are found).
+    // None is to wait: that gains up to a quarter where lengths differ, and costs as much where they are equal (192
+    // units, fp32, K = V = 64, of U[1,1500] and of 1500 rows with a window of 1024: 14.5 and 24.6 us; parts 16.4, 19.2).
     constexpr struct {
         int ctas, room;
         double join;
-    } clusters[] = {{2, 100, 1.2}, {4, 102, 1.2}, {8, 89, 1.7}, {16, 73, 2.4}};
+    } clusters[] = {{2, 100, 1.2}, {4, 96, 1.2}, {8, 89, 1.7}, {16, 73, 2.4}};
     for (const auto& x : clusters) {
         if (all * x.ctas * 100 > (int64_t)slots * x.room || x.ctas >= 2 * turns) continue;
         const double cost = x.join + (turns + x.ctas - 1) / x.ctas + begin(all * x.ctas);
@@ -966,9 +969,11 @@ cudaError_t launch_join(const AttendArgs& a, cudaStream_t st) {
     return launch_after(k_attend_join<TI, V, HT, VS, G, THREADS, false>, a, grid, THREADS, st);
 }
 // `parts`: of a unit, with equal lengths. A batch of loads is to cover them.
+int join_groups(int64_t parts) { return parts <= kJoinBatch ? 1 : parts <= 4 * kJoinBatch ? 4 : 32; }
 template <typename TI, int V, int HT> cudaError_t launch_join(const AttendArgs& a, int64_t parts, cudaStream_t st) {
-    if (parts <= kJoinBatch) return launch_join<TI, V, HT, V, 1, 128>(a, st);
-    if (parts <= 4 * kJoinBatch) return launch_join<TI, V, HT, V, 4, 128>(a, st);
+    const int groups = join_groups(parts);
+    if (groups == 1) return launch_join<TI, V, HT, V, 1, 128>(a, st);
+    if (groups == 4) return launch_join<TI, V, HT, V, 4, 128>(a, st);
     return launch_join<TI, V, HT, 32, 32, 256>(a, st);
 }
 template <int V> cudaError_t launch_join(const AttendArgs& a, bool bf16, int ht, int64_t parts, cudaStream_t st) {
@@ -977,6 +982,11 @@ template <int V> cudaError_t launch_join(const AttendArgs& a, bool bf16, int ht,
     return ht == 1   ? launch_join<float, V, 1>(a, parts, st)
            : ht == 4 ? launch_join<float, V, 4>(a, parts, st)
                      : launch_join<float, V, 8>(a, parts, st);
+}
+
+// Parts of a unit, with equal lengths (kParts, kShares).
+int64_t unit_parts(const Plan& p, int N) {
+    return p.split == kParts ? p.parts : p.parts / ((int64_t)(N > 0 ? N : 1) * p.units) + 2;
 }
 
 cudaError_t launch_attend(const AttendArgs& a, const Plan& p, cudaStream_t st) {
@@ -991,8 +1001,7 @@ cudaError_t launch_attend(const AttendArgs& a, const Plan& p, cudaStream_t st) {
                                         "cache_attend_shares"};
     note_launch(names[p.split], st);
     if (p.split < kParts) return cudaSuccess;
-    // of a unit, with equal lengths
-    const int64_t parts = p.split == kParts ? p.parts : p.parts / ((int64_t)a.N * p.units) + 2;
+    const int64_t parts = unit_parts(p, a.N);
     e = V == 128 ? launch_join<128>(a, bf16, p.ht, parts, st) : launch_join<64>(a, bf16, p.ht, parts, st);
     if (e != cudaSuccess) return e;
     note_launch("cache_attend_join", st);
@@ -1017,6 +1026,19 @@ extern "C" size_t kda_cache_attend_workspace_bytes(const kda_cache* c, int32_t H
                                                    int32_t window) {
     if (check_sizes(c, HQ, N, max_pages, window) != KDA_OK) return 0;
     return plan_of(c, HQ, N, max_pages, window).ws_bytes;
+}
+
+extern "C" kda_status kda_debug_attend_plan(const kda_cache* c, int32_t HQ, int32_t N, int32_t max_pages, int32_t window,
+                                            int32_t* plan) {
+    const kda_status s = check_sizes(c, HQ, N, max_pages, window);
+    if (s != KDA_OK) return s;
+    if (!plan) return KDA_ERR_INVALID_ARG;
+    const Plan p = plan_of(c, HQ, N, max_pages, window);
+    plan[0] = p.split;
+    plan[1] = p.parts;
+    plan[2] = p.split < kParts ? 0 : join_groups(unit_parts(p, N));
+    plan[3] = p.units * (N > 0 ? N : 1);
+    return KDA_OK;
 }
 
 extern "C" kda_status kda_cache_attend(const kda_cache* c, const void* q, int64_t q_stride, int32_t HQ, int32_t N,

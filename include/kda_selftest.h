@@ -13,6 +13,7 @@
 #include <stdint.h>
 
 #include "kda.h"
+#include "kda_serve.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -56,6 +57,17 @@ kda_status kda_debug_bwd_stages(const kda_dims* dims, const void* q, const void*
  * library's tile layout; "egc" is fp32). KDA_ERR_UNSUPPORTED off that path.
  */
 kda_status kda_debug_ws_region(const kda_dims* dims, int32_t pass, const char* name, size_t* offset, size_t* bytes);
+
+/*
+ * How kda_cache_attend gives these sizes' rows to CTAs: plan[0] 0: a CTA a
+ * unit (a sequence, a cache head and a tile of its query heads), 1: a cluster
+ * of plan[1] CTAs a unit, 2: plan[1] parts a unit and a second kernel that
+ * joins them, 3: shares of plan[1] CTAs, and that kernel; plan[2]: the groups
+ * that join a unit's parts (0: no second kernel); plan[3]: units. Errors as
+ * kda_cache_attend_workspace_bytes has them. Launches nothing.
+ */
+kda_status kda_debug_attend_plan(const kda_cache* cache, int32_t HQ, int32_t N, int32_t max_pages, int32_t window,
+                                 int32_t plan[4]);
 
 #ifdef __cplusplus
 }
