@@ -877,7 +877,11 @@ struct Plan {
     dim3 grid;
     size_t acc_bytes, ml_bytes, ws_bytes;  // of the workspace
 };
-Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window) {
+// What a plan goes by besides the sizes: the device's SMs, and the largest cluster that the kernel can be placed in.
+struct Gpu {
+    int sms, cluster;
+};
+Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window, const Gpu& gpu) {
     const bool bf16 = c->dtype == KDA_DTYPE_BF16;
     const int group = HQ / c->HKV, ht = head_tile(c, HQ), units = c->HKV * ((group + ht - 1) / ht);
     const int turn = kWarps * (bf16 ? 16 : simt_rows(ht));
@@ -885,14 +889,14 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window) {
     if (window > 0 && window < rows) rows = window;
     const int64_t turns = rows > turn ? (rows + turn - 1) / turn : 1;  // of a unit
     const int64_t all = (int64_t)(N > 0 ? N : 1) * units;              // units
-    const int slots = 152 * (bf16 ? mma_ctas(ht / 8, c->K, c->V) : simt_ctas(ht, c->K, c->V));
+    const int slots = gpu.sms * (bf16 ? mma_ctas(ht / 8, c->K, c->V) : simt_ctas(ht, c->K, c->V));
     Plan p{kWhole, 1, ht, units, turn};
     // What each split costs, in turns (0.6 to 0.9 us) of a CTA that takes all of its rows in turn: fitted to 1600 times
     // of all splits. The CTAs of an SM start one after the other. Those that do not fit take the places of others that
     // end: with lengths that differ, the sequences of a batch have about 0.7 of the rows of all as long as the longest
     // that fits; with equal lengths the last wave takes almost as long as a full one. The cost is the mean of the two.
     const double mean = N > 1 ? 0.7 : 1.0;
-    const auto begin = [&](int64_t ctas) { return (double)(ctas < slots ? ctas : slots) / 152; };
+    const auto begin = [&](int64_t ctas) { return (double)(ctas < slots ? ctas : slots) / gpu.sms; };
     const auto queue = [&](int64_t ctas) {
         const double x = (double)ctas / slots;
         return x > 1 ? (1 + mean) / 2 * x + (1 - mean) / 2 + 0.4 * (ceil(x) - x) : 1.0;
@@ -908,7 +912,7 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window) {
         double join;
     } clusters[] = {{2, 100, 1.2}, {4, 96, 1.2}, {8, 89, 1.7}, {16, 73, 2.4}};
     for (const auto& x : clusters) {
-        if (all * x.ctas * 100 > (int64_t)slots * x.room || x.ctas >= 2 * turns) continue;
+        if (all * x.ctas * 100 > (int64_t)slots * x.room || x.ctas >= 2 * turns || x.ctas > gpu.cluster) continue;
         const double cost = x.join + (turns + x.ctas - 1) / x.ctas + begin(all * x.ctas);
         if (cost >= least) continue;
         least = cost;
@@ -960,6 +964,21 @@ template <int K, int V> Kernel kernel_of(bool bf16, int ht, Split split) {
            : ht == 4 ? k_attend_simt<K, V, 4, simt_rows(4)>
                      : k_attend_simt<K, V, 8, simt_rows(8)>;
 }
+Kernel kernel_of(const kda_cache& c, int ht, Split split) {
+    const bool bf16 = c.dtype == KDA_DTYPE_BF16;
+    return c.K == 128 ? (c.V == 128 ? kernel_of<128, 128>(bf16, ht, split) : kernel_of<128, 64>(bf16, ht, split))
+                      : (c.V == 128 ? kernel_of<64, 128>(bf16, ht, split) : kernel_of<64, 64>(bf16, ht, split));
+}
+// The present device and what it can do with the kernel for these sizes; without a device, what a GB300 can. A part of
+// a GPU may have fewer SMs, and none of its processing clusters 16 of them.
+Gpu gpu_for(const kda_cache* c, int HQ) {
+    static std::atomic<int> known[5][2][2][kDevices];
+    const int ht = head_tile(c, HQ);
+    const int tile = c->dtype == KDA_DTYPE_BF16 ? ht / 16 : ht == 1 ? 2 : ht == 4 ? 3 : 4;
+    return {sm_count(), largest_cluster((const void*)kernel_of(*c, ht, kCluster), kWarps * 32, kMaxCluster,
+                                        known[tile][c->K / 128][c->V / 128])};
+}
+
 template <typename TI, int V, int HT, int VS, int G, int THREADS>
 cudaError_t launch_join(const AttendArgs& a, cudaStream_t st) {
     const int64_t threads = (int64_t)a.N * a.HQ * (V / 4) * G;
@@ -991,11 +1010,8 @@ int64_t unit_parts(const Plan& p, int N) {
 
 cudaError_t launch_attend(const AttendArgs& a, const Plan& p, cudaStream_t st) {
     const bool bf16 = a.c.dtype == KDA_DTYPE_BF16;
-    const int K = a.c.K, V = a.c.V;
-    const Kernel kernel =
-        K == 128 ? (V == 128 ? kernel_of<128, 128>(bf16, p.ht, p.split) : kernel_of<128, 64>(bf16, p.ht, p.split))
-                 : (V == 128 ? kernel_of<64, 128>(bf16, p.ht, p.split) : kernel_of<64, 64>(bf16, p.ht, p.split));
-    cudaError_t e = launch_after(kernel, a, p.grid, kWarps * 32, st, p.split == kCluster ? p.parts : 1);
+    const int V = a.c.V;
+    cudaError_t e = launch_after(kernel_of(a.c, p.ht, p.split), a, p.grid, kWarps * 32, st, p.split == kCluster ? p.parts : 1);
     if (e != cudaSuccess) return e;
     static const char* const names[] = {"cache_attend", "cache_attend_cluster", "cache_attend_parts",
                                         "cache_attend_shares"};
@@ -1025,15 +1041,16 @@ using namespace kda;
 extern "C" size_t kda_cache_attend_workspace_bytes(const kda_cache* c, int32_t HQ, int32_t N, int32_t max_pages,
                                                    int32_t window) {
     if (check_sizes(c, HQ, N, max_pages, window) != KDA_OK) return 0;
-    return plan_of(c, HQ, N, max_pages, window).ws_bytes;
+    return plan_of(c, HQ, N, max_pages, window, gpu_for(c, HQ)).ws_bytes;
 }
 
 extern "C" kda_status kda_debug_attend_plan(const kda_cache* c, int32_t HQ, int32_t N, int32_t max_pages, int32_t window,
-                                            int32_t* plan) {
+                                            int32_t sms, int32_t cluster, int32_t* plan) {
     const kda_status s = check_sizes(c, HQ, N, max_pages, window);
     if (s != KDA_OK) return s;
     if (!plan) return KDA_ERR_INVALID_ARG;
-    const Plan p = plan_of(c, HQ, N, max_pages, window);
+    const Gpu gpu = sms > 0 ? Gpu{sms, cluster} : gpu_for(c, HQ);
+    const Plan p = plan_of(c, HQ, N, max_pages, window, gpu);
     plan[0] = p.split;
     plan[1] = p.parts;
     plan[2] = p.split < kParts ? 0 : join_groups(unit_parts(p, N));
@@ -1054,7 +1071,7 @@ extern "C" kda_status kda_cache_attend(const kda_cache* c, const void* q, int64_
     if (!aligned16(q) || !aligned16(o) || ((uintptr_t)lse & 3u) || ((uintptr_t)page_table & 3u) ||
         ((uintptr_t)kv_lens & 3u) || ((uintptr_t)status & 3u))
         return KDA_ERR_INVALID_ARG;
-    const Plan plan = plan_of(c, HQ, N, max_pages, window);
+    const Plan plan = plan_of(c, HQ, N, max_pages, window, gpu_for(c, HQ));
     if (!ws || !aligned16(ws) || ws_bytes < plan.ws_bytes) return KDA_ERR_WORKSPACE;
     char* w = (char*)ws;
     const int step = plan.turn * (plan.split == kShares ? 1 : plan.parts);

@@ -213,8 +213,9 @@ extern "C" kda_status kda_cache_append(const kda_cache* c, const void* k, int64_
     const int64_t uk = (c->K - (interleaved ? 0 : rope_dim / 2)) / unit;
     const int64_t units = (HQ + c->HKV) * uk + c->HKV * (c->V / unit);  // of a row
     const bool few = units <= 64;
-    int most = few ? 256 : R <= 2 * 152 ? 512 : 64;  // threads of a CTA; measured: see the top of this file
-    while (most < 256 && R * most < 152 * 2048) most *= 2;
+    const int sms = sm_count();
+    int most = few ? 256 : R <= 2 * sms ? 512 : 64;  // threads of a CTA; measured: see the top of this file
+    while (most < 256 && R * most < sms * (int64_t)2048) most *= 2;
     const int64_t turns = (units + most - 1) / most;
     const int lanes = (int)((units + turns - 1) / turns), rows = few ? most / lanes : 1;
     const int threads = (lanes * rows + 31) / 32 * 32;

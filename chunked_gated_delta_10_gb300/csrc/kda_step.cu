@@ -273,7 +273,7 @@ extern "C" kda_status kda_step(const kda_step_dims* d, const void* q, const void
     StepArgs a{q, k, v, beta, g, state, slots, o, status, d->N, d->T, d->H, d->HV, d->num_slots, d->scale};
     cudaStream_t st = (cudaStream_t)stream;
     begin_launches(st);
-    const int C = (int64_t)d->N * d->HV * (d->V / 64) >= 152 ? 2 : 1;
+    const int C = (int64_t)d->N * d->HV * (d->V / 64) >= sm_count() ? 2 : 1;
     const auto kernel = d->dtype == KDA_DTYPE_BF16 ? kernel_of<__nv_bfloat16>(d->K, d->V, d->T, C)
                                                    : kernel_of<float>(d->K, d->V, d->T, C);
     const cudaError_t e = launch_after(kernel, a, (unsigned)(d->N * d->HV * (d->V / (32 * C))), kThreads, st);

@@ -6,7 +6,43 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 namespace kda {
+
+// What is asked of a device once and kept, by its number: a whole launch takes 1.6 us.
+constexpr int kDevices = 32;
+constexpr int kGb300Sms = 152;
+
+// SMs of the present device; without one, those of a GB300.
+inline int sm_count() {
+    static std::atomic<int> known[kDevices];
+    int device, n = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return kGb300Sms;
+    if (device < kDevices && (n = known[device].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n <= 0) return kGb300Sms;
+    if (device < kDevices) known[device].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// The largest cluster, of at most `most` CTAs, that the present device can place the kernel in (without one: `most`).
+// `known` is the kernel's own.
+inline int largest_cluster(const void* kernel, int threads, int most, std::atomic<int> (&known)[kDevices]) {
+    int device, n = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return most;
+    if (device < kDevices && (n = known[device].load(std::memory_order_relaxed)) > 0) return n;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(most);
+    cfg.blockDim = dim3(threads);
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaOccupancyMaxPotentialClusterSize(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = 1;
+    }
+    if (n > most) n = most;
+    if (device < kDevices) known[device].store(n, std::memory_order_relaxed);
+    return n;
+}
 
 // Every thread of a kernel launched by launch_after calls this first, whatever it does then: a kernel that ended
 // without having waited would let the one after it start before the one before it has ended.
@@ -15,6 +51,7 @@ __device__ __forceinline__ void after_previous() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// A cluster of more than 8 CTAs is one that largest_cluster allowed on this device.
 template <typename Args>
 cudaError_t launch_after(void (*kernel)(Args), const Args& a, dim3 grid, int threads, cudaStream_t st,
                          int cluster = 1) {
@@ -32,19 +69,6 @@ cudaError_t launch_after(void (*kernel)(Args), const Args& a, dim3 grid, int thr
         attr[1].val.clusterDim.x = cluster;
         attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
         cfg.numAttrs = 2;
-    }
-    if (cluster > 8) {  // (the attribute stays with the kernel on its device: set it again only where that may differ)
-        thread_local const void* set_for = nullptr;
-        thread_local int set_on = -1;
-        int device;
-        cudaError_t e = cudaGetDevice(&device);
-        if (e != cudaSuccess) return e;
-        if (set_for != (const void*)kernel || set_on != device) {
-            e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (e != cudaSuccess) return e;
-            set_for = (const void*)kernel;
-            set_on = device;
-        }
     }
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }

@@ -63,11 +63,13 @@ kda_status kda_debug_ws_region(const kda_dims* dims, int32_t pass, const char* n
  * unit (a sequence, a cache head and a tile of its query heads), 1: a cluster
  * of plan[1] CTAs a unit, 2: plan[1] parts a unit and a second kernel that
  * joins them, 3: shares of plan[1] CTAs, and that kernel; plan[2]: the groups
- * that join a unit's parts (0: no second kernel); plan[3]: units. Errors as
- * kda_cache_attend_workspace_bytes has them. Launches nothing.
+ * that join a unit's parts (0: no second kernel); plan[3]: units. On a device
+ * of `sms` SMs that places clusters of at most `cluster` CTAs (sms 0: on the
+ * present device). Errors are those of kda_cache_attend's sizes. Launches
+ * nothing.
  */
 kda_status kda_debug_attend_plan(const kda_cache* cache, int32_t HQ, int32_t N, int32_t max_pages, int32_t window,
-                                 int32_t plan[4]);
+                                 int32_t sms, int32_t cluster, int32_t plan[4]);
 
 #ifdef __cplusplus
 }
