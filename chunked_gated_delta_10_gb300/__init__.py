@@ -337,6 +337,9 @@ def _serve():
     global _serve_module
     if _serve_module is None:
         load()
+        if not os.path.exists(SERVE):
+            raise RuntimeError(f"KDA single-token module not built ({SERVE}); call chunked_gated_delta_10_gb300.build() with "
+                               "a PyTorch with CUDA and Python's headers")
         spec = importlib.util.spec_from_file_location("_kda_serve", SERVE)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

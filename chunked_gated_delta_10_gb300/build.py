@@ -6,7 +6,9 @@ library has a plain C ABI (``include/kda.h``, ``include/kda_serve.h``) and links
 only the static CUDA runtime (TMA descriptors are encoded through the driver
 entry point obtained at run time, so libcuda is not linked). Beside it
 ``lib/_kda_serve.so``: the Python module of the single-token operators, compiled
-against PyTorch's headers (``csrc/serve_binding.cpp``).
+against PyTorch's headers (``csrc/serve_binding.cpp``). Where those or Python's are
+not there (a PyTorch without CUDA, no ``Python.h``) it is left out, with a warning:
+the library is built and the chunked operators run all the same.
 """
 from __future__ import annotations
 
@@ -15,9 +17,9 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
-
-import torch
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -55,8 +57,31 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _read(path):
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
+def _serve_missing():
+    """What the Python module of the single-token operators cannot be compiled without and is not there, or None."""
+    import torch
+
+    if torch.version.cuda is None:
+        return "a PyTorch with CUDA"
+    for path in (os.path.join(sysconfig.get_paths()["include"], "Python.h"),
+                 os.path.join(os.path.dirname(os.path.abspath(torch.__file__)), "include", "ATen", "cuda", "EmptyTensor.h")):
+        if not os.path.exists(path):
+            return path
+    return None
+
+
 def _serve_commands(nvcc, obj):
     """Compile and link commands of the Python module of the single-token operators."""
+    import torch
+
     top = os.path.dirname(os.path.abspath(torch.__file__))
     include = [os.path.join(top, "include"), os.path.join(top, "include", "torch", "csrc", "api", "include"),
                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include"),
@@ -67,6 +92,13 @@ def _serve_commands(nvcc, obj):
     link = [cxx, "-shared", obj, LIB, "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(top, "lib"), "-ltorch_python", "-ltorch",
             "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10"]
     return compile_, link
+
+
+def _serve_made_by(commands):
+    """What the module depends on besides its files: an object for another PyTorch or Python does not load, or worse."""
+    import torch
+
+    return "\n".join([torch.__version__, torch.__file__, sys.version, *(" ".join(c) for c in commands)])
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -84,9 +116,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             cmd = [nvcc, *ARCH, *NVCC_FLAGS, *extra_flags, "-c", src, "-o", obj]
             jobs.append(cmd)
     serve_obj = os.path.join(OBJ, "serve_binding.o")
-    compile_serve, link_serve = _serve_commands(nvcc, serve_obj)
-    if force or _stale(serve_obj, [SERVE_SRC] + headers):
-        jobs.insert(0, compile_serve)
+    missing = _serve_missing()
+    if missing:
+        warnings.warn(f"{missing} is missing: {os.path.basename(SERVE)}, the Python module of the single-token operators, is "
+                      "not built")
+        if os.path.exists(SERVE):
+            os.remove(SERVE)  # (another PyTorch's)
+    else:
+        compile_serve, link_serve = _serve_commands(nvcc, serve_obj)
+        made_by, record = _serve_made_by([compile_serve, link_serve]), serve_obj + ".made_by"
+        new = force or _stale(serve_obj, [SERVE_SRC] + headers) or _read(record) != made_by
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -97,21 +136,24 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr)
         return r
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
+        serve = ex.submit(run, compile_serve) if not missing and new else None
         list(ex.map(run, jobs))
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-Xlinker", "-soname=" + os.path.basename(LIB), "-o", tmp, *objs, "-lcudart_static",
              "-lrt", "-ldl", "-lpthread"])
         os.replace(tmp, LIB)
-    if force or _stale(SERVE, [serve_obj, LIB]):
+    if serve:
+        serve.result()  # (raises if it did not compile; the library is there by now)
+    if not missing and (new or _stale(SERVE, [serve_obj, LIB])):
         tmp = SERVE + f".tmp{os.getpid()}"
         run([*link_serve, "-o", tmp])
         os.replace(tmp, SERVE)
+        with open(record, "w") as f:
+            f.write(made_by)
     return LIB
 
 
 if __name__ == "__main__":
-    import sys
-
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
