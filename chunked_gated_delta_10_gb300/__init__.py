@@ -23,8 +23,8 @@ import torch
 from .build import LIB, SERVE, build  # noqa: F401
 
 __all__ = ["build", "load", "Dims", "prepare_chunks", "workspace_bytes", "saved_bytes", "chunk_fwd", "chunk_bwd",
-           "chunk_fwd_save", "chunk_bwd_from_saved", "step", "new_cache", "cache_append", "cache_attend", "KdaError",
-           "STATUS", "DTYPE_BF16", "DTYPE_F32", "PASS_FWD", "PASS_BWD"]
+           "chunk_fwd_save", "chunk_bwd_from_saved", "step", "new_cache", "cache_append", "cache_attend",
+           "cache_attend_workspace_bytes", "KdaError", "STATUS", "DTYPE_BF16", "DTYPE_F32", "PASS_FWD", "PASS_BWD"]
 
 DTYPE_BF16, DTYPE_F32 = 0, 1
 PASS_FWD, PASS_BWD = 0, 1
@@ -389,8 +389,26 @@ def cache_attend(q, k_cache, v_cache, page_table, kv_lens, scale=None, window=0,
 
     q [N,HQ,K]; the cache, ``page_table`` and ``status`` as in :func:`cache_append`; ``kv_lens`` int32 [N], the
     rows to attend, the new token's own among them (none: o is 0 and lse -inf). Returns (o [N,HQ,V], lse fp32
-    [N,HQ])."""
+    [N,HQ]): new tensors, or ``out`` as o. ``ws`` (contiguous uint8) is scratch memory, of
+    :func:`cache_attend_workspace_bytes` bytes or more; without it, or with less, the call allocates its own for as
+    long as it takes. What it holds does not matter, but two calls that may overlap on the GPU cannot share one."""
     r = (_serve_module or _serve()).attend(q, k_cache, v_cache, page_table, kv_lens, scale, window, ws, out, status)
     if type(r) is int:
         raise KdaError(r, "kda_cache_attend")
     return r
+
+
+def cache_attend_workspace_bytes(q, k_cache, v_cache, page_table, window=0) -> int:
+    """Bytes of ``ws`` that :func:`cache_attend` wants for these tensors (their sizes count, and the device)."""
+    (N, max_pages), HQ = page_table.shape, q.shape[1]
+    pages, rows, heads, K = k_cache.shape
+    dtype = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}.get(k_cache.dtype)
+    if dtype is None:
+        raise TypeError(f"unsupported dtype {k_cache.dtype} of k_cache")
+    c = Cache(k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.stride()[:3], *v_cache.stride()[:3], pages, rows, heads, K,
+              v_cache.shape[3], dtype)
+    with torch.cuda.device(k_cache.device):
+        need = int(load().kda_cache_attend_workspace_bytes(ctypes.byref(c), HQ, N, max_pages, window))
+    if need == 0:
+        raise KdaError(1, "kda_cache_attend_workspace_bytes")
+    return need

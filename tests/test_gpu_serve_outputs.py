@@ -29,3 +29,27 @@ def test_attend_outputs_are_tensors_of_their_own(kda, N, L, dtype):  # noqa: F81
         file.seek(0)
         again = torch.load(file)
         assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("N, L", [(2, 50), (1, 9000)])
+def test_attend_workspace(kda, N, L):  # noqa: F811
+    """A workspace of the size that is asked for serves, one that is too small is not touched, and the results are the same."""
+    gen = _gen(42)
+    width = -(-L // 16)
+    kc, vc = (torch.randn(N * width, 16, 2, 64, generator=gen).bfloat16().cuda() for _ in range(2))
+    table = torch.arange(N * width, dtype=torch.int32, device="cuda").view(N, width)
+    q, lens = torch.randn(N, 4, 64, generator=gen).bfloat16().cuda(), torch.full((N,), L, dtype=torch.int32, device="cuda")
+    need = kda.cache_attend_workspace_bytes(q, kc, vc, table)
+    want = kda.cache_attend(q, kc, vc, table, lens)
+    assert "parts" in kda.load().kda_launch_name(0).decode() or L < 9000
+    for size in (need, need + 64, need - 1):
+        ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        got = kda.cache_attend(q, kc, vc, table, lens, ws=ws)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        used = not bool((ws == 255).all())
+        assert used == (size >= need and L == 9000)
+    assert kda.cache_attend_workspace_bytes(q, kc, vc, table, window=10) <= need
+    with pytest.raises(kda.KdaError):
+        kda.cache_attend_workspace_bytes(q[:, :3], kc, vc, table)
+    with pytest.raises(TypeError):
+        kda.cache_attend_workspace_bytes(q.half(), kc.half(), vc.half(), table)
