@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from tests.test_gpu_serve import kda  # noqa: F401
+from tests.test_gpu_serve import DT, ROUND, U, _gen, kda, make_cache, make_table, rope_table, to_gpu, turn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -18,3 +18,41 @@ def test_rows_beyond_32_bits(kda, HQ, HKV, turned):  # noqa: F811
     table, lens = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((1, 1), (1,)))
     out = kda.cache_append(k, v, kc, vc, table, lens, q=q, rope=rope)
     assert torch.equal(out, q) and torch.equal(kc[0], k) and torch.equal(vc[0], v)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens, T, HQ, HKV, K, V, size, rot, inter, layout", [
+    ([4, 0], 3, 2, 1, 64, 64, 4, 64, False, "heads first"),  # several rows to a CTA
+    ([0, 31, 5], 40, 8, 2, 128, 64, 16, 64, False, "rows first"),
+    ([100, 7, 0, 63, 64], 129, 16, 4, 64, 128, 27, 32, True, "shared pool"),
+    ([11] * 30, 70, 6, 3, 128, 128, 64, 0, False, "heads first"),
+])
+def test_as_many_rows_for_each_sequence(kda, lens, T, HQ, HKV, K, V, size, rot, inter, layout, dtype):  # noqa: F811
+    """Without cu_seqlens R / N rows belong to each sequence; and the same rows with cu_seqlens, into a cache of their own."""
+    gen, dt, N = _gen(51), DT[dtype], len(lens)
+    reach = [x + T for x in lens]
+    pages = sum(-(-x // size) for x in reach) + 2
+    kc, vc = make_cache(gen, pages, size, HKV, K, V, dtype, layout)
+    table = make_table(gen, reach, size, pages)
+    q, k, v = (torch.randn(N * T, h, d, generator=gen).to(dt) for h, d in ((HQ, K), (HKV, K), (HKV, V)))
+    rope = rope_table(max(reach), rot) if rot else None
+    n = torch.arange(N * T) // T
+    pos = torch.tensor(lens)[n] + torch.arange(N * T) % T
+    page = table[n, pos // size].long()
+    wq, size_q = turn(q, pos, rope, inter)
+    wk, size_k = turn(k, pos, rope, inter)
+    bound = lambda want, mag: (3 * U * mag + ROUND[dtype] * want.abs() * (mag > 0)) * 1.01  # noqa: E731
+    for cu in (None, (torch.arange(N + 1) * T).cuda()):
+        gk, gv = to_gpu(kc), to_gpu(vc)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = kda.cache_append(k.cuda(), v.cuda(), gk, gv, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                               q=q.cuda(), rope=None if rope is None else rope.cuda(), interleaved=inter, cu_seqlens=cu,
+                               status=status)
+        assert int(status) == 0
+        assert ((out.double().cpu() - wq).abs() <= bound(wq, size_q)).all()
+        assert ((gk.cpu()[page, pos % size].double() - wk).abs() <= bound(wk, size_k)).all()
+        assert torch.equal(gv.cpu()[page, pos % size], v)
+        for now, before in ((gk.cpu(), kc), (gv.cpu(), vc)):
+            keep = torch.ones(pages, size, dtype=torch.bool)
+            keep[page, pos % size] = False
+            assert torch.equal(now[keep], before[keep])
