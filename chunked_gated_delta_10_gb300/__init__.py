@@ -405,8 +405,8 @@ def cache_attend_workspace_bytes(q, k_cache, v_cache, page_table, window=0) -> i
     dtype = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}.get(k_cache.dtype)
     if dtype is None:
         raise TypeError(f"unsupported dtype {k_cache.dtype} of k_cache")
-    c = Cache(k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.stride()[:3], *v_cache.stride()[:3], pages, rows, heads, K,
-              v_cache.shape[3], dtype)
+    strides = [s if n > 1 else 0 for t in (k_cache, v_cache) for n, s in zip(t.shape[:3], t.stride())]
+    c = Cache(k_cache.data_ptr(), v_cache.data_ptr(), *strides, pages, rows, heads, K, v_cache.shape[3], dtype)
     with torch.cuda.device(k_cache.device):
         need = int(load().kda_cache_attend_workspace_bytes(ctypes.byref(c), HQ, N, max_pages, window))
     if need == 0:

@@ -171,7 +171,9 @@ CacheArgs cache_of(PyObject* ko, PyObject* vo, PyObject* table, PyObject* lens) 
     const Tensor& t = cuda_tensor(table, "page_table", 2);
     if (t.scalar_type() != at::kInt || t.device() != k.device() || (t.size(1) > 1 && t.stride(1) != 1))
         refuse("page_table", "int32 [N, max_pages] of contiguous rows, on the cache's device", &t);
-    CacheArgs x{{k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), v.stride(0), v.stride(1), v.stride(2),
+    // (the stride of a dimension of one says nothing)
+    const auto stride = [](const Tensor& c, int i) { return c.size(i) > 1 ? c.stride(i) : 0; };
+    CacheArgs x{{k.data_ptr(), v.data_ptr(), stride(k, 0), stride(k, 1), stride(k, 2), stride(v, 0), stride(v, 1), stride(v, 2),
                  int32_of(k.size(0), "the number of pages"), int32_of(k.size(1), "the page size"),
                  int32_of(k.size(2), "the number of heads"), int32_of(k.size(3), "K"), int32_of(v.size(3), "V"),
                  dtype_of(k, "k_cache")},

@@ -1,4 +1,5 @@
-"""What the single-token calls return: tensors of their own, that live, are saved and are freed apart from each other."""
+"""What the single-token calls take and return: strides that say nothing, workspaces, and outputs of their own, that live,
+are saved and are freed apart from each other."""
 import io
 
 import pytest
@@ -53,3 +54,21 @@ def test_attend_workspace(kda, N, L):  # noqa: F811
         kda.cache_attend_workspace_bytes(q[:, :3], kc, vc, table)
     with pytest.raises(TypeError):
         kda.cache_attend_workspace_bytes(q.half(), kc.half(), vc.half(), table)
+
+
+def test_strides_of_dimensions_of_one(kda):  # noqa: F811
+    """A cache of one page, one row a page or one head may have any stride there."""
+    gen = _gen(43)
+    z = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    for pages, rows, heads in ((1, 16, 2), (16, 1, 2), (4, 4, 1), (1, 16, 1), (16, 1, 1)):
+        plain = [torch.randn(pages, rows, heads, 64, generator=gen).bfloat16().cuda() for _ in range(2)]
+        odd = [t.clone().as_strided(t.shape, [3 if n == 1 else s for n, s in zip(t.shape, t.stride())]) for t in plain]
+        table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+        k, v = (torch.randn(5, heads, 64, generator=gen).bfloat16().cuda() for _ in range(2))
+        q = torch.randn(1, 2 * heads, 64, generator=gen).bfloat16().cuda()
+        got = []
+        for kc, vc in (plain, odd):
+            kda.cache_append(k, v, kc, vc, table, z(1) + 11)
+            got.append(kda.cache_attend(q, kc, vc, table, z(1) + 16) + (kc, vc))
+            assert kda.cache_attend_workspace_bytes(q, kc, vc, table) > 0
+        assert all(torch.equal(x, y) for x, y in zip(*got))
