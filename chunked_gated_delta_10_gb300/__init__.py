@@ -376,7 +376,8 @@ def cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q=None, rope=None,
     channels; ``page_table`` int32 [N, max_pages]; ``kv_lens`` int32 [N], the rows already there (not changed;
     negative: inactive). ``rope`` fp32 [positions, r]: r/2 cosines, then r/2 sines; channel i turns with i + r/2, or,
     ``interleaved``, 2i with 2i+1. Returns the rotated queries (``q_out``, if given), or None without q.
-    ``status`` (int32 [1], zeroed by the caller) is set where a page or position does not exist."""
+    ``status`` (int32 [1], zeroed by the caller) is set where a page or position does not exist, or a row lies in
+    no sequence of ``cu_seqlens``."""
     r = (_serve_module or _serve()).append(k, v, k_cache, v_cache, page_table, kv_lens, q, rope, interleaved, cu_seqlens,
                                            q_out, status)
     if type(r) is int:

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(MOST, SHORT ? 6 : MOST == 64 ? 24 : 2) k_appen
     if (a.cu) {
         n = seq_of(a.cu, a.N, (unsigned)r);
         const int64_t begin = a.cu[n];
-        ok = begin <= r;
+        ok = begin <= r && r < a.cu[n + 1];
         idx = (unsigned)(r - begin);
     } else {
         n = (unsigned)r / a.per;

@@ -13,12 +13,13 @@
  * no synchronisation, kernels enqueued on `stream`, argument errors returned
  * before any launch, outputs fully overwritten, bit-identical reruns.
  *
- * Indices that live on the device (slots, page tables, lengths) cannot be
- * checked by the host. The kernels check each before it is used: what it
- * would have reached is not touched, and the optional device word `status`
- * receives KDA_ERR_INVALID_ARG. The word is only ever set, never cleared: the
- * caller zeroes it and reads it when it wants to know. A negative slot or
- * length is no error: it marks an inactive row of a padded batch.
+ * Indices that live on the device (slots, page tables, lengths, offsets of
+ * packed sequences) cannot be checked by the host. The kernels check each
+ * before it is used: what it would have reached is not touched, and the
+ * optional device word `status` receives KDA_ERR_INVALID_ARG. The word is only
+ * ever set, never cleared: the caller zeroes it and reads it when it wants to
+ * know. A negative slot or length is no error: it marks an inactive row of a
+ * padded batch.
  */
 #ifndef KDA_GB300_SERVE_H
 #define KDA_GB300_SERVE_H
@@ -99,8 +100,9 @@ typedef struct {
  *   kv_lens     int32 [N]: rows already in the cache; not changed. Negative:
  *     the sequence is inactive (nothing is appended, its q_out rows are 0).
  *   status      nullable: set where a position needs a page beyond max_pages,
- *     a page outside [0, num_pages) or a rope row beyond rope_len; such a row
- *     is not appended and its q_out row is 0.
+ *     a page outside [0, num_pages) or a rope row beyond rope_len, and where
+ *     a row lies outside its sequence in cu_seqlens; such a row is not
+ *     appended and its q_out row is 0.
  * R == 0 is KDA_OK and launches nothing. R is at most 2^31 - 1 and HQ + 2 HKV
  * less than 2^26 - 32 (else KDA_ERR_UNSUPPORTED).
  * Errors: KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED before any launch;

@@ -56,3 +56,23 @@ def test_as_many_rows_for_each_sequence(kda, lens, T, HQ, HKV, K, V, size, rot, 
             keep = torch.ones(pages, size, dtype=torch.bool)
             keep[page, pos % size] = False
             assert torch.equal(now[keep], before[keep])
+
+
+@pytest.mark.parametrize("cu, kept", [([0, 2, 5], [0, 1, 2, 3, 4]), ([0, 2, 4], [0, 1, 2, 3]), ([1, 2, 5], [1, 2, 3, 4]),
+                                      ([0, 0, 0], []), ([0, 2, 2], [0, 1])])
+def test_rows_outside_the_packed_sequences(kda, cu, kept):  # noqa: F811
+    """Rows before the first sequence or behind the last one belong to none: not appended, their queries 0, and flagged."""
+    gen = _gen(52)
+    k, v, q = (torch.randn(5, 2, 64, generator=gen).bfloat16().cuda() for _ in range(3))
+    kc, vc = kda.new_cache(4, 8, 2, 64, 64)
+    table = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device="cuda")
+    lens, status = torch.tensor([6, 7], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = kda.cache_append(k, v, kc, vc, table, lens, q=q, cu_seqlens=torch.tensor(cu, device="cuda"), status=status)
+    assert int(status) == (len(kept) < 5)
+    want_k, want_q = torch.zeros_like(kc), torch.zeros_like(q)
+    for r in kept:
+        n = 0 if r < cu[1] else 1
+        pos = int(lens[n]) + r - cu[n]
+        want_k[table[n, pos // 8].long(), pos % 8] = k[r]
+        want_q[r] = q[r]
+    assert torch.equal(kc, want_k) and torch.equal(out, want_q) and int((vc != 0).flatten(2).any(2).sum()) == len(kept)
