@@ -945,7 +945,7 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window, const
         p.parts = slots;
     }
     p.grid = p.split == kShares ? dim3(p.parts) : dim3(units * p.parts, N);
-    p.ws_bytes = 256;
+    p.ws_bytes = KDA_ATTEND_WORKSPACE_MIN;
     if (p.split >= kParts) {
         const size_t held = p.split == kParts ? (size_t)all * p.parts : (size_t)p.parts * 2;
         p.acc_bytes = held * ht * c->V * sizeof(float);
@@ -975,8 +975,9 @@ Gpu gpu_for(const kda_cache* c, int HQ) {
     static std::atomic<int> known[5][2][2][kDevices];
     const int ht = head_tile(c, HQ);
     const int tile = c->dtype == KDA_DTYPE_BF16 ? ht / 16 : ht == 1 ? 2 : ht == 4 ? 3 : 4;
-    return {sm_count(), largest_cluster((const void*)kernel_of(*c, ht, kCluster), kWarps * 32, kMaxCluster,
-                                        known[tile][c->K / 128][c->V / 128])};
+    const int device = present_device();
+    return {sm_count(device), largest_cluster(device, (const void*)kernel_of(*c, ht, kCluster), kWarps * 32, kMaxCluster,
+                                              known[tile][c->K / 128][c->V / 128])};
 }
 
 template <typename TI, int V, int HT, int VS, int G, int THREADS>

@@ -14,22 +14,29 @@ namespace kda {
 constexpr int kDevices = 32;
 constexpr int kGb300Sms = 152;
 
-// SMs of the present device; without one, those of a GB300.
-inline int sm_count() {
+// The present device, or -1 without one.
+inline int present_device() {
+    int device;
+    return cudaGetDevice(&device) == cudaSuccess ? device : -1;
+}
+
+// SMs of the device; without one, those of a GB300.
+inline int sm_count(int device) {
     static std::atomic<int> known[kDevices];
-    int device, n = 0;
-    if (cudaGetDevice(&device) != cudaSuccess) return kGb300Sms;
+    int n = 0;
+    if (device < 0) return kGb300Sms;
     if (device < kDevices && (n = known[device].load(std::memory_order_relaxed)) > 0) return n;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n <= 0) return kGb300Sms;
     if (device < kDevices) known[device].store(n, std::memory_order_relaxed);
     return n;
 }
+inline int sm_count() { return sm_count(present_device()); }
 
-// The largest cluster, of at most `most` CTAs, that the present device can place the kernel in (without one: `most`).
-// `known` is the kernel's own.
-inline int largest_cluster(const void* kernel, int threads, int most, std::atomic<int> (&known)[kDevices]) {
-    int device, n = 0;
-    if (cudaGetDevice(&device) != cudaSuccess) return most;
+// The largest cluster, of at most `most` CTAs, that the device, which is the present one, can place the kernel in
+// (without one: `most`). `known` is the kernel's own.
+inline int largest_cluster(int device, const void* kernel, int threads, int most, std::atomic<int> (&known)[kDevices]) {
+    int n = 0;
+    if (device < 0) return most;
     if (device < kDevices && (n = known[device].load(std::memory_order_relaxed)) > 0) return n;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(most);

@@ -148,7 +148,12 @@ kda_status kda_cache_attend(const kda_cache* cache, const void* q, int64_t q_str
                             const int32_t* kv_lens, int32_t window, float scale, void* o, float* lse, int32_t* status,
                             void* ws, size_t ws_bytes, kda_stream_t stream);
 
-/* Bytes of workspace kda_cache_attend needs for these sizes on the present device (0 if they are invalid). */
+/*
+ * Bytes of workspace kda_cache_attend needs for these sizes on the present
+ * device (0 if they are invalid): KDA_ATTEND_WORKSPACE_MIN, which is then
+ * neither read nor written, or more.
+ */
+#define KDA_ATTEND_WORKSPACE_MIN 256
 size_t kda_cache_attend_workspace_bytes(const kda_cache* cache, int32_t HQ, int32_t N, int32_t max_pages,
                                         int32_t window);
 
