@@ -564,7 +564,7 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 constexpr float kBelow = 1.f - 0x1p-12f;
 
 // CTAs of k_attend_mma to an SM.
-constexpr int mma_ctas(int NT, int K, int V) { return (K + V == 128 ? 5 : 3) - (NT - 1); }
+constexpr int mma_ctas(int NT, int K, int V) { return K + V == 128 ? 4 : 4 - NT; }
 
 // Tensor-core kernel: a unit has up to 8 NT query heads, each warp a tile of 16 rows at a time. The products are taken
 // transposed,
@@ -581,8 +581,9 @@ constexpr int mma_ctas(int NT, int K, int V) { return (K + V == 128 ? 5 : 3) - (
 //     where memory is the bound, 10 % where a CTA's few turns are, 4000 rows 8.3 -> 9.1 us, and 12 % with 9 to 16 heads
 //     of K = V = 64.)
 // Groups of 9 to 16 heads take two such columns of heads (NT = 2) at two CTAs an SM: reading the rows twice instead
-// takes 80 us where this takes 50 (64 sequences of 8000 rows, 16 heads on one). K = V = 64 leaves registers for five CTAs
-// (40 sequences of U[1,8000] rows, 16 heads on 16: 111.6 us; with three, whose rows under way are too few, 120).
+// takes 80 us where this takes 50 (64 sequences of 8000 rows, 16 heads on one). K = V = 64 leaves registers for four CTAs
+// (40 sequences of U[1,8000] rows, 16 heads on 16: 94.1 us; with five, which spill, 95.5; with three, whose rows under way
+// are too few, 99.8. 128 of 1000 rows, eight heads on two: 14.4 and 16.2 us with four and five).
 // A tensor core of the fifth generation wants its operands in shared memory and 128 rows in a product; here 8 to 16
 // columns of the product are of use, and with the memory at its rate the tensor cores are busy 14 % of the time as it is.
 template <int K, int V, int NT, bool SHARES>

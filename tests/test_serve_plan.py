@@ -25,7 +25,7 @@ def plan(lib, HQ, HKV, K, V, dtype, N, rows, window=0, page=1, sms=152, cluster=
 def places(group, K, V, dtype, sms=152):
     """CTAs of the attention kernels that the SMs hold."""
     if dtype == kda.DTYPE_BF16:
-        return sms * ((5 if K + V == 128 else 3) - (group > 8))
+        return sms * (4 if K + V == 128 else 2 if group > 8 else 3)
     ht = 1 if group == 1 else 4 if group <= 4 else 8
     return sms * ((4 if ht == 1 else 3) + ((K + V < 256) if ht == 4 else (V == 64)))
 
