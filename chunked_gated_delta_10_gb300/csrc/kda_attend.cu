@@ -8,21 +8,23 @@
 //
 // Bound: the cached keys and values are read once. Measured on one GB300 (time of
 // a call among others; GB/s of the cached rows), bf16, K = V = 128:
-//   64 sequences of U[1,8192] rows, 32 query heads on 8: 154.4 to 156.3 us,
+//   64 sequences of U[1,8192] rows, 32 query heads on 8: 154.5 to 157.4 us,
 //     6.8 to 6.9 TB/s, a little above a plain copy's rate;
-//   one of 65536 rows, 16 heads on 2: 15.9 us (9.9 at that rate): the length, the
+//   one of 65536 rows, 16 heads on 2: 17.0 us (9.9 at that rate): the length, the
 //     pages and the first rows are read one after the other before the stream is
-//     full (1.5 us), its end is uneven (4 or 5 turns a CTA), and the second kernel
-//     takes 2 us;
-//   one of 2048 rows, 32 heads on 8: 5.4 us, all of it latency (1.2 us of rows).
-// What was tried and is slower: two tiles under way in a warp's registers (two CTAs
-// an SM instead of three: 180 us for the first of these); the tile after the next
-// asked into L2 (166 us; fp32 with eight heads alone gains, 48 -> 44 us); joins of
-// the parts by reading the other CTAs' shared memory instead of pushing to it (1.5
-// us more); clusters for large batches (169 to 180 us: a cluster waits for room for
-// all of its CTAs); shares of the rows alone, without a weight for a unit's ends
-// (160 us for the first of these); the sequences of a batch side by side instead of
-// a sequence's heads, which share its pages (fp32, 12 sequences: 15.7 against 13.6).
+//     full (1.5 us), 410 CTAs of five turns each are three to some SMs and two to
+//     others, and the second kernel takes 2 us;
+//   one of 2048 rows, 32 heads on 8: 5.8 us in a graph, all of it latency (1.2 us of
+//     rows).
+// What was tried and is slower (measured with weights of two parts): two tiles under
+// way in a warp's registers (two CTAs an SM instead of three: 180 us for the first of
+// these); the tile after the next asked into L2 (166 us; fp32 with eight heads alone
+// gains, 48 -> 44 us); joins of the parts by reading the other CTAs' shared memory
+// instead of pushing to it (1.5 us more); clusters for large batches (169 to 180 us: a
+// cluster waits for room for all of its CTAs); shares of the rows alone, without a
+// weight for a unit's ends (160 us for the first of these); the sequences of a batch
+// side by side instead of a sequence's heads, which share its pages (fp32, 12
+// sequences: 15.7 against 13.6).
 #include "../../include/kda_selftest.h"
 #include "kda_cache.cuh"
 
@@ -581,11 +583,11 @@ constexpr int mma_ctas(int NT, int K, int V) { return K + V == 128 ? 4 : 4 - NT;
 //     where memory is the bound, 10 % where a CTA's few turns are, 4000 rows 8.3 -> 9.1 us, and 12 % with 9 to 16 heads
 //     of K = V = 64.)
 // Groups of 9 to 16 heads take two such columns of heads (NT = 2) at two CTAs an SM: reading the rows twice instead
-// takes 80 us where this takes 50 (64 sequences of 8000 rows, 16 heads on one). K = V = 64 leaves registers for four CTAs
+// takes 81 us where this takes 51 (64 sequences of 8000 rows, 16 heads on one). K = V = 64 leaves registers for four CTAs
 // (40 sequences of U[1,8000] rows, 16 heads on 16: 94.1 us; with five, which spill, 95.5; with three, whose rows under way
 // are too few, 99.8. 128 of 1000 rows, eight heads on two: 14.4 and 16.2 us with four and five).
 // A tensor core of the fifth generation wants its operands in shared memory and 128 rows in a product; here 8 to 16
-// columns of the product are of use, and with the memory at its rate the tensor cores are busy 14 % of the time as it is.
+// columns of the product are of use, and with the memory at its rate the tensor cores are busy 19 % of the time as it is.
 template <int K, int V, int NT, bool SHARES>
 __global__ void __launch_bounds__(kWarps * 32, mma_ctas(NT, K, V)) k_attend_mma(AttendArgs a) {
     using TI = __nv_bfloat16;
