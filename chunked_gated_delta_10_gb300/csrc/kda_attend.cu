@@ -562,7 +562,7 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 }
 // The three parts of a weight above 0 are all above 0: the first two are cut off a little below what is left, not rounded.
 // A part of 0, or one of the other sign, would make a NaN of an infinite value of V. What is left for the third part
-// is less than 2^-13.8 of the weight, so rounding it loses 2^-22.8 at most.
+// is less than 2^-13.9 of the weight, so rounding it loses 2^-21.9 at most. (Weights of 2^-100 and more keep to that.)
 constexpr float kBelow = 1.f - 0x1p-12f;
 
 // CTAs of k_attend_mma to an SM.

@@ -127,7 +127,7 @@ kda_status kda_cache_append(const kda_cache* cache, const void* k, int64_t k_str
  * o is 0 and lse is -inf. Rows outside the range are never read, whatever
  * they hold. Softmax statistics, weights and sums are held in fp32 (with a bf16
  * cache the weights enter the products as three bf16 values that add up to
- * them within 2^-22), and each output is rounded once.
+ * them within 2^-21.9), and each output is rounded once.
  * Values that are not finite come out as the sum says: an infinite one makes
  * its channel infinite, a NaN, or infinities of both signs, make it NaN. (A
  * weight below 2^-90 of the largest may count as 0, and 0 times an infinite

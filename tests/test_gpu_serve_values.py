@@ -15,7 +15,7 @@ def test_weights_are_as_precise_as_the_sums(kda, dtype):  # noqa: F811
     is left) hides nothing: what remains is the weights' error.
 
     A row's score is one product, so a weight errs by what the scaling to log2 units does to the score (|s| <= 0.51 log2
-    units: 3 u |s|, less than 2^-23), by its exponential (2^-22) and by what the product with V holds of it (2^-22); the
+    units: 3 u |s|, less than 2^-23), by its exponential (2^-22) and by what the product with V holds of it (2^-21.9); the
     sum of two terms may be truncated at 2^-23 each. In all less than 2^-20 of the terms' magnitudes."""
     gen, dt, N, H, D = _gen(31), DT[dtype], 4, 64, 64
     x = -(torch.rand(N, H, generator=gen) * 0.3 + 0.05).to(torch.bfloat16).double()
