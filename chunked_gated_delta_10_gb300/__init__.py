@@ -117,6 +117,11 @@ def load():
                                              ctypes.c_float, _P, _P, _P, _P, ctypes.c_size_t, _P]
             lib.kda_cache_attend_workspace_bytes.restype = ctypes.c_size_t
             lib.kda_cache_attend_workspace_bytes.argtypes = [ctypes.POINTER(Cache), i32, i32, i32, i32]
+            lib.kda_cache_attend_sinks.restype = ctypes.c_int
+            lib.kda_cache_attend_sinks.argtypes = [ctypes.POINTER(Cache), _P, i64, i32, i32, _P, i64, i32, _P, i32, i32,
+                                                   ctypes.c_float, _P, _P, _P, _P, ctypes.c_size_t, _P]
+            lib.kda_cache_attend_sinks_workspace_bytes.restype = ctypes.c_size_t
+            lib.kda_cache_attend_sinks_workspace_bytes.argtypes = [ctypes.POINTER(Cache), i32, i32, i32, i32, i32]
             _lib = lib
     return _lib
 
@@ -385,21 +390,22 @@ def cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q=None, rope=None,
     return r
 
 
-def cache_attend(q, k_cache, v_cache, page_table, kv_lens, scale=None, window=0, ws=None, out=None, status=None):
-    """Attention of one new token per sequence over its cached rows (the last ``window`` of them, if positive).
+def cache_attend(q, k_cache, v_cache, page_table, kv_lens, scale=None, window=0, ws=None, out=None, status=None, sinks=0):
+    """Attention of one new token per sequence over its cached rows: all of them, or, if ``window`` is positive, the last
+    ``window`` of them and the first ``sinks``.
 
     q [N,HQ,K]; the cache, ``page_table`` and ``status`` as in :func:`cache_append`; ``kv_lens`` int32 [N], the
     rows to attend, the new token's own among them (none: o is 0 and lse -inf). Returns (o [N,HQ,V], lse fp32
     [N,HQ]): new tensors, or ``out`` as o. ``ws`` (contiguous uint8) is scratch memory, of
     :func:`cache_attend_workspace_bytes` bytes or more; without it, or with less, the call allocates its own for as
     long as it takes. What it holds does not matter, but two calls that may overlap on the GPU cannot share one."""
-    r = (_serve_module or _serve()).attend(q, k_cache, v_cache, page_table, kv_lens, scale, window, ws, out, status)
+    r = (_serve_module or _serve()).attend(q, k_cache, v_cache, page_table, kv_lens, scale, window, ws, out, status, sinks)
     if type(r) is int:
         raise KdaError(r, "kda_cache_attend")
     return r
 
 
-def cache_attend_workspace_bytes(q, k_cache, v_cache, page_table, window=0) -> int:
+def cache_attend_workspace_bytes(q, k_cache, v_cache, page_table, window=0, sinks=0) -> int:
     """Bytes of ``ws`` that :func:`cache_attend` wants for these tensors (their sizes count, and the device)."""
     (N, max_pages), HQ = page_table.shape, q.shape[1]
     pages, rows, heads, K = k_cache.shape
@@ -409,7 +415,7 @@ def cache_attend_workspace_bytes(q, k_cache, v_cache, page_table, window=0) -> i
     strides = [s if n > 1 else 0 for t in (k_cache, v_cache) for n, s in zip(t.shape[:3], t.stride())]
     c = Cache(k_cache.data_ptr(), v_cache.data_ptr(), *strides, pages, rows, heads, K, v_cache.shape[3], dtype)
     with torch.cuda.device(k_cache.device):
-        need = int(load().kda_cache_attend_workspace_bytes(ctypes.byref(c), HQ, N, max_pages, window))
+        need = int(load().kda_cache_attend_sinks_workspace_bytes(ctypes.byref(c), HQ, N, max_pages, window, sinks))
     if need == 0:
         raise KdaError(1, "kda_cache_attend_workspace_bytes")
     return need

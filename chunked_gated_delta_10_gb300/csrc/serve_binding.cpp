@@ -264,18 +264,19 @@ void* untouched(int device) {
     return known[device];
 }
 
-// attend(q, k_cache, v_cache, page_table, kv_lens, scale, window, ws, out, status)
+// attend(q, k_cache, v_cache, page_table, kv_lens, scale, window, ws, out, status, sinks)
 PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    expect(n, 10);
+    expect(n, 11);
     const CacheArgs x = cache_of(a[1], a[2], a[3], a[4]);
     const Tensor& qt = cuda_tensor(a[0], "q", 3);
-    const int32_t HQ = int32_of(qt.size(1), "the number of query heads"), window = int32_of(whole_of(a[6]), "window");
+    const int32_t HQ = int32_of(qt.size(1), "the number of query heads"), window = int32_of(whole_of(a[6]), "window"),
+                  sinks = int32_of(whole_of(a[10]), "sinks");
     const Rows q = rows_of(a[0], "q", x.N, HQ, x.c.K, x);
     const float scale = scale_of(a[5], x.c.K);
     void* status = like(a[9], "status", {1}, at::kInt, x.dev, true);
     const c10::cuda::CUDAGuard guard(x.dev);
-    const size_t need = kda_cache_attend_workspace_bytes(&x.c, HQ, x.N, x.width, window);
+    const size_t need = kda_cache_attend_sinks_workspace_bytes(&x.c, HQ, x.N, x.width, window, sinks);
     void* wp = nullptr;
     size_t room = 0;
     if (a[7] != Py_None) {
@@ -308,8 +309,8 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
             wp = scratch.get();
             room = need;
         }
-        s = kda_cache_attend(&x.c, q.p, q.stride, HQ, x.N, x.table, x.table_stride, x.width, x.lens, window, scale, op,
-                             (float*)lse.data_ptr(), (int32_t*)status, wp, room, stream_of(x.dev));
+        s = kda_cache_attend_sinks(&x.c, q.p, q.stride, HQ, x.N, x.table, x.table_stride, x.width, x.lens, window, sinks,
+                                   scale, op, (float*)lse.data_ptr(), (int32_t*)status, wp, room, stream_of(x.dev));
     }
     THPObjectPtr first(given ? Py_NewRef(a[8]) : THPVariable_Wrap(std::move(made))), second(THPVariable_Wrap(std::move(lse)));
     if (!first || !second) throw python_error();
@@ -320,7 +321,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {
     {"step", (PyCFunction)(void*)step, METH_FASTCALL, "kda_step"},
     {"append", (PyCFunction)(void*)append, METH_FASTCALL, "kda_cache_append"},
-    {"attend", (PyCFunction)(void*)attend, METH_FASTCALL, "kda_cache_attend"},
+    {"attend", (PyCFunction)(void*)attend, METH_FASTCALL, "kda_cache_attend_sinks"},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_serve", nullptr, -1, methods};

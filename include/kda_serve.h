@@ -157,6 +157,19 @@ kda_status kda_cache_attend(const kda_cache* cache, const void* q, int64_t q_str
 size_t kda_cache_attend_workspace_bytes(const kda_cache* cache, int32_t HQ, int32_t N, int32_t max_pages,
                                         int32_t window);
 
+/*
+ * The same, with the first `sinks` rows of each sequence visible beside a
+ * window: t runs over 0 .. sinks - 1 and kv_lens[n] - window .. kv_lens[n] - 1,
+ * each row once. Without a window (0) all rows are visible, and sinks says
+ * nothing. The rows keep the positions that they were rotated by.
+ */
+kda_status kda_cache_attend_sinks(const kda_cache* cache, const void* q, int64_t q_stride, int32_t HQ, int32_t N,
+                                  const int32_t* page_table, int64_t table_stride, int32_t max_pages,
+                                  const int32_t* kv_lens, int32_t window, int32_t sinks, float scale, void* o, float* lse,
+                                  int32_t* status, void* ws, size_t ws_bytes, kda_stream_t stream);
+size_t kda_cache_attend_sinks_workspace_bytes(const kda_cache* cache, int32_t HQ, int32_t N, int32_t max_pages,
+                                              int32_t window, int32_t sinks);
+
 #ifdef __cplusplus
 }
 #endif

@@ -129,3 +129,18 @@ def test_structures_match_the_header():
     """The sizes that a C compiler gives the two structures."""
     assert ctypes.sizeof(kda.StepDims) == 9 * 4
     assert ctypes.sizeof(kda.Cache) == 8 * 8 + 6 * 4
+
+
+def _sinks(lib, cache=None, **kw):
+    a = dict(q=A, q_stride=2048, HQ=16, N=2, table=A, table_stride=5, max_pages=5, lens=A, window=8, sinks=2, scale=0.1, o=A,
+             lse=A, status=None, ws=A, ws_bytes=1 << 30, stream=None)
+    a.update(kw)
+    return lib.kda_cache_attend_sinks(cache or _cache(), *a.values())
+
+
+@pytest.mark.parametrize("bad, code", [(dict(sinks=-1), INVALID), (dict(window=-1), INVALID), (dict(q=None), INVALID),
+                                       (dict(ws_bytes=8), WORKSPACE), (dict(N=2**28), UNSUPPORTED)])
+def test_attend_sinks_refuses(lib, bad, code):
+    assert _sinks(lib, **bad) == code
+    assert _sinks(lib, N=0, q=None, o=None) == 0
+    assert lib.kda_cache_attend_sinks_workspace_bytes(_cache(), 16, 2, 5, 8, -1) == 0
