@@ -24,9 +24,9 @@ from .build import LIB, SERVE, build  # noqa: F401
 
 __all__ = ["build", "load", "Dims", "prepare_chunks", "workspace_bytes", "saved_bytes", "chunk_fwd", "chunk_bwd",
            "chunk_fwd_save", "chunk_bwd_from_saved", "step", "new_cache", "cache_append", "cache_attend",
-           "cache_attend_workspace_bytes", "KdaError", "STATUS", "DTYPE_BF16", "DTYPE_F32", "PASS_FWD", "PASS_BWD"]
+           "cache_attend_workspace_bytes", "KdaError", "STATUS", "DTYPE_BF16", "DTYPE_F32", "DTYPE_E4M3", "PASS_FWD", "PASS_BWD"]
 
-DTYPE_BF16, DTYPE_F32 = 0, 1
+DTYPE_BF16, DTYPE_F32, DTYPE_E4M3 = 0, 1, 2
 PASS_FWD, PASS_BWD = 0, 1
 CHUNK = 64
 STATUS = {0: "KDA_OK", 1: "KDA_ERR_INVALID_ARG", 2: "KDA_ERR_UNSUPPORTED", 3: "KDA_ERR_WORKSPACE", 4: "KDA_ERR_CUDA",
@@ -62,6 +62,14 @@ class Cache(ctypes.Structure):
                 ("k_head", ctypes.c_int64), ("v_page", ctypes.c_int64), ("v_row", ctypes.c_int64),
                 ("v_head", ctypes.c_int64), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("HKV", ctypes.c_int32), ("K", ctypes.c_int32), ("V", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class Cache8(ctypes.Structure):
+    """Mirror of ``kda_cache8``."""
+    _fields_ = [("cache", Cache), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("k_scale_page", ctypes.c_int64),
+                ("k_scale_block", ctypes.c_int64), ("k_scale_head", ctypes.c_int64), ("v_scale_page", ctypes.c_int64),
+                ("v_scale_block", ctypes.c_int64), ("v_scale_head", ctypes.c_int64), ("block", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -122,6 +130,12 @@ def load():
                                                    ctypes.c_float, _P, _P, _P, _P, ctypes.c_size_t, _P]
             lib.kda_cache_attend_sinks_workspace_bytes.restype = ctypes.c_size_t
             lib.kda_cache_attend_sinks_workspace_bytes.argtypes = [ctypes.POINTER(Cache), i32, i32, i32, i32, i32]
+            lib.kda_cache8_append.restype = ctypes.c_int
+            lib.kda_cache8_append.argtypes = [ctypes.POINTER(Cache8)] + lib.kda_cache_append.argtypes[1:]
+            lib.kda_cache8_attend.restype = ctypes.c_int
+            lib.kda_cache8_attend.argtypes = [ctypes.POINTER(Cache8)] + lib.kda_cache_attend_sinks.argtypes[1:]
+            lib.kda_cache8_attend_workspace_bytes.restype = ctypes.c_size_t
+            lib.kda_cache8_attend_workspace_bytes.argtypes = [ctypes.POINTER(Cache8), i32, i32, i32, i32, i32]
             _lib = lib
     return _lib
 
@@ -365,15 +379,26 @@ def step(q, k, v, g, beta, state, scale=None, slots=None, out=None, status=None)
     return r
 
 
-def new_cache(num_pages, page_size, heads, K, V, dtype=torch.bfloat16, device="cuda"):
+def new_cache(num_pages, page_size, heads, K, V, dtype=torch.bfloat16, device="cuda", scale_block=None):
     """An empty paged cache (k_cache [num_pages, page_size, heads, K], v_cache likewise with V), each head's rows
-    of a page contiguous: the layout that :func:`cache_attend` reads in the longest runs."""
-    return tuple(torch.zeros(num_pages, heads, page_size, d, dtype=dtype, device=device).transpose(1, 2)
-                 for d in (K, V))
+    of a page contiguous: the layout that :func:`cache_attend` reads in the longest runs.
+
+    With ``dtype`` torch.float8_e4m3fn a cache in 8 bits, and the scales of its blocks of ``scale_block`` rows (which
+    divide a page; without it 16, or a page that 16 does not divide): (k_cache, v_cache, k_scale, v_scale), scales fp32
+    [num_pages, page_size / scale_block, heads]."""
+    pair = tuple(torch.zeros(num_pages, heads, page_size, d, dtype=dtype, device=device).transpose(1, 2) for d in (K, V))
+    if dtype != torch.float8_e4m3fn:
+        if scale_block is not None:
+            raise ValueError("scale_block is for a cache in float8_e4m3fn")
+        return pair
+    block = scale_block or (16 if page_size % 16 == 0 else page_size)
+    if block < 0 or page_size % block:
+        raise ValueError(f"scale_block {block} does not divide the page size {page_size}")
+    return pair + tuple(torch.zeros(num_pages, heads, page_size // block, device=device).transpose(1, 2) for _ in range(2))
 
 
 def cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q=None, rope=None, interleaved=False, cu_seqlens=None,
-                 q_out=None, status=None):
+                 q_out=None, status=None, k_scale=None, v_scale=None):
     """Append new keys and values to a paged cache, keys (and queries) rotated by their position on the way.
 
     k [R,HKV,K], v [R,HKV,V] and q [R,HQ,K] hold the new rows of all sequences: R / N each, or as ``cu_seqlens``
@@ -382,15 +407,21 @@ def cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q=None, rope=None,
     negative: inactive). ``rope`` fp32 [positions, r]: r/2 cosines, then r/2 sines; channel i turns with i + r/2, or,
     ``interleaved``, 2i with 2i+1. Returns the rotated queries (``q_out``, if given), or None without q.
     ``status`` (int32 [1], zeroed by the caller) is set where a page or position does not exist, or a row lies in
-    no sequence of ``cu_seqlens``."""
+    no sequence of ``cu_seqlens``.
+
+    A cache in torch.float8_e4m3fn has ``k_scale`` and ``v_scale`` beside it (fp32 [pages, blocks, HKV], any strides; see
+    :func:`new_cache`): a row is stored in units of its block's scale, the smallest power of two by which the block's
+    values come to 448 at most. A block that has rows already is written again where its scale has to grow. The rows are
+    bf16 or fp32 then, whichever k is, and the queries too."""
     r = (_serve_module or _serve()).append(k, v, k_cache, v_cache, page_table, kv_lens, q, rope, interleaved, cu_seqlens,
-                                           q_out, status)
+                                           q_out, status, k_scale, v_scale)
     if type(r) is int:
         raise KdaError(r, "kda_cache_append")
     return r
 
 
-def cache_attend(q, k_cache, v_cache, page_table, kv_lens, scale=None, window=0, ws=None, out=None, status=None, sinks=0):
+def cache_attend(q, k_cache, v_cache, page_table, kv_lens, scale=None, window=0, ws=None, out=None, status=None, sinks=0,
+                 k_scale=None, v_scale=None):
     """Attention of one new token per sequence over its cached rows: all of them, or, if ``window`` is positive, the last
     ``window`` of them and the first ``sinks``.
 
@@ -398,8 +429,10 @@ def cache_attend(q, k_cache, v_cache, page_table, kv_lens, scale=None, window=0,
     rows to attend, the new token's own among them (none: o is 0 and lse -inf). Returns (o [N,HQ,V], lse fp32
     [N,HQ]): new tensors, or ``out`` as o. ``ws`` (contiguous uint8) is scratch memory, of
     :func:`cache_attend_workspace_bytes` bytes or more; without it, or with less, the call allocates its own for as
-    long as it takes. What it holds does not matter, but two calls that may overlap on the GPU cannot share one."""
-    r = (_serve_module or _serve()).attend(q, k_cache, v_cache, page_table, kv_lens, scale, window, ws, out, status, sinks)
+    long as it takes. What it holds does not matter, but two calls that may overlap on the GPU cannot share one. ``k_scale`` and ``v_scale`` are those of a
+    cache in 8 bits, as in :func:`cache_append`; q, in bf16 or fp32, says o's type then."""
+    r = (_serve_module or _serve()).attend(q, k_cache, v_cache, page_table, kv_lens, scale, window, ws, out, status, sinks,
+                                           k_scale, v_scale)
     if type(r) is int:
         raise KdaError(r, "kda_cache_attend")
     return r
@@ -409,13 +442,18 @@ def cache_attend_workspace_bytes(q, k_cache, v_cache, page_table, window=0, sink
     """Bytes of ``ws`` that :func:`cache_attend` wants for these tensors (their sizes count, and the device)."""
     (N, max_pages), HQ = page_table.shape, q.shape[1]
     pages, rows, heads, K = k_cache.shape
-    dtype = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}.get(k_cache.dtype)
-    if dtype is None:
-        raise TypeError(f"unsupported dtype {k_cache.dtype} of k_cache")
+    dtypes = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32, torch.float8_e4m3fn: DTYPE_E4M3}
+    for t, n in ((k_cache, "k_cache"), (q, "q")):
+        if t.dtype not in dtypes:
+            raise TypeError(f"unsupported dtype {t.dtype} of {n}")
     strides = [s if n > 1 else 0 for t in (k_cache, v_cache) for n, s in zip(t.shape[:3], t.stride())]
-    c = Cache(k_cache.data_ptr(), v_cache.data_ptr(), *strides, pages, rows, heads, K, v_cache.shape[3], dtype)
+    c = Cache(k_cache.data_ptr(), v_cache.data_ptr(), *strides, pages, rows, heads, K, v_cache.shape[3], dtypes[k_cache.dtype])
     with torch.cuda.device(k_cache.device):
-        need = int(load().kda_cache_attend_sinks_workspace_bytes(ctypes.byref(c), HQ, N, max_pages, window, sinks))
+        if k_cache.dtype == torch.float8_e4m3fn:  # (where the scales are does not count)
+            c8 = Cache8(c, k_cache.data_ptr(), v_cache.data_ptr(), 0, 0, 0, 0, 0, 0, 1, dtypes[q.dtype])
+            need = int(load().kda_cache8_attend_workspace_bytes(ctypes.byref(c8), HQ, N, max_pages, window, sinks))
+        else:
+            need = int(load().kda_cache_attend_sinks_workspace_bytes(ctypes.byref(c), HQ, N, max_pages, window, sinks))
     if need == 0:
         raise KdaError(1, "kda_cache_attend_workspace_bytes")
     return need

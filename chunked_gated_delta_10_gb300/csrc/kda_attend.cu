@@ -154,7 +154,8 @@ template <int V> cudaError_t launch_join(const AttendArgs& a, bool bf16, int ht,
         return ht == 8 ? launch_join<__nv_bfloat16, V, 8>(a, parts, st) : launch_join<__nv_bfloat16, V, 16>(a, parts, st);
     return ht == 1   ? launch_join<float, V, 1>(a, parts, st)
            : ht == 4 ? launch_join<float, V, 4>(a, parts, st)
-                     : launch_join<float, V, 8>(a, parts, st);
+           : ht == 8 ? launch_join<float, V, 8>(a, parts, st)
+                     : launch_join<float, V, 16>(a, parts, st);
 }
 
 // Parts of a unit, with equal lengths (kParts, kShares).

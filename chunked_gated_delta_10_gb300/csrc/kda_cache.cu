@@ -191,25 +191,10 @@ extern "C" kda_status kda_cache_append(const kda_cache* c, const void* k, int64_
     const kda_status s = check_cache(c);
     if (s != KDA_OK) return s;
     const int64_t unit = c->dtype == KDA_DTYPE_BF16 ? 8 : 4;
-    if (N < 0 || R < 0 || HQ < 0 || max_pages < 0 || table_stride < 0) return KDA_ERR_INVALID_ARG;
-    if (R > 0 && (N == 0 || (!cu_seqlens && R % N != 0))) return KDA_ERR_INVALID_ARG;
-    if ((HQ > 0) != (q != nullptr) && R > 0) return KDA_ERR_INVALID_ARG;
-    if ((q != nullptr) != (q_out != nullptr)) return KDA_ERR_INVALID_ARG;
-    if (k_stride < (int64_t)c->HKV * c->K || v_stride < (int64_t)c->HKV * c->V || k_stride % unit || v_stride % unit)
-        return KDA_ERR_INVALID_ARG;
-    if (q && (q_stride < (int64_t)HQ * c->K || q_stride % unit)) return KDA_ERR_INVALID_ARG;
-    if (q && q == q_out && q_stride != (int64_t)HQ * c->K) return KDA_ERR_INVALID_ARG;
-    if (rope_dim < 0 || rope_dim % 16 != 0 || rope_dim > c->K || rope_len < 0 || (rope != nullptr) != (rope_dim > 0))
-        return KDA_ERR_INVALID_ARG;
-    if (R == 0) return KDA_OK;
-    if (!k || !v || !kv_lens || (!page_table && max_pages > 0)) return KDA_ERR_INVALID_ARG;
-    for (const void* x : {k, v, q, (const void*)q_out, (const void*)rope})
-        if (!aligned16(x)) return KDA_ERR_INVALID_ARG;
-    if (((uintptr_t)page_table & 3u) || ((uintptr_t)kv_lens & 3u) || ((uintptr_t)status & 3u) ||
-        ((uintptr_t)cu_seqlens & 7u))
-        return KDA_ERR_INVALID_ARG;
-    // (a row's units are counted in 32 bits, in steps of 1024 at most)
-    if (R > INT32_MAX || ((int64_t)HQ + 2 * (int64_t)c->HKV) * 32 > INT32_MAX - 1024) return KDA_ERR_UNSUPPORTED;
+    const AppendCall x{k, k_stride, v, v_stride, q, q_stride, q_out, HQ, N, R, cu_seqlens, rope, rope_len, rope_dim,
+                       page_table, table_stride, max_pages, kv_lens, status};
+    const kda_status checked = check_append(c, x, unit);
+    if (checked != KDA_OK || R == 0) return checked;
     const int64_t uk = (c->K - (interleaved ? 0 : rope_dim / 2)) / unit;
     const int64_t units = (HQ + c->HKV) * uk + c->HKV * (c->V / unit);  // of a row
     const bool few = units <= 64;

@@ -7,15 +7,73 @@
 
 namespace kda {
 
-// The host-side checks that both operators make of the cache description.
-inline kda_status check_cache(const kda_cache* c) {
-    if (!c || c->num_pages < 1 || c->page_size < 1 || c->HKV < 1) return KDA_ERR_INVALID_ARG;
-    if (c->dtype != KDA_DTYPE_BF16 && c->dtype != KDA_DTYPE_F32) return KDA_ERR_INVALID_ARG;
+// The host-side checks that all operators make of the cache description, but for its type; `unit`: elements of 16 bytes.
+inline kda_status check_cache(const kda_cache* c, int64_t unit) {
+    if (c->num_pages < 1 || c->page_size < 1 || c->HKV < 1) return KDA_ERR_INVALID_ARG;
     if (!((c->K == 64 || c->K == 128) && (c->V == 64 || c->V == 128))) return KDA_ERR_UNSUPPORTED;
-    const int64_t unit = c->dtype == KDA_DTYPE_BF16 ? 8 : 4;  // elements of 16 bytes
     for (const int64_t s : {c->k_page, c->k_row, c->k_head, c->v_page, c->v_row, c->v_head})
         if (s < 0 || s % unit != 0) return KDA_ERR_INVALID_ARG;
     if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+inline kda_status check_cache(const kda_cache* c) {
+    if (!c || (c->dtype != KDA_DTYPE_BF16 && c->dtype != KDA_DTYPE_F32)) return KDA_ERR_INVALID_ARG;
+    return check_cache(c, c->dtype == KDA_DTYPE_BF16 ? 8 : 4);
+}
+inline kda_status check_cache(const kda_cache8* c) {
+    if (!c || c->cache.dtype != KDA_DTYPE_E4M3 || (c->dtype != KDA_DTYPE_BF16 && c->dtype != KDA_DTYPE_F32))
+        return KDA_ERR_INVALID_ARG;
+    const kda_status s = check_cache(&c->cache, 16);
+    if (s != KDA_OK) return s;
+    if (c->block < 1 || c->cache.page_size % c->block != 0 || !c->k_scale || !c->v_scale ||
+        ((uintptr_t)c->k_scale & 3u) || ((uintptr_t)c->v_scale & 3u))
+        return KDA_ERR_INVALID_ARG;
+    for (const int64_t x : {c->k_scale_page, c->k_scale_block, c->k_scale_head, c->v_scale_page, c->v_scale_block,
+                            c->v_scale_head})
+        if (x < 0) return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+
+// What an append is given besides the cache.
+struct AppendCall {
+    const void* k;
+    int64_t k_stride;
+    const void* v;
+    int64_t v_stride;
+    const void* q;
+    int64_t q_stride;
+    const void* q_out;
+    int32_t HQ, N;
+    int64_t R;
+    const int64_t* cu_seqlens;
+    const float* rope;
+    int32_t rope_len, rope_dim;
+    const int32_t* page_table;
+    int64_t table_stride;
+    int32_t max_pages;
+    const int32_t *kv_lens, *status;
+};
+// Its checks (`unit`: elements of 16 bytes of the rows).
+inline kda_status check_append(const kda_cache* c, const AppendCall& x, int64_t unit) {
+    if (x.N < 0 || x.R < 0 || x.HQ < 0 || x.max_pages < 0 || x.table_stride < 0) return KDA_ERR_INVALID_ARG;
+    if (x.R > 0 && (x.N == 0 || (!x.cu_seqlens && x.R % x.N != 0))) return KDA_ERR_INVALID_ARG;
+    if ((x.HQ > 0) != (x.q != nullptr) && x.R > 0) return KDA_ERR_INVALID_ARG;
+    if ((x.q != nullptr) != (x.q_out != nullptr)) return KDA_ERR_INVALID_ARG;
+    if (x.k_stride < (int64_t)c->HKV * c->K || x.v_stride < (int64_t)c->HKV * c->V || x.k_stride % unit || x.v_stride % unit)
+        return KDA_ERR_INVALID_ARG;
+    if (x.q && (x.q_stride < (int64_t)x.HQ * c->K || x.q_stride % unit)) return KDA_ERR_INVALID_ARG;
+    if (x.q && x.q == x.q_out && x.q_stride != (int64_t)x.HQ * c->K) return KDA_ERR_INVALID_ARG;
+    if (x.rope_dim < 0 || x.rope_dim % 16 != 0 || x.rope_dim > c->K || x.rope_len < 0 || (x.rope != nullptr) != (x.rope_dim > 0))
+        return KDA_ERR_INVALID_ARG;
+    if (x.R == 0) return KDA_OK;
+    if (!x.k || !x.v || !x.kv_lens || (!x.page_table && x.max_pages > 0)) return KDA_ERR_INVALID_ARG;
+    for (const void* p : {x.k, x.v, x.q, (const void*)x.q_out, (const void*)x.rope})
+        if (!aligned16(p)) return KDA_ERR_INVALID_ARG;
+    if (((uintptr_t)x.page_table & 3u) || ((uintptr_t)x.kv_lens & 3u) || ((uintptr_t)x.status & 3u) ||
+        ((uintptr_t)x.cu_seqlens & 7u))
+        return KDA_ERR_INVALID_ARG;
+    // (a row's units are counted in 32 bits, in steps of 1024 at most)
+    if (x.R > INT32_MAX || ((int64_t)x.HQ + 2 * (int64_t)c->HKV) * 32 > INT32_MAX - 1024) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 

@@ -153,17 +153,32 @@ PyObject* step(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // ------------------------------------------------------------------ the paged cache
 
-struct CacheArgs {
-    kda_cache c;
-    at::ScalarType type;
+struct CacheArgs : kda_cache8 {  // (of a cache in 16 or 32 bits: its `cache` alone)
+    at::ScalarType type;         // of rows, queries and outputs
     at::Device dev;
     const int32_t *table, *lens;
     int64_t table_stride;
     int32_t width, N;
+    bool eight() const { return cache.dtype == KDA_DTYPE_E4M3; }
 };
 
-// k_cache, v_cache [pages, page_size, heads, channels]; page_table [N, width]; kv_lens [N].
-CacheArgs cache_of(PyObject* ko, PyObject* vo, PyObject* table, PyObject* lens) {
+// The scales of a cache in 8 bits, [pages, blocks of a page, heads] in fp32; returns the blocks.
+int64_t scales_of(PyObject* o, const char* name, const kda_cache& c, at::Device dev, float*& p, int64_t& page, int64_t& block,
+                  int64_t& head) {
+    const Tensor& t = cuda_tensor(o, name, 3);
+    if (t.scalar_type() != at::kFloat || t.device() != dev || t.size(0) != c.num_pages || t.size(2) != c.HKV ||
+        t.size(1) < 1 || c.page_size % t.size(1) != 0)
+        refuse(name, "fp32 [pages, blocks, heads] on the cache's device, of blocks that divide its pages", &t);
+    p = t.data_ptr<float>();
+    page = t.size(0) > 1 ? t.stride(0) : 0;
+    block = t.size(1) > 1 ? t.stride(1) : 0;
+    head = t.size(2) > 1 ? t.stride(2) : 0;
+    return t.size(1);
+}
+
+// k_cache, v_cache [pages, page_size, heads, channels]; page_table [N, width]; kv_lens [N]; with a cache in 8 bits the
+// scales, and the rows or queries, which say what type goes in and out.
+CacheArgs cache_of(PyObject* ko, PyObject* vo, PyObject* table, PyObject* lens, PyObject* ks, PyObject* vs, const Tensor& rows) {
     const Tensor &k = cuda_tensor(ko, "k_cache", 4), &v = cuda_tensor(vo, "v_cache", 4);
     if (v.sizes().slice(0, 3) != k.sizes().slice(0, 3) || v.scalar_type() != k.scalar_type() || v.device() != k.device())
         refuse("v_cache", "of k_cache's pages, rows, heads, type and device", &v);
@@ -174,12 +189,24 @@ CacheArgs cache_of(PyObject* ko, PyObject* vo, PyObject* table, PyObject* lens) 
         refuse("page_table", "int32 [N, max_pages] of contiguous rows, on the cache's device", &t);
     // (the stride of a dimension of one says nothing)
     const auto stride = [](const Tensor& c, int i) { return c.size(i) > 1 ? c.stride(i) : 0; };
-    CacheArgs x{{k.data_ptr(), v.data_ptr(), stride(k, 0), stride(k, 1), stride(k, 2), stride(v, 0), stride(v, 1), stride(v, 2),
-                 int32_of(k.size(0), "the number of pages"), int32_of(k.size(1), "the page size"),
-                 int32_of(k.size(2), "the number of heads"), int32_of(k.size(3), "K"), int32_of(v.size(3), "V"),
-                 dtype_of(k, "k_cache")},
+    CacheArgs x{{{k.data_ptr(), v.data_ptr(), stride(k, 0), stride(k, 1), stride(k, 2), stride(v, 0), stride(v, 1),
+                  stride(v, 2), int32_of(k.size(0), "the number of pages"), int32_of(k.size(1), "the page size"),
+                  int32_of(k.size(2), "the number of heads"), int32_of(k.size(3), "K"), int32_of(v.size(3), "V"),
+                  k.scalar_type() == at::kFloat8_e4m3fn ? KDA_DTYPE_E4M3 : dtype_of(k, "k_cache")}},
                 k.scalar_type(), k.device(), t.data_ptr<int32_t>(), nullptr, t.stride(0),
                 int32_of(t.size(1), "max_pages"), int32_of(t.size(0), "N")};
+    if (x.eight()) {
+        TORCH_CHECK_VALUE(x.cache.num_pages > 0 && x.cache.page_size > 0, "k_cache must have pages and rows");
+        x.type = rows.scalar_type();
+        x.dtype = dtype_of(rows, "the rows");
+        kda_cache8& c = x;
+        const int64_t blocks = scales_of(ks, "k_scale", x.cache, x.dev, c.k_scale, c.k_scale_page, c.k_scale_block, c.k_scale_head);
+        if (scales_of(vs, "v_scale", x.cache, x.dev, c.v_scale, c.v_scale_page, c.v_scale_block, c.v_scale_head) != blocks)
+            refuse("v_scale", "of k_scale's blocks", &tensor(vs, "v_scale"));
+        c.block = (int32_t)(x.cache.page_size / blocks);
+    } else {
+        TORCH_CHECK_VALUE(ks == Py_None && vs == Py_None, "k_scale and v_scale are for a cache in float8_e4m3fn");
+    }
     x.lens = (const int32_t*)like(lens, "kv_lens", {t.size(0)}, at::kInt, x.dev);
     return x;
 }
@@ -202,13 +229,14 @@ Rows rows_of(PyObject* o, const char* name, int64_t rows, int64_t heads, int64_t
     return {t.data_ptr(), rows > 1 ? t.stride(0) : heads * channels};
 }
 
-// append(k, v, k_cache, v_cache, page_table, kv_lens, q, rope, interleaved, cu_seqlens, q_out, status)
+// append(k, v, k_cache, v_cache, page_table, kv_lens, q, rope, interleaved, cu_seqlens, q_out, status, k_scale, v_scale)
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    expect(n, 12);
-    const CacheArgs x = cache_of(a[2], a[3], a[4], a[5]);
-    const int64_t R = cuda_tensor(a[0], "k", 3).size(0);
-    const Rows k = rows_of(a[0], "k", R, x.c.HKV, x.c.K, x), v = rows_of(a[1], "v", R, x.c.HKV, x.c.V, x);
+    expect(n, 14);
+    const Tensor& kt = cuda_tensor(a[0], "k", 3);
+    const CacheArgs x = cache_of(a[2], a[3], a[4], a[5], a[12], a[13], kt);
+    const int64_t R = kt.size(0);
+    const Rows k = rows_of(a[0], "k", R, x.cache.HKV, x.cache.K, x), v = rows_of(a[1], "v", R, x.cache.HKV, x.cache.V, x);
     void* cu = like(a[9], "cu_seqlens", {x.N + (int64_t)1}, at::kLong, x.dev, true);
     void* status = like(a[11], "status", {1}, at::kInt, x.dev, true);
     const float* rope = nullptr;
@@ -226,11 +254,11 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t HQ = 0;
     void* op = nullptr;
     const bool given = a[10] != Py_None;
-    int64_t shape[3] = {R, 0, x.c.K};
+    int64_t shape[3] = {R, 0, x.cache.K};
     if (a[6] != Py_None) {
         const Tensor& t = cuda_tensor(a[6], "q", 3);
         HQ = int32_of(t.size(1), "the number of query heads");
-        q = rows_of(a[6], "q", R, HQ, x.c.K, x);
+        q = rows_of(a[6], "q", R, HQ, x.cache.K, x);
         shape[1] = HQ;
         if (given) op = like(a[10], "q_out", shape, x.type, x.dev);
     } else if (given) {
@@ -244,9 +272,12 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
             made = make(shape, x.type, x.dev);
             op = made.data_ptr();
         }
-        s = kda_cache_append(&x.c, k.p, k.stride, v.p, v.stride, q.p, q.stride, op, HQ, x.N, R, (const int64_t*)cu, rope,
-                             positions, turned, inter, x.table, x.table_stride, x.width, x.lens, (int32_t*)status,
-                             stream_of(x.dev));
+        s = x.eight() ? kda_cache8_append(&x, k.p, k.stride, v.p, v.stride, q.p, q.stride, op, HQ, x.N, R,
+                                          (const int64_t*)cu, rope, positions, turned, inter, x.table, x.table_stride,
+                                          x.width, x.lens, (int32_t*)status, stream_of(x.dev))
+                      : kda_cache_append(&x.cache, k.p, k.stride, v.p, v.stride, q.p, q.stride, op, HQ, x.N, R,
+                                         (const int64_t*)cu, rope, positions, turned, inter, x.table, x.table_stride,
+                                         x.width, x.lens, (int32_t*)status, stream_of(x.dev));
     }
     return finish(s, made.defined() ? THPVariable_Wrap(std::move(made)) : Py_NewRef(a[10]));  // (None without q)
     END_HANDLE_TH_ERRORS
@@ -264,19 +295,20 @@ void* untouched(int device) {
     return known[device];
 }
 
-// attend(q, k_cache, v_cache, page_table, kv_lens, scale, window, ws, out, status, sinks)
+// attend(q, k_cache, v_cache, page_table, kv_lens, scale, window, ws, out, status, sinks, k_scale, v_scale)
 PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    expect(n, 11);
-    const CacheArgs x = cache_of(a[1], a[2], a[3], a[4]);
+    expect(n, 13);
     const Tensor& qt = cuda_tensor(a[0], "q", 3);
+    const CacheArgs x = cache_of(a[1], a[2], a[3], a[4], a[11], a[12], qt);
     const int32_t HQ = int32_of(qt.size(1), "the number of query heads"), window = int32_of(whole_of(a[6]), "window"),
                   sinks = int32_of(whole_of(a[10]), "sinks");
-    const Rows q = rows_of(a[0], "q", x.N, HQ, x.c.K, x);
-    const float scale = scale_of(a[5], x.c.K);
+    const Rows q = rows_of(a[0], "q", x.N, HQ, x.cache.K, x);
+    const float scale = scale_of(a[5], x.cache.K);
     void* status = like(a[9], "status", {1}, at::kInt, x.dev, true);
     const c10::cuda::CUDAGuard guard(x.dev);
-    const size_t need = kda_cache_attend_sinks_workspace_bytes(&x.c, HQ, x.N, x.width, window, sinks);
+    const size_t need = x.eight() ? kda_cache8_attend_workspace_bytes(&x, HQ, x.N, x.width, window, sinks)
+                                  : kda_cache_attend_sinks_workspace_bytes(&x.cache, HQ, x.N, x.width, window, sinks);
     void* wp = nullptr;
     size_t room = 0;
     if (a[7] != Py_None) {
@@ -288,7 +320,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
             room = t.numel();
         }
     }
-    const int64_t shape[3] = {x.N, HQ, x.c.V};
+    const int64_t shape[3] = {x.N, HQ, x.cache.V};
     const bool given = a[8] != Py_None;
     void* op = given ? like(a[8], "out", shape, x.type, x.dev) : nullptr;
     Tensor made, lse;
@@ -309,8 +341,12 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
             wp = scratch.get();
             room = need;
         }
-        s = kda_cache_attend_sinks(&x.c, q.p, q.stride, HQ, x.N, x.table, x.table_stride, x.width, x.lens, window, sinks,
-                                   scale, op, (float*)lse.data_ptr(), (int32_t*)status, wp, room, stream_of(x.dev));
+        float* lp = (float*)lse.data_ptr();
+        s = x.eight() ? kda_cache8_attend(&x, q.p, q.stride, HQ, x.N, x.table, x.table_stride, x.width, x.lens, window,
+                                          sinks, scale, op, lp, (int32_t*)status, wp, room, stream_of(x.dev))
+                      : kda_cache_attend_sinks(&x.cache, q.p, q.stride, HQ, x.N, x.table, x.table_stride, x.width, x.lens,
+                                               window, sinks, scale, op, lp, (int32_t*)status, wp, room,
+                                               stream_of(x.dev));
     }
     THPObjectPtr first(given ? Py_NewRef(a[8]) : THPVariable_Wrap(std::move(made))), second(THPVariable_Wrap(std::move(lse)));
     if (!first || !second) throw python_error();

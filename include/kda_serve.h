@@ -7,6 +7,8 @@
  *   kda_cache_append  new keys and values into a paged cache, keys and queries
  *                     rotated by their position on the way
  *   kda_cache_attend  attention of one new token per sequence over that cache
+ *                     (_sinks: a window and a few first rows)
+ *   kda_cache8_*      the same on a cache in 8 bits with a scale for each block
  *
  * Conventions are those of kda.h: device pointers owned by the caller and
  * 16-byte aligned (int32 arrays: 4-byte, int64 arrays: 8-byte), no allocation,
@@ -169,6 +171,63 @@ kda_status kda_cache_attend_sinks(const kda_cache* cache, const void* q, int64_t
                                   int32_t* status, void* ws, size_t ws_bytes, kda_stream_t stream);
 size_t kda_cache_attend_sinks_workspace_bytes(const kda_cache* cache, int32_t HQ, int32_t N, int32_t max_pages,
                                               int32_t window, int32_t sinks);
+
+/*
+ * A paged cache in 8 bits: values in e4m3 (4 bits of exponent, 3 of mantissa,
+ * no infinity), in units of a scale for each block of `block` rows of a page
+ * and head. cache.dtype is KDA_DTYPE_E4M3, its strides multiples of 16. Block b
+ * of a page, rows b block .. (b + 1) block - 1, has for head h the scale
+ *   k_scale[p * k_scale_page + b * k_scale_block + h * k_scale_head]
+ * (strides in elements, non-negative; to append, blocks do not share a scale);
+ * v_scale likewise. `block` divides
+ * page_size. `dtype` is that of the rows appended, of q and of o.
+ */
+#define KDA_DTYPE_E4M3 2
+typedef struct {
+    kda_cache cache;
+    float* k_scale;
+    float* v_scale;
+    int64_t k_scale_page, k_scale_block, k_scale_head;
+    int64_t v_scale_page, v_scale_block, v_scale_head;
+    int32_t block, dtype;
+} kda_cache8;
+
+/*
+ * kda_cache_append into such a cache; arguments and errors are the same. Keys
+ * are rotated in fp32, each product and each sum rounded by itself, and go from
+ * there to 8 bits; q_out is in `dtype`. A block's scale is the smallest power
+ * of two, 2^-126 at least, by which its finite values come to 448 at most, and
+ * a value is stored as x / scale, rounded to the nearest e4m3 (ties to even);
+ * what is not finite becomes a NaN. Of a block that has rows already
+ * (positions below kv_lens[n]) the scale only grows, to what the new rows want
+ * (a scale that is not a power of two: to the next one, 2^126 at most, beyond
+ * which values become a NaN too); its rows are then
+ * written again in the new units, rounded once more where they fall below
+ * e4m3's normal values. Scales of blocks without rows are not read. Rows that
+ * are dropped count for nothing. Two sequences that append to the same page
+ * race.
+ */
+kda_status kda_cache8_append(const kda_cache8* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             const void* q, int64_t q_stride, void* q_out, int32_t HQ, int32_t N, int64_t R,
+                             const int64_t* cu_seqlens, const float* rope, int32_t rope_len, int32_t rope_dim,
+                             int32_t interleaved, const int32_t* page_table, int64_t table_stride, int32_t max_pages,
+                             const int32_t* kv_lens, int32_t* status, kda_stream_t stream);
+
+/*
+ * kda_cache_attend_sinks over such a cache: K[t] and V[t] are the values that
+ * the rows stand for, e4m3 times the block's scale (of any sign and size; not
+ * only those that kda_cache8_append leaves). Scores are sums of exact products
+ * in fp32, of bf16 queries as they are and of fp32 queries to 22 bits. Weights
+ * times the scales of V enter the products as two fp16 values, to 2^-22, or
+ * 2^-35 of the largest. q and o are in `dtype`; arguments, limits and errors
+ * are otherwise the same.
+ */
+kda_status kda_cache8_attend(const kda_cache8* cache, const void* q, int64_t q_stride, int32_t HQ, int32_t N,
+                             const int32_t* page_table, int64_t table_stride, int32_t max_pages, const int32_t* kv_lens,
+                             int32_t window, int32_t sinks, float scale, void* o, float* lse, int32_t* status, void* ws,
+                             size_t ws_bytes, kda_stream_t stream);
+size_t kda_cache8_attend_workspace_bytes(const kda_cache8* cache, int32_t HQ, int32_t N, int32_t max_pages,
+                                         int32_t window, int32_t sinks);
 
 #ifdef __cplusplus
 }

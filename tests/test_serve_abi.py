@@ -144,3 +144,75 @@ def test_attend_sinks_refuses(lib, bad, code):
     assert _sinks(lib, **bad) == code
     assert _sinks(lib, N=0, q=None, o=None) == 0
     assert lib.kda_cache_attend_sinks_workspace_bytes(_cache(), 16, 2, 5, 8, -1) == 0
+
+
+def _cache8(cache=None, **kw):
+    c = dict(cache=_cache(**{**dict(dtype=2, k_page=8 * 64 * 128, v_page=8 * 64 * 64), **(cache or {})}), k_scale=A, v_scale=A,
+             k_scale_page=32, k_scale_block=1, k_scale_head=4, v_scale_page=32, v_scale_block=1, v_scale_head=4, block=16,
+             dtype=0)
+    c.update(kw)
+    return kda.Cache8(**c)
+
+
+BAD_CACHES8 = [(dict(cache=b), code) for b, code in BAD_CACHES if b != dict(k_row=132)] + [
+    (dict(cache=dict(dtype=0)), INVALID), (dict(cache=dict(k_row=136)), INVALID), (dict(block=0), INVALID), (dict(block=-16), INVALID),
+    (dict(block=24), INVALID), (dict(block=128), INVALID), (dict(k_scale=None), INVALID), (dict(v_scale=A + 2), INVALID),
+    (dict(k_scale_page=-1), INVALID), (dict(v_scale_block=-1), INVALID), (dict(v_scale_head=-4), INVALID), (dict(dtype=2), INVALID),
+    (dict(dtype=-1), INVALID)]
+
+
+def _append8(lib, cache=None, **kw):
+    a = dict(k=A, k_stride=1024, v=A, v_stride=512, q=A, q_stride=2048, q_out=2 * A, HQ=16, N=2, R=4, cu=None, rope=A,
+             rope_len=100, rope_dim=64, interleaved=0, table=A, table_stride=5, max_pages=5, lens=A, status=None,
+             stream=None)
+    a.update(kw)
+    return lib.kda_cache8_append(cache or _cache8(), *a.values())
+
+
+def _attend8(lib, cache=None, **kw):
+    a = dict(q=A, q_stride=2048, HQ=16, N=2, table=A, table_stride=5, max_pages=5, lens=A, window=0, sinks=0, scale=0.1, o=A,
+             lse=A, status=None, ws=A, ws_bytes=1 << 30, stream=None)
+    a.update(kw)
+    return lib.kda_cache8_attend(cache or _cache8(), *a.values())
+
+
+@pytest.mark.parametrize("bad, code", BAD_CACHES8)
+def test_cache8_refused(lib, bad, code):
+    assert _append8(lib, _cache8(**bad)) == code
+    assert _attend8(lib, _cache8(**bad)) == code
+    assert lib.kda_cache8_attend_workspace_bytes(_cache8(**bad), 16, 2, 5, 0, 0) == 0
+
+
+@pytest.mark.parametrize("bad", [
+    dict(N=-1), dict(N=0), dict(R=-1), dict(R=5), dict(HQ=0), dict(q=None), dict(q_out=None), dict(k=None), dict(v=A + 8),
+    dict(k_stride=1000), dict(k_stride=1028), dict(q_out=A, q_stride=4096), dict(rope=None), dict(rope_dim=24),
+    dict(rope_dim=144), dict(table=None), dict(lens=None), dict(status=A + 2), dict(cu=A + 4)])
+def test_append8_refuses(lib, bad):
+    assert _append8(lib, **bad) == INVALID
+
+
+def test_append8_refuses_shared_scales(lib):
+    for name in ("k_scale_page", "v_scale_block", "v_scale_head"):
+        assert _append8(lib, _cache8(**{name: 0})) == INVALID
+
+
+def test_cache8_of_nothing(lib):
+    assert _append8(lib, R=0, k=None, v=None) == 0
+    assert _append8(lib, R=2**31, N=2) == UNSUPPORTED
+    assert _append8(lib, _cache8(block=1), R=2**31 - 2, cu=A, HQ=0, q=None, q_out=None) == UNSUPPORTED  # too many CTAs
+    assert lib.kda_cache8_append(None, *([None, 0] * 3), None, 0, 0, 0, None, None, 0, 0, 0, None, 0, 0, None, None,
+                                 None) == INVALID
+    assert _attend8(lib, N=0, q=None, o=None) == 0
+    assert lib.kda_cache8_attend_workspace_bytes(_cache8(), 16, 2, 5, 0, 0) > 0
+
+
+@pytest.mark.parametrize("bad, code", [
+    (dict(N=-1), INVALID), (dict(HQ=12), INVALID), (dict(window=-1), INVALID), (dict(sinks=-1), INVALID), (dict(q=None), INVALID),
+    (dict(q_stride=2052), INVALID), (dict(o=A + 4), INVALID), (dict(ws=None), WORKSPACE), (dict(ws_bytes=8), WORKSPACE),
+    (dict(max_pages=2**26), UNSUPPORTED), (dict(N=2**28), UNSUPPORTED)])
+def test_attend8_refuses(lib, bad, code):
+    assert _attend8(lib, **bad) == code
+
+
+def test_the_structure_of_a_cache_in_8_bits():
+    assert ctypes.sizeof(kda.Cache8) == 8 * 8 + 6 * 4 + 8 * 8 + 2 * 4
