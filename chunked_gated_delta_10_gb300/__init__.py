@@ -24,7 +24,7 @@ from .build import LIB, SERVE, build  # noqa: F401
 
 __all__ = ["build", "load", "Dims", "prepare_chunks", "workspace_bytes", "saved_bytes", "chunk_fwd", "chunk_bwd",
            "chunk_fwd_save", "chunk_bwd_from_saved", "step", "new_cache", "cache_append", "cache_attend",
-           "cache_attend_workspace_bytes", "KdaError", "STATUS", "DTYPE_BF16", "DTYPE_F32", "DTYPE_E4M3", "PASS_FWD", "PASS_BWD"]
+           "cache_attend_workspace_bytes", "cache_resize", "KdaError", "STATUS", "DTYPE_BF16", "DTYPE_F32", "DTYPE_E4M3", "PASS_FWD", "PASS_BWD"]
 
 DTYPE_BF16, DTYPE_F32, DTYPE_E4M3 = 0, 1, 2
 PASS_FWD, PASS_BWD = 0, 1
@@ -136,6 +136,11 @@ def load():
             lib.kda_cache8_attend.argtypes = [ctypes.POINTER(Cache8)] + lib.kda_cache_attend_sinks.argtypes[1:]
             lib.kda_cache8_attend_workspace_bytes.restype = ctypes.c_size_t
             lib.kda_cache8_attend_workspace_bytes.argtypes = [ctypes.POINTER(Cache8), i32, i32, i32, i32, i32]
+            lib.kda_cache_resize.restype = ctypes.c_int
+            lib.kda_cache_resize.argtypes = [_P, i64, i32, i32, i32, _P, _P, _P, i32, _P, _P, _P, i64, _P, _P, _P,
+                                             ctypes.c_size_t, _P]
+            lib.kda_cache_resize_workspace_bytes.restype = ctypes.c_size_t
+            lib.kda_cache_resize_workspace_bytes.argtypes = [i32, i32, i64]
             _lib = lib
     return _lib
 
@@ -457,3 +462,23 @@ def cache_attend_workspace_bytes(q, k_cache, v_cache, page_table, window=0, sink
     if need == 0:
         raise KdaError(1, "kda_cache_attend_workspace_bytes")
     return need
+
+
+def cache_resize(page_table, kv_lens, new_lens, free_pages, free_count, page_size, rows=0, status=None):
+    """Pages for new lengths: a paged cache's table brought from ``kv_lens`` to ``new_lens`` rows, on the GPU alone.
+
+    ``page_table`` int32 [N, max_pages], changed in place: entries that ``new_lens`` (int32 [N]) needs beyond those of
+    ``kv_lens`` (int32 [N]; negative: none) are filled, entries that it does not need become -1. The pages come from the
+    end of ``free_pages`` (int32 [pages of the cache]), of which the first ``free_count`` (int32 [1]) are free, and go to
+    it: all that go back first, so that they can be taken in the same call. A sequence whose pages, after those of the
+    sequences before it, are not there gets none.
+
+    Returns (cu_seqlens int64 [N+1], slots int64 [``rows``], granted int32 [N]): the new rows' offsets as
+    :func:`cache_append` takes them; where each new row goes, its page times ``page_size`` plus its row in the page, or -1
+    (of a sequence that was not served, and behind the last new row); and each sequence's length now, ``new_lens`` or,
+    not served, ``kv_lens``. ``status`` (int32 [1], zeroed by the caller) is set where a sequence is not served, an entry
+    is no page, or the new rows are more than ``rows``, if that is not 0."""
+    r = (_serve_module or _serve()).resize(page_table, kv_lens, new_lens, free_pages, free_count, page_size, rows, status)
+    if type(r) is int:
+        raise KdaError(r, "kda_cache_resize")
+    return r

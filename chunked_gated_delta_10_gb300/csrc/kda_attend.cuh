@@ -7,20 +7,6 @@
 namespace kda {
 namespace attend {
 
-// Division of numbers below 2^31 by an invariant d (Granlund and Montgomery, 1994): with 2^s >= d, floor(n / d) =
-// floor(n ceil(2^(31 + s) / d) / 2^(31 + s)).
-struct Divisor {
-    unsigned factor, shift;
-    Divisor() = default;
-    __host__ explicit Divisor(unsigned d) : shift(31) {
-        while (1ull << (shift - 31) < d) ++shift;
-        factor = (unsigned)(((1ull << shift) + d - 1) / d);
-    }
-    __device__ __forceinline__ unsigned operator()(unsigned n) const {
-        return (unsigned)((uint64_t)n * factor >> shift);
-    }
-};
-
 // How the rows are given to CTAs (see Work).
 enum Split { kWhole, kCluster, kParts, kShares };
 

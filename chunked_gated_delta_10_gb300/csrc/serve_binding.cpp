@@ -354,10 +354,55 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// ------------------------------------------------------------------ kda_cache_resize
+
+// resize(page_table, kv_lens, new_lens, free_pages, free_count, page_size, rows, status)
+PyObject* resize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 8);
+    const Tensor& t = cuda_tensor(a[0], "page_table", 2);
+    if (t.scalar_type() != at::kInt || (t.size(1) > 1 && t.stride(1) != 1))
+        refuse("page_table", "int32 [N, max_pages] of contiguous rows", &t);
+    const auto dev = t.device();
+    const int64_t N = t.size(0), rows = whole_of(a[6]);
+    TORCH_CHECK_VALUE(rows >= 0, "rows must not be negative");
+    void* lens = like(a[1], "kv_lens", {N}, at::kInt, dev);
+    void* wanted = like(a[2], "new_lens", {N}, at::kInt, dev);
+    const Tensor& list = cuda_tensor(a[3], "free_pages", 1);
+    void* free = like(a[3], "free_pages", list.sizes(), at::kInt, dev);
+    void* count = like(a[4], "free_count", {1}, at::kInt, dev);
+    void* status = like(a[7], "status", {1}, at::kInt, dev, true);
+    const int32_t width = int32_of(t.size(1), "max_pages"), size = int32_of(whole_of(a[5]), "page_size"),
+                  pages = int32_of(list.numel(), "the number of pages"), seqs = int32_of(N, "N");
+    // (the stride of a dimension of one says nothing)
+    const int64_t stride = N > 1 ? t.stride(0) : t.size(1);
+    const c10::cuda::CUDAGuard guard(dev);
+    const size_t need = kda_cache_resize_workspace_bytes(seqs, width, rows);
+    Tensor cu, slots, granted;
+    kda_status s;
+    {
+        const WithoutGil others;
+        cu = make({N + 1}, at::kLong, dev);
+        slots = make({rows}, at::kLong, dev);
+        granted = make({N}, at::kInt, dev);
+        c10::DataPtr scratch;  // (its memory is free again for what follows on this stream)
+        if (need > 0) scratch = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+        s = kda_cache_resize(t.data_ptr<int32_t>(), stride, width, seqs, size, (const int32_t*)lens, (const int32_t*)wanted,
+                             (int32_t*)free, pages, (int32_t*)count, cu.data_ptr<int64_t>(),
+                             rows > 0 ? slots.data_ptr<int64_t>() : nullptr, rows, (int32_t*)granted.data_ptr(),
+                             (int32_t*)status, scratch.get(), need, stream_of(dev));
+    }
+    THPObjectPtr x(THPVariable_Wrap(std::move(cu))), y(THPVariable_Wrap(std::move(slots))), z(THPVariable_Wrap(std::move(granted)));
+    if (!x || !y || !z) throw python_error();
+    return finish(s, PyTuple_Pack(3, x.get(), y.get(), z.get()));
+    END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
     {"step", (PyCFunction)(void*)step, METH_FASTCALL, "kda_step"},
-    {"append", (PyCFunction)(void*)append, METH_FASTCALL, "kda_cache_append"},
-    {"attend", (PyCFunction)(void*)attend, METH_FASTCALL, "kda_cache_attend_sinks"},
+    {"append", (PyCFunction)(void*)append, METH_FASTCALL, "kda_cache_append, kda_cache8_append"},
+    {"attend", (PyCFunction)(void*)attend, METH_FASTCALL, "kda_cache_attend_sinks, kda_cache8_attend"},
+    {"resize", (PyCFunction)(void*)resize, METH_FASTCALL, "kda_cache_resize"},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_serve", nullptr, -1, methods};

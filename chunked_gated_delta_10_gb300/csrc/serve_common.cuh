@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cstdint>
 
 namespace kda {
 
@@ -50,6 +51,20 @@ inline int largest_cluster(int device, const void* kernel, int threads, int most
     if (device < kDevices) known[device].store(n, std::memory_order_relaxed);
     return n;
 }
+
+// Division of numbers below 2^31 by an invariant d (Granlund and Montgomery, 1994): with 2^s >= d, floor(n / d) =
+// floor(n ceil(2^(31 + s) / d) / 2^(31 + s)).
+struct Divisor {
+    unsigned factor, shift;
+    Divisor() = default;
+    __host__ explicit Divisor(unsigned d) : shift(31) {
+        while (1ull << (shift - 31) < d) ++shift;
+        factor = (unsigned)(((1ull << shift) + d - 1) / d);
+    }
+    __device__ __forceinline__ unsigned operator()(unsigned n) const {
+        return (unsigned)((uint64_t)n * factor >> shift);
+    }
+};
 
 // Every thread of a kernel launched by launch_after calls this first, whatever it does then: a kernel that ended
 // without having waited would let the one after it start before the one before it has ended.

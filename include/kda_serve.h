@@ -9,6 +9,7 @@
  *   kda_cache_attend  attention of one new token per sequence over that cache
  *                     (_sinks: a window and a few first rows)
  *   kda_cache8_*      the same on a cache in 8 bits with a scale for each block
+ *   kda_cache_resize  pages for new lengths: page tables, slots and offsets
  *
  * Conventions are those of kda.h: device pointers owned by the caller and
  * 16-byte aligned (int32 arrays: 4-byte, int64 arrays: 8-byte), no allocation,
@@ -228,6 +229,50 @@ kda_status kda_cache8_attend(const kda_cache8* cache, const void* q, int64_t q_s
                              size_t ws_bytes, kda_stream_t stream);
 size_t kda_cache8_attend_workspace_bytes(const kda_cache8* cache, int32_t HQ, int32_t N, int32_t max_pages,
                                          int32_t window, int32_t sinks);
+
+/*
+ * Pages for new lengths of N sequences, from a list of free pages and back to
+ * it, and where their new rows go. Sequence n holds the pages of its
+ * kv_lens[n] rows, ceil(kv_lens[n] / page_size) entries of its row of the page
+ * table; new_lens[n] rows want ceil(new_lens[n] / page_size). A negative length
+ * counts as 0. In this order:
+ *   1. pages beyond the new length go back: those of sequence 0 first, each
+ *      sequence's in the order of its rows; their entries become -1;
+ *   2. missing pages are taken, for sequence 0 first and in the order of its
+ *      rows. A sequence is served if its pages and those of all before it are
+ *      there, and it wants no more than max_pages; if not it gets none, keeps
+ *      those it has, and status is set.
+ *   page_table  int32 [N, max_pages], row stride table_stride; other entries
+ *               stay as they are
+ *   free_pages  int32 [num_pages], of which the first free_count[0] are the
+ *               free pages; pages come from its end and go to its end. An entry
+ *               that goes back is moved as it is (status is set where it is no
+ *               page of [0, num_pages), or the list has no room for it: then it
+ *               is dropped); one that is taken and is no page becomes -1, and
+ *               status is set.
+ *   cu_seqlens  int64 [N + 1], nullable: the new rows of each sequence,
+ *               max(0, new_lens[n] - kv_lens[n]) of them, one sequence after the
+ *               other, as kda_cache_append takes them
+ *   slots       int64 [rows], nullable: of each new row, its page * page_size
+ *               plus its row in the page; -1 where it has no page or its
+ *               sequence was not served, and behind the last new row. Where
+ *               there are more than `rows`, status is set.
+ *   granted     int32 [N], nullable: new_lens[n], or kv_lens[n] where the
+ *               sequence was not served
+ *   status      int32, nullable
+ *   ws          kda_cache_resize_workspace_bytes(N, max_pages, rows) bytes, 16-byte
+ *               aligned (NULL where that is 0)
+ * Kernel launches only: nothing waits for the host. Overlapping calls on the
+ * same table, list or workspace race. N == 0 is KDA_OK; cu_seqlens and slots are
+ * written all the same. N is at most 65535, N * max_pages at most 2^30 and rows
+ * at most 2^31 - 1 (else KDA_ERR_UNSUPPORTED). Errors: KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED,
+ * KDA_ERR_WORKSPACE before any launch; KDA_ERR_CUDA if a launch fails.
+ */
+kda_status kda_cache_resize(int32_t* page_table, int64_t table_stride, int32_t max_pages, int32_t N, int32_t page_size,
+                            const int32_t* kv_lens, const int32_t* new_lens, int32_t* free_pages, int32_t num_pages,
+                            int32_t* free_count, int64_t* cu_seqlens, int64_t* slots, int64_t rows, int32_t* granted,
+                            int32_t* status, void* ws, size_t ws_bytes, kda_stream_t stream);
+size_t kda_cache_resize_workspace_bytes(int32_t N, int32_t max_pages, int64_t rows);
 
 #ifdef __cplusplus
 }

@@ -216,3 +216,29 @@ def test_attend8_refuses(lib, bad, code):
 
 def test_the_structure_of_a_cache_in_8_bits():
     assert ctypes.sizeof(kda.Cache8) == 8 * 8 + 6 * 4 + 8 * 8 + 2 * 4
+
+
+def _resize(lib, **kw):
+    a = dict(table=A, table_stride=8, max_pages=8, N=2, page_size=16, lens=A, wanted=A, free=A, num_pages=16, count=A, cu=A,
+             slots=A, rows=9000, granted=A, status=A, ws=A, ws_bytes=1 << 20, stream=None)
+    a.update(kw)
+    return lib.kda_cache_resize(*a.values())
+
+
+@pytest.mark.parametrize("bad, code", [
+    (dict(max_pages=-1), INVALID), (dict(N=-1), INVALID), (dict(page_size=0), INVALID), (dict(num_pages=-1), INVALID),
+    (dict(rows=-1), INVALID), (dict(table_stride=-8), INVALID), (dict(table_stride=7), INVALID), (dict(lens=None), INVALID),
+    (dict(wanted=None), INVALID), (dict(table=None), INVALID), (dict(free=None), INVALID), (dict(count=None), INVALID),
+    (dict(table=A + 2), INVALID), (dict(lens=A + 1), INVALID), (dict(wanted=A + 2), INVALID), (dict(free=A + 2), INVALID),
+    (dict(count=A + 2), INVALID), (dict(cu=A + 4), INVALID), (dict(slots=A + 4), INVALID), (dict(granted=A + 2), INVALID),
+    (dict(status=A + 1), INVALID), (dict(ws=None), WORKSPACE), (dict(ws=A + 8), WORKSPACE), (dict(ws_bytes=16), WORKSPACE),
+    (dict(N=65536), UNSUPPORTED), (dict(rows=2**31), UNSUPPORTED),
+    (dict(max_pages=2**30, table_stride=2**30), UNSUPPORTED)])
+def test_resize_refuses(lib, bad, code):
+    assert _resize(lib, **bad) == code
+
+
+def test_resize_workspace(lib):
+    need = lib.kda_cache_resize_workspace_bytes
+    assert need(1, 1, 1) == 0 and need(0, 0, 0) == 0 and need(-1, 1, 1) == 0  # one CTA, no workspace
+    assert need(2, 8, 9000) == (2 * 2 + 3) * 8 and need(2000, 1, 0) > 0
