@@ -7,8 +7,19 @@
 // more than s_old, c_old <- e4m3(c_old s_old / s). A power of two divides without rounding, so a value is rounded once, and
 // again only where it comes to lie below e4m3's normal values.
 //
-// A warp has a block of one head, of keys or of values, to itself, so that nothing is shared: it finds the largest value,
-// then writes. Queries, which go on in their own type, are rows of other CTAs of the same launch.
+// Bound: every new row is read once and written once in half or a quarter of its bytes, every query read and written.
+//   Several rows of each sequence: tiles of 16 rows or more in whole blocks, eight threads to a row, one head after the
+//     other. A thread keeps its angles for all heads; rows come in ahead of their use through shared memory (cp.async: without
+//     it 4 us more); the largest value of a block is an atomicMax in shared memory, whose order does not matter. 16 packed
+//     prompts of U[1,4096] tokens, 32 query and 8 cache heads of 128, bf16, blocks of 16 (760 MB): 126 us, 6.0 TB/s, of which
+//     the cache's 202 MB take 42 (70 % of the issue slots: 260 instructions for 16 values of a thread, before pairs of
+//     values went to one instruction and divisions to multiplications; now about 200) and the queries 84, at 95 % of a
+//     plain copy's rate. A warp to a block of one head, which reads the rows twice and angles for each head: 163 us.
+//   Few rows of each sequence (less than 8 on average) or blocks longer than 128: a warp has a block of one head to itself.
+//     One token of each of 128 sequences 4.1 us in a graph, of one 2.4 (tiles, most of whose threads have no row: 5.2 to 13
+//     and 2.5; from 8 rows on they are faster: 16 x 16 rows 4.4 and 8.1 us).
+//   Queries go with the same launch where that is small, as CTAs of their own, and otherwise to a launch of 64 threads a
+//     CTA, 16 to an SM (20 and 12 of them: 133 and 137 us for the prompts above, of 128 threads: 142).
 #include <cfloat>
 
 #include "kda_cache.cuh"
@@ -17,7 +28,7 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 128, kWarps = kThreads / 32;
-constexpr int kHeld = 4;  // turns of a block's rows that a warp holds in registers
+constexpr int kTileThreads = 1024;  // at most
 
 struct Append8Args {
     kda_cache8 c;
@@ -32,84 +43,139 @@ struct Append8Args {
     const int32_t *table, *kv_lens;
     int max_pages;
     int32_t* status;
-    unsigned items, splits;  // blocks of rows, at most; CTAs of each
-    unsigned most;           // blocks of a sequence, where there is no cu
+    int unit;                  // rows of an item: of a block, or of a tile of blocks
+    unsigned items, splits;    // items, at most; CTAs of each
+    unsigned most;             // items of a sequence, where there is no cu
     unsigned q_lanes, q_rows;  // query rows: threads of a row, rows of a CTA
+    Divisor by_unit, by_most, by_per, by_block, by_page;
+};
+// The page of a position. (Divisor is for numbers below 2^31.)
+__device__ __forceinline__ unsigned page_of(const Append8Args& a, unsigned pos) {
+    return pos < 1u << 31 ? a.by_page(pos) : pos / (unsigned)a.c.cache.page_size;
+}
+
+// Two fp32 values to an instruction; each is rounded as by itself.
+struct Two {
+    uint64_t v;
+    __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ Two operator*(Two a, const Two& b) {
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+    return a;
+}
+__device__ __forceinline__ Two operator+(Two a, const Two& b) {
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+    return a;
+}
+
+// C channels of a row (4 or 8) as they are.
+template <typename TI, int C> struct Run {
+    static constexpr int kBytes = C * sizeof(TI);
+    uint32_t w[kBytes / 4];
+    __device__ __forceinline__ void load(const TI* p) {
+        if constexpr (kBytes == 8) {
+            const uint2 x = *(const uint2*)p;
+            w[0] = x.x, w[1] = x.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kBytes / 16; ++i) {
+                const uint4 x = ((const uint4*)p)[i];
+                w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void store(TI* p) const {
+        if constexpr (kBytes == 8) {
+            *(uint2*)p = make_uint2(w[0], w[1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kBytes / 16; ++i) ((uint4*)p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+    }
+    __device__ __forceinline__ void values(float* x) const {
+#pragma unroll
+        for (int i = 0; i < kBytes / 4; ++i) {
+            if constexpr (sizeof(TI) == 2) {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            } else {
+                x[i] = __uint_as_float(w[i]);
+            }
+        }
+    }
+    __device__ __forceinline__ void set(const float* x) {
+#pragma unroll
+        for (int i = 0; i < kBytes / 4; ++i) {
+            if constexpr (sizeof(TI) == 2) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *(const uint32_t*)&b;
+            } else {
+                w[i] = __float_as_uint(x[i]);
+            }
+        }
+    }
 };
 
-// 8 channels of a row in fp32, and back.
-__device__ __forceinline__ void load_8(const __nv_bfloat16* p, float* x) {
-    Unit<__nv_bfloat16>::load(p, *(float(*)[8])x);
-}
-__device__ __forceinline__ void load_8(const float* p, float* x) {
-    Unit<float>::load(p, *(float(*)[4])x);
-    Unit<float>::load(p + 4, *(float(*)[4])(x + 4));
-}
-__device__ __forceinline__ void store_8(__nv_bfloat16* p, const float* x) {
-    Unit<__nv_bfloat16>::store(p, *(const float(*)[8])x);
-}
-__device__ __forceinline__ void store_8(float* p, const float* x) {
-    Unit<float>::store(p, *(const float(*)[4])x);
-    Unit<float>::store(p + 4, *(const float(*)[4])(x + 4));
-}
-
-// A lane's share of a row: 8 channels from `a` on and 8 from `b` on. Where they turn, channel a + i turns with b + i, or,
-// in pairs, with its neighbour.
-struct Share {
+// A lane's share of a row: C channels from `a` on and C from `b` on. Where they turn, channel a + i turns with b + i, or, in
+// pairs, with its neighbour. (rope_dim is a multiple of 16.)
+template <int C> struct Share {
     int a, b;
     bool turns;
     __device__ __forceinline__ Share(int u, int rope_dim, int interleaved) {
-        const int pairs = interleaved ? 0 : rope_dim / 16;
-        turns = u < (interleaved ? rope_dim / 16 : pairs);
-        a = u < pairs ? 8 * u : 16 * u;
-        b = u < pairs ? 8 * u + rope_dim / 2 : 16 * u + 8;
+        const int apart = interleaved ? 0 : rope_dim / (2 * C);
+        turns = u < rope_dim / (2 * C);
+        a = u < apart ? C * u : 2 * C * u;
+        b = u < apart ? C * u + rope_dim / 2 : 2 * C * u + C;
+    }
+};
+// The cosines and sines of a lane's share at a position.
+template <int C> struct Angles {
+    float co[C], si[C];
+    __device__ __forceinline__ void load(const Share<C>& s, const float* rope, int64_t pos, int rope_dim, int interleaved) {
+        const float* p = rope + pos * rope_dim + (interleaved ? s.a / 2 : s.a);
+        Run<float, C> x, y;
+        x.load(p);
+        y.load(p + rope_dim / 2);
+        x.values(co);
+        y.values(si);
+    }
+    // Channels p and q of angles i and i + 1.
+    __device__ __forceinline__ void pair(float& p0, float& p1, float& q0, float& q1, int i) const {
+        const Two p(p0, p1), q(q0, q1), c(co[i], co[i + 1]);
+        (p * c + q * Two(-si[i], -si[i + 1])).get(p0, p1);
+        (q * c + p * Two(si[i], si[i + 1])).get(q0, q1);
+    }
+    // The rotation, each product and each sum rounded by itself (so that the scales, which go by the largest value, do not
+    // depend on how a compiler joins them).
+    __device__ __forceinline__ void turn(float (&x)[2 * C], int interleaved) const {
+        if (interleaved) {
+#pragma unroll
+            for (int i = 0; i < C; i += 2) pair(x[2 * i], x[2 * i + 2], x[2 * i + 1], x[2 * i + 3], i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < C; i += 2) pair(x[i], x[i + 1], x[C + i], x[C + i + 1], i);
+        }
     }
 };
 
-// The rotation, each product and each sum rounded by itself (so that the scales, which go by the largest value, do not
-// depend on how a compiler joins them). cs: the position's cosines and sines.
-__device__ __forceinline__ void turn(float (&x)[16], const Share& s, const float* cs, int rope_dim, int interleaved) {
-    const int half = rope_dim / 2;
-    if (interleaved) {
-        float co[8], si[8];
-        load_8(cs + s.a / 2, co);
-        load_8(cs + half + s.a / 2, si);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float p = x[2 * i], q = x[2 * i + 1];
-            x[2 * i] = __fsub_rn(__fmul_rn(p, co[i]), __fmul_rn(q, si[i]));
-            x[2 * i + 1] = __fadd_rn(__fmul_rn(q, co[i]), __fmul_rn(p, si[i]));
-        }
-    } else {
-        float co[8], si[8];
-        load_8(cs + s.a, co);
-        load_8(cs + half + s.a, si);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float p = x[i], q = x[8 + i];
-            x[i] = __fsub_rn(__fmul_rn(p, co[i]), __fmul_rn(q, si[i]));
-            x[8 + i] = __fadd_rn(__fmul_rn(q, co[i]), __fmul_rn(p, si[i]));
-        }
-    }
+// 4 values times f as e4m3 (a NaN as one; an infinite value would become the largest).
+__device__ __forceinline__ uint32_t to_e4m3(const float* x, float f) {
+    float y[4];
+    (Two(x[0], x[1]) * Two(f, f)).get(y[0], y[1]);
+    (Two(x[2], x[3]) * Two(f, f)).get(y[2], y[3]);
+    uint32_t w;
+    asm("{.reg .b16 lo, hi; cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1; cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;"
+        " mov.b32 %0, {lo, hi};}"
+        : "=r"(w)
+        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]));
+    return w;
 }
-
-// 8 values times f as e4m3; what is not finite becomes a NaN (x 0 + x), which rounding alone would make the largest value.
-__device__ __forceinline__ uint2 to_e4m3(const float* x, float f) {
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        float y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            y[e] = x[4 * i + e] * f;
-            y[e] = fmaf(y[e], 0.f, y[e]);
-        }
-        asm("{.reg .b16 lo, hi; cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1; cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;"
-            " mov.b32 %0, {lo, hi};}"
-            : "=r"(w[i])
-            : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]));
-    }
-    return make_uint2(w[0], w[1]);
+template <int C> __device__ __forceinline__ void store_e4m3(unsigned char* p, const float* x, float f) {
+    if constexpr (C == 8)
+        *(uint2*)p = make_uint2(to_e4m3(x, f), to_e4m3(x + 4, f));
+    else
+        *(uint32_t*)p = to_e4m3(x, f);
 }
 // 4 e4m3 values in fp32.
 __device__ __forceinline__ void from_e4m3(uint32_t x, float* y) {
@@ -130,6 +196,46 @@ __device__ __forceinline__ int held_scale(float s) {
     return bits >= 0x7f800000 || bits == 0 ? 0 : min(max((bits + 0x7fffff) >> 23, 1), 253);
 }
 
+// N old values in the units of another scale (ratio: old to new; of one that is not finite they are NaNs).
+template <int N> __device__ __forceinline__ void again(unsigned char* p, float ratio) {
+    uint32_t* w = (uint32_t*)p;
+    if (!(fabsf(ratio) <= FLT_MAX)) ratio = NAN;
+    uint32_t old[N / 4];
+    if constexpr (N == 16) {
+        const uint4 x = *(const uint4*)p;
+        old[0] = x.x, old[1] = x.y, old[2] = x.z, old[3] = x.w;
+    } else {
+        const uint2 x = *(const uint2*)p;
+        old[0] = x.x, old[1] = x.y;
+    }
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+        float y[4];
+        from_e4m3(old[i], y);
+        if (fabsf(ratio) > 1.f) {  // (a scale above 2^126: what it makes larger than 448 2^126 is not held)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (fabsf(y[e] * ratio) > 448.f) y[e] = NAN;
+        }
+        w[i] = to_e4m3(y, ratio);
+    }
+}
+// The largest finite magnitude; infinite values become NaNs.
+template <int N> __device__ __forceinline__ float largest(float (&x)[N]) {
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) top = fmaxf(top, fabsf(x[e]));  // (not of a NaN)
+    if (top == INFINITY) {
+        top = 0.f;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            if (fabsf(x[e]) == INFINITY) x[e] = NAN;
+            top = fmaxf(top, fabsf(x[e]));
+        }
+    }
+    return top;
+}
+
 // Rows [first, last) of the positions of a block that begins at `start`, of one head: D channels each of `x`, whose row of
 // position `first` is at `from` (rows `stride` apart), into `to`, position `start`'s row of the cache, rows `step` apart.
 template <typename TI, int D>
@@ -138,71 +244,54 @@ __device__ __forceinline__ void write_block(const Append8Args& a, const TI* from
                                             unsigned last, bool rotated) {
     constexpr int L = D / 16, P = 32 / L;  // lanes of a row, rows of a turn
     const int lane = threadIdx.x % 32, in = lane / L;
-    const Share s(lane % L, rotated ? a.rope_dim : 0, rotated ? a.interleaved : 1);
+    const Share<8> s(lane % L, rotated ? a.rope_dim : 0, a.interleaved);
     const float before = start < old_end ? *scale : 0.f;
     const unsigned rows = last - first;
-    float x[kHeld][16], top = 0.f;
-    const auto load = [&](unsigned row, float (&y)[16]) {
+    float x[16], top = 0.f;
+    const auto load = [&](unsigned row) {
         const TI* p = from + (int64_t)row * stride;
-        load_8(p + s.a, y);
-        load_8(p + s.b, y + 8);
-        if (s.turns) turn(y, s, a.rope + (int64_t)(first + row) * a.rope_dim, a.rope_dim, a.interleaved);
+        Run<TI, 8> lo, hi;
+        Angles<8> angles;
+        lo.load(p + s.a);
+        hi.load(p + s.b);
+        if (s.turns) angles.load(s, a.rope, first + row, a.rope_dim, a.interleaved);
+        lo.values(x);
+        hi.values(x + 8);
+        if (s.turns) angles.turn(x, a.interleaved);
     };
-    for (unsigned at = 0; at < rows; at += kHeld * P) {
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            const unsigned row = at + i * P + in;
-            if (row >= rows) continue;
-            load(row, x[i]);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float m = fabsf(x[i][e]);
-                if (m <= FLT_MAX) top = fmaxf(top, m);
-            }
-        }
+#pragma unroll 1
+    for (unsigned row = in; row < rows; row += P) {
+        load(row);
+        top = fmaxf(top, largest(x));
     }
 #pragma unroll
     for (int w = 1; w < 32; w *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
     const int field = max(least_scale(top), held_scale(before));
     const float now = __int_as_float(field << 23), f = __int_as_float((254 - field) << 23);
-    if (start < old_end && before != now) {  // the block's rows in the new units
-        const float ratio = before * f;
-        for (unsigned row = in; row < old_end - start; row += P) {
-            uint4* p = (uint4*)(to + row * step + (lane % L) * 16);
-            const uint4 old = *p;
-            float y[16];
-            from_e4m3(old.x, y), from_e4m3(old.y, y + 4), from_e4m3(old.z, y + 8), from_e4m3(old.w, y + 12);
-            if (fabsf(ratio) > 1.f) {  // (a scale above 2^126: what it makes larger than 448 2^126 is not held)
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (fabsf(y[e] * ratio) > 448.f) y[e] = INFINITY;
-            }
-            const uint2 lo = to_e4m3(y, ratio), hi = to_e4m3(y + 8, ratio);
-            *p = make_uint4(lo.x, lo.y, hi.x, hi.y);
-        }
-    }
+    if (start < old_end && before != now)  // the block's rows in the new units
+#pragma unroll 2
+        for (unsigned row = in; row < old_end - start; row += P) again<16>(to + row * step + (lane % L) * 16, before * f);
     if (lane == 0 && before != now) *scale = now;
-    for (unsigned at = 0; at < rows; at += kHeld * P) {
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            const unsigned row = at + i * P + in;
-            if (row >= rows) continue;
-            if (rows > kHeld * P) load(row, x[i]);
-            unsigned char* p = to + (first - start + row) * step;
-            *(uint2*)(p + s.a) = to_e4m3(x[i], f);
-            *(uint2*)(p + s.b) = to_e4m3(x[i] + 8, f);
+#pragma unroll 1
+    for (unsigned row = in; row < rows; row += P) {
+        if (rows > P) {
+            load(row);
+            largest(x);
         }
+        unsigned char* p = to + (first - start + row) * step;
+        store_e4m3<8>(p + s.a, x, f);
+        store_e4m3<8>(p + s.b, x + 8, f);
     }
 }
 
-// The sequence that new row r or, with `block`, block r of the launch's belongs to: the last n that begins at or before it.
-// A sequence whose first row is cu[n] has blocks from cu[n] / block + 2 n on: two more than its rows fill, as many as it may
-// begin and end in.
-__device__ __forceinline__ int seq_of(const int64_t* cu, int N, int64_t r, int block) {
+// The sequence that new row r or, with `unit`, item r of the launch's belongs to: the last n that begins at or before it. A
+// sequence whose first row is cu[n] has items of so many rows from cu[n] / unit + 2 n on: two more than its rows fill, as
+// many as it may begin and end in.
+__device__ __forceinline__ int seq_of(const int64_t* cu, int N, int64_t r, const Divisor* unit) {
     int lo = 0, hi = N - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if ((block ? cu[mid] / block + 2 * mid : cu[mid]) <= r)
+        if ((unit ? (*unit)((unsigned)cu[mid]) + 2 * (int64_t)mid : cu[mid]) <= r)
             lo = mid;
         else
             hi = mid - 1;
@@ -214,36 +303,48 @@ __device__ __forceinline__ void flag(const Append8Args& a) {
     if (a.status) *a.status = KDA_ERR_INVALID_ARG;
 }
 
-// Block `item` of the launch's, the CTA's share of its heads.
-template <typename TI> __device__ __forceinline__ void append_block(const Append8Args& a, unsigned item, unsigned split) {
-    const int block = a.c.block;
-    const kda_cache& c = a.c.cache;
+// The positions that item `item` of the launch appends, a.unit of them at most, from a multiple of it on:
+// [max(start, len), stop) of sequence n, whose first new row is `begin`. False if there are none.
+struct Item {
+    int n, len;
+    int64_t begin, start, stop;
+};
+__device__ __forceinline__ bool find_item(const Append8Args& a, unsigned item, Item& x) {
     int n;
     unsigned j;
     int64_t begin, end;
     if (a.cu) {
-        n = seq_of(a.cu, a.N, item, block);
+        n = seq_of(a.cu, a.N, item, &a.by_unit);
         begin = a.cu[n];
         end = a.cu[n + 1];
         if (item == 0 && threadIdx.x == 0 && (a.cu[0] != 0 || a.cu[a.N] != a.R)) flag(a);  // rows of no sequence
         if (begin < 0 || end < begin || end > a.R) {
             if (threadIdx.x == 0) flag(a);
-            return;
+            return false;
         }
-        j = (unsigned)(item - (begin / block + 2 * n));
+        j = item - (a.by_unit((unsigned)begin) + 2 * n);
     } else {
-        n = item / a.most;
+        n = a.by_most(item);
         j = item - n * a.most;
         begin = (int64_t)n * a.per;
         end = begin + a.per;
     }
     const int len = a.kv_lens[n];
-    if (len < 0 || begin == end) return;
-    const int64_t start = ((int64_t)(len / block) + j) * block, stop = len + (end - begin);
-    if (start >= stop) return;
-    const unsigned from = (unsigned)start, first = max(from, (unsigned)len);
-    unsigned last = (unsigned)min(stop, start + block);
-    const unsigned pg = from / (unsigned)c.page_size, row = from - pg * c.page_size;
+    if (len < 0 || begin == end) return false;
+    const int64_t start = ((int64_t)a.by_unit(len) + j) * a.unit, stop = len + (end - begin);
+    x = {n, len, begin, start, min(stop, start + a.unit)};
+    return start < stop;
+}
+
+// A block of rows, the CTA's share of its heads.
+template <typename TI> __device__ __forceinline__ void append_block(const Append8Args& a, unsigned item, unsigned split) {
+    const kda_cache& c = a.c.cache;
+    Item it;
+    if (!find_item(a, item, it)) return;
+    const int n = it.n, len = it.len;
+    const unsigned from = (unsigned)it.start, first = max(from, (unsigned)len);
+    unsigned last = (unsigned)it.stop;
+    const unsigned pg = page_of(a, from), row = from - pg * c.page_size;
     int64_t page = -1;
     if (pg < (unsigned)a.max_pages) page = a.table[n * a.table_stride + pg];
     if (page < 0 || page >= c.num_pages || (a.rope && last > (unsigned)a.rope_len)) {
@@ -252,7 +353,7 @@ template <typename TI> __device__ __forceinline__ void append_block(const Append
         last = min(last, (unsigned)a.rope_len);
         if (first >= last) return;
     }
-    const int64_t r = begin + (first - (unsigned)len), b = row / (unsigned)block;
+    const int64_t r = it.begin + (first - (unsigned)len), b = a.by_block(row);
     const unsigned slabs = 2 * (unsigned)c.HKV;
     for (unsigned i = split * kWarps + threadIdx.x / 32; i < slabs; i += a.splits * kWarps) {
         const bool keys = i < (unsigned)c.HKV;
@@ -272,6 +373,133 @@ template <typename TI> __device__ __forceinline__ void append_block(const Append
     }
 }
 
+// A thread's share of a row on its way to shared memory, of the heads ahead: C channels, twice, in pieces of 16 bytes or 8,
+// the threads' pieces side by side.
+template <typename TI, int C> struct Ahead {
+    static constexpr int kHeads = sizeof(TI) == 2 ? 4 : 3;  // under way or in use
+    static constexpr int kPiece = C * sizeof(TI) < 16 ? 8 : 16, kOfRun = C * sizeof(TI) / kPiece;
+    static constexpr size_t bytes(int threads) { return (size_t)kHeads * threads * 2 * C * sizeof(TI); }
+    uint32_t at, stage = 0, stages;
+    __device__ __forceinline__ explicit Ahead(const void* shared) {
+        at = (uint32_t)__cvta_generic_to_shared(shared) + threadIdx.x * kPiece;
+        stages = blockDim.x * 2 * C * sizeof(TI);
+    }
+    // Piece i of the head that is `ahead` of the present one.
+    __device__ __forceinline__ uint32_t piece(int ahead, int i) const {
+        const uint32_t k = stage + ahead;
+        return at + (k < kHeads ? k : k - kHeads) * stages + i * blockDim.x * kPiece;
+    }
+    __device__ __forceinline__ void fetch(int ahead, const TI* a, const TI* b) const {
+#pragma unroll
+        for (int i = 0; i < 2 * kOfRun; ++i) {
+            const char* p = (const char*)(i < kOfRun ? a : b) + i % kOfRun * kPiece;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(piece(ahead, i)), "l"(p), "n"(kPiece) : "memory");
+        }
+    }
+    __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    // The present head's, once all groups but the newest kHeads - 1 are there.
+    __device__ __forceinline__ void take(Run<TI, C>& a, Run<TI, C>& b) const {
+#pragma unroll
+        for (int i = 0; i < 2 * kOfRun; ++i) {
+            uint32_t* w = (i < kOfRun ? a : b).w + i % kOfRun * (kPiece / 4);
+            if constexpr (kPiece == 8)
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(piece(0, i)) : "memory");
+            else
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                             : "r"(piece(0, i))
+                             : "memory");
+        }
+    }
+    __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(kHeads - 1) : "memory"); }
+    __device__ __forceinline__ void next() { stage = stage + 1 == kHeads ? 0 : stage + 1; }
+};
+
+// A tile of rows, a.unit of them at most, in whole blocks, of some heads of keys or of values: eight threads to a row, each
+// with the angles of its channels in registers, one head after the other, the next ones' rows on their way meanwhile.
+template <typename TI, int D, bool KEYS>
+__device__ __forceinline__ void append_tile(const Append8Args& a, unsigned item, int head, int heads) {
+    constexpr int C = D / 16;
+    __shared__ unsigned tops[3][kTileThreads / 8];  // of each block, of a head, of the next one, and of the one after
+    extern __shared__ uint4 shared[];
+    const kda_cache& c = a.c.cache;
+    const int block = a.c.block, row = threadIdx.x / 8, u = threadIdx.x % 8, mine = a.by_block(row);
+    Item it;
+    if (!find_item(a, item, it)) return;
+    const int len = it.len;
+    const int64_t pos = it.start + row, first = it.start + mine * block;  // the row's, and its block's first
+    const int64_t first_new = max(first, (int64_t)len);
+    const bool rotated = KEYS && a.rope;
+    bool live = row < a.unit && first + block > len && first_new < it.stop;  // the block has a new row
+    int64_t page = -1;
+    unsigned in = 0;
+    if (live) {
+        const unsigned pg = page_of(a, (unsigned)pos);
+        in = (unsigned)pos - pg * c.page_size;
+        if (pg < (unsigned)a.max_pages) page = a.table[it.n * a.table_stride + pg];
+        const bool no_page = page < 0 || page >= c.num_pages, no_angle = a.rope && pos < it.stop && pos >= a.rope_len;
+        if (u == 0 && (no_page || no_angle)) flag(a);
+        live = !no_page && !(a.rope && first_new >= a.rope_len);
+    }
+    const bool fresh = live && pos >= len && pos < it.stop && !(a.rope && pos >= a.rope_len);
+    const bool old = live && pos < len, held = live && first < len;
+    const Share<C> s(u, rotated ? a.rope_dim : 0, a.interleaved);
+    Angles<C> angles;
+    const bool turns = fresh && s.turns;
+    if (turns) angles.load(s, a.rope, pos, a.rope_dim, a.interleaved);
+    const TI* from = (KEYS ? (const TI*)a.k : (const TI*)a.v) + head * D;
+    unsigned char* to = KEYS ? (unsigned char*)c.k + head * c.k_head : (unsigned char*)c.v + head * c.v_head;
+    float* scale = KEYS ? a.c.k_scale + head * a.c.k_scale_head : a.c.v_scale + head * a.c.v_scale_head;
+    if (live) {
+        from += (it.begin + (pos - len)) * (KEYS ? a.k_stride : a.v_stride);
+        to += page * (KEYS ? c.k_page : c.v_page) + in * (KEYS ? c.k_row : c.v_row);
+        scale += page * (KEYS ? a.c.k_scale_page : a.c.v_scale_page) + a.by_block(in) * (KEYS ? a.c.k_scale_block : a.c.v_scale_block);
+    }
+    for (int i = threadIdx.x; i < 3 * (kTileThreads / 8); i += blockDim.x) ((unsigned*)tops)[i] = 0;
+    Ahead<TI, C> ahead(shared);
+#pragma unroll
+    for (int i = 0; i < ahead.kHeads - 1; ++i) {
+        if (fresh && i < heads) ahead.fetch(i, from + i * D + s.a, from + i * D + s.b);
+        ahead.commit();
+    }
+    from += (ahead.kHeads - 1) * D;
+    __syncthreads();
+    for (int h = 0, now_top = 0; h < heads; ++h) {
+        float x[2 * C], top = 0.f, before = 0.f;
+        if (held) before = *scale;
+        if (fresh && h + ahead.kHeads - 1 < heads) ahead.fetch(ahead.kHeads - 1, from + s.a, from + s.b);
+        ahead.commit();
+        from += D;
+        ahead.wait();
+        if (fresh) {
+            Run<TI, C> lo, hi;
+            ahead.take(lo, hi);
+            lo.values(x);
+            hi.values(x + C);
+            if (turns) angles.turn(x, a.interleaved);
+            top = largest(x);
+        }
+#pragma unroll
+        for (int w = 1; w < 8; w *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+        if (u == 0 && fresh) atomicMax(&tops[now_top][mine], __float_as_uint(top));  // (the order does not matter)
+        __syncthreads();
+        const int field = max(least_scale(__uint_as_float(tops[now_top][mine])), held_scale(before));
+        const float now = __int_as_float(field << 23), f = __int_as_float((254 - field) << 23);
+        now_top = now_top == 2 ? 0 : now_top + 1;
+        if (u == 0) tops[now_top == 2 ? 0 : now_top + 1][mine] = 0;  // (of the head after the next; last read before the barrier)
+        if (fresh) {
+            store_e4m3<C>(to + s.a, x, f);
+            store_e4m3<C>(to + s.b, x + C, f);
+            if (u == 0 && pos == first_new && before != now) *scale = now;
+        } else if (old && before != now) {
+            again<2 * C>(to + u * 2 * C, before * f);
+        }
+        ahead.next();
+        to += KEYS ? c.k_head : c.v_head;
+        scale += KEYS ? a.c.k_scale_head : a.c.v_scale_head;
+    }
+}
+
 // Query rows: rotated, in their own type; 0 where the token's row is dropped or inactive.
 template <typename TI> __device__ __forceinline__ void turn_queries(const Append8Args& a, unsigned cta) {
     const kda_cache& c = a.c.cache;
@@ -284,16 +512,16 @@ template <typename TI> __device__ __forceinline__ void turn_queries(const Append
     unsigned idx;
     bool ok = true;
     if (a.cu) {
-        n = seq_of(a.cu, a.N, r, 0);
+        n = seq_of(a.cu, a.N, r, nullptr);
         const int64_t begin = a.cu[n];
         ok = begin <= r && r < a.cu[n + 1];
         idx = (unsigned)(r - begin);
     } else {
-        n = (unsigned)r / a.per;
+        n = a.by_per((unsigned)r);
         idx = (unsigned)r - n * a.per;
     }
     const int len = a.kv_lens[n];
-    const unsigned pos = (unsigned)len + idx, pg = pos / (unsigned)c.page_size;
+    const unsigned pos = (unsigned)len + idx, pg = page_of(a, pos);
     int64_t page = -1;
     if (len >= 0) {
         ok = ok && pg < (unsigned)a.max_pages && (!a.rope || pos < (unsigned)a.rope_len);
@@ -303,33 +531,126 @@ template <typename TI> __device__ __forceinline__ void turn_queries(const Append
             if (lane == 0) flag(a);
         }
     }
-    const unsigned L = c.K / 16, tasks = a.HQ * L;
-    for (unsigned i = lane; i < tasks; i += a.q_lanes) {
-        const unsigned h = i / L;
-        const Share s(i - h * L, a.rope_dim, a.interleaved);
-        float x[16];
+    // (a thread has the same channels of several heads, so it reads its angles once)
+    const unsigned L = c.K / 16, u = lane % L, step = a.q_lanes / L;
+    const Share<8> s(u, a.rope_dim, a.interleaved);
+    const bool turns = s.turns && page >= 0;
+    Angles<8> angles;
+    if (turns) angles.load(s, a.rope, pos, a.rope_dim, a.interleaved);
+    const TI* from = (const TI*)a.q + r * a.q_stride;
+    TI* to = (TI*)a.q_out + r * a.HQ * c.K;
+    for (unsigned h = lane / L; h < (unsigned)a.HQ; h += step) {
+        const int64_t at = (int64_t)h * c.K;
+        Run<TI, 8> lo{}, hi{};
         if (page >= 0) {
-            const TI* p = (const TI*)a.q + r * a.q_stride + (int64_t)h * c.K;
-            load_8(p + s.a, x);
-            load_8(p + s.b, x + 8);
-            if (s.turns) turn(x, s, a.rope + (int64_t)pos * a.rope_dim, a.rope_dim, a.interleaved);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = 0.f;
+            lo.load(from + at + s.a);
+            hi.load(from + at + s.b);
         }
-        TI* p = (TI*)a.q_out + (r * a.HQ + h) * c.K;
-        store_8(p + s.a, x);
-        store_8(p + s.b, x + 8);
+        if (turns) {
+            float x[16];
+            lo.values(x);
+            hi.values(x + 8);
+            angles.turn(x, a.interleaved);
+            lo.set(x);
+            hi.set(x + 8);
+        }
+        lo.store(to + at + s.a);
+        hi.store(to + at + s.b);
     }
 }
 
-template <typename TI> __global__ void __launch_bounds__(kThreads) k_append8(Append8Args a) {
+// Blocks and queries in one launch where that has no more than so many CTAs to an SM; else each in its own.
+constexpr int kFew = 32;
+template <typename TI> __global__ void __launch_bounds__(kThreads, 4) k_append8(Append8Args a) {
     after_previous();
     const unsigned blocks = a.items * a.splits;
     if (blockIdx.x < blocks)
         append_block<TI>(a, blockIdx.x / a.splits, blockIdx.x % a.splits);
     else
         turn_queries<TI>(a, blockIdx.x - blocks);
+}
+constexpr int kQueryThreads = 64;
+template <typename TI> __global__ void __launch_bounds__(kQueryThreads, 16) k_append8_queries(Append8Args a) {
+    after_previous();
+    turn_queries<TI>(a, blockIdx.x);
+}
+template <typename TI, int K, int V> __global__ void __launch_bounds__(kTileThreads) k_append8_tiles(Append8Args a) {
+    after_previous();
+    const unsigned tiles = a.items * a.splits;
+    if (blockIdx.x >= tiles) {
+        turn_queries<TI>(a, blockIdx.x - tiles);
+        return;
+    }
+    // (keys, then values, their heads in a.splits / 2 parts)
+    const unsigned item = blockIdx.x / a.splits, split = blockIdx.x - item * a.splits, parts = a.splits / 2;
+    const unsigned part = split < parts ? split : split - parts;
+    const int head = part * a.c.cache.HKV / parts, end = (part + 1) * a.c.cache.HKV / parts;
+    if (split < parts)
+        append_tile<TI, K, true>(a, item, head, end - head);
+    else
+        append_tile<TI, V, false>(a, item, head, end - head);
+}
+template <typename TI, int K, int V>
+cudaError_t launch_tiles(const Append8Args& a, unsigned ctas, int threads, cudaStream_t st) {
+    // (the most that a kernel may ask for is set once on each device)
+    static std::atomic<bool> known[kDevices];
+    constexpr int C = (K > V ? K : V) / 16;
+    const size_t shared = Ahead<TI, C>::bytes(threads);
+    const int device = present_device();
+    if (shared > 32 << 10 && (device < 0 || device >= kDevices || !known[device].load(std::memory_order_relaxed))) {
+        const cudaError_t e = cudaFuncSetAttribute(k_append8_tiles<TI, K, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)Ahead<TI, C>::bytes(kTileThreads));
+        if (e != cudaSuccess) return e;
+        if (device >= 0 && device < kDevices) known[device].store(true, std::memory_order_relaxed);
+    }
+    return launch_after(k_append8_tiles<TI, K, V>, a, ctas, threads, st, 1, shared);
+}
+template <typename TI> cudaError_t launch_tiles(const Append8Args& a, unsigned ctas, int threads, cudaStream_t st) {
+    const int K = a.c.cache.K, V = a.c.cache.V;
+    if (K == 128) return V == 128 ? launch_tiles<TI, 128, 128>(a, ctas, threads, st) : launch_tiles<TI, 128, 64>(a, ctas, threads, st);
+    return V == 128 ? launch_tiles<TI, 64, 128>(a, ctas, threads, st) : launch_tiles<TI, 64, 64>(a, ctas, threads, st);
+}
+// Rows of a tile of whole blocks, and the threads for them: the fewest, from 16 rows on, of which most have a row. 0 where a
+// block is longer than a CTA.
+int tile_of(int block, int& threads) {
+    int best = 0;
+    threads = 0;
+    for (int rows = 16; rows <= kTileThreads / 8; rows *= 2) {
+        const int tile = rows / block * block;
+        if (tile == 0 || (best > 0 && tile * (threads / 8) <= best * rows)) continue;  // no larger part of the threads
+        best = tile;
+        threads = 8 * rows;
+        if (10 * tile >= 8 * rows) break;
+    }
+    return best;
+}
+// CTAs that append in units of so many rows, at most.
+int64_t items_of(int64_t R, int64_t N, bool packed, int64_t unit) {
+    const int64_t per = R / N;
+    return packed ? R / unit + 2 * N : N * (per > 0 ? (per + unit - 2) / unit + 1 : 0);
+}
+// Query rows of a CTA of so many threads, and threads of a row.
+unsigned queries_of(Append8Args& a, int threads) {
+    const unsigned tasks = a.HQ * (a.c.cache.K / 16);
+    if (tasks == 0) return 0;
+    a.q_lanes = tasks < (unsigned)threads ? tasks : threads;
+    a.q_rows = threads / a.q_lanes;
+    return (a.R + a.q_rows - 1) / a.q_rows;
+}
+template <typename TI> cudaError_t launch(Append8Args a, bool tiles, int threads, cudaStream_t st) {
+    const unsigned blocks = a.items * a.splits;
+    unsigned queries = queries_of(a, tiles ? threads : kThreads);
+    const bool both = (int64_t)blocks + queries <= kFew * (int64_t)sm_count();
+    if (!both) queries = 0;
+    cudaError_t e = cudaSuccess;
+    if (tiles)
+        e = launch_tiles<TI>(a, blocks + queries, threads, st);
+    else
+        e = launch_after(k_append8<TI>, a, blocks + queries, kThreads, st);
+    if (e != cudaSuccess || both) return e;
+    queries = queries_of(a, kQueryThreads);
+    if (queries) e = launch_after(k_append8_queries<TI>, a, queries, kQueryThreads, st);
+    return e;
 }
 
 }  // namespace
@@ -355,24 +676,28 @@ extern "C" kda_status kda_cache8_append(const kda_cache8* c8, const void* k, int
                        page_table, table_stride, max_pages, kv_lens, status};
     const kda_status checked = check_append(c, x, bf16 ? 8 : 4);
     if (checked != KDA_OK || R == 0) return checked;
-    const int64_t per = R / N, block = c8->block;
-    const int64_t most = per > 0 ? (per + block - 2) / block + 1 : 0;
-    const int64_t items = cu_seqlens ? R / block + 2 * (int64_t)N : N * most;
+    // many rows of each sequence: tiles
+    int threads;
+    const int tile = tile_of(c8->block, threads);
+    const bool tiles = tile > 0 && R / N >= 8;
+    const int unit = tiles ? tile : c8->block;
+    const int64_t items = items_of(R, N, cu_seqlens != nullptr, unit);
     // few blocks: as many CTAs of each as leave every warp one head
     const int64_t slabs = 2 * (int64_t)c->HKV, all = (slabs + kWarps - 1) / kWarps;
     int64_t splits = 8 * (int64_t)sm_count() / (items > 0 ? items : 1);
-    if (splits > all) splits = all;
+    if (splits > (tiles ? slabs : all)) splits = tiles ? slabs : all;
     if (splits < 1) splits = 1;
-    const int64_t tasks = (int64_t)HQ * (c->K / 16);
-    const int64_t lanes = tasks == 0 ? kThreads : tasks < kThreads ? tasks : kThreads, rows = kThreads / lanes;
-    const int64_t grid = items * splits + (HQ > 0 ? (R + rows - 1) / rows : 0);
-    if (grid > INT32_MAX) return KDA_ERR_UNSUPPORTED;
-    const Append8Args a{*c8, k, v, q, q_out, k_stride, v_stride, q_stride, table_stride, HQ, N, (unsigned)R, (unsigned)per,
+    if (tiles) splits = splits < 2 ? 2 : splits / 2 * 2;
+    if (items * splits > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    const int64_t most = cu_seqlens ? 0 : items / N;
+    const Append8Args a{*c8, k, v, q, q_out, k_stride, v_stride, q_stride, table_stride, HQ, N, (unsigned)R, (unsigned)(R / N),
                         cu_seqlens, rope, rope_len, rope_dim, interleaved, page_table, kv_lens, max_pages, status,
-                        (unsigned)items, (unsigned)splits, (unsigned)most, (unsigned)lanes, (unsigned)rows};
+                        unit,
+                        (unsigned)items, (unsigned)splits, (unsigned)most, 1, 1, Divisor(unit),
+                        Divisor(most > 0 ? most : 1), Divisor(R / N > 0 ? R / N : 1), Divisor(c8->block), Divisor(c->page_size)};
     cudaStream_t st = (cudaStream_t)stream;
     begin_launches(st);
-    const cudaError_t e = launch_after(bf16 ? k_append8<__nv_bfloat16> : k_append8<float>, a, (unsigned)grid, kThreads, st);
+    const cudaError_t e = bf16 ? launch<__nv_bfloat16>(a, tiles, threads, st) : launch<float>(a, tiles, threads, st);
     if (e != cudaSuccess) return cuda_fail(e);
     note_launch("cache8_append", st);
     return KDA_OK;

@@ -76,13 +76,14 @@ __device__ __forceinline__ void after_previous() {
 // A cluster of more than 8 CTAs is one that largest_cluster allowed on this device.
 template <typename Args>
 cudaError_t launch_after(void (*kernel)(Args), const Args& a, dim3 grid, int threads, cudaStream_t st,
-                         int cluster = 1) {
+                         int cluster = 1, size_t shared = 0) {
     cudaLaunchAttribute attr[2] = {};
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = shared;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
