@@ -11,9 +11,9 @@
 //   Several rows of each sequence: tiles of 16 rows or more in whole blocks, eight threads to a row, one head after the
 //     other. A thread keeps its angles for all heads; rows come in ahead of their use through shared memory (cp.async: without
 //     it 4 us more); the largest value of a block is an atomicMax in shared memory, whose order does not matter. 16 packed
-//     prompts of U[1,4096] tokens, 32 query and 8 cache heads of 128, bf16, blocks of 16 (760 MB): 126 us, 6.0 TB/s, of which
-//     the cache's 202 MB take 42 (70 % of the issue slots: 260 instructions for 16 values of a thread, before pairs of
-//     values went to one instruction and divisions to multiplications; now about 200) and the queries 84, at 95 % of a
+//     prompts of U[1,4096] tokens, 32 query and 8 cache heads of 128, bf16, blocks of 16 (760 MB): 122 us, 6.2 TB/s, of which
+//     the cache's 202 MB take 40 (70 % of the issue slots: 260 instructions for 16 values of a thread, before divisions became
+//     multiplications) and the queries 84, at 95 % of a
 //     plain copy's rate. A warp to a block of one head, which reads the rows twice and angles for each head: 163 us.
 //   Few rows of each sequence (less than 8 on average) or blocks longer than 128: a warp has a block of one head to itself.
 //     One token of each of 128 sequences 4.1 us in a graph, of one 2.4 (tiles, most of whose threads have no row: 5.2 to 13
@@ -52,21 +52,6 @@ struct Append8Args {
 // The page of a position. (Divisor is for numbers below 2^31.)
 __device__ __forceinline__ unsigned page_of(const Append8Args& a, unsigned pos) {
     return pos < 1u << 31 ? a.by_page(pos) : pos / (unsigned)a.c.cache.page_size;
-}
-
-// Two fp32 values to an instruction; each is rounded as by itself.
-struct Two {
-    uint64_t v;
-    __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
-    __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-};
-__device__ __forceinline__ Two operator*(Two a, const Two& b) {
-    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
-    return a;
-}
-__device__ __forceinline__ Two operator+(Two a, const Two& b) {
-    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
-    return a;
 }
 
 // C channels of a row (4 or 8) as they are.
@@ -140,35 +125,31 @@ template <int C> struct Angles {
         x.values(co);
         y.values(si);
     }
-    // Channels p and q of angles i and i + 1.
-    __device__ __forceinline__ void pair(float& p0, float& p1, float& q0, float& q1, int i) const {
-        const Two p(p0, p1), q(q0, q1), c(co[i], co[i + 1]);
-        (p * c + q * Two(-si[i], -si[i + 1])).get(p0, p1);
-        (q * c + p * Two(si[i], si[i + 1])).get(q0, q1);
+    __device__ __forceinline__ void pair(float& p, float& q, int i) const {
+        const float u = __fsub_rn(__fmul_rn(p, co[i]), __fmul_rn(q, si[i]));
+        q = __fadd_rn(__fmul_rn(q, co[i]), __fmul_rn(p, si[i]));
+        p = u;
     }
-    // The rotation, each product and each sum rounded by itself (so that the scales, which go by the largest value, do not
-    // depend on how a compiler joins them).
+    // The rotation, each product and each sum rounded by itself, so that the scales, which go by the largest value, do not
+    // depend on how a compiler joins them. (Instructions for two values at once are joined even where they say .rn.)
     __device__ __forceinline__ void turn(float (&x)[2 * C], int interleaved) const {
         if (interleaved) {
 #pragma unroll
-            for (int i = 0; i < C; i += 2) pair(x[2 * i], x[2 * i + 2], x[2 * i + 1], x[2 * i + 3], i);
+            for (int i = 0; i < C; ++i) pair(x[2 * i], x[2 * i + 1], i);
         } else {
 #pragma unroll
-            for (int i = 0; i < C; i += 2) pair(x[i], x[i + 1], x[C + i], x[C + i + 1], i);
+            for (int i = 0; i < C; ++i) pair(x[i], x[C + i], i);
         }
     }
 };
 
 // 4 values times f as e4m3 (a NaN as one; an infinite value would become the largest).
 __device__ __forceinline__ uint32_t to_e4m3(const float* x, float f) {
-    float y[4];
-    (Two(x[0], x[1]) * Two(f, f)).get(y[0], y[1]);
-    (Two(x[2], x[3]) * Two(f, f)).get(y[2], y[3]);
     uint32_t w;
     asm("{.reg .b16 lo, hi; cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1; cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;"
         " mov.b32 %0, {lo, hi};}"
         : "=r"(w)
-        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]));
+        : "f"(x[0] * f), "f"(x[1] * f), "f"(x[2] * f), "f"(x[3] * f));
     return w;
 }
 template <int C> __device__ __forceinline__ void store_e4m3(unsigned char* p, const float* x, float f) {

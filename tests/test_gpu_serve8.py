@@ -168,6 +168,35 @@ def test_append8(kda, case, dtype):  # noqa: F811
         assert torch.equal(bits(a), bits(b))
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N, T", [(3, 40), (50, 1)])
+def test_append8_rounds_each_product_and_sum(kda, N, T, dtype, interleaved):  # noqa: F811
+    """Keys are what separate products and sums in fp32 make of them, in every bit: the scales do not hang on a compiler."""
+    gen, size, H, K = _gen(6), 16, 4, 128
+    x = torch.randn(N * T, H, K, generator=gen).to(DT[dtype])
+    rope = rope_table(T + 9, K)
+    lens = torch.randint(0, 9, (N,), generator=gen).to(torch.int32)
+    width = -(-(T + 9) // size)
+    table = torch.randperm(N * width, generator=gen).to(torch.int32).view(N, width)
+    kc, vc, ks, vs = kda.new_cache(N * width, size, H, K, K, dtype=E4M3, scale_block=1)
+    q = kda.cache_append(x.cuda(), x.cuda(), kc, vc, table.cuda(), lens.cuda(), q=x.cuda(), rope=rope.cuda(),
+                         interleaved=interleaved, k_scale=ks, v_scale=vs)
+    n = torch.arange(N).repeat_interleave(T)
+    pos = lens.long()[n] + torch.arange(T).repeat(N)
+    c, s = (t[:, None] for t in rope[pos].chunk(2, 1))
+    f = x.float()
+    a, b = (f[..., ::2], f[..., 1::2]) if interleaved else f.chunk(2, -1)
+    ac, bs, bc, as_ = a * c, b * s, b * c, a * s
+    u, v = ac - bs, bc + as_
+    want = torch.stack([u, v], -1).flatten(-2) if interleaved else torch.cat([u, v], -1)
+    assert torch.equal(q.cpu(), want.to(DT[dtype]))
+    at, row = table[n, pos // size].long(), pos % size
+    scale = torch.tensor([least(float(t)) for t in want.abs().amax(-1).flatten()]).view(N * T, H)
+    assert torch.equal(ks.cpu()[at, row], scale)
+    assert torch.equal(kc.float().cpu()[at, row], (want / scale[..., None]).to(E4M3).float())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("block", [4, 16, 64])
 def test_append8_values(kda, block, dtype):  # noqa: F811
