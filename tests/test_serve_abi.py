@@ -199,7 +199,7 @@ def test_append8_refuses_shared_scales(lib):
 def test_cache8_of_nothing(lib):
     assert _append8(lib, R=0, k=None, v=None) == 0
     assert _append8(lib, R=2**31, N=2) == UNSUPPORTED
-    assert _append8(lib, _cache8(block=1), R=2**31 - 2, cu=A, HQ=0, q=None, q_out=None) == UNSUPPORTED  # too many CTAs
+    assert _append8(lib, R=2**31 - 2, N=2**30, cu=A, HQ=0, q=None, q_out=None) == UNSUPPORTED  # too many CTAs
     assert lib.kda_cache8_append(None, *([None, 0] * 3), None, 0, 0, 0, None, None, 0, 0, 0, None, 0, 0, None, None,
                                  None) == INVALID
     assert _attend8(lib, N=0, q=None, o=None) == 0
@@ -241,4 +241,4 @@ def test_resize_refuses(lib, bad, code):
 def test_resize_workspace(lib):
     need = lib.kda_cache_resize_workspace_bytes
     assert need(1, 1, 1) == 0 and need(0, 0, 0) == 0 and need(-1, 1, 1) == 0  # one CTA, no workspace
-    assert need(2, 8, 9000) == (2 * 2 + 3) * 8 and need(2000, 1, 0) > 0
+    assert need(2, 8, 9000) == 3 * 8 + 4 * 4 and need(2000, 1, 0) > 0
