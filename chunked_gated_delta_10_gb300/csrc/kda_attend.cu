@@ -56,6 +56,7 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window, int s
     const int64_t all = (int64_t)(N > 0 ? N : 1) * units;              // units
     const int slots = gpu.sms * form.ctas;
     Plan p{kWhole, 1, ht, units, turn};
+    p.together = 1;
     // What each split costs, in turns (0.6 to 0.9 us) of a CTA that takes all of its rows in turn: fitted to 1600 times
     // of all splits. The CTAs of an SM start one after the other. Those that do not fit take the places of others that
     // end: with lengths that differ, the sequences of a batch have about 0.7 of the rows of all as long as the longest
@@ -108,11 +109,17 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window, int s
     if (form.even && (turns + kUnitTurns) * all < INT32_MAX && shares < least) {
         p.split = kShares;
         p.parts = slots;
+        // (as many units together as divide a sequence's and leave few places empty)
+        if (form.together)
+            for (int t = units; t > 1 && p.together == 1; --t)
+                if (units % t == 0 && slots / t * t * 100 >= slots * 97) p.together = t;
+        p.parts = slots / p.together;
     }
-    p.grid = p.split == kShares ? dim3(p.parts) : dim3(units * p.parts, N);
+    p.grid = p.split == kShares ? dim3(p.parts * p.together) : dim3(units * p.parts, N);
     p.ws_bytes = KDA_ATTEND_WORKSPACE_MIN;
+    p.shared = form.shared;
     if (p.split >= kParts) {
-        const size_t held = p.split == kParts ? (size_t)all * p.parts : (size_t)p.parts * 2;
+        const size_t held = p.split == kParts ? (size_t)all * p.parts : (size_t)p.parts * p.together * 2;
         p.acc_bytes = held * ht * c->V * sizeof(float);
         p.ml_bytes = held * ht * sizeof(float2);
         p.ws_bytes += p.acc_bytes + p.ml_bytes + (size_t)all * sizeof(int2);
@@ -137,7 +144,7 @@ template <typename TI, int V, int HT, int VS, int G, int THREADS>
 cudaError_t launch_join(const AttendArgs& a, cudaStream_t st) {
     const int64_t threads = (int64_t)a.N * a.HQ * (V / 4) * G;
     const unsigned grid = (unsigned)((threads + THREADS - 1) / THREADS);
-    if constexpr (sizeof(TI) == 2)
+    if constexpr (sizeof(TI) == 2 || HT >= 8)  // (fp32 with fewer heads has no shares)
         if (a.split == kShares) return launch_after(k_attend_join<TI, V, HT, VS, G, THREADS, true>, a, grid, THREADS, st);
     return launch_after(k_attend_join<TI, V, HT, VS, G, THREADS, false>, a, grid, THREADS, st);
 }
@@ -160,7 +167,7 @@ template <int V> cudaError_t launch_join(const AttendArgs& a, bool bf16, int ht,
 
 // Parts of a unit, with equal lengths (kParts, kShares).
 int64_t unit_parts(const Plan& p, int N) {
-    return p.split == kParts ? p.parts : p.parts / ((int64_t)(N > 0 ? N : 1) * p.units) + 2;
+    return p.split == kParts ? p.parts : (int64_t)p.parts * p.together / ((int64_t)(N > 0 ? N : 1) * p.units) + 2;
 }
 
 }  // namespace
@@ -171,7 +178,7 @@ kda_status launch(const AttendArgs& a, const Plan& p, Kernel kernel, bool bf16, 
                   cudaStream_t st) {
     const int V = a.c.V;
     begin_launches(st);
-    cudaError_t e = launch_after(kernel, a, p.grid, kWarps * 32, st, p.split == kCluster ? p.parts : 1);
+    cudaError_t e = launch_after(kernel, a, p.grid, kWarps * 32, st, p.split == kCluster ? p.parts : 1, p.shared);
     if (e != cudaSuccess) return cuda_fail(e);
     note_launch(names[p.split], st);
     if (p.split < kParts) return KDA_OK;
@@ -229,6 +236,7 @@ AttendArgs args_of(const kda_cache* c, const Call& x, const Plan& plan) {
     a.parts = plan.parts;
     a.by_parts = Divisor(plan.parts);
     a.turn = plan.turn;
+    a.together = plan.together;
     a.part_acc = (float4*)w;
     a.part_ml = (float2*)(w + plan.acc_bytes);
     a.unit_parts = (int2*)(w + plan.acc_bytes + plan.ml_bytes);

@@ -30,6 +30,7 @@ struct AttendArgs {
     int split, parts;  // parts: kCluster, kParts: CTAs of a unit; kShares: CTAs in all; kWhole: 1
     Divisor by_parts;
     int turn;  // rows that a CTA takes at a time
+    int together;  // kShares: units that have a share together, a CTA each (1 but for a cache in 8 bits)
     // What a CTA has of a unit that it does not have whole, head by head: the weighted sum relative to its maximum, and
     // its maximum (log2 units) and sum of weights. kParts: [units, parts, HT, V] and [units, parts, HT]; kShares: of the
     // unit that it ends (0) and of the one that it begins (1), [parts, 2, HT, V] and [parts, 2, HT], and of each unit the
@@ -166,11 +167,13 @@ template <int C> __device__ __forceinline__ void load_channels(const float* p, b
 //             kUnitTurns more than it has, about what it costs to begin and end one; else the CTAs with many short units
 //             would be the last (64 sequences of U[1,8192] rows, 32 heads on 8: 160 -> 154 us; 11 of U[1,4240], 256
 //             heads on 16: 42 -> 28 us). A unit that falls to several CTAs is joined by a second kernel.
+//             Over a cache in 8 bits the units of a sequence have a share together, as many of them as divide them all and
+//             leave few places empty: they read the same pages at the same time.
 constexpr int kUnitTurns = 2;
 constexpr int kWarps = 4;
 constexpr int kMaxCluster = 16;
 
-template <int R, int HT, bool SHARES, bool SINKS> struct Work {
+template <int R, int HT, bool SHARES, bool SINKS, bool TOGETHER = false> struct Work {
     static constexpr int W = kWarps, kTurn = W * R;
     int n, hkv, h0, heads, warp;
     int left;  // rows from the warp's first one to the end
@@ -246,9 +249,13 @@ template <int R, int HT, bool SHARES, bool SINKS> struct Work {
         const int each = total / ctas, more = total % ctas, both = more * (each + 1);
         return y < both ? y / (each + 1) : more + (y - both) / each;
     }
-    // kShares: the CTA's share, and the sequence that it begins in.
+    // kShares: the CTA's share, and the sequence that it begins in. Units are counted in bundles of `together`.
+    __device__ __forceinline__ static int together(const AttendArgs& a) { return TOGETHER ? a.together : 1; }
+    __device__ __forceinline__ static int my_share(const AttendArgs& a) {
+        return TOGETHER ? (int)(blockIdx.x / (unsigned)a.together) : (int)blockIdx.x;
+    }
     __device__ __forceinline__ void find_share(const AttendArgs& a, Share& share) {
-        const int units = a.units;
+        const int units = TOGETHER ? a.units / a.together : a.units, mine_is = my_share(a);
         const int per = (a.N + W * 32 - 1) / (W * 32), lane = threadIdx.x % 32;
         const int n0 = min((int)threadIdx.x * per, a.N), n1 = min(n0 + per, a.N);
         int mine = 0, begin, last;
@@ -272,8 +279,8 @@ template <int R, int HT, bool SHARES, bool SINKS> struct Work {
             total += share.sums[w];
         }
         const int ctas = min(a.parts, total);  // with fewer turns than CTAs, those that have one
-        const int at = first_turn(min((int)blockIdx.x, ctas), total, ctas);
-        if (blockIdx.x >= ctas && threadIdx.x == 0) share.state[0].at = share.stop = 0;
+        const int at = first_turn(min(mine_is, ctas), total, ctas);
+        if (mine_is >= ctas && threadIdx.x == 0) share.state[0].at = share.stop = 0;
         if (at >= before && at < before + mine) {
             int i = n0;
             for (;; ++i) {
@@ -282,7 +289,7 @@ template <int R, int HT, bool SHARES, bool SINKS> struct Work {
                 if (at < before + turns) break;
                 before += turns;
             }
-            share.stop = first_turn(blockIdx.x + 1, total, ctas);
+            share.stop = first_turn(mine_is + 1, total, ctas);
             share.total = total;
             share.state[0] = {at, i, before};
         }
@@ -290,7 +297,7 @@ template <int R, int HT, bool SHARES, bool SINKS> struct Work {
     }
     // kShares: the next unit, or part of one, of the CTA's share; false if there is none.
     __device__ __forceinline__ bool next(const AttendArgs& a, Share& share) {
-        const int stop = share.stop, units = a.units;
+        const int stop = share.stop, units = TOGETHER ? a.units / a.together : a.units;
         int at = share.state[odd].at, begin, last, border, turns, each, t0, seq = share.state[odd].seq;
         unsigned u;
         n = share.state[odd].n;
@@ -308,11 +315,17 @@ template <int R, int HT, bool SHARES, bool SINKS> struct Work {
             if (t0 < turns) break;
         }
         const int t1 = min(turns, t0 + stop - at);
-        set_unit(a, u, t0 == 0 && t1 == turns, 2 * blockIdx.x + (t0 == 0), share);
+        int part = 2 * my_share(a) + (t0 == 0);
+        if constexpr (TOGETHER) {
+            const unsigned member = blockIdx.x % (unsigned)a.together;
+            u = u * a.together + member;
+            part = part * a.together + member;
+        }
+        set_unit(a, u, t0 == 0 && t1 == turns, part, share);
         odd ^= 1;
         if (threadIdx.x == 0) {
             share.state[odd] = {at + (t1 < turns ? t1 : each) - t0, n, seq};
-            share.unit = t0 == 0 ? (int64_t)n * units + u : -1;
+            share.unit = t0 == 0 ? (int64_t)n * a.units + u : -1;
             share.last_turn = at + turns - 1;
         }
         const int first = begin + (t0 * W + warp) * R, end = min(last, begin + t1 * kTurn);
@@ -365,19 +378,23 @@ __device__ __forceinline__ void write_result(const AttendArgs& a, int64_t at, in
     if (d == 0 && a.lse) a.lse[at] = (finite_base(m) + log2f(l / kAtMostOne)) * kLn2;
 }
 
-// The results of a CTA's warps for HT heads: maxima m, sums of weights l, and weighted sums acc relative to m. In a
-// cluster: what its CTAs send of the channels that this one joins, and of every head their m and l.
+// The results of a CTA's warps for HT heads: maxima m, sums of weights l, and weighted sums acc relative to m.
 template <int HT, int V> struct Partial {
     float m[kWarps][HT], l[kWarps][HT];
     float4 acc[kWarps][HT][V / 4 + 1];
-    float4 in_acc[HT * V / 4 + kMaxCluster];
-    float2 in_ml[kMaxCluster][HT];
+};
+// In a cluster: what its CTAs send of the channels that this one joins, and of every head their m and l. They may do so
+// while this one still has rows to attend.
+template <int HT, int V> struct Inbox {
+    float4 acc[HT * V / 4 + kMaxCluster];
+    float2 ml[kMaxCluster][HT];
 };
 
 // Joins the warps of a CTA and, in a cluster, its CTAs, and writes the unit's result, or, where the CTA does not have
 // all of the unit, its part. The order of the sums is fixed.
 template <typename TI, int V, int HT, bool SHARES, typename Wk>
-__device__ __forceinline__ void join(const AttendArgs& a, const typename Wk::Share& unit, Partial<HT, V>& p) {
+__device__ __forceinline__ void join(const AttendArgs& a, const typename Wk::Share& unit, Partial<HT, V>& p,
+                                     Inbox<HT, V>& in) {
     const bool cluster = !SHARES && a.split == kCluster;
     if (cluster) cluster_wait();  // for the others to have started
     __syncthreads();
@@ -387,7 +404,7 @@ __device__ __forceinline__ void join(const AttendArgs& a, const typename Wk::Sha
     if constexpr (SHARES) {
         if (threadIdx.x == kWarps * 32 - 1 && unit.unit >= 0)
             a.unit_parts[unit.unit] =
-                make_int2(blockIdx.x, Wk::cta_of(unit.last_turn, unit.total, min(a.parts, unit.total)));
+                make_int2(Wk::my_share(a), Wk::cta_of(unit.last_turn, unit.total, min(a.parts, unit.total)));
     }
     for (int i = threadIdx.x; i < items; i += kWarps * 32) {
         const int h = i / (V / 4), u = i % (V / 4);
@@ -404,8 +421,8 @@ __device__ __forceinline__ void join(const AttendArgs& a, const typename Wk::Sha
             add_scaled(x, p.acc[w][h][u], f);
         }
         if (cluster) {
-            push(&p.in_acc[part * share + i % share], i / share, x);
-            if (u < a.parts) push(&p.in_ml[part][h], u, make_float2(m, l));
+            push(&in.acc[part * share + i % share], i / share, x);
+            if (u < a.parts) push(&in.ml[part][h], u, make_float2(m, l));
         } else if (unit.whole) {
             write_result<TI>(a, head + h, V, 4 * u, m, l, x);
         } else {
@@ -419,16 +436,16 @@ __device__ __forceinline__ void join(const AttendArgs& a, const typename Wk::Sha
     cluster_wait();
     for (int j = threadIdx.x; j < share && part * share + j < items; j += kWarps * 32) {
         const int i = part * share + j, h = i / (V / 4), u = i % (V / 4);
-        float m = p.in_ml[0][h].x;
-        for (int c = 1; c < a.parts; ++c) m = fmaxf(m, p.in_ml[c][h].x);
+        float m = in.ml[0][h].x;
+        for (int c = 1; c < a.parts; ++c) m = fmaxf(m, in.ml[c][h].x);
         const float base = finite_base(m);
         float l = 0.f;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int c = 0; c < a.parts; ++c) {
-            const float f = ex2(p.in_ml[c][h].x - base);
-            l = fmaf(p.in_ml[c][h].y, f, l);
-            add_scaled(x, p.in_acc[c * share + j], f);
+            const float f = ex2(in.ml[c][h].x - base);
+            l = fmaf(in.ml[c][h].y, f, l);
+            add_scaled(x, in.acc[c * share + j], f);
         }
         write_result<TI>(a, head + h, V, 4 * u, m, l, x);
     }
@@ -454,9 +471,10 @@ __global__ void __launch_bounds__(THREADS) k_attend_join(AttendArgs a) {
     // the first of them)
     const int64_t unit = (int64_t)n * a.units + hkv * a.tiles + qt;
     int64_t first;
-    int count;
+    int count, member = 0;
     if constexpr (SHARES) {
         const int2 range = a.unit_parts[unit];
+        member = (hkv * a.tiles + qt) % (unsigned)a.together;
         first = 2 * (int64_t)range.x;
         count = range.y - range.x + 1;
     } else {
@@ -474,7 +492,7 @@ __global__ void __launch_bounds__(THREADS) k_attend_join(AttendArgs a) {
 #pragma unroll
             for (int i = 0; i < kJoinBatch; ++i) {
                 const int c = s + i * G;
-                const int64_t from = (first + (SHARES ? 2 * c + (c == 0) : c)) * HT + h;
+                const int64_t from = (SHARES ? (first + 2 * c + (c == 0)) * a.together + member : first + c) * HT + h;
                 e[i] = c < count ? a.part_ml[from] : make_float2(-INFINITY, 0.f);
                 y[i] = c < count ? a.part_acc[from * (V / 4) + u] : make_float4(0.f, 0.f, 0.f, 0.f);
             }
@@ -556,6 +574,8 @@ struct Form {
     int tile;  // rows of a warp's tile
     int ctas;  // CTAs to an SM
     bool even; // it has kShares
+    size_t shared = 0;  // bytes of shared memory that a launch asks for
+    bool together = false;  // units have a share together
 };
 // Of a device: its SMs, and the largest cluster that the kernel can be placed in.
 struct Gpu {
@@ -566,6 +586,8 @@ struct Plan {
     int parts, ht, units, turn;
     dim3 grid;
     size_t acc_bytes, ml_bytes, ws_bytes;  // of the workspace
+    size_t shared;
+    int together;
 };
 Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window, int sinks, const Form& form, const Gpu& gpu);
 

@@ -12,7 +12,22 @@
 //   - the weights p sv times 2^(m - M + 11), M a running whole number like the maximum m itself, raised where one of them
 //     passes 2^15. Each is two fp16 values: to 2^-22 of itself, or 2^-35 of the largest.
 // m and M are whole numbers (log2 units), so that rescaling l and acc rounds nothing.
+//
+// Bound: the cached values are read once. Measured on one GB300 (time of a call in a graph; GB/s of the cached rows and
+// scales), bf16 queries, K = V = 128:
+//   64 sequences of U[1,8192] rows, 32 query heads on 8: 87 to 89 us, 6.0 TB/s (77 at a plain copy's rate); of 32768 rows
+//     each 622 us, 6.9 TB/s. The start (lengths, shares, pages, first rows), uneven SMs and the second kernel take 10 us.
+//     570 instructions of a warp to 8 KB, 39 % of the issue slots; tensor cores busy 26 % of the time;
+//   one of 65536 rows, 16 heads on 2: 12.9 us (5.0 at that rate); one of 2048 rows, 32 heads on 8: 6.0 us; both latency;
+//   with 16 heads to a cache head, twice the products and weights to a byte, 112 us for the first of these.
+// Where the rows come from matters more than how many are under way: the heads of a sequence take the same rows at the same
+// time (shares of all heads together: 93 -> 87 us; pages of 512 rows instead of 64 gain 3 %), and one tile of a warp under
+// way is faster than two (87 and 92 us, 12 warps to an SM; 8 warps of two tiles 95, 16 of one tile 95). Rows in registers, as
+// k_attend_mma holds them, took 92 us, with 720 instructions to a tile: 24 shuffles of addresses, now read from shared
+// memory, and loads of 16 bytes with a condition each, now asked only of tiles with a row that is not there.
 #include <cuda_fp16.h>
+
+#include <cfloat>
 
 #include "kda_attend.cuh"
 
@@ -20,11 +35,12 @@ namespace kda {
 namespace attend {
 namespace {
 
-// How far above the running maximum a score, or a weighted scale, may lie (log2 units) before l and acc are rescaled; and
-// the power of two that a weight at the running maximum has in fp16.
-constexpr float kSlack8 = 3.f;
+// How large a weight, relative to the running maximum, may be before l and acc are rescaled; the power of two that one times
+// its scale has in fp16 where it is at the running maximum of these; and the most that it may have.
+constexpr float kMostP8 = 8.f;  // 2^3
 constexpr int kTop8 = 11;
 constexpr float kMost8 = 32768.f;  // of a weight in fp16, which holds 65504
+constexpr float kNone8 = -FLT_MAX;  // of the maximum, before any score
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -47,6 +63,20 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *(const uint32_t*)&h;
 }
+// Two fp32 values to an instruction.
+struct Two {
+    uint64_t v;
+    __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ Two operator*(Two a, const Two& b) {
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+    return a;
+}
+__device__ __forceinline__ Two operator+(Two a, const Two& b) {
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+    return a;
+}
 __device__ __forceinline__ float2 unpack_f16(uint32_t x) { return __half22float2(*(const __half2*)&x); }
 // 2^x of a whole number x, 0 below 2^-126; x is at most 127. (-inf: 0)
 __device__ __forceinline__ float power(float x) {
@@ -57,11 +87,70 @@ __device__ __forceinline__ float max_of_rows(float x) {
     for (int w = 4; w < 32; w *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
     return x;
 }
-// 8 bytes of a row.
-__device__ __forceinline__ uint2 load8(const void* p, bool ok) {
-    uint2 x = make_uint2(0, 0);
-    if (ok) x = __ldcs((const uint2*)p);
+// A warp's tile of 32 rows in shared memory: K8, V8, the scales of K and of V, and the addresses of the rows. The units of 16
+// bytes of a row are permuted so that eight lanes that read together find all banks.
+template <int K, int V> struct Tile {
+    static constexpr int kScales = 32 * (K + V), kPlaces = kScales + 2 * 32 * 4, kWarp = kPlaces + 2 * 32 * 8,
+                         kBytes = kWarps * kWarp;
+    // K8: lanes read unit t of rows g; V8: unit g of rows 2 t
+    __device__ __forceinline__ static int k_at(int row, int unit) {
+        return row * K + (K == 128 ? unit ^ (row & 1) << 2 : unit) * 16;
+    }
+    __device__ __forceinline__ static int v_at(int row, int unit) {
+        if constexpr (V == 128) return 32 * K + row * V + (unit ^ (row & 6)) * 16;
+        return 32 * K + (row ^ (row >> 1 & 1)) * V + (unit ^ (row >> 1 & 2)) * 16;
+    }
+};
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 x;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
     return x;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t at) {
+    uint2 x;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(at) : "memory");
+    return x;
+}
+__device__ __forceinline__ void sts8(uint32_t at, const char* x) {
+    asm volatile("st.shared.b64 [%0], %1;" ::"r"(at), "l"(x) : "memory");
+}
+// 16 or 4 bytes to shared memory; zeros if not `ok`.
+__device__ __forceinline__ void fetch16(uint32_t to, const char* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void fetch16(uint32_t to, const char* from, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void fetch4(uint32_t to, const float* from, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(ok ? 4 : 0) : "memory");
+}
+// The units of 16 bytes of a tile's rows, whose addresses lie at `places`, to where `at` says; rows that are not valid as
+// zeros. D / 16 lanes to a row, and as many rows to a lane, whose addresses it reads two at a time.
+template <int D, typename At> __device__ __forceinline__ void fetch_rows(uint32_t places, unsigned valid, At at) {
+    constexpr int U = D / 16;
+    const int lane = threadIdx.x % 32, unit = lane % U, first = lane / U * U;
+    const auto address = [&](uint32_t lo, uint32_t hi) { return (const char*)((uint64_t)hi << 32 | lo) + unit * 16; };
+    if (valid == 0xffffffffu) {
+#pragma unroll
+        for (int i = 0; i < U; i += 2) {
+            const uint4 x = lds16(places + (first + i) * 8);
+            fetch16(at(first + i, unit), address(x.x, x.y));
+            fetch16(at(first + i + 1, unit), address(x.z, x.w));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < U; i += 2) {
+            const uint4 x = lds16(places + (first + i) * 8);
+            fetch16(at(first + i, unit), address(x.x, x.y), valid >> (first + i) & 1);
+            fetch16(at(first + i + 1, unit), address(x.z, x.w), valid >> (first + i + 1) & 1);
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All groups but the newest N are there, of every lane.
+template <int N> __device__ __forceinline__ void await() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    __syncwarp();
 }
 
 // CTAs of k_attend8 to an SM.
@@ -82,24 +171,50 @@ template <typename TI> __device__ __forceinline__ void load4(const TI* p, bool o
 
 // A unit has up to 8 NT query heads, each warp a tile of 32 rows at a time, a lane looking up one. The products are taken
 // transposed, as over a cache in 16 bits (k_attend_mma): S^T [32 rows x 8 heads] = K8 Q^T, O^T [V x 8 heads] += V8^T P^T.
-//   - lane 4 g + t loads 16-byte units t, t + 4, .. of rows g, g + 8, .. of K8; four channels of two rows are one product's
+//   - lane 4 g + t has 16-byte units t, t + 4, .. of rows g, g + 8, .. of K8; four channels of two rows are one product's
 //     share of the lane, and Q has the same order.
-//   - of V8 it loads V / 8 channels, from V / 8 g on, of rows 2 t, 2 t + 1, 2 t + 8, ..; a byte permutation pairs the
-//     rows, and row i of the j-th product is channel V / 8 (i % 8) + j.
+//   - of V8 it has V / 8 channels, from V / 8 g on, of rows 2 t, 2 t + 1, 2 t + 8, ..; a byte permutation pairs the rows,
+//     and row i of the j-th product is channel V / 8 (i % 8) + j.
+// The rows come through shared memory: K8 of the next tile is asked for once the scores of this one are there, V8 once its
+// sums are.
 template <typename TI, int K, int V, int NT, bool SHARES>
 __global__ void __launch_bounds__(kWarps * 32, ctas8(NT, K, V)) k_attend8(AttendArgs a) {
     constexpr int KI = K / 64, CW = V / 8, VJ = V / 16, HT = 8 * NT, QP = sizeof(TI) / 2;
-    __shared__ Partial<HT, V> sm;
+    typedef Tile<K, V> T;
+    extern __shared__ uint4 shared[];
+    Partial<HT, V>& sm = *(Partial<HT, V>*)shared;  // (once the rows are done with)
+    __shared__ Inbox<HT, V> in;
     const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     if (!SHARES && a.split == kCluster) cluster_started();
     after_previous();
-    typedef Work<32, HT, SHARES, true> Wk;
+    typedef Work<32, HT, SHARES, true, true> Wk;
     Wk wk;
     __shared__ typename Wk::Share share;
 #pragma unroll 1
     for (bool more = wk.start(a, share); more; more = wk.next(a, share)) {
         const int h0 = wk.h0, heads = wk.heads, warp = wk.warp;
         Rows<32, true>& rows = wk.rows;
+        const uint32_t tile = (uint32_t)__cvta_generic_to_shared(shared) + warp * T::kWarp;
+        const char *kh = (const char*)a.c.k + wk.hkv * a.c.k_head, *vh = (const char*)a.c.v + wk.hkv * a.c.v_head;
+        const float *ksh = a.k_scale + wk.hkv * a.ks_head, *vsh = a.v_scale + wk.hkv * a.vs_head;
+        // the next tile: K8 and the scales, then V8
+        auto fetch_k = [&]() {
+            rows.next(a);
+            const bool mine = rows.valid >> lane & 1;
+            const uint32_t page = (uint32_t)rows.at, block = a.block(rows.at_off);
+            const uint32_t places = tile + T::kPlaces, scale = tile + T::kScales + (4 * (lane % 8) + lane / 8) * 4;
+            sts8(places + lane * 8, kh + rows.k_off);
+            sts8(places + 256 + lane * 8, vh + rows.v_off);
+            fetch4(scale, ksh + ((uint64_t)page * (uint64_t)a.ks_page + (uint64_t)block * (uint64_t)a.ks_block), mine);
+            fetch4(scale + 128, vsh + ((uint64_t)page * (uint64_t)a.vs_page + (uint64_t)block * (uint64_t)a.vs_block), mine);
+            __syncwarp();
+            fetch_rows<K>(places, rows.valid, [&](int row, int unit) { return tile + T::k_at(row, unit); });
+        };
+        auto fetch_v = [&]() {
+            fetch_rows<V>(tile + T::kPlaces + 256, rows.valid, [&](int row, int unit) { return tile + T::v_at(row, unit); });
+        };
+        fetch_k();
+        fetch_v();
         uint32_t q[NT][QP][KI][4][2];
         float qf[NT][2];  // what the scores of heads 2 t, 2 t + 1 are multiplied by
 #pragma unroll
@@ -142,7 +257,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas8(NT, K, V)) k_attend8(Attend
         for (int j = 0; j < NT; ++j) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                m[j][e] = big[j][e] = -INFINITY;
+                m[j][e] = big[j][e] = kNone8;
                 l[j][e] = pf[j][e] = 0.f;
             }
 #pragma unroll
@@ -150,94 +265,70 @@ __global__ void __launch_bounds__(kWarps * 32, ctas8(NT, K, V)) k_attend8(Attend
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[j][i][e] = 0.f;
         }
-        const char* kh = (const char*)a.c.k + wk.hkv * a.c.k_head + t * 16;
-        const char* vh = (const char*)a.c.v + wk.hkv * a.c.v_head + g * CW;
-        const float *ksh = a.k_scale + wk.hkv * a.ks_head, *vsh = a.v_scale + wk.hkv * a.vs_head;
-        uint4 kr[4][KI], vr[8][(CW + 15) / 16];
-        uint2 vh8[CW == 8 ? 8 : 1];
-        float ks, vs;  // the scales of this lane's row
-        auto load_k = [&]() {
-            const bool mine = rows.valid >> lane & 1;
-            const int64_t block = a.block(rows.at_off);
-            ks = mine ? ksh[rows.at * a.ks_page + block * a.ks_block] : 0.f;
-            vs = mine ? vsh[rows.at * a.vs_page + block * a.vs_block] : 0.f;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const char* p = kh + rows.k_of(g + 8 * r);
-                const bool ok = rows.valid >> (g + 8 * r) & 1;
-#pragma unroll
-                for (int i = 0; i < KI; ++i) kr[r][i] = load16(p + 64 * i, ok);
-            }
-        };
-        auto load_v = [&]() {
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const int at = 2 * t + (r & 1) + 4 * (r & 2) + 4 * (r & 4);
-                const char* p = vh + rows.v_of(at);
-                const bool ok = rows.valid >> at & 1;
-                if constexpr (CW == 16)
-                    vr[r][0] = load16(p, ok);
-                else
-                    vh8[r] = load8(p, ok);
-            }
-        };
-        rows.next(a);
-        load_k();
-        load_v();
 #pragma unroll 1
         for (int left = wk.left; left > 0; left -= a.step) {
             float s[NT][2][4];  // of rows g, g + 8 (and 16 more) and heads 2 t, 2 t + 1
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-#pragma unroll
-                for (int j = 0; j < NT; ++j) s[j][b][0] = s[j][b][1] = s[j][b][2] = s[j][b][3] = 0.f;
-#pragma unroll
-                for (int i = 0; i < KI; ++i) {
-                    const uint32_t* r0 = (const uint32_t*)&kr[2 * b][i];
-                    const uint32_t* r1 = (const uint32_t*)&kr[2 * b + 1][i];
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const uint32_t a0 = lower2(r0[w]), a1 = lower2(r1[w]), a2 = upper2(r0[w]), a3 = upper2(r1[w]);
-#pragma unroll
-                        for (int j = 0; j < NT; ++j)
-#pragma unroll
-                            for (int c = 0; c < QP; ++c)
-                                mma_f16(s[j][b], a0, a1, a2, a3, q[j][c][i][w][0], q[j][c][i][w][1]);
-                    }
-                }
-            }
-            float vf[4];
-            const unsigned in = rows.valid;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float kf = __shfl_sync(0xffffffffu, ks, g + 8 * r);
-                vf[r] = __shfl_sync(0xffffffffu, vs, g + 8 * r);
-                const bool ok = in >> (g + 8 * r) & 1;
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float& x = s[j][r / 2][2 * (r % 2) + e];
-                        x = ok ? x * qf[j][e] * kf : -INFINITY;
-                    }
-            }
-            rows.next(a);
-            load_k();
-            // weights (p), and what they are times the scales of V (w)
-            float p[NT][4][2], w[NT][4][2];
-            bool higher = false;
+            await<1>();
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
+                for (int b = 0; b < 2; ++b) s[j][b][0] = s[j][b][1] = s[j][b][2] = s[j][b][3] = 0.f;
+            // (products that follow one another go to different sums)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float x = s[j][r / 2][2 * (r % 2) + e];
-                        p[j][r][e] = ex2(x - finite_base(m[j][e]));
-                        w[j][r][e] = p[j][r][e] * pf[j][e] * vf[r];
-                        higher |= x > m[j][e] + kSlack8 || fabsf(w[j][r][e]) > kMost8;
+            for (int i = 0; i < KI; ++i) {
+                uint32_t x[4][4];  // unit 4 i + t of rows g, g + 8, ..
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const uint4 y = lds16(tile + T::k_at(g + 8 * r, 4 * i + t));
+                    x[r][0] = y.x, x[r][1] = y.y, x[r][2] = y.z, x[r][3] = y.w;
+                }
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+#pragma unroll
+                    for (int c = 0; c < QP; ++c)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int j = 0; j < NT; ++j)
+                                mma_f16(s[j][b], lower2(x[2 * b][w]), lower2(x[2 * b + 1][w]), upper2(x[2 * b][w]),
+                                        upper2(x[2 * b + 1][w]), q[j][c][i][w][0], q[j][c][i][w][1]);
+            }
+            const uint4 k4 = lds16(tile + T::kScales + g * 16), v4 = lds16(tile + T::kScales + 128 + g * 16);
+            const float kf[4] = {__uint_as_float(k4.x), __uint_as_float(k4.y), __uint_as_float(k4.z), __uint_as_float(k4.w)};
+            const float vf[4] = {__uint_as_float(v4.x), __uint_as_float(v4.y), __uint_as_float(v4.z), __uint_as_float(v4.w)};
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float* x = s[j][r / 2] + 2 * (r % 2);
+                    (Two(x[0], x[1]) * Two(qf[j][0], qf[j][1]) * Two(kf[r], kf[r])).get(x[0], x[1]);
+                }
+            if (rows.valid != 0xffffffffu) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (!(rows.valid >> (g + 8 * r) & 1)) {
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) s[j][r / 2][2 * (r % 2)] = s[j][r / 2][2 * (r % 2) + 1] = -INFINITY;
                     }
-            if (__any_sync(0xffffffffu, higher)) {
+            }
+            __syncwarp();  // (the tile's K8 and scales, and the last tile's places, are read)
+            fetch_k();
+            // weights (p), and what they are times the scales of V (w)
+            float p[NT][4][2], w[NT][4][2], most_p = 0.f, most_w = 0.f;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float* x = s[j][r / 2] + 2 * (r % 2);
+                    float d[2];
+                    (Two(x[0], x[1]) + Two(-m[j][0], -m[j][1])).get(d[0], d[1]);
+                    p[j][r][0] = ex2(d[0]);
+                    p[j][r][1] = ex2(d[1]);
+                    (Two(p[j][r][0], p[j][r][1]) * Two(pf[j][0], pf[j][1]) * Two(vf[r], vf[r])).get(w[j][r][0], w[j][r][1]);
+                    most_p = fmaxf(most_p, fmaxf(p[j][r][0], p[j][r][1]));
+                    most_w = fmaxf(most_w, fmaxf(fabsf(w[j][r][0]), fabsf(w[j][r][1])));
+                }
+            if (__any_sync(0xffffffffu, most_p > kMostP8 || most_w > kMost8)) {
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -246,21 +337,19 @@ __global__ void __launch_bounds__(kWarps * 32, ctas8(NT, K, V)) k_attend8(Attend
 #pragma unroll
                         for (int r = 0; r < 4; ++r) top = fmaxf(top, s[j][r / 2][2 * (r % 2) + e]);
                         top = fmaxf(m[j][e], ceilf(max_of_rows(top)));
-                        const float base = finite_base(top);
-                        l[j][e] *= power(m[j][e] - base);
+                        l[j][e] *= power(m[j][e] - top);
                         m[j][e] = top;
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            p[j][r][e] = ex2(s[j][r / 2][2 * (r % 2) + e] - base);
+                            p[j][r][e] = ex2(s[j][r / 2][2 * (r % 2) + e] - top);
                             most = fmaxf(most, fabsf(p[j][r][e] * vf[r]));
                         }
                         // 2^(exponent of `most`, rounded up), as far from m as fp32 holds 2^(m - M + kTop8)
                         const int up = ((__float_as_int(max_of_rows(most)) + 0x7fffff) >> 23) - 127;
-                        const float to =
-                            top == -INFINITY ? big[j][e] : fmaxf(big[j][e], base + (float)max(up, kTop8 - 126));
+                        const float to = fmaxf(big[j][e], top + (float)max(up, kTop8 - 126));
                         const float f = power(big[j][e] - to);
                         big[j][e] = to;
-                        pf[j][e] = power(fmaxf(base - to + kTop8, -126.f));
+                        pf[j][e] = power(fmaxf(top - to + kTop8, -126.f));
 #pragma unroll
                         for (int i = 0; i < VJ; ++i) {
                             acc[j][i][e] *= f;
@@ -282,23 +371,29 @@ __global__ void __launch_bounds__(kWarps * 32, ctas8(NT, K, V)) k_attend8(Attend
                     pt[j][0][r] = transpose8(hi);
                     pt[j][1][r] = transpose8(pack_f16(w[j][r][0] - y.x, w[j][r][1] - y.y));
                 }
+            await<1>();
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < 2; ++b) {
+                uint32_t vr[4][CW / 4];  // rows 16 b + 2 t, + 1, + 8, + 9
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * b + 2 * t + (r & 1) + 4 * (r & 2);
+                    if constexpr (CW == 16) {
+                        const uint4 x = lds16(tile + T::v_at(row, g));
+                        vr[r][0] = x.x, vr[r][1] = x.y, vr[r][CW / 8] = x.z, vr[r][CW / 4 - 1] = x.w;
+                    } else {
+                        const uint2 x = lds8(tile + T::v_at(row, g / 2) + g % 2 * 8);
+                        vr[r][0] = x.x, vr[r][1] = x.y;
+                    }
+                }
 #pragma unroll
                 for (int c = 0; c < VJ / 4; ++c) {
                     // four products: rows 0-7 of the j-th are channels CW g + j, rows 8-15 channels CW g + j + CW / 2
                     uint32_t x[4][4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int word = c + (e & 1) * (VJ / 4), r = 4 * b + (e & 2);
-                        uint32_t even, odd;
-                        if constexpr (CW == 16) {
-                            even = ((const uint32_t*)&vr[r][0])[word];
-                            odd = ((const uint32_t*)&vr[r + 1][0])[word];
-                        } else {
-                            even = ((const uint32_t*)&vh8[r])[word];
-                            odd = ((const uint32_t*)&vh8[r + 1])[word];
-                        }
+                        const int word = c + (e & 1) * (VJ / 4);
+                        const uint32_t even = vr[e & 2][word], odd = vr[(e & 2) + 1][word];
                         const uint32_t lo = __byte_perm(even, odd, 0x5140), hi = __byte_perm(even, odd, 0x7362);
                         x[0][e] = lower2(lo);
                         x[1][e] = upper2(lo);
@@ -306,16 +401,20 @@ __global__ void __launch_bounds__(kWarps * 32, ctas8(NT, K, V)) k_attend8(Attend
                         x[3][e] = upper2(hi);
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int part = 0; part < 2; ++part)
 #pragma unroll
-                        for (int j = 0; j < NT; ++j)
+                        for (int i = 0; i < 4; ++i)
 #pragma unroll
-                            for (int part = 0; part < 2; ++part)
+                            for (int j = 0; j < NT; ++j)
                                 mma_f16(acc[j][4 * c + i], x[i][0], x[i][1], x[i][2], x[i][3], pt[j][part][2 * b],
                                         pt[j][part][2 * b + 1]);
                 }
-            load_v();
+            }
+            __syncwarp();  // (the tile's V8 is read)
+            fetch_v();
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();  // (all rows are done with)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -324,11 +423,11 @@ __global__ void __launch_bounds__(kWarps * 32, ctas8(NT, K, V)) k_attend8(Attend
 #pragma unroll
                 for (int d = 4; d < 32; d *= 2) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], d);
                 if (g == 0) {
-                    sm.m[warp][h] = m[j][e];
+                    sm.m[warp][h] = m[j][e] == kNone8 ? -INFINITY : m[j][e];
                     sm.l[warp][h] = l[j][e] * kAtMostOne;
                 }
                 // relative to m as the join wants it, in two steps that fp32 holds
-                const float apart = m[j][e] == -INFINITY ? 0.f : big[j][e] - m[j][e] - kTop8, half = rintf(0.5f * apart);
+                const float apart = m[j][e] == kNone8 ? 0.f : big[j][e] - m[j][e] - kTop8, half = rintf(0.5f * apart);
                 const float f0 = power(half) * kAtMostOne, f1 = power(apart - half);
                 float* row = (float*)sm.acc[warp][h] + CW * g;
 #pragma unroll
@@ -339,17 +438,18 @@ __global__ void __launch_bounds__(kWarps * 32, ctas8(NT, K, V)) k_attend8(Attend
                             make_float4(acc[j][i][e + 2 * r] * f0 * f1, acc[j][i + 1][e + 2 * r] * f0 * f1,
                                         acc[j][i + 2][e + 2 * r] * f0 * f1, acc[j][i + 3][e + 2 * r] * f0 * f1);
             }
-        join<TI, V, HT, SHARES, Wk>(a, share, sm);
+        join<TI, V, HT, SHARES, Wk>(a, share, sm, in);
         if constexpr (!SHARES) return;
         __syncthreads();  // the shared memory is free for the next unit
     }
 }
 
+template <typename TI, int K, int V> Kernel kernel_of(int ht, Split split) {
+    if (split == kShares) return ht == 8 ? k_attend8<TI, K, V, 1, true> : k_attend8<TI, K, V, 2, true>;
+    return ht == 8 ? k_attend8<TI, K, V, 1, false> : k_attend8<TI, K, V, 2, false>;
+}
 template <int K, int V> Kernel kernel_of(bool bf16, int ht, Split split) {
-    using B = __nv_bfloat16;
-    if (!bf16) return ht == 8 ? k_attend8<float, K, V, 1, false> : k_attend8<float, K, V, 2, false>;
-    if (split == kShares) return ht == 8 ? k_attend8<B, K, V, 1, true> : k_attend8<B, K, V, 2, true>;
-    return ht == 8 ? k_attend8<B, K, V, 1, false> : k_attend8<B, K, V, 2, false>;
+    return bf16 ? kernel_of<__nv_bfloat16, K, V>(ht, split) : kernel_of<float, K, V>(ht, split);
 }
 Kernel kernel_of(const kda_cache8& c, int ht, Split split) {
     const bool bf16 = c.dtype == KDA_DTYPE_BF16;
@@ -358,16 +458,37 @@ Kernel kernel_of(const kda_cache8& c, int ht, Split split) {
                     : (V == 128 ? kernel_of<64, 128>(bf16, ht, split) : kernel_of<64, 64>(bf16, ht, split));
 }
 
+template <int K, int V> constexpr size_t shared8(int ht) {
+    const size_t results = ht == 8 ? sizeof(Partial<8, V>) : sizeof(Partial<16, V>);
+    return results > Tile<K, V>::kBytes ? results : Tile<K, V>::kBytes;
+}
+size_t shared8(int ht, int K, int V) {
+    return K == 128 ? (V == 128 ? shared8<128, 128>(ht) : shared8<128, 64>(ht)) : (V == 128 ? shared8<64, 128>(ht) : shared8<64, 64>(ht));
+}
+
+// (The kernels of a form are allowed the shared memory that they ask for once on each device.)
 kda_status plan_for(const kda_cache8* c, int32_t HQ, int32_t N, int32_t max_pages, int32_t window, int32_t sinks, Plan& plan) {
     static std::atomic<int> known[2][2][2][2][kDevices];
+    static std::atomic<bool> allowed[2][2][2][2][kDevices];
     kda_status s = check_cache(c);
     if (s == KDA_OK) s = check_sizes(&c->cache, HQ, N, max_pages, window, sinks);
     if (s != KDA_OK) return s;
     const int K = c->cache.K, V = c->cache.V, ht = HQ / c->cache.HKV <= 8 ? 8 : 16, device = present_device();
     const bool bf16 = c->dtype == KDA_DTYPE_BF16;
-    const Form form{ht, 32, ctas8(ht / 8, K, V), bf16};
-    const Gpu gpu{sm_count(device), largest_cluster(device, (const void*)kernel_of(*c, ht, kCluster), kWarps * 32,
-                                                    kMaxCluster, known[bf16][ht / 16][K / 128][V / 128])};
+    const Form form{ht, 32, ctas8(ht / 8, K, V), true, shared8(ht, K, V), true};
+    if (device >= 0) {
+        std::atomic<bool>* done = device < kDevices ? &allowed[bf16][ht / 16][K / 128][V / 128][device] : nullptr;
+        if (!done || !done->load(std::memory_order_relaxed)) {
+            for (const Split split : {kCluster, kShares}) {
+                const cudaError_t e = cudaFuncSetAttribute(kernel_of(*c, ht, split), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                           (int)form.shared);
+                if (e != cudaSuccess) return cuda_fail(e);
+            }
+            if (done) done->store(true, std::memory_order_relaxed);
+        }
+    }
+    const Gpu gpu{sm_count(device), largest_cluster(device, (const void*)kernel_of(*c, ht, kCluster), kWarps * 32, kMaxCluster,
+                                                    known[bf16][ht / 16][K / 128][V / 128], form.shared)};
     plan = plan_of(&c->cache, HQ, N, max_pages, window, sinks, form, gpu);
     return KDA_OK;
 }

@@ -50,6 +50,7 @@ __global__ void __launch_bounds__(kWarps * 32, mma_ctas(NT, K, V)) k_attend_mma(
     using TI = __nv_bfloat16;
     constexpr int KI = K / 32, VC = V / 64, VJ = V / 16, HT = 8 * NT;
     __shared__ Partial<HT, V> sm;
+    __shared__ Inbox<HT, V> in;
     const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     if (!SHARES && a.split == kCluster) cluster_started();
     after_previous();
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(kWarps * 32, mma_ctas(NT, K, V)) k_attend_mma(
                             make_float4(acc[j][i][e + 2 * r], acc[j][i + 1][e + 2 * r], acc[j][i + 2][e + 2 * r],
                                         acc[j][i + 3][e + 2 * r]);
             }
-        join<TI, V, HT, SHARES, Wk>(a, share, sm);
+        join<TI, V, HT, SHARES, Wk>(a, share, sm, in);
         if constexpr (!SHARES) return;
         __syncthreads();  // the shared memory is free for the next unit
     }
@@ -227,6 +228,7 @@ template <int K, int V, int HT, int R, bool SINKS>
 __global__ void __launch_bounds__(kWarps * 32, simt_ctas(HT, K, V)) k_attend_simt(AttendArgs a) {
     constexpr int KL = K / 32, VL = V / 32, NV = R * HT;
     __shared__ Partial<HT, V> sm;
+    __shared__ Inbox<HT, V> in;
     const int lane = threadIdx.x % 32;
     if (a.split == kCluster) cluster_started();
     after_previous();
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(kWarps * 32, simt_ctas(HT, K, V)) k_attend_sim
     for (int h = 0; h < HT; ++h)
 #pragma unroll
         for (int i = 0; i < VL; ++i) ((float*)sm.acc[warp][h])[lane * VL + i] = acc[h][i];
-    join<float, V, HT, false, Wk>(a, share, sm);
+    join<float, V, HT, false, Wk>(a, share, sm, in);
 }
 
 // ------------------------------------------------------------------ which

@@ -35,13 +35,15 @@ inline int sm_count() { return sm_count(present_device()); }
 
 // The largest cluster, of at most `most` CTAs, that the device, which is the present one, can place the kernel in
 // (without one: `most`). `known` is the kernel's own.
-inline int largest_cluster(int device, const void* kernel, int threads, int most, std::atomic<int> (&known)[kDevices]) {
+inline int largest_cluster(int device, const void* kernel, int threads, int most, std::atomic<int> (&known)[kDevices],
+                           size_t shared = 0) {
     int n = 0;
     if (device < 0) return most;
     if (device < kDevices && (n = known[device].load(std::memory_order_relaxed)) > 0) return n;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(most);
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = shared;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
         cudaOccupancyMaxPotentialClusterSize(&n, kernel, &cfg) != cudaSuccess || n < 1) {
         cudaGetLastError();
