@@ -276,12 +276,22 @@ extern "C" size_t kda_cache_attend_sinks_workspace_bytes(const kda_cache* c, int
 extern "C" kda_status kda_debug_attend_plan(const kda_cache* c, int32_t HQ, int32_t N, int32_t max_pages, int32_t window,
                                             int32_t sms, int32_t cluster, int32_t* out) {
     Plan p;
-    const kda_status s = plan_for(c, HQ, N, max_pages, window, 0, p);
-    if (s != KDA_OK) return s;
+    if (c && c->dtype == KDA_DTYPE_E4M3) {
+        kda_cache8 c8{};
+        c8.cache = *c;
+        c8.dtype = KDA_DTYPE_BF16;
+        c8.block = 1;
+        c8.k_scale = c8.v_scale = (float*)c->k;  // (a plan does not go by them)
+        const kda_status s = plan_for8(&c8, HQ, N, max_pages, window, 0, sms > 0 ? Gpu{sms, cluster} : Gpu{}, p);
+        if (s != KDA_OK) return s;
+    } else {
+        const kda_status s = plan_for(c, HQ, N, max_pages, window, 0, p);
+        if (s != KDA_OK) return s;
+        if (sms > 0) p = plan_of(c, HQ, N, max_pages, window, 0, form_of(c, HQ), Gpu{sms, cluster});
+    }
     if (!out) return KDA_ERR_INVALID_ARG;
-    if (sms > 0) p = plan_of(c, HQ, N, max_pages, window, 0, form_of(c, HQ), Gpu{sms, cluster});
     out[0] = p.split;
-    out[1] = p.parts;
+    out[1] = p.parts * p.together;
     out[2] = p.split < kParts ? 0 : join_groups(unit_parts(p, N));
     out[3] = p.units * (N > 0 ? N : 1);
     return KDA_OK;

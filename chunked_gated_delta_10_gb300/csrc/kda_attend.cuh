@@ -579,7 +579,7 @@ struct Form {
 };
 // Of a device: its SMs, and the largest cluster that the kernel can be placed in.
 struct Gpu {
-    int sms, cluster;
+    int sms = 0, cluster = 0;
 };
 struct Plan {
     Split split;
@@ -590,6 +590,10 @@ struct Plan {
     int together;
 };
 Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window, int sinks, const Form& form, const Gpu& gpu);
+
+// The plan of a call on a cache in 8 bits (gpu.sms 0: on the present device).
+kda_status plan_for8(const kda_cache8* c, int32_t HQ, int32_t N, int32_t max_pages, int32_t window, int32_t sinks, Gpu gpu,
+                     Plan& plan);
 
 // The sizes that all forms of the operator refuse.
 kda_status check_sizes(const kda_cache* c, int32_t HQ, int32_t N, int32_t max_pages, int32_t window, int32_t sinks);

@@ -466,8 +466,11 @@ size_t shared8(int ht, int K, int V) {
     return K == 128 ? (V == 128 ? shared8<128, 128>(ht) : shared8<128, 64>(ht)) : (V == 128 ? shared8<64, 128>(ht) : shared8<64, 64>(ht));
 }
 
+}  // namespace
+
 // (The kernels of a form are allowed the shared memory that they ask for once on each device.)
-kda_status plan_for(const kda_cache8* c, int32_t HQ, int32_t N, int32_t max_pages, int32_t window, int32_t sinks, Plan& plan) {
+kda_status plan_for8(const kda_cache8* c, int32_t HQ, int32_t N, int32_t max_pages, int32_t window, int32_t sinks, Gpu gpu,
+                     Plan& plan) {
     static std::atomic<int> known[2][2][2][2][kDevices];
     static std::atomic<bool> allowed[2][2][2][2][kDevices];
     kda_status s = check_cache(c);
@@ -487,13 +490,13 @@ kda_status plan_for(const kda_cache8* c, int32_t HQ, int32_t N, int32_t max_page
             if (done) done->store(true, std::memory_order_relaxed);
         }
     }
-    const Gpu gpu{sm_count(device), largest_cluster(device, (const void*)kernel_of(*c, ht, kCluster), kWarps * 32, kMaxCluster,
-                                                    known[bf16][ht / 16][K / 128][V / 128], form.shared)};
+    if (gpu.sms == 0)
+        gpu = {sm_count(device), largest_cluster(device, (const void*)kernel_of(*c, ht, kCluster), kWarps * 32, kMaxCluster,
+                                                 known[bf16][ht / 16][K / 128][V / 128], form.shared)};
     plan = plan_of(&c->cache, HQ, N, max_pages, window, sinks, form, gpu);
     return KDA_OK;
 }
 
-}  // namespace
 }  // namespace attend
 }  // namespace kda
 
@@ -503,7 +506,7 @@ using namespace kda::attend;
 extern "C" size_t kda_cache8_attend_workspace_bytes(const kda_cache8* c, int32_t HQ, int32_t N, int32_t max_pages,
                                                     int32_t window, int32_t sinks) {
     Plan plan;
-    return plan_for(c, HQ, N, max_pages, window, sinks, plan) == KDA_OK ? plan.ws_bytes : 0;
+    return plan_for8(c, HQ, N, max_pages, window, sinks, Gpu{}, plan) == KDA_OK ? plan.ws_bytes : 0;
 }
 
 extern "C" kda_status kda_cache8_attend(const kda_cache8* c, const void* q, int64_t q_stride, int32_t HQ, int32_t N,
@@ -511,7 +514,7 @@ extern "C" kda_status kda_cache8_attend(const kda_cache8* c, const void* q, int6
                                         const int32_t* kv_lens, int32_t window, int32_t sinks, float scale, void* o,
                                         float* lse, int32_t* status, void* ws, size_t ws_bytes, kda_stream_t stream) {
     Plan plan;
-    kda_status s = plan_for(c, HQ, N, max_pages, window, sinks, plan);
+    kda_status s = plan_for8(c, HQ, N, max_pages, window, sinks, Gpu{}, plan);
     if (s != KDA_OK) return s;
     const bool bf16 = c->dtype == KDA_DTYPE_BF16;
     const Call x{q, q_stride, HQ, N, page_table, table_stride, max_pages, kv_lens, window, sinks, scale, o, lse, status, ws,

@@ -1,6 +1,7 @@
 """A small hybrid language model served token by token: three KDA layers to one layer of full attention.
 
     python examples/serve_hybrid.py [--layers 4] [--batch 4] [--prompt 200] [--tokens 32] [--no-graph]
+                                    [--eight-bit] [--window 64 --sinks 4]
 
 The weights are random (no checkpoint is involved); what the example shows is the path of a prompt and of the tokens
 after it:
@@ -9,7 +10,10 @@ after it:
   its final states go to the slots of the batch; attention layers append all rows to the paged cache at once
   (``cache_append``) and attend row by row (``cache_attend``, each prompt row a sequence of its own over its pages);
 * every token after them is one ``step`` per KDA layer and one ``cache_append`` + ``cache_attend`` per attention layer,
-  captured once in a CUDA graph and replayed.
+  captured once in a CUDA graph and replayed;
+* the pages of the caches come from a list of free ones and go back to it (``cache_resize``), on the GPU, within the graph;
+* the caches hold 16 bits or 8 (``--eight-bit``), and a token attends to all rows before it or to the last ``--window``
+  and the first ``--sinks``.
 
 At the end the whole sequences are run once more as prompts: their logits have to be those of the decoding.
 """
@@ -67,10 +71,12 @@ class KdaLayer:
 class AttentionLayer:
     """Grouped queries over a paged cache, positions by rotation."""
 
-    def __init__(self, rand, batch, pages, **_):
+    def __init__(self, rand, batch, pages, eight_bit, window, sinks):
         self.sizes = [QUERY * D, CACHE * D, CACHE * D]
         self.into, self.out = rand(DIM, sum(self.sizes)), rand(QUERY * D, DIM)
-        self.cache = kda.new_cache(pages, PAGE, CACHE, D, D)
+        cache = kda.new_cache(pages, PAGE, CACHE, D, D, dtype=torch.float8_e4m3fn if eight_bit else torch.bfloat16)
+        self.cache, self.scales = cache[:2], dict(zip(("k_scale", "v_scale"), cache[2:]))
+        self.seen = dict(window=window, sinks=sinks)
 
     def inputs(self, x):  # rows of one projection: the heads of a row are contiguous, the rows lie apart
         return [t.unflatten(-1, (n, D)) for t, n in zip((x @ self.into).split(self.sizes, -1), (QUERY, CACHE, CACHE))]
@@ -78,29 +84,33 @@ class AttentionLayer:
     def prompt(self, x, batch):
         q, k, v = self.inputs(x)
         q = kda.cache_append(k, v, *self.cache, batch["table"], torch.zeros_like(batch["lens"]), q=q, rope=batch["rope"],
-                             cu_seqlens=batch["cu"], status=batch["status"])
-        o, _ = kda.cache_attend(q, *self.cache, batch["row_table"], batch["row_lens"], status=batch["status"])
+                             cu_seqlens=batch["cu"], status=batch["status"], **self.scales)
+        o, _ = kda.cache_attend(q, *self.cache, batch["row_table"], batch["row_lens"], status=batch["status"], **self.seen,
+                                **self.scales)
         return o.flatten(1) @ self.out
 
     def token(self, x, batch):
         q, k, v = self.inputs(x)
         q = kda.cache_append(k, v, *self.cache, batch["table"], batch["lens"], q=q, rope=batch["rope"],
-                             status=batch["status"])
-        o, _ = kda.cache_attend(q, *self.cache, batch["table"], batch["lens"] + 1, status=batch["status"])
+                             status=batch["status"], **self.scales)
+        o, _ = kda.cache_attend(q, *self.cache, batch["table"], batch["longer"], status=batch["status"], **self.seen,
+                                **self.scales)
         return o.flatten(1) @ self.out
 
 
 class Model:
-    def __init__(self, layers, batch, longest, seed=0):
+    def __init__(self, layers, batch, longest, seed=0, eight_bit=False, window=0, sinks=0):
         gen = torch.Generator(device="cuda").manual_seed(seed)
         rand = lambda a, b: (torch.randn(a, b, generator=gen, device="cuda") / a ** 0.5).bfloat16()  # noqa: E731
         width = -(-longest // PAGE)
         self.embed = rand(VOCAB, DIM) * VOCAB ** 0.5
-        self.layers = [(AttentionLayer if i % 4 == 3 else KdaLayer)(rand, batch=batch, pages=batch * width)
-                       for i in range(layers)]
-        table = torch.randperm(batch * width, generator=gen, device="cuda").to(torch.int32).view(batch, width)
-        self.batch = dict(table=table, lens=torch.zeros(batch, dtype=torch.int32, device="cuda"),
-                          rope=rope_table(longest, "cuda"), status=torch.zeros(1, dtype=torch.int32, device="cuda"))
+        self.layers = [(AttentionLayer if i % 4 == 3 else KdaLayer)(
+            rand, batch=batch, pages=batch * width, eight_bit=eight_bit, window=window, sinks=sinks) for i in range(layers)]
+        i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+        # one table and one list of free pages for the caches of all layers
+        self.batch = dict(table=i32(batch, width) - 1, lens=i32(batch), longer=i32(batch), rope=rope_table(longest, "cuda"),
+                          free=torch.randperm(batch * width, generator=gen, device="cuda").to(torch.int32),
+                          count=i32(1) + batch * width, status=i32(1))
 
     def run(self, tokens, how):
         x = self.embed[tokens]
@@ -108,11 +118,18 @@ class Model:
             x = x + getattr(layer, how)(norm(x), self.batch)
         return norm(x).float() @ self.embed.float().T
 
+    def resize(self, new):
+        """Pages for `new` rows of each sequence; the new rows' offsets."""
+        b = self.batch
+        return kda.cache_resize(b["table"], b["lens"], new, b["free"], b["count"], PAGE, status=b["status"])[0]
+
     def prompts(self, prompts):
-        """Logits of every row of the packed prompts."""
+        """Logits of every row of the packed prompts. What the sequences held before goes."""
         b, lens = self.batch, torch.tensor([len(p) for p in prompts])
+        self.resize(torch.zeros_like(b["lens"]))
+        b["lens"].zero_()
         b["cu_host"] = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)])
-        b["cu"] = b["cu_host"].cuda()
+        b["cu"] = self.resize(lens.to(torch.int32).cuda())
         of = torch.repeat_interleave(torch.arange(len(prompts)), lens).cuda()
         b["row_table"] = b["table"][of]
         b["row_lens"] = torch.cat([torch.arange(1, n + 1) for n in lens.tolist()]).to(torch.int32).cuda()
@@ -122,8 +139,11 @@ class Model:
 
     def token(self, tokens):
         """Logits of one more token of every sequence."""
+        b = self.batch
+        torch.add(b["lens"], 1, out=b["longer"])
+        self.resize(b["longer"])
         logits = self.run(tokens, "token")
-        self.batch["lens"].add_(1)
+        b["lens"].copy_(b["longer"])
         return logits
 
 
@@ -134,12 +154,15 @@ def main(argv=None):
     ap.add_argument("--prompt", type=int, default=200, help="longest prompt")
     ap.add_argument("--tokens", type=int, default=32)
     ap.add_argument("--no-graph", action="store_true")
+    ap.add_argument("--eight-bit", action="store_true", help="caches in 8 bits, a scale for each 16 tokens and head")
+    ap.add_argument("--window", type=int, default=0, help="rows that a token attends to, its own among them (0: all)")
+    ap.add_argument("--sinks", type=int, default=0, help="first rows that stay visible beside the window")
     a = ap.parse_args(argv)
     kda.build()
     gen = torch.Generator().manual_seed(1)
     lens = torch.randint(1, a.prompt + 1, (a.batch,), generator=gen).tolist()
     prompts = [torch.randint(0, VOCAB, (n,), generator=gen) for n in lens]
-    model = Model(a.layers, a.batch, a.prompt + a.tokens)
+    model = Model(a.layers, a.batch, a.prompt + a.tokens, eight_bit=a.eight_bit, window=a.window, sinks=a.sinks)
 
     ends = torch.tensor(lens).cumsum(0) - 1
     logits = model.prompts(prompts)[ends.cuda()]
@@ -147,7 +170,9 @@ def main(argv=None):
     token = said[0].clone()
     step = model.token
     if not a.no_graph:
-        saved = [x.clone() for x in (model.batch["lens"], *(y.state for y in model.layers if isinstance(y, KdaLayer)))]
+        state = [*(model.batch[x] for x in ("lens", "table", "free", "count")),
+                 *(y.state for y in model.layers if isinstance(y, KdaLayer))]
+        saved = [x.clone() for x in state]
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
@@ -156,7 +181,7 @@ def main(argv=None):
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             out = model.token(token)
-        for x, y in zip((model.batch["lens"], *(y.state for y in model.layers if isinstance(y, KdaLayer))), saved):
+        for x, y in zip(state, saved):
             x.copy_(y)
 
         def step(_):

@@ -65,7 +65,8 @@ kda_status kda_debug_ws_region(const kda_dims* dims, int32_t pass, const char* n
  * joins them, 3: shares of plan[1] CTAs, and that kernel; plan[2]: the groups
  * that join a unit's parts (0: no second kernel); plan[3]: units. On a device
  * of `sms` SMs that places clusters of at most `cluster` CTAs (sms 0: on the
- * present device). Errors are those of kda_cache_attend's sizes. Launches
+ * present device). A cache whose dtype is KDA_DTYPE_E4M3: of
+ * kda_cache8_attend. Errors are those of kda_cache_attend's sizes. Launches
  * nothing.
  */
 kda_status kda_debug_attend_plan(const kda_cache* cache, int32_t HQ, int32_t N, int32_t max_pages, int32_t window,

@@ -391,18 +391,20 @@ def test_attend8(kda, case, dtype):  # noqa: F811
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("split, N, L", [("cache8_attend", 300, 100), ("cache8_attend_cluster", 2, 2000),
-                                         ("cache8_attend_parts", 1, 30000), ("cache8_attend_shares", 48, 6000)])
-def test_attend8_of_each_split(kda, split, N, L, dtype):  # noqa: F811
-    gen, size, heads, D, some = _gen(7), 20, 8 if N == 48 else 2, 64, 4
+@pytest.mark.parametrize("split, N, L, heads, group", [
+    ("cache8_attend", 300, 100, 2, 2), ("cache8_attend_cluster", 2, 2000, 2, 2), ("cache8_attend_parts", 1, 30000, 2, 2),
+    # shares of all heads of a sequence together, and of some; of tiles of query heads; of one alone
+    ("cache8_attend_shares", 48, 6000, 8, 2), ("cache8_attend_shares", 90, 3000, 5, 1), ("cache8_attend_shares", 70, 3000, 7, 12),
+    ("cache8_attend_shares", 40, 3000, 3, 40), ("cache8_attend_shares", 12, 5000, 50, 1), ("cache8_attend_shares", 450, 5000, 1, 3)])
+def test_attend8_of_each_split(kda, split, N, L, heads, group, dtype):  # noqa: F811
+    gen, size, D, some = _gen(7), 20, 64, 4
     width = -(-L // size)
     cache = make_cache8(gen, some * width, size, heads, D, D, 10)
     table = (torch.arange(N)[:, None] % some * width + torch.arange(width)).to(torch.int32)
     lens = [(L, 0, L // 2 + 1, L - 7)[n % 4] for n in range(N)]
-    q = torch.randn(some, 2 * heads, D, generator=gen).to(DT[dtype])
+    q = torch.randn(some, group * heads, D, generator=gen).to(DT[dtype])
     got = run8(kda, q[torch.arange(N) % some], cache, table, lens)
-    if dtype == "bf16":
-        assert kda.load().kda_launch_name(0).decode() == split
+    assert kda.load().kda_launch_name(0).decode() == split
     few = list(range(min(N, some)))
     ref = attend8_ref(q[few], *cache, table[few], lens, D ** -0.5, 0, 0)
     check8(dtype, (got[0][few], got[1][few]), ref)

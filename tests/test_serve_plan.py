@@ -84,3 +84,30 @@ def test_plan_without_a_device_is_a_gb300s(lib):  # noqa: F811
         pytest.skip("the present device's plan")
     for N, rows in ((1, 2048), (1, 65536), (64, 8192), (300, 40)):
         assert plan(lib, 32, 8, 128, 128, 0, N, rows, sms=0) == plan(lib, 32, 8, 128, 128, 0, N, rows)
+
+
+def places8(group, K, V, sms=152):
+    """CTAs of the attention kernel over a cache in 8 bits that the SMs hold."""
+    return sms * ((5 if K + V == 128 else 4) - (2 if group > 8 else 1))
+
+
+def test_no_cluster_waits_for_another_in_8_bits(lib):  # noqa: F811
+    seen = set()
+    for K, V in ((64, 64), (64, 128), (128, 64), (128, 128)):
+        for group in (1, 8, 16):
+            for units in list(range(1, 60, 7)) + list(range(60, 420, 5)):
+                for rows in (130, 260, 700, 1024, 3000):
+                    split, parts, _, of = plan(lib, group, 1, K, V, kda.DTYPE_E4M3, units, rows)
+                    if split == CLUSTER:
+                        seen.add(parts)
+                        assert of * parts <= places8(group, K, V) * ROOM[parts], (K, V, group, units, rows)
+    assert seen == set(ROOM)
+
+
+@pytest.mark.parametrize("heads", [1, 2, 3, 5, 7, 8, 12, 31, 48, 50, 97, 152])
+def test_shares_of_heads_together(lib, heads):  # noqa: F811
+    """As many CTAs as there are places, or nearly, in whole bundles of heads that make up a sequence's."""
+    split, ctas, _, _ = plan(lib, heads, heads, 128, 128, kda.DTYPE_E4M3, 64, 8192)
+    assert split == SHARES
+    assert 0.97 * places8(1, 128, 128) <= ctas <= places8(1, 128, 128)
+    assert any(heads % t == 0 and ctas % t == 0 for t in range(min(heads, 2), heads + 1)) or ctas == places8(1, 128, 128)
