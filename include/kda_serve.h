@@ -220,7 +220,7 @@ kda_status kda_cache8_append(const kda_cache8* cache, const void* k, int64_t k_s
  * only those that kda_cache8_append leaves). Scores are sums of exact products
  * in fp32, of bf16 queries as they are and of fp32 queries to 22 bits. Weights
  * times the scales of V enter the products as two fp16 values, to 2^-22, or
- * 2^-35 of the largest. q and o are in `dtype`; arguments, limits and errors
+ * 2^-35 of the largest (scales of 2^-100 and more). q and o are in `dtype`; arguments, limits and errors
  * are otherwise the same.
  */
 kda_status kda_cache8_attend(const kda_cache8* cache, const void* q, int64_t q_stride, int32_t HQ, int32_t N,
@@ -243,7 +243,8 @@ size_t kda_cache8_attend_workspace_bytes(const kda_cache8* cache, int32_t HQ, in
  *      there, and it wants no more than max_pages; if not it gets none, keeps
  *      those it has, and status is set.
  *   page_table  int32 [N, max_pages], row stride table_stride; other entries
- *               stay as they are
+ *               stay as they are. A page is in one place: held by one
+ *               sequence, or free (one that two sequences share goes back twice)
  *   free_pages  int32 [num_pages], of which the first free_count[0] are the
  *               free pages; pages come from its end and go to its end. An entry
  *               that goes back is moved as it is (status is set where it is no

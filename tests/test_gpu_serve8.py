@@ -414,6 +414,28 @@ def test_attend8_of_each_split(kda, split, N, L, heads, group, dtype):  # noqa: 
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("split, N, L, heads, window, sinks", [
+    ("cache8_attend", 300, 300, 2, 70, 20), ("cache8_attend_cluster", 2, 4000, 2, 1500, 100),
+    ("cache8_attend_parts", 1, 60000, 2, 25000, 1001), ("cache8_attend_shares", 60, 9000, 8, 5000, 70)])
+def test_attend8_sinks_of_each_split(kda, split, N, L, heads, window, sinks, dtype):  # noqa: F811
+    """First rows that end inside a tile, a turn, a block and a page; lengths at which they and the window meet."""
+    gen, size, D, some = _gen(13), 27, 64, 4
+    width = -(-L // size)
+    cache = make_cache8(gen, some * width, size, heads, D, D, 9)
+    table = (torch.arange(N)[:, None] % some * width + torch.arange(width)).to(torch.int32)
+    lens = [(L, window + sinks, window + sinks // 2, L - 77)[n % 4] for n in range(N)]
+    q = torch.randn(some, 2 * heads, D, generator=gen).to(DT[dtype])
+    got = run8(kda, q[torch.arange(N) % some], cache, table, lens, window=window, sinks=sinks)
+    assert kda.load().kda_launch_name(0).decode() == split
+    few = list(range(min(N, some)))
+    ref = attend8_ref(q[few], *cache, table[few], lens, D ** -0.5, window, sinks)
+    check8(dtype, (got[0][few], got[1][few]), ref)
+    for n in range(N):
+        i = n % some
+        assert ((got[0][n].double().cpu() - ref[0][i]).abs() <= 1.01 * (ref[2][i] + ROUND[dtype] * ref[0][i].abs())).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attend8_scales(kda, dtype):  # noqa: F811
     """Scales of V that differ by many powers of two and signs, in an order that makes the greatest come last or first;
     zero blocks of the smallest scale; scales of K that take scores far from 0; large and small queries."""
