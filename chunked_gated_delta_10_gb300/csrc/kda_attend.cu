@@ -144,9 +144,12 @@ template <typename TI, int V, int HT, int VS, int G, int THREADS>
 cudaError_t launch_join(const AttendArgs& a, cudaStream_t st) {
     const int64_t threads = (int64_t)a.N * a.HQ * (V / 4) * G;
     const unsigned grid = (unsigned)((threads + THREADS - 1) / THREADS);
-    if constexpr (sizeof(TI) == 2 || HT >= 8)  // (fp32 with fewer heads has no shares)
-        if (a.split == kShares) return launch_after(k_attend_join<TI, V, HT, VS, G, THREADS, true>, a, grid, THREADS, st);
-    return launch_after(k_attend_join<TI, V, HT, VS, G, THREADS, false>, a, grid, THREADS, st);
+    if constexpr (sizeof(TI) == 2 || HT >= 8) {  // (fp32 with fewer heads has no shares)
+        if (a.split == kShares && a.together > 1)
+            return launch_after(k_attend_join<TI, V, HT, VS, G, THREADS, true, true>, a, grid, THREADS, st);
+        if (a.split == kShares) return launch_after(k_attend_join<TI, V, HT, VS, G, THREADS, true, false>, a, grid, THREADS, st);
+    }
+    return launch_after(k_attend_join<TI, V, HT, VS, G, THREADS, false, false>, a, grid, THREADS, st);
 }
 // `parts`: of a unit, with equal lengths. A batch of loads is to cover them.
 int join_groups(int64_t parts) { return parts <= kJoinBatch ? 1 : parts <= 4 * kJoinBatch ? 4 : 32; }
@@ -250,8 +253,9 @@ kda_status plan_for(const kda_cache* c, int32_t HQ, int32_t N, int32_t max_pages
     kda_status s = check_cache(c);
     if (s == KDA_OK) s = check_sizes(c, HQ, N, max_pages, window, sinks);
     if (s != KDA_OK) return s;
-    const Form form = form_of(c, HQ);
-    plan = plan_of(c, HQ, N, max_pages, window, sinks, form, gpu_for(c, form, window > 0 && sinks > 0));
+    Form form = form_of(c, HQ);
+    form.together = window > 0 && sinks > 0;
+    plan = plan_of(c, HQ, N, max_pages, window, sinks, form, gpu_for(c, form, form.together));
     return KDA_OK;
 }
 

@@ -30,7 +30,7 @@ struct AttendArgs {
     int split, parts;  // parts: kCluster, kParts: CTAs of a unit; kShares: CTAs in all; kWhole: 1
     Divisor by_parts;
     int turn;  // rows that a CTA takes at a time
-    int together;  // kShares: units that have a share together, a CTA each (1 but for a cache in 8 bits)
+    int together;  // kShares: units that have a share together, a CTA each
     // What a CTA has of a unit that it does not have whole, head by head: the weighted sum relative to its maximum, and
     // its maximum (log2 units) and sum of weights. kParts: [units, parts, HT, V] and [units, parts, HT]; kShares: of the
     // unit that it ends (0) and of the one that it begins (1), [parts, 2, HT, V] and [parts, 2, HT], and of each unit the
@@ -167,8 +167,10 @@ template <int C> __device__ __forceinline__ void load_channels(const float* p, b
 //             kUnitTurns more than it has, about what it costs to begin and end one; else the CTAs with many short units
 //             would be the last (64 sequences of U[1,8192] rows, 32 heads on 8: 160 -> 154 us; 11 of U[1,4240], 256
 //             heads on 16: 42 -> 28 us). A unit that falls to several CTAs is joined by a second kernel.
-//             Over a cache in 8 bits the units of a sequence have a share together, as many of them as divide them all and
-//             leave few places empty: they read the same pages at the same time.
+//             Over a cache in 8 bits, and with first rows beside a window, the units of a sequence have a share together, as
+//             many of them as divide them all and leave few places empty: they read the same pages at the same time
+//             (64 sequences of U[1,8192] rows in 8 bits, 32 heads on 8: 93 -> 87 us; of U[1,16384] in 16 bits that see
+//             4160 of them: 138 -> 136).
 constexpr int kUnitTurns = 2;
 constexpr int kWarps = 4;
 constexpr int kMaxCluster = 16;
@@ -455,7 +457,7 @@ __device__ __forceinline__ void join(const AttendArgs& a, const typename Wk::Sha
 // Group g of G groups of VS / 4 threads takes parts g, g + G, .., a batch of them at a time; the groups are joined in
 // shared memory.
 constexpr int kJoinBatch = 8;
-template <typename TI, int V, int HT, int VS, int G, int THREADS, bool SHARES>
+template <typename TI, int V, int HT, int VS, int G, int THREADS, bool SHARES, bool TOGETHER>
 __global__ void __launch_bounds__(THREADS) k_attend_join(AttendArgs a) {
     constexpr int U = VS / 4, S = V / VS, HB = THREADS / (G * U);  // slices of a head; (head, slice) pairs of a CTA
     constexpr int GW = U < 32 && G > 1 ? 32 / U : 1;  // groups of a warp
@@ -471,11 +473,11 @@ __global__ void __launch_bounds__(THREADS) k_attend_join(AttendArgs a) {
     // the first of them)
     const int64_t unit = (int64_t)n * a.units + hkv * a.tiles + qt;
     int64_t first;
-    int count, member = 0;
+    int count;
     if constexpr (SHARES) {
         const int2 range = a.unit_parts[unit];
-        member = (hkv * a.tiles + qt) % (unsigned)a.together;
         first = 2 * (int64_t)range.x;
+        if constexpr (TOGETHER) first = first * a.together + (hkv * a.tiles + qt) % (unsigned)a.together;
         count = range.y - range.x + 1;
     } else {
         first = unit * a.parts;
@@ -492,7 +494,7 @@ __global__ void __launch_bounds__(THREADS) k_attend_join(AttendArgs a) {
 #pragma unroll
             for (int i = 0; i < kJoinBatch; ++i) {
                 const int c = s + i * G;
-                const int64_t from = (SHARES ? (first + 2 * c + (c == 0)) * a.together + member : first + c) * HT + h;
+                const int64_t part = SHARES ? 2 * c + (c == 0) : c, from = (first + (TOGETHER ? part * a.together : part)) * HT + h;
                 e[i] = c < count ? a.part_ml[from] : make_float2(-INFINITY, 0.f);
                 y[i] = c < count ? a.part_acc[from * (V / 4) + u] : make_float4(0.f, 0.f, 0.f, 0.f);
             }

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kWarps * 32, mma_ctas(NT, K, V)) k_attend_mma(
     const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     if (!SHARES && a.split == kCluster) cluster_started();
     after_previous();
-    typedef Work<16, HT, SHARES, SINKS> Wk;
+    typedef Work<16, HT, SHARES, SINKS, SINKS> Wk;
     Wk wk;
     __shared__ typename Wk::Share share;
 #pragma unroll 1
