@@ -59,8 +59,7 @@ inline int largest_cluster(int device, const void* kernel, int threads, int most
 struct Divisor {
     unsigned factor, shift;
     Divisor() = default;
-    __host__ explicit Divisor(unsigned d) : shift(31) {
-        while (1ull << (shift - 31) < d) ++shift;
+    __host__ explicit Divisor(unsigned d) : shift(31 + (d > 1 ? 32 - __builtin_clz(d - 1) : 0)) {
         factor = (unsigned)(((1ull << shift) + d - 1) / d);
     }
     __device__ __forceinline__ unsigned operator()(unsigned n) const {
