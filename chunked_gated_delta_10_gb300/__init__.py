@@ -396,8 +396,8 @@ def new_cache(num_pages, page_size, heads, K, V, dtype=torch.bfloat16, device="c
         if scale_block is not None:
             raise ValueError("scale_block is for a cache in float8_e4m3fn")
         return pair
-    block = scale_block or (16 if page_size % 16 == 0 else page_size)
-    if block < 0 or page_size % block:
+    block = (16 if page_size % 16 == 0 else page_size) if scale_block is None else scale_block
+    if block < 1 or page_size % block:
         raise ValueError(f"scale_block {block} does not divide the page size {page_size}")
     return pair + tuple(torch.zeros(num_pages, heads, page_size // block, device=device).transpose(1, 2) for _ in range(2))
 

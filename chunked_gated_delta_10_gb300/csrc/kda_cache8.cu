@@ -12,9 +12,8 @@
 //     other. A thread keeps its angles for all heads; rows come in ahead of their use through shared memory (cp.async: without
 //     it 4 us more); the largest value of a block is an atomicMax in shared memory, whose order does not matter. 16 packed
 //     prompts of U[1,4096] tokens, 32 query and 8 cache heads of 128, bf16, blocks of 16 (760 MB): 122 us, 6.2 TB/s, of which
-//     the cache's 202 MB take 40 (70 % of the issue slots: 260 instructions for 16 values of a thread, before divisions became
-//     multiplications) and the queries 84, at 95 % of a
-//     plain copy's rate. A warp to a block of one head, which reads the rows twice and angles for each head: 163 us.
+//     the cache's 202 MB take 40 (72 % of the issue slots, 245 instructions for 16 values of a thread) and the queries 83, at
+//     95 % of a plain copy's rate. A warp to a block of one head, which reads the rows twice and angles for each head: 163 us.
 //   Few rows of each sequence (less than 8 on average) or blocks longer than 128: a warp has a block of one head to itself.
 //     One token of each of 128 sequences 4.1 us in a graph, of one 2.4 (tiles, most of whose threads have no row: 5.2 to 13
 //     and 2.5; from 8 rows on they are faster: 16 x 16 rows 4.4 and 8.1 us).
@@ -565,7 +564,7 @@ template <typename TI, int K, int V> __global__ void __launch_bounds__(kTileThre
     // (keys, then values, their heads in a.splits / 2 parts)
     const unsigned item = blockIdx.x / a.splits, split = blockIdx.x - item * a.splits, parts = a.splits / 2;
     const unsigned part = split < parts ? split : split - parts;
-    const int head = part * a.c.cache.HKV / parts, end = (part + 1) * a.c.cache.HKV / parts;
+    const int head = (int)((uint64_t)part * a.c.cache.HKV / parts), end = (int)((uint64_t)(part + 1) * a.c.cache.HKV / parts);
     if (split < parts)
         append_tile<TI, K, true>(a, item, head, end - head);
     else
@@ -673,9 +672,9 @@ extern "C" kda_status kda_cache8_append(const kda_cache8* c8, const void* k, int
     const int64_t most = cu_seqlens ? 0 : items / N;
     const Append8Args a{*c8, k, v, q, q_out, k_stride, v_stride, q_stride, table_stride, HQ, N, (unsigned)R, (unsigned)(R / N),
                         cu_seqlens, rope, rope_len, rope_dim, interleaved, page_table, kv_lens, max_pages, status,
-                        unit,
-                        (unsigned)items, (unsigned)splits, (unsigned)most, 1, 1, Divisor(unit),
-                        Divisor(most > 0 ? most : 1), Divisor(R / N > 0 ? R / N : 1), Divisor(c8->block), Divisor(c->page_size)};
+                        unit, (unsigned)items, (unsigned)splits, (unsigned)most, 1, 1,
+                        Divisor(unit), Divisor(most > 0 ? most : 1), Divisor(R / N > 0 ? R / N : 1), Divisor(c8->block),
+                        Divisor(c->page_size)};
     cudaStream_t st = (cudaStream_t)stream;
     begin_launches(st);
     const cudaError_t e = bf16 ? launch<__nv_bfloat16>(a, tiles, threads, st) : launch<float>(a, tiles, threads, st);
