@@ -73,10 +73,10 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window, int s
     // places; 110 take 26.0 instead of 22.9 us, 111 31.5, where parts take 24.1. In 608 and 760 places 97 % are found).
     // None is to wait: that gains up to a quarter where lengths differ, and costs as much where they are equal (192
     // units, fp32, K = V = 64, of U[1,1500] and of 1500 rows with a window of 1024: 14.5 and 24.6 us; parts 16.4, 19.2).
-    constexpr struct {
+    const struct {
         int ctas, room;
         double join;
-    } clusters[] = {{2, 100, 1.2}, {4, 96, 1.2}, {8, 89, 1.7}, {16, 73, 2.4}};
+    } clusters[] = {{2, 100, form.join2}, {4, 96, form.join4}, {8, 89, form.join8}, {16, 73, 2.4}};
     for (const auto& x : clusters) {
         if (all * x.ctas * 100 > (int64_t)slots * x.room || x.ctas >= 2 * turns || x.ctas > gpu.cluster) continue;
         const double cost = x.join + (turns + x.ctas - 1) / x.ctas + begin(all * x.ctas);
@@ -96,7 +96,7 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window, int s
     if (parts > 1) {
         const int64_t each = (turns + parts - 1) / parts;
         parts = (turns + each - 1) / each;
-        const double cost = 3.6 + each * queue(all * parts) + begin(all * parts);
+        const double cost = form.join_parts + each * queue(all * parts) + begin(all * parts);
         if (cost < least) {
             least = cost;
             p.split = kParts;
@@ -105,7 +105,7 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window, int s
     }
     // Shares add up the lengths first, and have the ends of units within them. With fp32 the loop over units costs
     // registers, and 20 to 50 % of the time.
-    const double shares = 6.0 + mean * (turns + kUnitTurns) * all / slots + begin(slots);
+    const double shares = form.join_shares + mean * (turns + kUnitTurns) * all / slots + begin(slots);
     if (form.even && (turns + kUnitTurns) * all < INT32_MAX && shares < least) {
         p.split = kShares;
         p.parts = slots;

@@ -578,6 +578,8 @@ struct Form {
     bool even; // it has kShares
     size_t shared = 0;  // bytes of shared memory that a launch asks for
     bool together = false;  // units have a share together
+    // what the joins cost, in turns of a CTA: of clusters of 2, 4 and 8, of parts, and of shares with their start
+    double join2 = 1.2, join4 = 1.2, join8 = 1.7, join_parts = 3.6, join_shares = 6.0;
 };
 // Of a device: its SMs, and the largest cluster that the kernel can be placed in.
 struct Gpu {

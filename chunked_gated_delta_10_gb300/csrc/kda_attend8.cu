@@ -478,7 +478,8 @@ kda_status plan_for8(const kda_cache8* c, int32_t HQ, int32_t N, int32_t max_pag
     if (s != KDA_OK) return s;
     const int K = c->cache.K, V = c->cache.V, ht = HQ / c->cache.HKV <= 8 ? 8 : 16, device = present_device();
     const bool bf16 = c->dtype == KDA_DTYPE_BF16;
-    const Form form{ht, 32, ctas8(ht / 8, K, V), true, shared8(ht, K, V), true};
+    // (the costs of the joins: fitted to times of all splits of 23,000 sizes, and on average 2 % above the best split)
+    const Form form{ht, 32, ctas8(ht / 8, K, V), true, shared8(ht, K, V), true, 2.6, 1.4, 1.8, 2.7, 5.6};
     if (device >= 0) {
         std::atomic<bool>* done = device < kDevices ? &allowed[bf16][ht / 16][K / 128][V / 128][device] : nullptr;
         if (!done || !done->load(std::memory_order_relaxed)) {
