@@ -84,3 +84,35 @@ def test_example_runs(args):
     example = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(example)
     assert example.main(args + ["--tokens", "20"]) <= 0.05  # what it asks when run as a script
+
+
+def test_on_another_stream(kda):  # noqa: F811
+    """The kernels run on the current stream: work queued there before and after them is in order with them."""
+    gen, N, size, pool = _gen(3), 3, 16, 64
+    side = torch.cuda.Stream()
+    cache = kda.new_cache(pool, size, 2, 128, 128, dtype=E4M3)
+    scales = dict(k_scale=cache[2], v_scale=cache[3])
+    rows = [300, 1, 200]
+    x = [torch.randn(sum(rows), 2, 128, generator=gen).bfloat16().pin_memory() for _ in range(2)]
+    q = torch.randn(N, 8, 128, generator=gen).bfloat16()
+    new = torch.tensor(rows, dtype=torch.int32).pin_memory()
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    table, lens, wanted, count, free = i32(N, 20) - 1, i32(N), i32(N), i32(1), torch.arange(pool, dtype=torch.int32, device="cuda")
+    gq = q.cuda()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        wanted.copy_(new, non_blocking=True)
+        count.fill_(pool)
+        k, v = (t.cuda(non_blocking=True) for t in x)
+        cu, _, granted = kda.cache_resize(table, lens, wanted, free, count, size)
+        kda.cache_append(k, v, *cache[:2], table, lens, cu_seqlens=cu, **scales)
+        o, lse = kda.cache_attend(gq, *cache[:2], table, granted, **scales)
+        o, lse = o + 0, lse + 0
+    side.synchronize()
+    back = [bits(t).cpu().view(t.dtype) for t in cache]
+    check8("bf16", (o, lse), attend8_ref(q, *back, table.cpu(), rows, 128 ** -0.5, 0, 0))
+    at = torch.cat([torch.arange(n) for n in rows])
+    page = table.cpu()[torch.repeat_interleave(torch.arange(N), torch.tensor(rows)), at // size].long()
+    stands = back[1].float()[page, at % size] * back[3][page, at % size // 16][..., None]
+    assert ((stands - x[1].float()).abs() <= 2.0 ** -4 * x[1].float().abs() + 2.0 ** -10 * back[3].max()).all()
