@@ -11,14 +11,14 @@
 //   Several rows of each sequence: tiles of 16 rows or more in whole blocks, eight threads to a row, one head after the
 //     other. A thread keeps its angles for all heads; rows come in ahead of their use through shared memory (cp.async: without
 //     it 4 us more); the largest value of a block is an atomicMax in shared memory, whose order does not matter. 16 packed
-//     prompts of U[1,4096] tokens, 32 query and 8 cache heads of 128, bf16, blocks of 16 (760 MB): 122 us, 6.2 TB/s, of which
-//     the cache's 202 MB take 40 (72 % of the issue slots, 245 instructions for 16 values of a thread) and the queries 83, at
-//     95 % of a plain copy's rate. A warp to a block of one head, which reads the rows twice and angles for each head: 163 us.
+//     prompts of U[1,4096] tokens, 32 query and 8 cache heads of 128, bf16, blocks of 16 (760 MB): 120 us, 6.3 TB/s. The tiles
+//     alone (202 MB) take 40, bound by issue slots (72 %, 245 instructions for 16 values of a thread), the queries alone 83,
+//     bound by the memory: a launch has them side by side, one CTA in nine a tile (one after the other: 124). A warp to a
+//     block of one head, which reads the rows twice and angles for each head: 163 us.
 //   Few rows of each sequence (less than 8 on average) or blocks longer than 128: a warp has a block of one head to itself.
-//     One token of each of 128 sequences 4.1 us in a graph, of one 2.4 (tiles, most of whose threads have no row: 5.2 to 13
-//     and 2.5; from 8 rows on they are faster: 16 x 16 rows 4.4 and 8.1 us).
-//   Queries go with the same launch where that is small, as CTAs of their own, and otherwise to a launch of 64 threads a
-//     CTA, 16 to an SM (20 and 12 of them: 133 and 137 us for the prompts above, of 128 threads: 142).
+//     One token of each of 128 sequences 3.5 us in a graph, of one 2.4 (tiles, most of whose threads have no row: 5.2 to 13
+//     and 2.5; from 8 rows on they are faster: 16 x 16 rows 4.4 and 8.1 us). Queries go with the same launch where that is
+//     small, as CTAs of their own, and otherwise to a launch of 64 threads a CTA, 16 to an SM.
 #include <cfloat>
 
 #include "kda_cache.cuh"
@@ -46,6 +46,7 @@ struct Append8Args {
     unsigned items, splits;    // items, at most; CTAs of each
     unsigned most;             // items of a sequence, where there is no cu
     unsigned q_lanes, q_rows;  // query rows: threads of a row, rows of a CTA
+    unsigned mix;              // CTAs of which one has a tile, the others queries
     Divisor by_unit, by_most, by_per, by_block, by_page;
 };
 // The page of a position. (Divisor is for numbers below 2^31.)
@@ -539,7 +540,7 @@ template <typename TI> __device__ __forceinline__ void turn_queries(const Append
     }
 }
 
-// Blocks and queries in one launch where that has no more than so many CTAs to an SM; else each in its own.
+// A warp to a block. Queries in the same launch where that has no more than so many CTAs to an SM; else in their own.
 constexpr int kFew = 32;
 template <typename TI> __global__ void __launch_bounds__(kThreads, 4) k_append8(Append8Args a) {
     after_previous();
@@ -556,13 +557,14 @@ template <typename TI> __global__ void __launch_bounds__(kQueryThreads, 16) k_ap
 }
 template <typename TI, int K, int V> __global__ void __launch_bounds__(kTileThreads) k_append8_tiles(Append8Args a) {
     after_previous();
-    const unsigned tiles = a.items * a.splits;
-    if (blockIdx.x >= tiles) {
-        turn_queries<TI>(a, blockIdx.x - tiles);
+    // (one CTA of a.mix has a tile, the others queries, so that what binds the ones leaves room for the others)
+    const unsigned tiles = a.items * a.splits, at = blockIdx.x / a.mix, tile = min(at, tiles);
+    if (at >= tiles || blockIdx.x != at * a.mix) {
+        turn_queries<TI>(a, blockIdx.x - min(at + 1, tiles));
         return;
     }
     // (keys, then values, their heads in a.splits / 2 parts)
-    const unsigned item = blockIdx.x / a.splits, split = blockIdx.x - item * a.splits, parts = a.splits / 2;
+    const unsigned item = tile / a.splits, split = tile - item * a.splits, parts = a.splits / 2;
     const unsigned part = split < parts ? split : split - parts;
     const int head = (int)((uint64_t)part * a.c.cache.HKV / parts), end = (int)((uint64_t)(part + 1) * a.c.cache.HKV / parts);
     if (split < parts)
@@ -610,27 +612,27 @@ int64_t items_of(int64_t R, int64_t N, bool packed, int64_t unit) {
     return packed ? R / unit + 2 * N : N * (per > 0 ? (per + unit - 2) / unit + 1 : 0);
 }
 // Query rows of a CTA of so many threads, and threads of a row.
+constexpr unsigned kRowThreads = 64;
 unsigned queries_of(Append8Args& a, int threads) {
-    const unsigned tasks = a.HQ * (a.c.cache.K / 16);
+    const unsigned tasks = a.HQ * (a.c.cache.K / 16), most = threads < kRowThreads ? threads : kRowThreads;
     if (tasks == 0) return 0;
-    a.q_lanes = tasks < (unsigned)threads ? tasks : threads;
+    a.q_lanes = tasks < most ? tasks : most;
     a.q_rows = threads / a.q_lanes;
     return (a.R + a.q_rows - 1) / a.q_rows;
 }
 template <typename TI> cudaError_t launch(Append8Args a, bool tiles, int threads, cudaStream_t st) {
     const unsigned blocks = a.items * a.splits;
-    unsigned queries = queries_of(a, tiles ? threads : kThreads);
+    if (tiles) {
+        const unsigned queries = queries_of(a, threads);
+        a.mix = queries / blocks + 1;
+        return launch_tiles<TI>(a, blocks + queries, threads, st);
+    }
+    unsigned queries = queries_of(a, kThreads);
     const bool both = (int64_t)blocks + queries <= kFew * (int64_t)sm_count();
-    if (!both) queries = 0;
-    cudaError_t e = cudaSuccess;
-    if (tiles)
-        e = launch_tiles<TI>(a, blocks + queries, threads, st);
-    else
-        e = launch_after(k_append8<TI>, a, blocks + queries, kThreads, st);
+    const cudaError_t e = launch_after(k_append8<TI>, a, both ? blocks + queries : blocks, kThreads, st);
     if (e != cudaSuccess || both) return e;
     queries = queries_of(a, kQueryThreads);
-    if (queries) e = launch_after(k_append8_queries<TI>, a, queries, kQueryThreads, st);
-    return e;
+    return queries ? launch_after(k_append8_queries<TI>, a, queries, kQueryThreads, st) : cudaSuccess;
 }
 
 }  // namespace
@@ -668,11 +670,11 @@ extern "C" kda_status kda_cache8_append(const kda_cache8* c8, const void* k, int
     if (splits > (tiles ? slabs : all)) splits = tiles ? slabs : all;
     if (splits < 1) splits = 1;
     if (tiles) splits = splits < 2 ? 2 : splits / 2 * 2;
-    if (items * splits > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if (items * splits + (tiles && HQ > 0 ? R : 0) > INT32_MAX) return KDA_ERR_UNSUPPORTED;
     const int64_t most = cu_seqlens ? 0 : items / N;
     const Append8Args a{*c8, k, v, q, q_out, k_stride, v_stride, q_stride, table_stride, HQ, N, (unsigned)R, (unsigned)(R / N),
                         cu_seqlens, rope, rope_len, rope_dim, interleaved, page_table, kv_lens, max_pages, status,
-                        unit, (unsigned)items, (unsigned)splits, (unsigned)most, 1, 1,
+                        unit, (unsigned)items, (unsigned)splits, (unsigned)most, 1, 1, 1,
                         Divisor(unit), Divisor(most > 0 ? most : 1), Divisor(R / N > 0 ? R / N : 1), Divisor(c8->block),
                         Divisor(c->page_size)};
     cudaStream_t st = (cudaStream_t)stream;
