@@ -13,7 +13,7 @@
 //     it 4 us more); the largest value of a block is an atomicMax in shared memory, whose order does not matter. 16 packed
 //     prompts of U[1,4096] tokens, 32 query and 8 cache heads of 128, bf16, blocks of 16 (760 MB): 120 us, 6.3 TB/s. The tiles
 //     alone (202 MB) take 40, bound by issue slots (72 %, 245 instructions for 16 values of a thread), the queries alone 83,
-//     bound by the memory: a launch has them side by side, one CTA in nine a tile (one after the other: 124). A warp to a
+//     bound by the memory: a launch has them side by side, one CTA in four a tile (one after the other: 124). A warp to a
 //     block of one head, which reads the rows twice and angles for each head: 163 us.
 //   Few rows of each sequence (less than 8 on average) or blocks longer than 128: a warp has a block of one head to itself.
 //     One token of each of 128 sequences 3.5 us in a graph, of one 2.4 (tiles, most of whose threads have no row: 5.2 to 13
