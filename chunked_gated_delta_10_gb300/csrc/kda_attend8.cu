@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas8(NT, K, V)) k_attend8(Attend
                 for (int b = 0; b < 2; ++b) s[j][b][0] = s[j][b][1] = s[j][b][2] = s[j][b][3] = 0.f;
             // Products that follow one another go to different sums. How a tensor core rounds what it adds to a sum is not
             // specified, so the two parts of an fp32 query have sums of their own, joined by an fp32 addition: the median error
-            // of 4000 drawn cases (1 to 65536 rows) fell from 4.0e-7 to 2.4e-7, and no form became slower.
+            // of 4000 drawn cases (1 to 65536 rows) fell from 4.0e-7 to 2.4e-7, and no time that was measured grew.
             float more[QP == 2 ? NT : 1][2][4];  // of the second parts of fp32 queries
             if constexpr (QP == 2) {
 #pragma unroll
@@ -417,14 +417,35 @@ __global__ void __launch_bounds__(kWarps * 32, ctas8(NT, K, V)) k_attend8(Attend
                         x[2][e] = lower2(hi);
                         x[3][e] = upper2(hi);
                     }
+                    if constexpr (QP == 2) {
+                        // Sums of 16 rows, added to acc in fp32 and not by the tensor core, as above: the largest error of
+                        // those cases fell from 2.4e-6 to 1.1e-6, for 1 % of the time with 4 heads to a cache head (4 % with 64
+                        // channels) and 4 % with 16. For bf16 queries the output's rounding hides the difference.
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
+                        for (int j = 0; j < NT; ++j) {
+                            float sum[4][4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                            for (int i = 0; i < 4; ++i) sum[i][0] = sum[i][1] = sum[i][2] = sum[i][3] = 0.f;
 #pragma unroll
-                            for (int j = 0; j < NT; ++j)
-                                mma_f16(acc[j][4 * c + i], x[i][0], x[i][1], x[i][2], x[i][3], pt[j][part][2 * b],
-                                        pt[j][part][2 * b + 1]);
+                            for (int part = 1; part >= 0; --part)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    mma_f16(sum[i], x[i][0], x[i][1], x[i][2], x[i][3], pt[j][part][2 * b], pt[j][part][2 * b + 1]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) acc[j][4 * c + i][e] += sum[i][e];
+                        }
+                    } else {
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int j = 0; j < NT; ++j)
+                                    mma_f16(acc[j][4 * c + i], x[i][0], x[i][1], x[i][2], x[i][3], pt[j][part][2 * b],
+                                            pt[j][part][2 * b + 1]);
+                    }
                 }
             }
             __syncwarp();  // (the tile's V8 is read)
