@@ -40,6 +40,10 @@ namespace {
 constexpr float kMostP8 = 8.f;  // 2^3
 constexpr int kTop8 = 11;
 constexpr float kMost8 = 32768.f;  // of a weight in fp16, which holds 65504
+// The least exponent of scaled weights that M follows (relative to m), so that 2^(m - M + kTop8) is 2^124 at most: times a
+// weight of kMostP8 it is finite in fp32, also where all scales so far were 0 (infinity times a scale of 0 is a NaN). The
+// largest scaled weight has all its bits from 2^-113 on.
+constexpr int kLeast8 = kTop8 - 124;
 constexpr float kNone8 = -FLT_MAX;  // of the maximum, before any score
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -361,9 +365,9 @@ __global__ void __launch_bounds__(kWarps * 32, ctas8(NT, K, V)) k_attend8(Attend
                             p[j][r][e] = ex2(s[j][r / 2][2 * (r % 2) + e] - top);
                             most = fmaxf(most, fabsf(p[j][r][e] * vf[r]));
                         }
-                        // 2^(exponent of `most`, rounded up), as far from m as fp32 holds 2^(m - M + kTop8)
+                        // 2^(exponent of `most`, rounded up)
                         const int up = ((__float_as_int(max_of_rows(most)) + 0x7fffff) >> 23) - 127;
-                        const float to = fmaxf(big[j][e], top + (float)max(up, kTop8 - 126));
+                        const float to = fmaxf(big[j][e], top + (float)max(up, kLeast8));
                         const float f = power(big[j][e] - to);
                         big[j][e] = to;
                         pf[j][e] = power(fmaxf(top - to + kTop8, -126.f));

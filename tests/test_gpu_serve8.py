@@ -623,3 +623,46 @@ def test_cache8_in_a_graph(kda):  # noqa: F811
         assert torch.equal(a, b)
     for a, t in zip(state, (kc, vc, ks, vs)):
         assert torch.equal(a, bits(t))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("where", ["all", "first", "every other", "some heads", "keys"])
+@pytest.mark.parametrize("split, N, L, heads, group", [
+    ("cache8_attend", 300, 600, 2, 2), ("cache8_attend_cluster", 3, 3000, 4, 2), ("cache8_attend_parts", 1, 60000, 2, 2),
+    ("cache8_attend_shares", 48, 6000, 8, 2), ("cache8_attend", 300, 600, 2, 12)])
+def test_attend8_scales_of_zero(kda, split, N, L, heads, group, where, dtype):  # noqa: F811
+    """Blocks whose scale is 0, as of values that are all 0: of V for all rows, the first ones, every other block or one
+    head, and of K. Scores are whole multiples of 2.5 (log2 units) that go up and down from 32 rows to the next, so that
+    some rows weigh four to eight times the largest before them."""
+    gen, size, D, some, block = _gen(14), 20, 64, 2, 10
+    width = -(-L // size)
+    kc, vc, ks, vs = make_cache8(gen, some * width, size, heads, D, D, block)
+    kc.view(torch.uint8)[:] = 0
+    at = (torch.arange(some * width)[:, None] % width * size + torch.arange(size)) // 32  # the 32 rows of a row
+    steps = torch.randint(0, 2, (some * width, heads), generator=gen)[at].float()  # [pages, rows, heads]
+    kc.view(torch.uint8)[..., 0] = steps.to(E4M3).view(torch.uint8)
+    ks.fill_(1.0)
+    number = torch.arange(some * width)[:, None] % width * (size // block) + torch.arange(size // block)  # of a block
+    if where == "all":
+        vs.zero_()
+    elif where == "first":
+        vs[number < width * (size // block) // 2] = 0.0
+    elif where == "every other":
+        vs[number % 2 == 0] = 0.0
+    elif where == "some heads":
+        vs[..., ::2] = 0.0
+    else:
+        ks[number % 3 > 0] = 0.0
+        vs[number % 2 == 0] = 0.0
+    table = (torch.arange(N)[:, None] % some * width + torch.arange(width)).to(torch.int32)
+    q = torch.zeros(some, group * heads, D)
+    q[..., 0] = 1.0
+    q[..., 1:] = torch.randn(some, group * heads, D - 1, generator=gen)  # (of keys that are 0)
+    q, scale, lens = q.to(DT[dtype]), 2.5 * math.log(2), [L if n % some == 0 else L - 45 for n in range(N)]
+    got = run8(kda, q[torch.arange(N) % some], (kc, vc, ks, vs), table, lens, scale=scale)
+    assert kda.load().kda_launch_name(0).decode() == split
+    few = list(range(min(N, some)))
+    ref = attend8_ref(q[few], kc, vc, ks, vs, table[few], lens, scale, 0, 0)
+    check8(dtype, (got[0][few], got[1][few]), ref)
+    for n in range(N):
+        assert ((got[0][n].double().cpu() - ref[0][n % some]).abs() <= 1.01 * (ref[2][n % some] + ROUND[dtype] * ref[0][n % some].abs())).all()
