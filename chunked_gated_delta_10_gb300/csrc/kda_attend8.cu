@@ -82,6 +82,14 @@ __device__ __forceinline__ Two operator+(Two a, const Two& b) {
     return a;
 }
 __device__ __forceinline__ float2 unpack_f16(uint32_t x) { return __half22float2(*(const __half2*)&x); }
+// What two fp32 values are beyond two fp16 values. It is 16 at most (of kMost8), but for an infinite value, of which
+// infinity - infinity is left: -64 in its place keeps it infinite.
+__device__ __forceinline__ uint32_t rest_f16(float lo, float hi, uint32_t of) {
+    const float2 y = unpack_f16(of);
+    uint32_t x = pack_f16(lo - y.x, hi - y.y);
+    asm("max.f16x2 %0, %0, %1;" : "+r"(x) : "r"(0xd400d400u));  // (of a NaN and a number: the number)
+    return x;
+}
 // 2^x of a whole number x, 0 below 2^-126; x is at most 127. (-inf: 0)
 __device__ __forceinline__ float power(float x) {
     return __int_as_float(((int)fmaxf(x, -127.f) + 127) << 23);
@@ -388,9 +396,8 @@ __global__ void __launch_bounds__(kWarps * 32, ctas8(NT, K, V)) k_attend8(Attend
                     l[j][0] += p[j][r][0];
                     l[j][1] += p[j][r][1];
                     const uint32_t hi = pack_f16(w[j][r][0], w[j][r][1]);
-                    const float2 y = unpack_f16(hi);
                     pt[j][0][r] = transpose8(hi);
-                    pt[j][1][r] = transpose8(pack_f16(w[j][r][0] - y.x, w[j][r][1] - y.y));
+                    pt[j][1][r] = transpose8(rest_f16(w[j][r][0], w[j][r][1], hi));
                 }
             await<1>();
 #pragma unroll

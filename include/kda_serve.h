@@ -220,7 +220,9 @@ kda_status kda_cache8_append(const kda_cache8* cache, const void* k, int64_t k_s
  * only those that kda_cache8_append leaves). Scores are sums of exact products
  * in fp32, of bf16 queries as they are and of fp32 queries to 22 bits. Weights
  * times the scales of V enter the products as two fp16 values, to 2^-22, or
- * 2^-35 of the largest (scales of 2^-100 and more). q and o are in `dtype`; arguments, limits and errors
+ * 2^-35 of the largest (scales of 2^-100 and more). A scale of K is a factor of
+ * its row's score; an infinite one of V makes its rows' values infinite (NaN
+ * where they are 0). q and o are in `dtype`; arguments, limits and errors
  * are otherwise the same.
  */
 kda_status kda_cache8_attend(const kda_cache8* cache, const void* q, int64_t q_stride, int32_t HQ, int32_t N,

@@ -666,3 +666,37 @@ def test_attend8_scales_of_zero(kda, split, N, L, heads, group, where, dtype):  
     check8(dtype, (got[0][few], got[1][few]), ref)
     for n in range(N):
         assert ((got[0][n].double().cpu() - ref[0][n % some]).abs() <= 1.01 * (ref[2][n % some] + ROUND[dtype] * ref[0][n % some].abs())).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("split, N, L, heads, group", [
+    ("cache8_attend", 300, 600, 2, 2), ("cache8_attend_cluster", 3, 3000, 4, 2), ("cache8_attend_parts", 1, 30000, 2, 2),
+    ("cache8_attend_shares", 48, 6000, 8, 2), ("cache8_attend", 300, 600, 2, 12)])
+def test_attend8_infinite_scales(kda, split, N, L, heads, group, dtype):  # noqa: F811
+    """A block of V whose scale is infinite makes its head's channels infinite, of the sign of its values (NaN where one of
+    them is 0, or where they have both signs); the other heads are as without it."""
+    gen, size, D, some, block = _gen(15), 20, 64, 2, 10
+    width = -(-L // size)
+    kc, vc, ks, vs = make_cache8(gen, some * width, size, heads, D, D, block, spread=0)
+    table = (torch.arange(N)[:, None] % some * width + torch.arange(width)).to(torch.int32)
+    lens = [L - 45 * (n % some) for n in range(N)]
+    q = torch.randn(some, group * heads, D, generator=gen).to(DT[dtype])
+    every = torch.arange(N) % some
+    whole = run8(kda, q[every], (kc, vc, ks, vs), table, lens)
+    at = [n * width + width // 3 for n in range(some)]
+    vc, vs = vc.clone(), vs.clone()
+    for n, p in enumerate(at):
+        rows = vc[p, :block, 1].float().abs().clamp_min(1.0) * torch.where(torch.arange(D) % 3 == n, -1.0, 1.0)
+        rows[2, 5], rows[3, 6] = 0.0, -rows[4, 6]
+        vc.view(torch.uint8)[p, :block, 1] = rows.to(E4M3).view(torch.uint8)
+        vs[p, 0, 1] = math.inf if n == 0 else -math.inf
+    o, lse = run8(kda, q[every], (kc, vc, ks, vs), table, lens)
+    assert kda.load().kda_launch_name(0).decode() == split
+    sign = torch.stack([torch.where(torch.arange(D) % 3 == n, -math.inf, math.inf) * (1 - 2 * n) for n in range(some)])
+    sign[:, 5:7] = math.nan
+    mine = slice(group, 2 * group)
+    want = sign[every][:, None, :].expand(N, group, D)
+    assert torch.equal(o[:, mine].float().cpu().nan_to_num(9.0, 1.0, -1.0), want.nan_to_num(9.0, 1.0, -1.0))
+    assert torch.equal(lse, whole[1])
+    for others in (slice(0, group), slice(2 * group, None)):
+        assert torch.equal(o[:, others], whole[0][:, others])
