@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(kWarps * 32, ctas8(NT, K, V)) k_attend8(Attend
             qf[j][0] = __shfl_sync(0xffffffffu, down, 8 * t);
             qf[j][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
         }
-        float acc[NT][VJ][4], m[NT][2], l[NT][2], big[NT][2], pf[NT][2];  // big: M; pf: 2^(m - M + kTop8)
+        // (M is held relative to m: scores may lie where fp32 has steps of more than one)
+        float acc[NT][VJ][4], m[NT][2], l[NT][2], big[NT][2], pf[NT][2];  // big: M - m; pf: 2^(m - M + kTop8)
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -366,7 +367,8 @@ __global__ void __launch_bounds__(kWarps * 32, ctas8(NT, K, V)) k_attend8(Attend
 #pragma unroll
                         for (int r = 0; r < 4; ++r) top = fmaxf(top, s[j][r / 2][2 * (r % 2) + e]);
                         top = fmaxf(m[j][e], ceilf(max_of_rows(top)));
-                        l[j][e] *= power(m[j][e] - top);
+                        const float down = m[j][e] - top, was = big[j][e] + down;
+                        l[j][e] *= power(down);
                         m[j][e] = top;
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
@@ -375,10 +377,9 @@ __global__ void __launch_bounds__(kWarps * 32, ctas8(NT, K, V)) k_attend8(Attend
                         }
                         // 2^(exponent of `most`, rounded up)
                         const int up = ((__float_as_int(max_of_rows(most)) + 0x7fffff) >> 23) - 127;
-                        const float to = fmaxf(big[j][e], top + (float)max(up, kLeast8));
-                        const float f = power(big[j][e] - to);
+                        const float to = fmaxf(was, (float)max(up, kLeast8)), f = power(was - to);
                         big[j][e] = to;
-                        pf[j][e] = power(fmaxf(top - to + kTop8, -126.f));
+                        pf[j][e] = power(kTop8 - to);  // (to: kLeast8 to 128)
 #pragma unroll
                         for (int i = 0; i < VJ; ++i) {
                             acc[j][i][e] *= f;
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas8(NT, K, V)) k_attend8(Attend
                     sm.l[warp][h] = l[j][e] * kAtMostOne;
                 }
                 // relative to m as the join wants it, in two steps that fp32 holds
-                const float apart = m[j][e] == kNone8 ? 0.f : big[j][e] - m[j][e] - kTop8, half = rintf(0.5f * apart);
+                const float apart = m[j][e] == kNone8 ? 0.f : big[j][e] - kTop8, half = rintf(0.5f * apart);
                 const float f0 = power(half) * kAtMostOne, f1 = power(apart - half);
                 float* row = (float*)sm.acc[warp][h] + CW * g;
 #pragma unroll

@@ -700,3 +700,37 @@ def test_attend8_infinite_scales(kda, split, N, L, heads, group, dtype):  # noqa
     assert torch.equal(lse, whole[1])
     for others in (slice(0, group), slice(2 * group, None)):
         assert torch.equal(o[:, others], whole[0][:, others])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("power", [20, 24, 26, 40, 100, -40])
+def test_attend8_far_scores_and_large_scales(kda, power, dtype):  # noqa: F811
+    """Scores so far from 0 that fp32 holds them in steps of more than one, of which one row's is above all others, and
+    scales of V that are large or small: o is that row's value, in an order of rows that has it come last, or that raises
+    the maximum with every 32 rows before it."""
+    gen, size, D, rows = _gen(17), 16, 64, 1280
+    table = torch.arange(rows // size, dtype=torch.int32)[None]
+    kc, vc, ks, vs = make_cache8(gen, rows // size, size, 1, D, D, size, spread=0)
+    q = torch.zeros(1, 3, D)
+    q[..., 0] = 1.0
+    q = q.to(DT[dtype])
+    for order in (torch.zeros(rows // 32), torch.arange(rows // 32) / 8, torch.linspace(-7, -1, rows // 32)):
+        for best in (5, rows - 7):
+            k = kc.clone()
+            k.view(torch.uint8)[:] = 0
+            x = order.repeat_interleave(32).clamp(max=7)
+            x[best] = 16.0
+            k.view(torch.uint8)[..., 0, 0] = x.to(E4M3).view(torch.uint8).view(rows // size, size)
+            for scale_of_v in (1.0, 2.0 ** 20, -(2.0 ** 90), 2.0 ** -60):
+                sv = torch.full_like(vs, scale_of_v)
+                kd = torch.full_like(ks, 2.0 ** power)
+                o, lse = run8(kda, q, (k, vc, kd, sv), table, [rows], scale=1.0)
+                ref = attend8_ref(q, k, vc, kd, sv, table, [rows], 1.0, 0, 0)
+                if power > 0:  # (the other rows weigh nothing: e to the power of -2^20 and less)
+                    want = vc.float().flatten(0, 1)[best, 0].double() * scale_of_v
+                    assert torch.equal(ref[0][0, 0], want)
+                    err = (2.0 ** -21 + ROUND[dtype]) * want.abs() + 2.0 ** -34 * abs(scale_of_v) * 448
+                    assert ((o.double().cpu() - want).abs() <= err).all(), (order[-1], best, scale_of_v)
+                    assert ((lse.double().cpu() - ref[1]).abs() <= 4 * U * ref[1].abs()).all()
+                else:
+                    check8(dtype, (o, lse), ref)
