@@ -265,14 +265,16 @@ __device__ __forceinline__ void write_block(const Append8Args& a, const TI* from
     }
 }
 
+// Where sequence n begins, of the rows that there are.
+__device__ __forceinline__ int64_t row_at(const int64_t* cu, int n, unsigned R) { return min(max(cu[n], (int64_t)0), (int64_t)R); }
 // The sequence that new row r or, with `unit`, item r of the launch's belongs to: the last n that begins at or before it. A
 // sequence whose first row is cu[n] has items of so many rows from cu[n] / unit + 2 n on: two more than its rows fill, as
 // many as it may begin and end in.
-__device__ __forceinline__ int seq_of(const int64_t* cu, int N, int64_t r, const Divisor* unit) {
+__device__ __forceinline__ int seq_of(const int64_t* cu, int N, int64_t r, unsigned R, const Divisor* unit) {
     int lo = 0, hi = N - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if ((unit ? (*unit)((unsigned)cu[mid]) + 2 * (int64_t)mid : cu[mid]) <= r)
+        if ((unit ? (*unit)((unsigned)row_at(cu, mid, R)) + 2 * (int64_t)mid : cu[mid]) <= r)
             lo = mid;
         else
             hi = mid - 1;
@@ -295,13 +297,14 @@ __device__ __forceinline__ bool find_item(const Append8Args& a, unsigned item, I
     unsigned j;
     int64_t begin, end;
     if (a.cu) {
-        n = seq_of(a.cu, a.N, item, &a.by_unit);
+        n = seq_of(a.cu, a.N, item, a.R, &a.by_unit);
         begin = a.cu[n];
         end = a.cu[n + 1];
         if (item == 0 && threadIdx.x == 0 && (a.cu[0] != 0 || a.cu[a.N] != a.R)) flag(a);  // rows of no sequence
         if (begin < 0 || end < begin || end > a.R) {
             if (threadIdx.x == 0) flag(a);
-            return false;
+            end = min(end, (int64_t)a.R);  // (rows that are there are appended)
+            if (begin < 0 || end < begin) return false;
         }
         j = item - (a.by_unit((unsigned)begin) + 2 * n);
     } else {
@@ -493,9 +496,9 @@ template <typename TI> __device__ __forceinline__ void turn_queries(const Append
     unsigned idx;
     bool ok = true;
     if (a.cu) {
-        n = seq_of(a.cu, a.N, r, nullptr);
+        n = seq_of(a.cu, a.N, r, a.R, nullptr);
         const int64_t begin = a.cu[n];
-        ok = begin <= r && r < a.cu[n + 1];
+        ok = begin >= 0 && begin <= r && r < a.cu[n + 1];
         idx = (unsigned)(r - begin);
     } else {
         n = a.by_per((unsigned)r);

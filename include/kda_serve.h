@@ -205,8 +205,10 @@ typedef struct {
  * which values become a NaN too); its rows are then
  * written again in the new units, rounded once more where they fall below
  * e4m3's normal values. Scales of blocks without rows are not read. Rows that
- * are dropped count for nothing. Two sequences that append to the same page
- * race.
+ * are dropped count for nothing. Where cu_seqlens does not go from 0 to R,
+ * status is set; the rows of a sequence that begins before row 0 are dropped,
+ * those up to R of one that ends behind it are appended. Two sequences that
+ * append to the same page race.
  */
 kda_status kda_cache8_append(const kda_cache8* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                              const void* q, int64_t q_stride, void* q_out, int32_t HQ, int32_t N, int64_t R,

@@ -734,3 +734,33 @@ def test_attend8_far_scores_and_large_scales(kda, power, dtype):  # noqa: F811
                     assert ((lse.double().cpu() - ref[1]).abs() <= 4 * U * ref[1].abs()).all()
                 else:
                     check8(dtype, (o, lse), ref)
+
+
+@pytest.mark.parametrize("times, block", [(1, 4), (1, 16), (5, 4), (5, 16)])
+def test_append8_offsets_and_queries_agree(kda, times, block):  # noqa: F811
+    """Whatever cu_seqlens holds, a row's queries are 0 where the row is not appended, and there alone; where offsets end
+    beyond the rows, those that there are are appended, as to a cache in 16 bits."""
+    gen, R, pages = _gen(16), 20 * times, 8 * times
+    x = torch.randn(R, 1, 64, generator=gen).bfloat16().cuda()
+    table = torch.arange(3 * pages, dtype=torch.int32).view(3, pages).cuda()
+    lens = torch.tensor([3, 0, 5], dtype=torch.int32).cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    far = 2 ** 40
+    for cu in ([0, 4, 9, 20], [0, 4, 9, 15], [2, 4, 9, 20], [0, 4, 4, 20], [0, 4, 9, 25], [-5, 4, 9, 20], [0, 4, far, 20],
+               [0, 4, far, far], [-far, 4, 9, far], [-9, -5, 9, 20], [20, 20, 20, 20], [0, 0, 0, 0], [5, 5, 25, 30], [-4, -3, -2, -1],
+               [22, 25, 25, 30]):
+        cu = torch.tensor([c if abs(c) == far else c * times for c in cu])
+        kc, vc, ks, vs = kda.new_cache(3 * pages, 16, 1, 64, 64, dtype=E4M3, scale_block=block)
+        status.zero_()
+        q = kda.cache_append(x, x, kc, vc, table, lens, q=x, cu_seqlens=cu.cuda(), status=status, k_scale=ks, v_scale=vs)
+        good = cu[0] == 0 and cu[-1] == R and bool((cu[1:] >= cu[:-1]).all())
+        assert bool(int(status)) != good, cu
+        stands = (vc.float() * vs.repeat_interleave(block, 1)[..., None])[..., 0, :].flatten(0, 1).cpu()
+        held = stands[stands.any(1)]
+        there = [bool((held - row).abs().le(2.0 ** -4 * row.abs() + 2.0 ** -10 * vs.max().item()).all(1).any()) for row in x[:, 0].float().cpu()]
+        assert [bool(y) for y in q.flatten(1).any(1)] == there, cu
+        assert len(held) == sum(there), cu
+        if cu.min() >= 0:
+            k16, v16 = kda.new_cache(3 * pages, 16, 1, 64, 64)
+            as16 = kda.cache_append(x, x, k16, v16, table, lens, q=x, cu_seqlens=cu.cuda())
+            assert torch.equal(as16, q) and torch.equal(v16.float().any(-1), stands.view(3 * pages, 16, 1, 64).cuda().any(-1)), cu
