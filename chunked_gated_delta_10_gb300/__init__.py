@@ -132,6 +132,9 @@ def load():
             lib.kda_cache_attend_sinks_workspace_bytes.argtypes = [ctypes.POINTER(Cache), i32, i32, i32, i32, i32]
             lib.kda_cache8_append.restype = ctypes.c_int
             lib.kda_cache8_append.argtypes = [ctypes.POINTER(Cache8)] + lib.kda_cache_append.argtypes[1:]
+            lib.kda_cache_append_granted.restype = lib.kda_cache8_append_granted.restype = ctypes.c_int
+            lib.kda_cache_append_granted.argtypes = lib.kda_cache_append.argtypes[:-2] + [_P, _P, _P]
+            lib.kda_cache8_append_granted.argtypes = lib.kda_cache8_append.argtypes[:-2] + [_P, _P, _P]
             lib.kda_cache8_attend.restype = ctypes.c_int
             lib.kda_cache8_attend.argtypes = [ctypes.POINTER(Cache8)] + lib.kda_cache_attend_sinks.argtypes[1:]
             lib.kda_cache8_attend_workspace_bytes.restype = ctypes.c_size_t
@@ -403,7 +406,7 @@ def new_cache(num_pages, page_size, heads, K, V, dtype=torch.bfloat16, device="c
 
 
 def cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q=None, rope=None, interleaved=False, cu_seqlens=None,
-                 q_out=None, status=None, k_scale=None, v_scale=None):
+                 q_out=None, status=None, k_scale=None, v_scale=None, granted=None):
     """Append new keys and values to a paged cache, keys (and queries) rotated by their position on the way.
 
     k [R,HKV,K], v [R,HKV,V] and q [R,HQ,K] hold the new rows of all sequences: R / N each, or as ``cu_seqlens``
@@ -412,14 +415,15 @@ def cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q=None, rope=None,
     negative: inactive). ``rope`` fp32 [positions, r]: r/2 cosines, then r/2 sines; channel i turns with i + r/2, or,
     ``interleaved``, 2i with 2i+1. Returns the rotated queries (``q_out``, if given), or None without q.
     ``status`` (int32 [1], zeroed by the caller) is set where a page or position does not exist, or a row lies in
-    no sequence of ``cu_seqlens``.
+    no sequence of ``cu_seqlens``. ``granted`` (int32 [N], as :func:`cache_resize` returns it) are lengths up to which rows
+    are appended: those beyond are dropped, and their queries are 0, as in an inactive sequence.
 
     A cache in torch.float8_e4m3fn has ``k_scale`` and ``v_scale`` beside it (fp32 [pages, blocks, HKV], any strides; see
     :func:`new_cache`): a row is stored in units of its block's scale, the smallest power of two by which the block's
     values come to 448 at most. A block that has rows already is written again where its scale has to grow. The rows are
     bf16 or fp32 then, whichever k is, and the queries too."""
     r = (_serve_module or _serve()).append(k, v, k_cache, v_cache, page_table, kv_lens, q, rope, interleaved, cu_seqlens,
-                                           q_out, status, k_scale, v_scale)
+                                           q_out, status, k_scale, v_scale, granted)
     if type(r) is int:
         raise KdaError(r, "kda_cache_append")
     return r
@@ -474,7 +478,7 @@ def cache_resize(page_table, kv_lens, new_lens, free_pages, free_count, page_siz
     sequences before it, are not there gets none.
 
     Returns (cu_seqlens int64 [N+1], slots int64 [``rows``], granted int32 [N]): the new rows' offsets as
-    :func:`cache_append` takes them; where each new row goes, its page times ``page_size`` plus its row in the page, or -1
+    :func:`cache_append` takes them (with ``granted``: the rows of a sequence that was not served have offsets too); where each new row goes, its page times ``page_size`` plus its row in the page, or -1
     (of a sequence that was not served, and behind the last new row); and each sequence's length now, ``new_lens`` or,
     not served, ``kv_lens``. ``status`` (int32 [1], zeroed by the caller) is set where a sequence is not served, an entry
     is no page, or the new rows are more than ``rows``, if that is not 0."""

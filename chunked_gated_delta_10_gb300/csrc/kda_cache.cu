@@ -39,7 +39,7 @@ struct AppendArgs {
     const int64_t* cu;
     const float* rope;
     int rope_len, rope_dim, interleaved;
-    const int32_t *table, *kv_lens;
+    const int32_t *table, *kv_lens, *granted;
     int max_pages;
     int32_t* status;
     unsigned lanes, rows;  // short rows: threads of a row, rows of a CTA
@@ -58,7 +58,8 @@ __device__ __forceinline__ int seq_of(const int64_t* cu, int N, unsigned r) {
     return lo;
 }
 
-template <typename TI, bool SHORT, int MOST>
+// GRANTED: rows have lengths to keep to. (A kernel of its own: to ask whether they have takes 0.1 us of a token's 2.2.)
+template <typename TI, bool SHORT, int MOST, bool GRANTED>
 __global__ void __launch_bounds__(MOST, SHORT ? 6 : MOST == 64 ? 24 : 2) k_append(AppendArgs a) {
     constexpr int E = Unit<TI>::n, kBatch = SHORT ? 1 : 2;  // units of a row; copies that a thread has under way
     after_previous();
@@ -85,7 +86,8 @@ __global__ void __launch_bounds__(MOST, SHORT ? 6 : MOST == 64 ? 24 : 2) k_appen
     const unsigned at_pos = (unsigned)len + idx, pg = at_pos / (unsigned)a.c.page_size;
     const int64_t pos = at_pos, row = at_pos - pg * a.c.page_size;
     int64_t page = -1;
-    if (len >= 0) {
+    // (a row that was not granted is dropped like one of an inactive sequence)
+    if (len >= 0 && !(GRANTED && ok && at_pos >= (unsigned)max(a.granted[n], 0))) {
         ok = ok && pg < (unsigned)a.max_pages && (!a.rope || pos < (unsigned)a.rope_len);
         if (ok) page = a.table[n * a.table_stride + pg];
         if (page < 0 || page >= a.c.num_pages) {
@@ -173,8 +175,13 @@ __global__ void __launch_bounds__(MOST, SHORT ? 6 : MOST == 64 ? 24 : 2) k_appen
     }
 }
 
-template <typename TI> void (*kernel_of(bool few, int most))(AppendArgs) {
-    return few ? k_append<TI, true, 256> : most == 64 ? k_append<TI, false, 64> : k_append<TI, false, 512>;
+template <typename TI, bool GRANTED> void (*kernel_of(bool few, int most))(AppendArgs) {
+    return few          ? k_append<TI, true, 256, GRANTED>
+           : most == 64 ? k_append<TI, false, 64, GRANTED>
+                        : k_append<TI, false, 512, GRANTED>;
+}
+template <typename TI> void (*kernel_of(bool few, int most, bool granted))(AppendArgs) {
+    return granted ? kernel_of<TI, true>(few, most) : kernel_of<TI, false>(few, most);
 }
 
 }  // namespace
@@ -188,11 +195,23 @@ extern "C" kda_status kda_cache_append(const kda_cache* c, const void* k, int64_
                                        int32_t rope_len, int32_t rope_dim, int32_t interleaved,
                                        const int32_t* page_table, int64_t table_stride, int32_t max_pages,
                                        const int32_t* kv_lens, int32_t* status, kda_stream_t stream) {
+    return kda_cache_append_granted(c, k, k_stride, v, v_stride, q, q_stride, q_out, HQ, N, R, cu_seqlens, rope, rope_len,
+                                    rope_dim, interleaved, page_table, table_stride, max_pages, kv_lens, nullptr, status,
+                                    stream);
+}
+
+extern "C" kda_status kda_cache_append_granted(const kda_cache* c, const void* k, int64_t k_stride, const void* v,
+                                               int64_t v_stride, const void* q, int64_t q_stride, void* q_out, int32_t HQ,
+                                               int32_t N, int64_t R, const int64_t* cu_seqlens, const float* rope,
+                                               int32_t rope_len, int32_t rope_dim, int32_t interleaved,
+                                               const int32_t* page_table, int64_t table_stride, int32_t max_pages,
+                                               const int32_t* kv_lens, const int32_t* granted, int32_t* status,
+                                               kda_stream_t stream) {
     const kda_status s = check_cache(c);
     if (s != KDA_OK) return s;
     const int64_t unit = c->dtype == KDA_DTYPE_BF16 ? 8 : 4;
     const AppendCall x{k, k_stride, v, v_stride, q, q_stride, q_out, HQ, N, R, cu_seqlens, rope, rope_len, rope_dim,
-                       page_table, table_stride, max_pages, kv_lens, status};
+                       page_table, table_stride, max_pages, kv_lens, granted, status};
     const kda_status checked = check_append(c, x, unit);
     if (checked != KDA_OK || R == 0) return checked;
     const int64_t uk = (c->K - (interleaved ? 0 : rope_dim / 2)) / unit;
@@ -206,11 +225,11 @@ extern "C" kda_status kda_cache_append(const kda_cache* c, const void* k, int64_
     const int threads = (lanes * rows + 31) / 32 * 32;
     const AppendArgs a{*c, k, v, q, q_out, k_stride, v_stride, q_stride, table_stride, HQ, N, (unsigned)R,
                        (unsigned)(R / N), cu_seqlens, rope, rope_len, rope_dim, interleaved, page_table, kv_lens,
-                       max_pages, status, (unsigned)lanes, (unsigned)rows};
+                       granted, max_pages, status, (unsigned)lanes, (unsigned)rows};
     cudaStream_t st = (cudaStream_t)stream;
     begin_launches(st);
     void (*const kernel)(AppendArgs) =
-        c->dtype == KDA_DTYPE_BF16 ? kernel_of<__nv_bfloat16>(few, most) : kernel_of<float>(few, most);
+        c->dtype == KDA_DTYPE_BF16 ? kernel_of<__nv_bfloat16>(few, most, granted) : kernel_of<float>(few, most, granted);
     const cudaError_t e = launch_after(kernel, a, (unsigned)((R + rows - 1) / rows), threads, st);
     if (e != cudaSuccess) return cuda_fail(e);
     note_launch("cache_append", st);

@@ -51,7 +51,7 @@ struct AppendCall {
     const int32_t* page_table;
     int64_t table_stride;
     int32_t max_pages;
-    const int32_t *kv_lens, *status;
+    const int32_t *kv_lens, *granted, *status;
 };
 // Its checks (`unit`: elements of 16 bytes of the rows).
 inline kda_status check_append(const kda_cache* c, const AppendCall& x, int64_t unit) {
@@ -69,8 +69,8 @@ inline kda_status check_append(const kda_cache* c, const AppendCall& x, int64_t 
     if (!x.k || !x.v || !x.kv_lens || (!x.page_table && x.max_pages > 0)) return KDA_ERR_INVALID_ARG;
     for (const void* p : {x.k, x.v, x.q, (const void*)x.q_out, (const void*)x.rope})
         if (!aligned16(p)) return KDA_ERR_INVALID_ARG;
-    if (((uintptr_t)x.page_table & 3u) || ((uintptr_t)x.kv_lens & 3u) || ((uintptr_t)x.status & 3u) ||
-        ((uintptr_t)x.cu_seqlens & 7u))
+    if (((uintptr_t)x.page_table & 3u) || ((uintptr_t)x.kv_lens & 3u) || ((uintptr_t)x.granted & 3u) ||
+        ((uintptr_t)x.status & 3u) || ((uintptr_t)x.cu_seqlens & 7u))
         return KDA_ERR_INVALID_ARG;
     // (a row's units are counted in 32 bits, in steps of 1024 at most)
     if (x.R > INT32_MAX || ((int64_t)x.HQ + 2 * (int64_t)c->HKV) * 32 > INT32_MAX - 1024) return KDA_ERR_UNSUPPORTED;

@@ -229,16 +229,18 @@ Rows rows_of(PyObject* o, const char* name, int64_t rows, int64_t heads, int64_t
     return {t.data_ptr(), rows > 1 ? t.stride(0) : heads * channels};
 }
 
-// append(k, v, k_cache, v_cache, page_table, kv_lens, q, rope, interleaved, cu_seqlens, q_out, status, k_scale, v_scale)
+// append(k, v, k_cache, v_cache, page_table, kv_lens, q, rope, interleaved, cu_seqlens, q_out, status, k_scale, v_scale,
+//        granted)
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    expect(n, 14);
+    expect(n, 15);
     const Tensor& kt = cuda_tensor(a[0], "k", 3);
     const CacheArgs x = cache_of(a[2], a[3], a[4], a[5], a[12], a[13], kt);
     const int64_t R = kt.size(0);
     const Rows k = rows_of(a[0], "k", R, x.cache.HKV, x.cache.K, x), v = rows_of(a[1], "v", R, x.cache.HKV, x.cache.V, x);
     void* cu = like(a[9], "cu_seqlens", {x.N + (int64_t)1}, at::kLong, x.dev, true);
     void* status = like(a[11], "status", {1}, at::kInt, x.dev, true);
+    void* granted = like(a[14], "granted", {x.N}, at::kInt, x.dev, true);
     const float* rope = nullptr;
     int32_t positions = 0, turned = 0;
     if (a[7] != Py_None) {
@@ -272,12 +274,14 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
             made = make(shape, x.type, x.dev);
             op = made.data_ptr();
         }
-        s = x.eight() ? kda_cache8_append(&x, k.p, k.stride, v.p, v.stride, q.p, q.stride, op, HQ, x.N, R,
-                                          (const int64_t*)cu, rope, positions, turned, inter, x.table, x.table_stride,
-                                          x.width, x.lens, (int32_t*)status, stream_of(x.dev))
-                      : kda_cache_append(&x.cache, k.p, k.stride, v.p, v.stride, q.p, q.stride, op, HQ, x.N, R,
-                                         (const int64_t*)cu, rope, positions, turned, inter, x.table, x.table_stride,
-                                         x.width, x.lens, (int32_t*)status, stream_of(x.dev));
+        s = x.eight() ? kda_cache8_append_granted(&x, k.p, k.stride, v.p, v.stride, q.p, q.stride, op, HQ, x.N, R,
+                                                  (const int64_t*)cu, rope, positions, turned, inter, x.table,
+                                                  x.table_stride, x.width, x.lens, (const int32_t*)granted,
+                                                  (int32_t*)status, stream_of(x.dev))
+                      : kda_cache_append_granted(&x.cache, k.p, k.stride, v.p, v.stride, q.p, q.stride, op, HQ, x.N, R,
+                                                 (const int64_t*)cu, rope, positions, turned, inter, x.table,
+                                                 x.table_stride, x.width, x.lens, (const int32_t*)granted,
+                                                 (int32_t*)status, stream_of(x.dev));
     }
     return finish(s, made.defined() ? THPVariable_Wrap(std::move(made)) : Py_NewRef(a[10]));  // (None without q)
     END_HANDLE_TH_ERRORS
@@ -400,7 +404,7 @@ PyObject* resize(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 PyMethodDef methods[] = {
     {"step", (PyCFunction)(void*)step, METH_FASTCALL, "kda_step"},
-    {"append", (PyCFunction)(void*)append, METH_FASTCALL, "kda_cache_append, kda_cache8_append"},
+    {"append", (PyCFunction)(void*)append, METH_FASTCALL, "kda_cache_append_granted, kda_cache8_append_granted"},
     {"attend", (PyCFunction)(void*)attend, METH_FASTCALL, "kda_cache_attend_sinks, kda_cache8_attend"},
     {"resize", (PyCFunction)(void*)resize, METH_FASTCALL, "kda_cache_resize"},
     {nullptr, nullptr, 0, nullptr},

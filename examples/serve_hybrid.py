@@ -84,7 +84,7 @@ class AttentionLayer:
     def prompt(self, x, batch):
         q, k, v = self.inputs(x)
         q = kda.cache_append(k, v, *self.cache, batch["table"], torch.zeros_like(batch["lens"]), q=q, rope=batch["rope"],
-                             cu_seqlens=batch["cu"], status=batch["status"], **self.scales)
+                             cu_seqlens=batch["cu"], granted=batch["granted"], status=batch["status"], **self.scales)
         o, _ = kda.cache_attend(q, *self.cache, batch["row_table"], batch["row_lens"], status=batch["status"], **self.seen,
                                 **self.scales)
         return o.flatten(1) @ self.out
@@ -92,8 +92,8 @@ class AttentionLayer:
     def token(self, x, batch):
         q, k, v = self.inputs(x)
         q = kda.cache_append(k, v, *self.cache, batch["table"], batch["lens"], q=q, rope=batch["rope"],
-                             status=batch["status"], **self.scales)
-        o, _ = kda.cache_attend(q, *self.cache, batch["table"], batch["longer"], status=batch["status"], **self.seen,
+                             granted=batch["granted"], status=batch["status"], **self.scales)
+        o, _ = kda.cache_attend(q, *self.cache, batch["table"], batch["granted"], status=batch["status"], **self.seen,
                                 **self.scales)
         return o.flatten(1) @ self.out
 
@@ -119,9 +119,11 @@ class Model:
         return norm(x).float() @ self.embed.float().T
 
     def resize(self, new):
-        """Pages for `new` rows of each sequence; the new rows' offsets."""
+        """Pages for `new` rows of each sequence; the new rows' offsets. (batch["granted"]: the lengths that there are pages
+        for. There are for all here; a server tries the others again, or takes another sequence's pages.)"""
         b = self.batch
-        return kda.cache_resize(b["table"], b["lens"], new, b["free"], b["count"], PAGE, status=b["status"])[0]
+        cu, _, b["granted"] = kda.cache_resize(b["table"], b["lens"], new, b["free"], b["count"], PAGE, status=b["status"])
+        return cu
 
     def prompts(self, prompts):
         """Logits of every row of the packed prompts. What the sequences held before goes."""
@@ -143,7 +145,7 @@ class Model:
         torch.add(b["lens"], 1, out=b["longer"])
         self.resize(b["longer"])
         logits = self.run(tokens, "token")
-        b["lens"].copy_(b["longer"])
+        b["lens"].copy_(b["granted"])
         return logits
 
 

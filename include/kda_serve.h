@@ -118,6 +118,20 @@ kda_status kda_cache_append(const kda_cache* cache, const void* k, int64_t k_str
                             const int32_t* kv_lens, int32_t* status, kda_stream_t stream);
 
 /*
+ * The same for lengths that were granted (kda_cache_resize): a row whose
+ * position is granted[n] or more (int32 [N]; NULL: no such limit) is not
+ * appended and its q_out row is 0, as in an inactive sequence; no error. So a
+ * sequence that got no pages keeps its cache as it is, also where its last page
+ * has room for some of the rows.
+ */
+kda_status kda_cache_append_granted(const kda_cache* cache, const void* k, int64_t k_stride, const void* v,
+                                    int64_t v_stride, const void* q, int64_t q_stride, void* q_out, int32_t HQ, int32_t N,
+                                    int64_t R, const int64_t* cu_seqlens, const float* rope, int32_t rope_len,
+                                    int32_t rope_dim, int32_t interleaved, const int32_t* page_table, int64_t table_stride,
+                                    int32_t max_pages, const int32_t* kv_lens, const int32_t* granted, int32_t* status,
+                                    kda_stream_t stream);
+
+/*
  * Attention of one token of each of N sequences over its cached rows:
  *   o[n, h] = sum_t p_t V[t],  p = softmax_t(scale q[n, h] . K[t]),
  * t from max(0, kv_lens[n] - window) (window > 0; else from 0) to kv_lens[n]
@@ -215,6 +229,12 @@ kda_status kda_cache8_append(const kda_cache8* cache, const void* k, int64_t k_s
                              const int64_t* cu_seqlens, const float* rope, int32_t rope_len, int32_t rope_dim,
                              int32_t interleaved, const int32_t* page_table, int64_t table_stride, int32_t max_pages,
                              const int32_t* kv_lens, int32_t* status, kda_stream_t stream);
+kda_status kda_cache8_append_granted(const kda_cache8* cache, const void* k, int64_t k_stride, const void* v,
+                                     int64_t v_stride, const void* q, int64_t q_stride, void* q_out, int32_t HQ, int32_t N,
+                                     int64_t R, const int64_t* cu_seqlens, const float* rope, int32_t rope_len,
+                                     int32_t rope_dim, int32_t interleaved, const int32_t* page_table,
+                                     int64_t table_stride, int32_t max_pages, const int32_t* kv_lens,
+                                     const int32_t* granted, int32_t* status, kda_stream_t stream);
 
 /*
  * kda_cache_attend_sinks over such a cache: K[t] and V[t] are the values that
@@ -257,7 +277,10 @@ size_t kda_cache8_attend_workspace_bytes(const kda_cache8* cache, int32_t HQ, in
  *               status is set.
  *   cu_seqlens  int64 [N + 1], nullable: the new rows of each sequence,
  *               max(0, new_lens[n] - kv_lens[n]) of them, one sequence after the
- *               other, as kda_cache_append takes them
+ *               other, as kda_cache_append takes them; those of a sequence that
+ *               was not served among them, so append with `granted`
+ *               (kda_cache_append_granted), or its last page takes as many of
+ *               them as it has room for
  *   slots       int64 [rows], nullable: of each new row, its page * page_size
  *               plus its row in the page; -1 where it has no page or its
  *               sequence was not served, and behind the last new row. Where

@@ -242,3 +242,13 @@ def test_resize_workspace(lib):
     need = lib.kda_cache_resize_workspace_bytes
     assert need(1, 1, 1) == 0 and need(0, 0, 0) == 0 and need(-1, 1, 1) == 0  # one CTA, no workspace
     assert need(2, 8, 9000) == 3 * 8 + 4 * 4 and need(2000, 1, 0) > 0
+
+
+def test_granted_lengths_refused(lib):
+    """The appends with granted lengths make the checks of those without, and of the lengths' alignment."""
+    a16 = [A, 1024, A, 512, A, 2048, 2 * A, 16, 2, 4, None, A, 100, 64, 0, A, 5, 5, A]
+    for call, cache in ((lib.kda_cache_append_granted, _cache()), (lib.kda_cache8_append_granted, _cache8())):
+        assert call(cache, *a16, A + 2, None, None) == INVALID
+        assert call(cache, *a16, A, A + 2, None) == INVALID
+        assert call(None, *a16, A, None, None) == INVALID
+        assert call(cache, None, 1024, None, 512, None, 2048, None, 16, 2, 0, *a16[10:], None, None, None) == 0  # no rows
