@@ -6,8 +6,8 @@
 //   with count' = count + B(N), page i of those it takes is free[count' - 1 - T(n) - i], T the sum of `take` before n;
 //   it is served if T(n) + take(n) <= count'; its new rows begin at the sum of new - len before it.
 // So every CTA adds up the lengths before its sequences by itself (they are few numbers, read from L2), and no CTA waits
-// for another. Pages are taken behind those that come back, so the second step is a launch of its own; where all is little
-// work one CTA does both.
+// for another. Pages are taken behind those that come back, so the second step is a launch of its own; for few sequences one
+// CTA does both (see alone).
 //
 // Bound: latencies, one after the other: the lengths, their sums, entries of the list or the table, and again for the second
 // step. 256 sequences of 4000 rows that get one more 4.4 us in a graph, one CTA; 1000 sequences that get U[1,4096] rows
@@ -24,7 +24,6 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMostAlone = 1024;  // sequences that one CTA does both steps for
 constexpr int kRows = 1024;       // new rows of a CTA in the second step
 
 constexpr int kBatch = 4;          // entries that a thread has under way
@@ -86,8 +85,8 @@ __device__ __forceinline__ int64_t free_count(const ResizeArgs& a) {
 }
 
 // The sum over all threads of the CTA, and over the threads before this one.
-template <int THREADS> __device__ __forceinline__ Sums add_up(const Sums& x, Sums& before) {
-    __shared__ Sums of_warp[THREADS / 32];
+__device__ __forceinline__ Sums add_up(const Sums& x, Sums& before) {
+    __shared__ Sums of_warp[kThreads / 32];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     before = x;
 #pragma unroll
@@ -104,17 +103,17 @@ template <int THREADS> __device__ __forceinline__ Sums add_up(const Sums& x, Sum
     before.rows -= x.rows;
     Sums all{};
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
         if (w == warp) before += all;
         all += of_warp[w];
     }
     return all;
 }
 
-// The first step, for sequences [begin, stop), THREADS of them at most: pages go back; what the second step has to know is
+// The first step, for sequences [begin, stop), kThreads of them at most: pages go back; what the second step has to know is
 // written. ALONE: they are all there are.
-template <int THREADS, bool ALONE> __device__ __forceinline__ void give_back(const ResizeArgs& a, int begin, int stop) {
-    __shared__ int from[THREADS], upto[THREADS];  // first entry to go back; entries of the CTA's sequences so far
+template <bool ALONE> __device__ __forceinline__ void give_back(const ResizeArgs& a, int begin, int stop) {
+    __shared__ int from[kThreads], upto[kThreads];  // first entry to go back; entries of the CTA's sequences so far
     const int n = begin + threadIdx.x;
     const int64_t count = free_count(a);
     const Change x(a, min(n, a.N - 1));
@@ -124,7 +123,7 @@ template <int THREADS, bool ALONE> __device__ __forceinline__ void give_back(con
         mine = x.sums(a);
         if (x.need > x.has ? !x.fits(a) : x.has > a.max_pages) flag(a);
     }
-    all = add_up<THREADS>(mine, before);
+    all = add_up(mine, before);
     const int entries = all.back();
     from[threadIdx.x] = x.need;
     upto[threadIdx.x] = before.back() + mine.back();
@@ -145,7 +144,7 @@ template <int THREADS, bool ALONE> __device__ __forceinline__ void give_back(con
     const auto read = [&](int first) {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int e = first + k * THREADS;
+            const int e = first + k * kThreads;
             entry[k] = e < entries ? entry_of(e) : nullptr;
             page[k] = entry[k] ? *entry[k] : -1;
         }
@@ -154,16 +153,16 @@ template <int THREADS, bool ALONE> __device__ __forceinline__ void give_back(con
     read(threadIdx.x);
     if constexpr (!ALONE) {
         Sums later{}, unused;
-        for (int i = threadIdx.x; i < a.N; i += THREADS) {
+        for (int i = threadIdx.x; i < a.N; i += kThreads) {
             if (i < begin)
                 earlier += Change(a, i).sums(a);
             else if (i >= stop)
                 later += Change(a, i).sums(a);
         }
-        earlier = add_up<THREADS>(earlier, unused);
+        earlier = add_up(earlier, unused);
         before += earlier;
         all += earlier;
-        all += add_up<THREADS>(later, unused);
+        all += add_up(later, unused);
     }
     const int64_t room = min(count + all.back(), (int64_t)a.num_pages);
     if (n < stop) {
@@ -183,12 +182,12 @@ template <int THREADS, bool ALONE> __device__ __forceinline__ void give_back(con
         if (*a.count != count || count + all.back() > room || (a.slots && all.rows > a.rows)) flag(a);
     }
     const int64_t to = count + earlier.back();
-    for (int first = threadIdx.x; first < entries; first += kBatch * THREADS) {
-        if (first >= kBatch * THREADS) read(first);
+    for (int first = threadIdx.x; first < entries; first += kBatch * kThreads) {
+        if (first >= kBatch * kThreads) read(first);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             if (!entry[k]) continue;
-            const int64_t at = to + first + k * THREADS;
+            const int64_t at = to + first + k * kThreads;
             if ((unsigned)page[k] >= (unsigned)a.num_pages) flag(a);
             if (at < a.num_pages) a.free[at] = page[k];
             *entry[k] = -1;
@@ -228,7 +227,7 @@ __device__ __forceinline__ int taken(const ResizeArgs& a, int room, int64_t i) {
 }
 
 // The second step: the pages that are taken, as many for each of `ctas` CTAs.
-template <int THREADS> __device__ __forceinline__ void take_pages(const ResizeArgs& a, int cta, int ctas) {
+__device__ __forceinline__ void take_pages(const ResizeArgs& a, int cta, int ctas) {
     __shared__ int range[2];
     const int room = a.ends[a.N], all = a.ends[a.N + 1], each = (all + ctas - 1) / ctas;
     const int begin = (int)min((int64_t)cta * each, (int64_t)all), end = min(begin + each, all);
@@ -238,7 +237,7 @@ template <int THREADS> __device__ __forceinline__ void take_pages(const ResizeAr
         if (threadIdx.x % 32 == 0) range[threadIdx.x / 32] = n;
     }
     __syncthreads();
-    for (int i = begin + threadIdx.x; i < end; i += THREADS) {
+    for (int i = begin + threadIdx.x; i < end; i += kThreads) {
         const int n = first_above(a.ends, range[0], range[1], i);
         a.table[n * a.table_stride + Change(a, n).need - (a.ends[n] - i)] = taken(a, room, i);
     }
@@ -262,14 +261,14 @@ struct Rows {
 
 // The second step, rows [r0, r0 + count): their slots, four to a thread. Where they are of few sequences, what is known of
 // these lies in shared memory.
-template <int THREADS> __device__ __forceinline__ void find_slots(const ResizeArgs& a, int64_t r0, int count) {
+__device__ __forceinline__ void find_slots(const ResizeArgs& a, int64_t r0, int count) {
     constexpr int kFew = 64;
     __shared__ int range[2];
     __shared__ Rows few[kFew];
     const int64_t rows = a.begin[a.N];
     const int room = a.ends[a.N];
     if (r0 >= rows) {  // (as where the lengths have become shorter)
-        for (int i = threadIdx.x; i < count; i += THREADS) a.slots[r0 + i] = -1;
+        for (int i = threadIdx.x; i < count; i += kThreads) a.slots[r0 + i] = -1;
         return;
     }
     if (threadIdx.x < 64) {  // sequences of the first and the last row: the first that ends behind it
@@ -281,7 +280,7 @@ template <int THREADS> __device__ __forceinline__ void find_slots(const ResizeAr
     const bool known = hi - lo < kFew;
     if (known && lo + (int)threadIdx.x <= hi) few[threadIdx.x] = Rows(a, lo + threadIdx.x);
     __syncthreads();
-    for (int i = 4 * threadIdx.x; i < count; i += 4 * THREADS) {
+    for (int i = 4 * threadIdx.x; i < count; i += 4 * kThreads) {
         int64_t slot[4];
         int64_t stop = -1, add = -1;  // of the rows that lie in one page: the last, and what makes a slot of a row
         int n = -1;
@@ -342,34 +341,34 @@ template <int THREADS> __device__ __forceinline__ void find_slots(const ResizeAr
 __global__ void __launch_bounds__(kThreads) k_resize_back(ResizeArgs a) {
     after_previous();
     const int begin = blockIdx.x * a.seqs;
-    give_back<kThreads, false>(a, begin, min(begin + a.seqs, a.N));
+    give_back<false>(a, begin, min(begin + a.seqs, a.N));
 }
 
 __global__ void __launch_bounds__(kThreads) k_resize_take(ResizeArgs a) {
     after_previous();
     if (blockIdx.x < a.page_ctas) {
         if (blockIdx.x == 0 && threadIdx.x == 0) *a.count = a.ends[a.N] - a.ends[a.N + 1];
-        take_pages<kThreads>(a, blockIdx.x, a.page_ctas);
+        take_pages(a, blockIdx.x, a.page_ctas);
     } else {
         const int64_t r0 = (int64_t)(blockIdx.x - a.page_ctas) * kRows;
-        find_slots<kThreads>(a, r0, (int)min((int64_t)kRows, a.rows - r0));
+        find_slots(a, r0, (int)min((int64_t)kRows, a.rows - r0));
     }
 }
 
-template <int THREADS> __global__ void __launch_bounds__(THREADS, 1) k_resize_alone(ResizeArgs a) {
-    __shared__ int ends[THREADS + 2];
-    __shared__ int64_t begin[THREADS + 1];
+__global__ void __launch_bounds__(kThreads, 1) k_resize_alone(ResizeArgs a) {
+    __shared__ int ends[kThreads + 2];
+    __shared__ int64_t begin[kThreads + 1];
     after_previous();
     int64_t* cu = a.begin;
     a.ends = ends;
     a.begin = begin;
-    give_back<THREADS, true>(a, 0, a.N);
+    give_back<true>(a, 0, a.N);
     __syncthreads();
     if (threadIdx.x == 0) *a.count = ends[a.N] - ends[a.N + 1];
     if (cu)
-        for (int n = threadIdx.x; n <= a.N; n += THREADS) cu[n] = begin[n];
-    take_pages<THREADS>(a, 0, 1);
-    if (a.rows > 0) find_slots<THREADS>(a, 0, (int)a.rows);
+        for (int n = threadIdx.x; n <= a.N; n += kThreads) cu[n] = begin[n];
+    take_pages(a, 0, 1);
+    if (a.rows > 0) find_slots(a, 0, (int)a.rows);
 }
 
 // No sequences: no row has a slot.
@@ -380,9 +379,14 @@ __global__ void __launch_bounds__(kThreads) k_resize_none(ResizeArgs a) {
     if (at < a.rows) a.slots[at] = -1;
 }
 
-// Whether one CTA does both steps.
+// Whether one CTA does both steps: the fastest where little changes, and the host does not know what does. One more token for
+// each of 1 to 256 sequences 2.2 to 3.2 us (without slots), of two launches 3.7 to 4.7; but a page that goes or comes takes it 1.5 to 2.2 ns,
+// two launches of many CTAs a tenth or less: 64 sequences of 64 pages that begin or end 10.3 and 4.9 us, 256 of 256 144 and
+// 5.5, 16 of 8192 201 and 22. So with this many pages at most it is ahead where all sequences change in fewer than one of
+// about 130 calls. (A CTA of 1024 threads for as many sequences took 7.3 to 8.9 us for a token where two launches take 5.1
+// to 5.9, and 21 to 111 us for 16 to 131 pages of 1000 sequences where they take 6.4 to 6.7.)
 bool alone(int32_t N, int32_t max_pages, int64_t rows) {
-    return N <= kMostAlone && (int64_t)N * max_pages <= 1 << 17 && rows <= 4 * kMostAlone;
+    return N <= kThreads && (int64_t)N * max_pages <= 1 << 17 && rows <= 4 * kRows;
 }
 
 }  // namespace
@@ -417,12 +421,8 @@ extern "C" kda_status kda_cache_resize(int32_t* page_table, int64_t table_stride
     begin_launches(st);
     cudaError_t e;
     if (need == 0) {
-        if (N == 0)
-            e = launch_after(k_resize_none, a, (unsigned)(a.rows / kThreads + 1), kThreads, st);
-        else if (N <= kThreads)
-            e = launch_after(k_resize_alone<kThreads>, a, 1, kThreads, st);
-        else
-            e = launch_after(k_resize_alone<kMostAlone>, a, 1, kMostAlone, st);
+        e = N == 0 ? launch_after(k_resize_none, a, (unsigned)(a.rows / kThreads + 1), kThreads, st)
+                   : launch_after(k_resize_alone, a, 1, kThreads, st);
         if (e != cudaSuccess) return cuda_fail(e);
         note_launch("cache_resize", st);
         return KDA_OK;

@@ -252,3 +252,10 @@ def test_granted_lengths_refused(lib):
         assert call(cache, *a16, A, A + 2, None) == INVALID
         assert call(None, *a16, A, None, None) == INVALID
         assert call(cache, None, 1024, None, 512, None, 2048, None, 16, 2, 0, *a16[10:], None, None, None) == 0  # no rows
+
+
+def test_resize_of_many_sequences_or_pages_is_no_work_of_one_cta(lib):
+    need = lib.kda_cache_resize_workspace_bytes
+    assert need(256, 512, 4096) == 0 and need(1, 1 << 17, 0) == 0
+    for N, pages, rows in ((257, 1, 0), (1000, 16, 0), (1024, 128, 4096), (256, 513, 0), (16, 8193, 0), (1, 1, 4097)):
+        assert need(N, pages, rows) == 8 * (N + 1) + 4 * (N + 2)
