@@ -453,7 +453,7 @@ def cache_attend_workspace_bytes(q, k_cache, v_cache, page_table, window=0, sink
     pages, rows, heads, K = k_cache.shape
     dtypes = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32, torch.float8_e4m3fn: DTYPE_E4M3}
     for t, n in ((k_cache, "k_cache"), (q, "q")):
-        if t.dtype not in dtypes:
+        if t.dtype not in dtypes and (t is k_cache or k_cache.dtype == torch.float8_e4m3fn):  # (else q's says nothing)
             raise TypeError(f"unsupported dtype {t.dtype} of {n}")
     strides = [s if n > 1 else 0 for t in (k_cache, v_cache) for n, s in zip(t.shape[:3], t.stride())]
     c = Cache(k_cache.data_ptr(), v_cache.data_ptr(), *strides, pages, rows, heads, K, v_cache.shape[3], dtypes[k_cache.dtype])

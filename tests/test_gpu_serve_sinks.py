@@ -157,3 +157,16 @@ def test_sinks_in_a_graph(kda):  # noqa: F811
         graph.replay()
         torch.cuda.synchronize()
         check_attend("bf16", (o, lse), sinks_ref(q, kc, vc, table, [now], 0.125, 10, 3, size))
+
+
+def test_workspace_bytes_go_by_sizes(kda):  # noqa: F811
+    """Of a cache in 16 or 32 bits q's sizes count, and not its type; of one in 8 bits the type is that of a call."""
+    table = torch.zeros(3, 200, dtype=torch.int32, device="cuda")
+    for dt in (torch.bfloat16, torch.float32):
+        kc, vc = kda.new_cache(4, 16, 2, 64, 128, dtype=dt)
+        need = {kda.cache_attend_workspace_bytes(torch.zeros(3, 4, 64, dtype=t, device="cuda"), kc, vc, table)
+                for t in (torch.bfloat16, torch.float32, torch.float16, torch.int8)}
+        assert len(need) == 1 and need.pop() > 0
+    kc, vc = kda.new_cache(4, 16, 2, 64, 128, dtype=torch.float8_e4m3fn)[:2]
+    with pytest.raises(TypeError, match="q"):
+        kda.cache_attend_workspace_bytes(torch.zeros(3, 4, 64, dtype=torch.float16, device="cuda"), kc, vc, table)
