@@ -24,7 +24,8 @@ from .build import LIB, SERVE, build  # noqa: F401
 
 __all__ = ["build", "load", "Dims", "prepare_chunks", "workspace_bytes", "saved_bytes", "chunk_fwd", "chunk_bwd",
            "chunk_fwd_save", "chunk_bwd_from_saved", "step", "new_cache", "cache_append", "cache_attend",
-           "cache_attend_workspace_bytes", "cache_resize", "KdaError", "STATUS", "DTYPE_BF16", "DTYPE_F32", "DTYPE_E4M3", "PASS_FWD", "PASS_BWD"]
+           "cache_attend_workspace_bytes", "cache_resize", "KdaError", "STATUS", "DTYPE_BF16", "DTYPE_F32", "DTYPE_E4M3",
+           "PASS_FWD", "PASS_BWD"]
 
 DTYPE_BF16, DTYPE_F32, DTYPE_E4M3 = 0, 1, 2
 PASS_FWD, PASS_BWD = 0, 1
@@ -438,8 +439,10 @@ def cache_attend(q, k_cache, v_cache, page_table, kv_lens, scale=None, window=0,
     rows to attend, the new token's own among them (none: o is 0 and lse -inf). Returns (o [N,HQ,V], lse fp32
     [N,HQ]): new tensors, or ``out`` as o. ``ws`` (contiguous uint8) is scratch memory, of
     :func:`cache_attend_workspace_bytes` bytes or more; without it, or with less, the call allocates its own for as
-    long as it takes. What it holds does not matter, but two calls that may overlap on the GPU cannot share one. ``k_scale`` and ``v_scale`` are those of a
-    cache in 8 bits, as in :func:`cache_append`; q, in bf16 or fp32, says o's type then."""
+    long as it takes. What it holds does not matter, but two calls that may overlap on the GPU cannot share one.
+
+    ``k_scale`` and ``v_scale`` are those of a cache in 8 bits, as in :func:`cache_append`; q, in bf16 or fp32, says o's
+    type then."""
     r = (_serve_module or _serve()).attend(q, k_cache, v_cache, page_table, kv_lens, scale, window, ws, out, status, sinks,
                                            k_scale, v_scale)
     if type(r) is int:
@@ -478,10 +481,11 @@ def cache_resize(page_table, kv_lens, new_lens, free_pages, free_count, page_siz
     sequences before it, are not there gets none.
 
     Returns (cu_seqlens int64 [N+1], slots int64 [``rows``], granted int32 [N]): the new rows' offsets as
-    :func:`cache_append` takes them (with ``granted``: the rows of a sequence that was not served have offsets too); where each new row goes, its page times ``page_size`` plus its row in the page, or -1
-    (of a sequence that was not served, and behind the last new row); and each sequence's length now, ``new_lens`` or,
-    not served, ``kv_lens``. ``status`` (int32 [1], zeroed by the caller) is set where a sequence is not served, an entry
-    is no page, or the new rows are more than ``rows``, if that is not 0."""
+    :func:`cache_append` takes them (with ``granted``: the rows of a sequence that was not served have offsets too); where
+    each new row goes, its page times ``page_size`` plus its row in the page, or -1 (of a sequence that was not served, and
+    behind the last new row), for kernels of one's own; and each sequence's length now, ``new_lens`` or, not served,
+    ``kv_lens``. ``status`` (int32 [1], zeroed by the caller) is set where a sequence is not served, an entry is no page,
+    or the new rows are more than ``rows``, if that is not 0."""
     r = (_serve_module or _serve()).resize(page_table, kv_lens, new_lens, free_pages, free_count, page_size, rows, status)
     if type(r) is int:
         raise KdaError(r, "kda_cache_resize")

@@ -85,7 +85,7 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window, int s
         p.split = kCluster;
         p.parts = x.ctas;
     }
-    // Parts, and the second kernel: as many as fit. fp32, sequences of several lengths: `times` as many, so that others
+    // Parts, and the second kernel: as many as fit. A cache in fp32, sequences of several lengths: `times` as many, so that others
     // take the places of those that end early, which evens them out: T turns of a CTA become T (mean + (1 - mean) /
     // times), and each time costs a start of 0.9. (152 sequences of U[1,16000], K = V = 128, five heads: 414 -> 266 us;
     // of 16000: 465 -> 480.)
@@ -103,8 +103,8 @@ Plan plan_of(const kda_cache* c, int HQ, int N, int max_pages, int window, int s
             p.parts = (int)parts;
         }
     }
-    // Shares add up the lengths first, and have the ends of units within them. With fp32 the loop over units costs
-    // registers, and 20 to 50 % of the time.
+    // Shares add up the lengths first, and have the ends of units within them. In k_attend_simt (a cache in fp32) the loop
+    // over units costs registers, and 20 to 50 % of the time, so it has none.
     const double shares = form.join_shares + mean * (turns + kUnitTurns) * all / slots + begin(slots);
     if (form.even && (turns + kUnitTurns) * all < INT32_MAX && shares < least) {
         p.split = kShares;

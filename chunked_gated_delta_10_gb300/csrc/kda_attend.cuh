@@ -161,9 +161,9 @@ template <int C> __device__ __forceinline__ void load_channels(const float* p, b
 //             depend on the length, and their pages are looked up while it is on its way) and join their results in
 //             shared memory: for few units of some turns, where latency counts;
 //   kParts    the same with more CTAs than a cluster has, joined by a second kernel: for few units of many turns, and
-//             with fp32 for all of many rows;
-//   kShares   (bf16) as many CTAs as the GPU holds at once, each with an equal share of all turns in the order of the
-//             units, whatever the lengths are: every CTA adds up the lengths to find its share. A unit counts for
+//             over a cache in fp32 (k_attend_simt) for all of many rows;
+//   kShares   (the tensor-core kernels: a cache in bf16, or in 8 bits with queries of either type) as many CTAs as the GPU
+//             holds at once, each with an equal share of all turns in the order of the units, whatever the lengths are: every CTA adds up the lengths to find its share. A unit counts for
 //             kUnitTurns more than it has, about what it costs to begin and end one; else the CTAs with many short units
 //             would be the last (64 sequences of U[1,8192] rows, 32 heads on 8: 160 -> 154 us; 11 of U[1,4240], 256
 //             heads on 16: 42 -> 28 us). A unit that falls to several CTAs is joined by a second kernel.

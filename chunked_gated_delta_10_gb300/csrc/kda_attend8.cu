@@ -8,7 +8,7 @@
 //
 // fp16 has five bits of exponent, so what the values meet there is held near the top of its range:
 //   - q times a power of two that brings the head's largest value to [2^14, 2^15): bf16's eight bits then are exact in
-//     fp16 down to 2^-31 of the largest. An fp32 query is two such values, 22 bits.
+//     fp16 down to 2^-31 of the largest. An fp32 query is two such values, 22 bits, or 2^-39 of the largest.
 //   - the weights p sv times 2^(m - M + 11), M a running whole number like the maximum m itself, raised where one of them
 //     passes 2^15. Each is two fp16 values: to 2^-22 of itself, or 2^-35 of the largest.
 // m and M are whole numbers (log2 units), so that rescaling l and acc rounds nothing.
@@ -19,7 +19,8 @@
 //     each 622 us, 6.9 TB/s. The start (lengths, shares, pages, first rows), uneven SMs and the second kernel take 10 us.
 //     570 instructions of a warp to 8 KB, 39 % of the issue slots; tensor cores busy 26 % of the time;
 //   one of 65536 rows, 16 heads on 2: 12.9 us (5.0 at that rate); one of 2048 rows, 32 heads on 8: 6.0 us; both latency;
-//   with 16 heads to a cache head, twice the products and weights to a byte, 112 us for the first of these.
+//   with 16 heads to a cache head, twice the products and weights to a byte, 113 us for the first of these: two CTAs an SM,
+//     whose instructions wait for one another (41 % of the issue slots, tensor cores busy 41 % of the time).
 // Where the rows come from matters more than how many are under way: the heads of a sequence take the same rows at the same
 // time (shares of all heads together: 93 -> 87 us; pages of 512 rows instead of 64 gain 3 %), and one tile of a warp under
 // way is faster than two (87 and 92 us, 12 warps to an SM; 8 warps of two tiles 95, 16 of one tile 95). Rows in registers, as
@@ -432,7 +433,10 @@ __global__ void __launch_bounds__(kWarps * 32, ctas8(NT, K, V)) k_attend8(Attend
                     if constexpr (QP == 2) {
                         // Sums of 16 rows, added to acc in fp32 and not by the tensor core, as above: the largest error of
                         // those cases fell from 2.4e-6 to 1.1e-6, for 1 % of the time with 4 heads to a cache head (4 % with 64
-                        // channels) and 4 % with 16. For bf16 queries the output's rounding hides the difference.
+                        // channels) and 4 % with 16. bf16 queries have their sums run on in the tensor core, over all of a
+                        // warp's rows: about 1e-5 of a sum over thousands of rows, where o's own rounding is 2^-9 to 2^-8 (of
+                        // outputs over 4096 to 32768 rows 0.1 to 0.25 % are not the exact value's rounding; of sums in fp32
+                        // at most 0.05 %).
 #pragma unroll
                         for (int j = 0; j < NT; ++j) {
                             float sum[4][4];

@@ -240,12 +240,15 @@ kda_status kda_cache8_append_granted(const kda_cache8* cache, const void* k, int
  * kda_cache_attend_sinks over such a cache: K[t] and V[t] are the values that
  * the rows stand for, e4m3 times the block's scale (of any sign and size; not
  * only those that kda_cache8_append leaves). Scores are sums of exact products
- * in fp32, of bf16 queries as they are and of fp32 queries to 22 bits. Weights
- * times the scales of V enter the products as two fp16 values, to 2^-22, or
- * 2^-35 of the largest (scales of 2^-100 and more). A scale of K is a factor of
- * its row's score; an infinite one of V makes its rows' values infinite (NaN
- * where they are 0). q and o are in `dtype`; arguments, limits and errors
- * are otherwise the same.
+ * q . K8 in fp32 (which have to be finite there before the scales count), of
+ * bf16 queries as they are down to 2^-31 of the head's largest value, of fp32
+ * queries to 22 bits, or 2^-39 of the largest (both of heads whose largest value
+ * is 2^-100 or more). Weights times the scales of V enter the products as two
+ * fp16 values, to 2^-22, or 2^-35 of the largest (scales of 2^-100 and more); a
+ * weight below 2^-90 of the largest may count as 0, however large its row's
+ * scale. A scale of K is a factor of its row's score; an infinite one of V makes
+ * its rows' values infinite (NaN where they are 0). q and o are in `dtype`;
+ * arguments, limits and errors are otherwise the same.
  */
 kda_status kda_cache8_attend(const kda_cache8* cache, const void* q, int64_t q_stride, int32_t HQ, int32_t N,
                              const int32_t* page_table, int64_t table_stride, int32_t max_pages, const int32_t* kv_lens,
@@ -284,9 +287,10 @@ size_t kda_cache8_attend_workspace_bytes(const kda_cache8* cache, int32_t HQ, in
  *   slots       int64 [rows], nullable: of each new row, its page * page_size
  *               plus its row in the page; -1 where it has no page or its
  *               sequence was not served, and behind the last new row. Where
- *               there are more than `rows`, status is set.
+ *               there are more than `rows`, status is set. (For a caller's own
+ *               kernels: kda_cache_append goes by the table.)
  *   granted     int32 [N], nullable: new_lens[n], or kv_lens[n] where the
- *               sequence was not served
+ *               sequence was not served. It overlaps neither of them.
  *   status      int32, nullable
  *   ws          kda_cache_resize_workspace_bytes(N, max_pages, rows) bytes, 16-byte
  *               aligned (NULL where that is 0)
